@@ -59,6 +59,8 @@ typedef enum {
 #define SV_DEV_BAD_BLOCK 0x1   /* a block-table entry outside [0, num_blocks) */
 #define SV_DEV_BAD_INDEX 0x2   /* a visual index outside [0, n_vis) */
 #define SV_DEV_BAD_LENGTH 0x4  /* a per-sequence length outside its capacity; that sequence is skipped */
+#define SV_DEV_BAD_POSITION 0x8  /* a rotation position outside the table; that token is skipped */
+#define SV_DEV_NO_PAGES  0x20  /* fewer free pages than a reservation needs; nothing was reserved */
 #define SV_DEV_TIMEOUT   0x10  /* a bounded wait inside a kernel gave up (2 s); results undefined */
 
 /* Tokens per KV page (fixed). */
@@ -102,8 +104,10 @@ typedef struct {
  * A sequence whose counts are out of range sets SV_DEV_BAD_LENGTH and is
  * skipped (its indices read -1, its attention output 0).
  * Accepted by sv_retrieve_topk, sv_retrieve_topk_noalloc,
- * sv_sparse_decode_attn and sv_kv_append; the other calls taking a batch
- * return SV_ERR_UNSUPPORTED when any of the arrays is set.
+ * sv_sparse_decode_attn, sv_decode_append_attn, sv_kv_append,
+ * sv_qk_norm_rope_append, sv_tree_attn, sv_kv_accept and sv_pages_reserve
+ * (sv_pages_fork and sv_pages_release read no lengths); the other calls taking
+ * a batch return SV_ERR_UNSUPPORTED when any of the arrays is set.
  * Zero-initialise the struct so that the arrays default to NULL.
  */
 typedef struct {
@@ -422,6 +426,203 @@ sv_status sv_decode_append_attn(const void* q, int H, float scale, const sv_kv_l
                                 const sv_seq_batch* seqs, const void* k_new, const void* v_new,
                                 const int32_t* vis_idx, int k, void* out, float* lse, void* ws,
                                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norm and rotation of queries and keys.  (No counterpart on the SparseVILA
+ * pages: their models bring it; the cache and the salience operands hold
+ * queries and keys after it.)
+ *
+ * For each head of each token, in fp32 with one rounding to bf16 at the end:
+ *   x' = x * rsqrt(mean(x^2) + eps) * w             (w NULL: x' = x)
+ *   pair p of x', (a, c), becomes (a cos - c sin, a sin + c cos) with
+ *   (cos, sin) = cos_sin[pos[axis(p)][b][t]][p],  p < rot_dim / 2
+ * Elements from rot_dim on are not rotated.
+ *
+ * cos_sin     : fp32 [n_pos][rot_dim / 2][2], 16-byte aligned.
+ * rot_dim     : a multiple of 8, at most the head dim; 0: no rotation
+ *               (cos_sin and pos are then not read).
+ * interleaved : 0: pair p is elements (p, rot_dim / 2 + p); else (2p, 2p + 1).
+ * pos         : DEVICE int32 [n_axes][B][T].  A position outside [0, n_pos)
+ *               sets SV_DEV_BAD_POSITION and that token's outputs are left as
+ *               they were.
+ * n_axes      : 1 to 3 positions per token; pairs are split between them in
+ *               consecutive sections of section[0], [1], ... pairs, which add
+ *               up to rot_dim / 2 (n_axes 1: section is not read).  Positions
+ *               of an axis whose section is empty are not read.
+ * q_weight, k_weight : bf16 [head dim], 16-byte aligned, or NULL: no norm.
+ */
+typedef struct {
+  const float* cos_sin;
+  int32_t n_pos;
+  int32_t rot_dim;
+  int32_t interleaved;
+  const int32_t* pos;
+  int32_t n_axes;
+  int32_t section[3];
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+} sv_rotation;
+
+/*
+ * Encoder form: token-major projections to the operands of
+ * sv_salience_prefill / sv_salience_summary.
+ * q, k         : bf16 [B][N][H][d] and [B][N][Hk][d]; consecutive tokens (of
+ *                all B * N) lie q_stride / k_stride elements apart, so slices
+ *                of a fused projection are read in place.  Strides: multiples
+ *                of 8, at least H * d and Hk * d.
+ * q_out, k_out : out bf16 [B][H][N][d], [B][Hk][N][d]; they must not overlap
+ *                the inputs or one another.
+ * d            : 64, 72, 80 or 128.
+ * ws           : sv_evict_workspace_bytes() (the status word).
+ */
+sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int B, int N,
+                          int H, int Hk, int d, const sv_rotation* rot, void* q_out, void* k_out, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * Decoder form: sv_kv_append of T new tokens whose queries and keys are
+ * normalised and rotated on the way; values are copied.
+ * q, k, v : bf16 [B][T][H][d], [B][T][Hkv][d] twice, with token strides as
+ *           above.  Keys and values go to positions n_vis + n_text + t
+ *           (n_vis_seq[b] + n_text_seq[b] + t), as by sv_kv_append; the caller
+ *           then adds T (or n_new[b]) to n_text.
+ * n_new   : optional DEVICE int32 [B]: only the first n_new[b] tokens of
+ *           sequence b are there; the rows behind them are neither read nor
+ *           written.  A count outside [0, T] sets SV_DEV_BAD_LENGTH and the
+ *           sequence is skipped.
+ * q_out   : out bf16 [B][T][H][d]; q itself (with q_stride == H * d) or apart
+ *           from q, k and v.
+ * A page outside the pool sets SV_DEV_BAD_BLOCK; the token's queries are
+ * still written.  d: 64 or 128.  ws: sv_evict_workspace_bytes().
+ */
+sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, int T, int H, const sv_rotation* rot,
+                                 const sv_kv_layer* layer, const sv_seq_batch* seqs, const int32_t* n_new,
+                                 void* q_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of T new tokens per sequence over the cache: drafted tokens under
+ * a tree mask (verification of a speculative draft), or the rows of a
+ * question.  (No counterpart on the SparseVILA pages: their decode takes one
+ * token at a time; the token set is that of sv_sparse_decode_attn.)
+ *
+ *   T[b][g] = vis_idx[b][g][0..k) U [n_vis, n_vis + n_text) U drafted
+ *   out[b][t][h] = softmax over T[b][g], g = h / G, of scale * q . K, times V
+ *
+ * The T tokens' own K / V have been appended at positions n_vis + n_text + s
+ * (sv_kv_append or sv_qk_norm_rope_append) and are not yet in n_text.
+ * tree_mask : DEVICE uint64 [B][T], T <= 64: token t sees drafted token s iff
+ *             bit s is set (its own bit included; bits from T or n_new[b] on
+ *             are ignored).  NULL: token t sees drafted tokens 0 .. t (any
+ *             T up to 65536), e.g. a question's prefill; lse then serves as
+ *             the lse of sv_retrieve_topk_softmax.
+ * n_new     : optional DEVICE int32 [B]: sequence b drafted n_new[b] <= T
+ *             tokens; rows of out and lse behind them are left as they were.
+ *             A count outside [0, T] sets SV_DEV_BAD_LENGTH; the sequence then
+ *             reads as one without tokens (all T rows out 0, lse -inf).
+ * vis_idx, k, seqs : as for sv_sparse_decode_attn (a skipped sequence's rows
+ *             read 0 and -inf; tokens of a page outside the pool are not
+ *             attended).
+ * q, out    : bf16 [B][T][H][d], 16-byte aligned; out may be q.
+ * lse       : optional out fp32 [B][T][H].  A row that sees no token at all
+ *             has out 0 and lse -inf.
+ * A drafted token that a row does not see has no part in it, whatever its K
+ * and V hold (infinities and NaN included).
+ * ws        : sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, d, n_tokens),
+ *             n_tokens = k + n_text + T (k = n_vis when vis_idx is NULL).
+ * scale     : finite, >= 0.  Supported: d in {64, 128}, G = H / Hkv <= 16.
+ */
+size_t sv_tree_attn_workspace_bytes(int B, int T, int H, int n_kv_heads, int head_dim, int n_tokens);
+sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_layer* layer,
+                       const sv_seq_batch* seqs, const int32_t* vis_idx, int k, const uint64_t* tree_mask,
+                       const int32_t* n_new, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Accepted path of a draft: in every layer, the K / V rows of drafted tokens
+ * path[b][0 .. n_path[b]) (positions n_vis + n_text + path[b][i]) become the
+ * rows at n_vis + n_text + i; the caller then adds n_path[b] to the text
+ * length.  What the draft's other rows hold afterwards is unspecified.
+ * layers : host array; all with the same num_blocks, n_kv_heads, head_dim.
+ * T      : drafted tokens per sequence (the capacity of the draft).
+ * path   : DEVICE int32 [B][P], P <= min(T, 64), ascending values in [0, T);
+ *          otherwise SV_DEV_BAD_INDEX and the sequence is skipped.
+ * n_path : optional DEVICE int32 [B], each in [0, P]; NULL: P for all.
+ * Pages that hold these positions must not be shared (sv_pages_reserve).
+ * ws     : sv_evict_workspace_bytes().
+ */
+sv_status sv_kv_accept(const sv_kv_layer* layers, int n_layers, const sv_seq_batch* seqs, int T,
+                       const int32_t* path, int P, const int32_t* n_path, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * Pages shared between the branches of a conversation.  (No counterpart on
+ * the SparseVILA pages: their cache keeps the visual tokens across rounds,
+ * which is what branches share.)
+ *
+ * ref       : DEVICE int32 [num_blocks], 16-byte aligned: how many block-table
+ *             entries hold each page; 0: the page is free.
+ * n_pages   : DEVICE int32 [batch]: sequence b holds the first n_pages[b]
+ *             entries of its block-table row.
+ * num_blocks: pages of every layer's pools.
+ * The three calls below write ref, n_pages and seqs->block_table (its const
+ * notwithstanding), all on the device and without a host copy, so that they
+ * can be captured in a CUDA graph.  Counts are int32 and the result does not
+ * depend on the order in which the GPU runs.
+ * ws : sv_pages_workspace_bytes(batch, max_blocks, num_blocks).
+ */
+typedef struct {
+  int32_t* ref;
+  int32_t* n_pages;
+  int32_t num_blocks;
+} sv_page_pool;
+
+size_t sv_pages_workspace_bytes(int batch, int max_blocks, int num_blocks);
+
+/*
+ * Drops the pages of every sequence behind its first keep[b] tokens: the
+ * entries read -1, each page loses one reference, n_pages[b] becomes
+ * min(n_pages[b], ceil(keep[b] / 16)).  keep: DEVICE int32 [batch]; -1 leaves
+ * the sequence alone; NULL releases everything.  An entry outside the pool or
+ * a page without references sets SV_DEV_BAD_BLOCK.
+ */
+sv_status sv_pages_release(const sv_page_pool* pool, const sv_seq_batch* seqs, const int32_t* keep, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * Forks sequences: row child[i] of the block table, which must hold no pages,
+ * takes the entries of row parent[i], and each page gains a reference.
+ * parent, child : DEVICE int32 [n].
+ * n_tok         : optional DEVICE int32 [n]: share only the pages of the
+ *                 parent's first n_tok[i] tokens (the last one may be partly
+ *                 filled); NULL: all.
+ * A row outside the batch, a child that is also a parent or an earlier child
+ * of this call sets SV_DEV_BAD_INDEX; a child that holds pages or an n_tok
+ * beyond the parent's pages sets SV_DEV_BAD_LENGTH; that pair is skipped.
+ */
+sv_status sv_pages_fork(const sv_page_pool* pool, const sv_seq_batch* seqs, const int32_t* parent,
+                        const int32_t* child, int n, const int32_t* n_tok, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/*
+ * Makes positions [len_b, len_b + T_b) of every sequence writable, len_b =
+ * n_vis + n_text (or the per-sequence lengths), T_b = T or n_new[b]: entries
+ * from n_pages[b] on get fresh pages, and entries among these positions whose
+ * page has more than one reference at the start of the call get private pages
+ * with the shared page's rows, copied in all n_layers layers (two sequences
+ * that share a page and both reserve it get a copy each).  New pages are the
+ * lowest free ones, in order of sequence and position.  With fewer free pages
+ * than that takes nothing changes and SV_DEV_NO_PAGES is set.  A sequence
+ * whose lengths are out of range is skipped (SV_DEV_BAD_LENGTH).
+ * Call it before sv_kv_append, sv_qk_norm_rope_append, sv_kv_accept or (with
+ * the length cut to text_begin and T the tokens that move) an eviction of a
+ * middle span, when the pages may be shared.
+ * layers : host array of layers (n_layers may be 0: no copies), all with
+ *          pool->num_blocks pages and the same n_kv_heads, head_dim.
+ */
+sv_status sv_pages_reserve(const sv_page_pool* pool, const sv_kv_layer* layers, int n_layers,
+                           const sv_seq_batch* seqs, int T, const int32_t* n_new, void* ws, size_t ws_bytes,
+                           void* stream);
 
 /*
  * Read (and optionally clear) the device status word of a workspace.

@@ -39,3 +39,10 @@ from .sparsevila import (  # noqa: F401
     evict_qa_tokens,
     append_tokens,
 )
+from .drafts import (  # noqa: F401
+    PageBook,
+    accept_path,
+    norm_rope,
+    tree_attention,
+    tree_sees,
+)

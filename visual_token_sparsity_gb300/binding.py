@@ -20,6 +20,9 @@ SV_OK = 0
 SV_DEV_BAD_BLOCK = 0x1
 SV_DEV_BAD_INDEX = 0x2
 SV_DEV_BAD_LENGTH = 0x4
+SV_DEV_BAD_POSITION = 0x8
+SV_DEV_TIMEOUT = 0x10
+SV_DEV_NO_PAGES = 0x20
 BLOCK_TOKENS = 16
 
 
@@ -40,6 +43,17 @@ class sv_seq_batch(ctypes.Structure):
                 ("max_blocks", ctypes.c_int32), ("n_vis", ctypes.c_int32),
                 ("n_text", ctypes.c_int32), ("n_vis_seq", ctypes.c_void_p),
                 ("n_text_seq", ctypes.c_void_p), ("k_seq", ctypes.c_void_p)]
+
+
+class sv_rotation(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("pos", ctypes.c_void_p), ("n_axes", ctypes.c_int32),
+                ("section", ctypes.c_int32 * 3), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class sv_page_pool(ctypes.Structure):
+    _fields_ = [("ref", ctypes.c_void_p), ("n_pages", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
 
 
 _VP, _SZ, _I, _F, _I64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float, ctypes.c_int64
@@ -79,6 +93,22 @@ _SIGS = {
     "sv_retrieve_softmax_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "sv_retrieve_topk_softmax": (_I, [_VP, _I, _I, ctypes.c_float, ctypes.POINTER(sv_kv_layer),
                                       ctypes.POINTER(sv_seq_batch), _VP, _I, _VP, _VP, _VP, _SZ, _VP]),
+    "sv_qk_norm_rope": (_I, [_VP, _I64, _VP, _I64, _I, _I, _I, _I, _I, ctypes.POINTER(sv_rotation), _VP, _VP, _VP,
+                             _SZ, _VP]),
+    "sv_qk_norm_rope_append": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _I, _I, ctypes.POINTER(sv_rotation),
+                                    ctypes.POINTER(sv_kv_layer), ctypes.POINTER(sv_seq_batch), _VP, _VP, _VP, _SZ,
+                                    _VP]),
+    "sv_tree_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "sv_tree_attn": (_I, [_VP, _I, _I, _F, ctypes.POINTER(sv_kv_layer), ctypes.POINTER(sv_seq_batch), _VP, _I, _VP,
+                          _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "sv_kv_accept": (_I, [ctypes.POINTER(sv_kv_layer), _I, ctypes.POINTER(sv_seq_batch), _I, _VP, _I, _VP, _VP, _SZ,
+                          _VP]),
+    "sv_pages_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "sv_pages_release": (_I, [ctypes.POINTER(sv_page_pool), ctypes.POINTER(sv_seq_batch), _VP, _VP, _SZ, _VP]),
+    "sv_pages_fork": (_I, [ctypes.POINTER(sv_page_pool), ctypes.POINTER(sv_seq_batch), _VP, _VP, _I, _VP, _VP, _SZ,
+                           _VP]),
+    "sv_pages_reserve": (_I, [ctypes.POINTER(sv_page_pool), ctypes.POINTER(sv_kv_layer), _I,
+                              ctypes.POINTER(sv_seq_batch), _I, _VP, _VP, _SZ, _VP]),
     "sv_read_device_status": (_I, [_VP, _I, ctypes.POINTER(ctypes.c_int32), _VP]),
 }
 EXPORTED = tuple(_SIGS)
@@ -181,6 +211,91 @@ class SeqBatch:
     @n_text.setter
     def n_text(self, v):
         self.c.n_text = int(v)
+
+
+class Rotation:
+    """Norm and rotation of queries and keys: cos_sin fp32 [n_pos][rot / 2][2]
+    (or None: no rotation), pos int32 [B][T] or, with ``sections`` (pairs of
+    each axis, adding up to rot / 2), [axes][B][T]; optional bf16 [d] weights of
+    the per-head RMS norm (None: not normalised)."""
+
+    def __init__(self, cos_sin, pos, sections=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6):
+        self.cos_sin, self.pos, self.q_weight, self.k_weight = cos_sin, pos, q_weight, k_weight
+        n_pos = rot = 0
+        n_axes, sec = 1, [0, 0, 0]
+        self.tokens = None
+        if cos_sin is not None:
+            if cos_sin.dim() != 3 or cos_sin.shape[2] != 2:
+                raise ValueError(f"cos_sin must be [n_pos][rot / 2][2], got {tuple(cos_sin.shape)}")
+            n_pos, rot = cos_sin.shape[0], 2 * cos_sin.shape[1]
+            if sections is not None:
+                n_axes = len(sections)
+                if not 1 <= n_axes <= 3:
+                    raise ValueError(f"1 to 3 sections, got {n_axes}")
+                sec[:n_axes] = [int(x) for x in sections]
+                if n_axes == 1 and sec[0] != rot // 2:
+                    raise ValueError(f"sections add up to {sec[0]}, not to {rot // 2}")
+            lead = (n_axes,) if pos is not None and pos.dim() == 3 else ()
+            if pos is None or pos.dim() != 2 + len(lead) or (n_axes > 1 and not lead) or pos.shape[:-2] != lead:
+                raise ValueError(f"pos must be [B][T] or [{n_axes}][B][T]")
+            self.tokens = tuple(pos.shape[-2:])
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None and w.dim() != 1:
+                raise ValueError(f"{name} must be [head_dim]")
+        self.c = sv_rotation(_ptr(cos_sin, torch.float32, "cos_sin"), n_pos, rot, 1 if interleaved else 0,
+                             _ptr(pos if cos_sin is not None else None, torch.int32, "pos"), n_axes,
+                             (ctypes.c_int32 * 3)(*sec), _ptr(q_weight, torch.bfloat16, "q_weight"),
+                             _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps))
+
+    def check(self, B, T, d):
+        """The call's tokens and head dim are the descriptor's."""
+        if self.tokens is not None and self.tokens != (B, T):
+            raise ValueError(f"pos is for {self.tokens} tokens, the call has {(B, T)}")
+        for w, name in ((self.q_weight, "q_weight"), (self.k_weight, "k_weight")):
+            if w is not None and w.shape[0] != d:
+                raise ValueError(f"{name} has {w.shape[0]} elements, head_dim is {d}")
+
+
+class PagePool:
+    """Reference counts of a cache's pages (ref int32 [num_blocks], 0: free)
+    and the block-table entries each sequence holds (n_pages int32 [batch])."""
+
+    def __init__(self, ref, n_pages):
+        if ref.dim() != 1 or n_pages.dim() != 1:
+            raise ValueError("ref must be [num_blocks], n_pages [batch]")
+        self.ref, self.n_pages = ref, n_pages
+        self.c = sv_page_pool(_ptr(ref, torch.int32, "ref"), _ptr(n_pages, torch.int32, "n_pages"), ref.shape[0])
+
+
+def _rows(t, dtype, name):
+    """Pointer and token stride of a [B][T][heads][d] tensor whose tokens lie
+    evenly apart (a slice of a fused projection, for instance)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    B, T, h, d = t.shape
+    sb, st, sh, sd = t.stride()
+    ptr = ctypes.c_void_p(t.data_ptr())
+    if t.numel() == 0:
+        return ptr, h * d
+    stride = st if T > 1 else sb if B > 1 else h * d
+    if (sd != 1 and d > 1) or (sh != d and h > 1) or (B > 1 and T > 1 and sb != T * st):
+        raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, strides {t.stride()}")
+    return ptr, stride
+
+
+def _here(*tensors):
+    """The launch goes to the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
+
+
+def _want(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 # ------------------------------------------------------------------ sizes
@@ -360,6 +475,127 @@ def sv_pack_kv(src, seqs, vis_idx, k, dst, dst_seqs, ws, stream=None):
     lib = load()
     _check(lib.sv_pack_kv(ctypes.byref(src.c), ctypes.byref(seqs.c), _ptr(vis_idx, torch.int32, "vis_idx"), int(k),
                           ctypes.byref(dst.c), ctypes.byref(dst_seqs.c), *_ws(ws), _stream(stream)))
+
+
+def sv_qk_norm_rope(q, k, rot, q_out, k_out, ws, stream=None):
+    """q bf16 [B][N][H][d], k bf16 [B][N][Hk][d] (tokens may be strided: slices of a fused projection),
+    normalised and rotated as ``rot`` says -> q_out [B][H][N][d], k_out [B][Hk][N][d] (written)."""
+    lib = load()
+    B, N, H, d = q.shape
+    Hk = k.shape[2]
+    _want(k, (B, N, Hk, d), "k")
+    _want(q_out, (B, H, N, d), "q_out")
+    _want(k_out, (B, Hk, N, d), "k_out")
+    rot.check(B, N, d)
+    _here(q, k, q_out, k_out, ws, rot.cos_sin, rot.pos, rot.q_weight, rot.k_weight)
+    _check(lib.sv_qk_norm_rope(*_rows(q, torch.bfloat16, "q"), *_rows(k, torch.bfloat16, "k"), B, N, H, Hk, d,
+                               ctypes.byref(rot.c), _ptr(q_out, torch.bfloat16, "q_out"),
+                               _ptr(k_out, torch.bfloat16, "k_out"), *_ws(ws), _stream(stream)))
+
+
+def sv_qk_norm_rope_append(q, k, v, rot, layer, seqs, q_out, ws, n_new=None, stream=None):
+    """T new tokens per sequence: q bf16 [B][T][H][d], k, v bf16 [B][T][Hkv][d] (tokens may be strided);
+    q normalised and rotated -> q_out [B][T][H][d]; k likewise, and v, -> the cache at n_vis + n_text + t;
+    n_text unchanged (the caller adds T or n_new).  n_new int32 [B]: new tokens of each sequence, or None."""
+    lib = load()
+    B, T, H, d = q.shape
+    Hkv = layer.c.n_kv_heads
+    _want(q, (seqs.c.batch, T, H, layer.c.head_dim), "q")
+    _want(k, (B, T, Hkv, d), "k")
+    _want(v, (B, T, Hkv, d), "v")
+    _want(q_out, (B, T, H, d), "q_out")
+    _want(n_new, (B,), "n_new")
+    rot.check(B, T, d)
+    _here(q, k, v, q_out, ws, n_new, layer.k_pool, layer.v_pool, seqs.block_table, rot.cos_sin, rot.pos, rot.q_weight,
+          rot.k_weight)
+    _check(lib.sv_qk_norm_rope_append(*_rows(q, torch.bfloat16, "q"), *_rows(k, torch.bfloat16, "k"),
+                                      *_rows(v, torch.bfloat16, "v"), T, H, ctypes.byref(rot.c),
+                                      ctypes.byref(layer.c), ctypes.byref(seqs.c), _ptr(n_new, torch.int32, "n_new"),
+                                      _ptr(q_out, torch.bfloat16, "q_out"), *_ws(ws), _stream(stream)))
+
+
+def sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens):
+    return load().sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens)
+
+
+def sv_tree_attn(q, scale, layer, seqs, vis_idx, k, tree_mask, out, lse, ws, n_new=None, stream=None):
+    """T drafted tokens per sequence, already appended behind n_text, over the cache: q, out bf16
+    [B][T][H][d]; vis_idx int32 [B][Hkv][k] or None; tree_mask int64 (or uint64) [B][T], bit s of row t: t sees
+    s, or None: causal; lse fp32 [B][T][H] or None; n_new int32 [B]: drafted tokens of each sequence, or None."""
+    lib = load()
+    B, T, H, d = q.shape
+    _want(q, (seqs.c.batch, T, H, layer.c.head_dim), "q")
+    if vis_idx is not None:
+        _want(vis_idx, (B, layer.c.n_kv_heads, k), "vis_idx")
+    if tree_mask is not None:
+        _want(tree_mask, (B, T), "tree_mask")
+        if tree_mask.dtype not in (torch.int64, torch.uint64):
+            raise ValueError(f"tree_mask must be 64-bit integers, got {tree_mask.dtype}")
+    _want(out, (B, T, H, d), "out")
+    _want(lse, (B, T, H), "lse")
+    _want(n_new, (B,), "n_new")
+    _here(q, out, lse, ws, n_new, vis_idx, tree_mask, layer.k_pool, layer.v_pool, seqs.block_table)
+    _check(lib.sv_tree_attn(_ptr(q, torch.bfloat16, "q"), T, H, float(scale), ctypes.byref(layer.c),
+                            ctypes.byref(seqs.c), _ptr(vis_idx, torch.int32, "vis_idx"), int(k),
+                            _ptr(tree_mask, None, "tree_mask"), _ptr(n_new, torch.int32, "n_new"),
+                            _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"), *_ws(ws),
+                            _stream(stream)))
+
+
+def _layer_array(layers):
+    return (sv_kv_layer * max(1, len(layers)))(*[l.c for l in layers])
+
+
+def sv_kv_accept(layers, seqs, T, path, ws, n_path=None, stream=None):
+    """Compacts the accepted path of a draft of T tokens in every layer: path int32 [B][P] ascending drafted
+    indices (the first n_path[b] of a row, or all); n_text unchanged (the caller adds the accepted count)."""
+    lib = load()
+    B, P = path.shape
+    _want(path, (seqs.c.batch, P), "path")
+    _want(n_path, (B,), "n_path")
+    _here(path, n_path, ws, seqs.block_table, *(x for l in layers for x in (l.k_pool, l.v_pool)))
+    _check(lib.sv_kv_accept(_layer_array(layers), len(layers), ctypes.byref(seqs.c), int(T),
+                            _ptr(path, torch.int32, "path"), P, _ptr(n_path, torch.int32, "n_path"), *_ws(ws),
+                            _stream(stream)))
+
+
+def sv_pages_workspace_bytes(batch, max_blocks, num_blocks):
+    return load().sv_pages_workspace_bytes(batch, max_blocks, num_blocks)
+
+
+def sv_pages_release(pool, seqs, keep, ws, stream=None):
+    """Drops every sequence's pages behind its first keep[b] tokens (int32 [B]; -1: leave it; None: drop all)."""
+    lib = load()
+    _want(pool.n_pages, (seqs.c.batch,), "n_pages")
+    _want(keep, (seqs.c.batch,), "keep")
+    _here(pool.ref, pool.n_pages, seqs.block_table, keep, ws)
+    _check(lib.sv_pages_release(ctypes.byref(pool.c), ctypes.byref(seqs.c), _ptr(keep, torch.int32, "keep"),
+                                *_ws(ws), _stream(stream)))
+
+
+def sv_pages_fork(pool, seqs, parent, child, ws, n_tok=None, stream=None):
+    """Rows child[i] (holding no pages) share the pages of rows parent[i] (int32 [n]), or of their first
+    n_tok[i] tokens."""
+    lib = load()
+    n, = parent.shape
+    _want(pool.n_pages, (seqs.c.batch,), "n_pages")
+    _want(child, (n,), "child")
+    _want(n_tok, (n,), "n_tok")
+    _here(pool.ref, pool.n_pages, seqs.block_table, parent, child, n_tok, ws)
+    _check(lib.sv_pages_fork(ctypes.byref(pool.c), ctypes.byref(seqs.c), _ptr(parent, torch.int32, "parent"),
+                             _ptr(child, torch.int32, "child"), n, _ptr(n_tok, torch.int32, "n_tok"), *_ws(ws),
+                             _stream(stream)))
+
+
+def sv_pages_reserve(pool, layers, seqs, T, ws, n_new=None, stream=None):
+    """Makes the T (or n_new[b], int32 [B]) positions behind each sequence's tokens writable: fresh pages, and
+    private copies, in every layer, of the shared pages among them."""
+    lib = load()
+    _want(pool.n_pages, (seqs.c.batch,), "n_pages")
+    _want(n_new, (seqs.c.batch,), "n_new")
+    _here(pool.ref, pool.n_pages, seqs.block_table, n_new, ws, *(x for l in layers for x in (l.k_pool, l.v_pool)))
+    _check(lib.sv_pages_reserve(ctypes.byref(pool.c), _layer_array(layers), len(layers), ctypes.byref(seqs.c),
+                                int(T), _ptr(n_new, torch.int32, "n_new"), *_ws(ws), _stream(stream)))
 
 
 def sv_read_device_status(ws, clear=False, stream=None):

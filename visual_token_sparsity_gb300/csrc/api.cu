@@ -121,6 +121,117 @@ sv_status check_retrieve_args(const void* q, int R, int H, const sv_kv_layer* la
 }
 }  // namespace sv
 
+namespace {
+
+// ---- checks of the new-token, draft and page calls
+
+// token-major bf16 rows `stride` elements apart
+sv_status check_rows(const char* name, const void* p, int64_t stride, long long row) {
+  if (!aligned16(p)) return fail(SV_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < row || stride % 8)
+    return fail(SV_ERR_INVALID_ARG, "%s_stride = %lld: need a multiple of 8, at least %lld", name, (long long)stride,
+                row);
+  return SV_OK;
+}
+
+size_t row_extent(long long tokens, int64_t stride, long long row) {
+  return ((size_t)(tokens - 1) * (size_t)stride + (size_t)row) * 2;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+sv_status check_rotation(const sv_rotation* r, int d, long long n_tok) {
+  if (!r) return fail(SV_ERR_INVALID_ARG, "rotation descriptor is NULL");
+  if (r->rot_dim < 0 || r->rot_dim > d || r->rot_dim % 8)
+    return fail(SV_ERR_INVALID_ARG, "rot_dim = %d: need a multiple of 8, at most the head dim %d", r->rot_dim, d);
+  if (!(r->eps >= 0.f) || !std::isfinite(r->eps)) return fail(SV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((r->q_weight && !aligned16(r->q_weight)) || (r->k_weight && !aligned16(r->k_weight)))
+    return fail(SV_ERR_INVALID_ARG, "norm weights must be 16-byte aligned");
+  if (n_tok > 0x7fffffffLL) return fail(SV_ERR_INVALID_ARG, "more than 2^31 tokens");
+  if (r->rot_dim == 0) return SV_OK;
+  if (!r->cos_sin || !r->pos) return fail(SV_ERR_INVALID_ARG, "cos_sin and pos must be non-NULL");
+  if (!aligned16(r->cos_sin)) return fail(SV_ERR_INVALID_ARG, "cos_sin must be 16-byte aligned");
+  if (r->n_pos <= 0) return fail(SV_ERR_INVALID_ARG, "n_pos must be positive");
+  if (r->n_axes < 1 || r->n_axes > 3) return fail(SV_ERR_UNSUPPORTED, "n_axes = %d (1 to 3)", r->n_axes);
+  if (r->n_axes > 1) {
+    long long sum = 0;
+    for (int x = 0; x < r->n_axes; ++x) {
+      if (r->section[x] < 0) return fail(SV_ERR_INVALID_ARG, "negative section");
+      sum += r->section[x];
+    }
+    if (sum != r->rot_dim / 2)
+      return fail(SV_ERR_INVALID_ARG, "sections add up to %lld, not to rot_dim / 2 = %d", sum, r->rot_dim / 2);
+  }
+  return SV_OK;
+}
+
+void fill_rotation(sv::NormRopeArgs& a, const sv_rotation* r) {
+  a.q_weight = static_cast<const uint16_t*>(r->q_weight);
+  a.k_weight = static_cast<const uint16_t*>(r->k_weight);
+  a.eps = r->eps;
+  a.cos_sin = r->cos_sin; a.pos = r->pos; a.n_pos = r->n_pos;
+  a.rot = r->rot_dim; a.interleaved = r->interleaved != 0; a.n_axes = r->n_axes;
+  int end = 0;
+  for (int x = 0; x < 3; ++x) {
+    end += r->n_axes == 1 ? (x == 0 ? r->rot_dim / 2 : 0) : (x < r->n_axes ? r->section[x] : 0);
+    a.sec_end[x] = end;
+  }
+}
+
+// T more tokens behind n_vis + n_text fit the block table
+sv_status check_new_tokens(const sv_seq_batch* S, int T) {
+  if ((long long)S->n_vis + S->n_text + T > (long long)S->max_blocks * SV_BLOCK_TOKENS)
+    return fail(SV_ERR_INVALID_ARG, "%d new tokens overflow the block table", T);
+  return SV_OK;
+}
+
+sv_status check_layers(const sv_kv_layer* layers, int n_layers, const sv_seq_batch* seqs) {
+  if (n_layers < 0 || (n_layers > 0 && !layers) || !seqs)
+    return fail(SV_ERR_INVALID_ARG, "layers and seqs must be non-NULL");
+  for (int l = 0; l < n_layers; ++l) {
+    sv_status s = sv::check_cache(&layers[l], seqs, true);
+    if (s != SV_OK) return s;
+    if (layers[l].num_blocks != layers[0].num_blocks || layers[l].n_kv_heads != layers[0].n_kv_heads ||
+        layers[l].head_dim != layers[0].head_dim)
+      return fail(SV_ERR_INVALID_ARG, "layer %d differs in num_blocks, n_kv_heads or head_dim", l);
+  }
+  return SV_OK;
+}
+
+sv::LayerPools pools_of(const sv_kv_layer* layers, int n) {
+  sv::LayerPools p = {};
+  for (int l = 0; l < n; ++l) {
+    p.k[l] = layers[l].k_pool;
+    p.v[l] = layers[l].v_pool;
+  }
+  return p;
+}
+
+sv_status check_pages(const sv_page_pool* pool, const sv_seq_batch* seqs, void* ws, size_t ws_bytes,
+                      sv::PagesArgs& a) {
+  if (!pool || !seqs) return fail(SV_ERR_INVALID_ARG, "pool or batch descriptor is NULL");
+  if (!pool->ref || !pool->n_pages || !seqs->block_table)
+    return fail(SV_ERR_INVALID_ARG, "ref, n_pages or block table pointer is NULL");
+  if (!aligned16(pool->ref)) return fail(SV_ERR_INVALID_ARG, "ref must be 16-byte aligned");
+  if (pool->num_blocks <= 0 || seqs->batch < 0 || seqs->max_blocks <= 0)
+    return fail(SV_ERR_INVALID_ARG, "num_blocks and max_blocks must be positive, batch >= 0");
+  if (pool->num_blocks > (1 << 30) || (long long)seqs->batch * seqs->max_blocks > (1LL << 30))
+    return fail(SV_ERR_UNSUPPORTED, "more than 2^30 pages or block-table entries");
+  a.ref = pool->ref;
+  a.n_pages = pool->n_pages;
+  a.num_pages = pool->num_blocks;
+  a.block_table = const_cast<int32_t*>(seqs->block_table);
+  a.batch = seqs->batch;
+  a.max_blocks = seqs->max_blocks;
+  a.status = status_word(ws);
+  return check_ws(ws, ws_bytes, sv_pages_workspace_bytes(seqs->batch, seqs->max_blocks, pool->num_blocks));
+}
+
+}  // namespace
+
 using sv::check_cache;
 
 extern "C" {
@@ -507,6 +618,191 @@ sv_status sv_kv_append(const sv_kv_layer* layer, const sv_seq_batch* seqs, const
                                           static_cast<cudaStream_t>(stream), lens_of(seqs), seqs->n_vis,
                                           seqs->n_text),
                      "sv_kv_append");
+}
+
+// ------------------------------------------------------------------ new tokens, drafts and branches
+
+sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int B, int N, int H,
+                          int Hk, int d, const sv_rotation* rot, void* q_out, void* k_out, void* ws,
+                          size_t ws_bytes, void* stream) {
+  if (!q || !k || !q_out || !k_out) return fail(SV_ERR_INVALID_ARG, "q, k, q_out and k_out must be non-NULL");
+  if (B < 0 || N < 0 || H <= 0 || Hk <= 0) return fail(SV_ERR_INVALID_ARG, "need B >= 0, N >= 0, H > 0, Hk > 0");
+  if (!sv::salience_head_dim_supported(d)) return fail(SV_ERR_UNSUPPORTED, "head_dim %d (64, 72, 80 or 128)", d);
+  const long long n_tok = (long long)B * N, qr = (long long)H * d, kr = (long long)Hk * d;
+  sv_status s = check_rows("q", q, q_stride, qr);
+  if (s == SV_OK) s = check_rows("k", k, k_stride, kr);
+  if (s == SV_OK) s = check_rotation(rot, d, n_tok);
+  if (s == SV_OK) s = check_ws(ws, ws_bytes, sv_evict_workspace_bytes());
+  if (s != SV_OK) return s;
+  if (!aligned16(q_out) || !aligned16(k_out))
+    return fail(SV_ERR_INVALID_ARG, "q_out and k_out must be 16-byte aligned");
+  if (n_tok == 0) return SV_OK;
+  const size_t q_in = row_extent(n_tok, q_stride, qr), k_in = row_extent(n_tok, k_stride, kr);
+  const size_t qb = (size_t)n_tok * qr * 2, kb = (size_t)n_tok * kr * 2;
+  if (overlap(q_out, qb, q, q_in) || overlap(q_out, qb, k, k_in) || overlap(k_out, kb, q, q_in) ||
+      overlap(k_out, kb, k, k_in) || overlap(q_out, qb, k_out, kb))
+    return fail(SV_ERR_INVALID_ARG, "q_out and k_out must not overlap the inputs or one another");
+  sv::NormRopeArgs a = {};
+  fill_rotation(a, rot);
+  a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k);
+  a.q_stride = q_stride; a.k_stride = k_stride;
+  a.B = B; a.T = N; a.H = H; a.Hk = Hk;
+  a.q_out = static_cast<uint16_t*>(q_out); a.k_out = static_cast<uint16_t*>(k_out);
+  a.status = status_word(ws);
+  return cuda_status(sv::launch_norm_rope(a, d, false, static_cast<cudaStream_t>(stream)), "sv_qk_norm_rope");
+}
+
+sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, int T, int H, const sv_rotation* rot, const sv_kv_layer* layer,
+                                 const sv_seq_batch* seqs, const int32_t* n_new, void* q_out, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  sv_status s = check_cache(layer, seqs, true);
+  if (s != SV_OK) return s;
+  if (!q || !k || !v || !q_out) return fail(SV_ERR_INVALID_ARG, "q, k, v and q_out must be non-NULL");
+  const int Hkv = layer->n_kv_heads, d = layer->head_dim;
+  if (T < 0) return fail(SV_ERR_INVALID_ARG, "T must be >= 0");
+  if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
+  s = check_new_tokens(seqs, T);
+  const long long n_tok = (long long)seqs->batch * T, qr = (long long)H * d, kv = (long long)Hkv * d;
+  if (s == SV_OK) s = check_rows("q", q, q_stride, qr);
+  if (s == SV_OK) s = check_rows("k", k, k_stride, kv);
+  if (s == SV_OK) s = check_rows("v", v, v_stride, kv);
+  if (s == SV_OK) s = check_rotation(rot, d, n_tok);
+  if (s == SV_OK) s = check_ws(ws, ws_bytes, sv_evict_workspace_bytes());
+  if (s != SV_OK) return s;
+  if (!aligned16(q_out)) return fail(SV_ERR_INVALID_ARG, "q_out must be 16-byte aligned");
+  if (n_tok == 0) return SV_OK;
+  const size_t qb = (size_t)n_tok * qr * 2;
+  const bool in_place = q_out == q && q_stride == qr;
+  if ((!in_place && overlap(q_out, qb, q, row_extent(n_tok, q_stride, qr))) ||
+      overlap(q_out, qb, k, row_extent(n_tok, k_stride, kv)) || overlap(q_out, qb, v, row_extent(n_tok, v_stride, kv)))
+    return fail(SV_ERR_INVALID_ARG, "q_out must be q itself or not overlap q, k and v");
+  sv::NormRopeArgs a = {};
+  fill_rotation(a, rot);
+  a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k); a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.B = seqs->batch; a.T = T; a.H = H; a.Hk = Hkv;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(layer->k_pool); a.v_out = static_cast<uint16_t*>(layer->v_pool);
+  a.status = status_word(ws);
+  a.block_table = seqs->block_table; a.num_blocks = layer->num_blocks; a.max_blocks = seqs->max_blocks;
+  a.n_vis = seqs->n_vis; a.n_text = seqs->n_text; a.lens = lens_of(seqs); a.n_new = n_new;
+  return cuda_status(sv::launch_norm_rope(a, d, true, static_cast<cudaStream_t>(stream)), "sv_qk_norm_rope_append");
+}
+
+size_t sv_tree_attn_workspace_bytes(int B, int T, int H, int n_kv_heads, int head_dim, int n_tokens) {
+  if (B < 0 || T < 0 || H <= 0 || n_kv_heads <= 0 || H % n_kv_heads || head_dim <= 0 || n_tokens < 0)
+    return kStatusBytes;
+  return kStatusBytes + round256(sv::tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens));
+}
+
+sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_layer* layer, const sv_seq_batch* seqs,
+                       const int32_t* vis_idx, int k, const uint64_t* tree_mask, const int32_t* n_new, void* out,
+                       float* lse, void* ws, size_t ws_bytes, void* stream) {
+  sv_status s = check_cache(layer, seqs, true);
+  if (s != SV_OK) return s;
+  if (!q || !out) return fail(SV_ERR_INVALID_ARG, "q and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(SV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const int Hkv = layer->n_kv_heads;
+  if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
+  if (H / Hkv > 16) return fail(SV_ERR_UNSUPPORTED, "query heads per KV head %d > 16", H / Hkv);
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(SV_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (T < 0 || T > 65536) return fail(SV_ERR_INVALID_ARG, "need 0 <= T <= 65536 (T = %d)", T);
+  if (tree_mask && T > 64) return fail(SV_ERR_UNSUPPORTED, "a tree mask holds at most 64 drafted tokens (T = %d)", T);
+  s = check_new_tokens(seqs, T);
+  if (s != SV_OK) return s;
+  const int k_vis = vis_idx ? k : seqs->n_vis;
+  if (vis_idx && (k < 0 || k > seqs->n_vis)) return fail(SV_ERR_INVALID_ARG, "need 0 <= k <= n_vis");
+  if ((long long)seqs->batch * T * H > 0x7fffffffLL) return fail(SV_ERR_INVALID_ARG, "batch * T * H too large");
+  const long long n_tok = (long long)k_vis + seqs->n_text + T;   // <= max_blocks * 16
+  if (n_tok > 0x7fffffffLL - 1024) return fail(SV_ERR_UNSUPPORTED, "more than 2^31 tokens");
+  s = check_ws(ws, ws_bytes,
+               sv_tree_attn_workspace_bytes(seqs->batch, T, H, Hkv, layer->head_dim, (int)n_tok));
+  if (s != SV_OK) return s;
+  if (seqs->batch == 0 || T == 0) return SV_OK;
+  sv::TreeArgs a = {};
+  a.q = q; a.T = T; a.H = H; a.scale_log2 = scale * 1.4426950408889634f;
+  a.k_pool = layer->k_pool; a.v_pool = layer->v_pool;
+  a.num_blocks = layer->num_blocks; a.Hkv = Hkv; a.D = layer->head_dim;
+  a.block_table = seqs->block_table; a.max_blocks = seqs->max_blocks;
+  a.vis_idx = vis_idx; a.k_vis = k_vis; a.n_vis = seqs->n_vis; a.n_text = seqs->n_text; a.batch = seqs->batch;
+  a.lens = lens_of(seqs);
+  a.tree_mask = tree_mask; a.n_new = n_new;
+  a.out = out; a.lse = lse;
+  a.ws = after_status(ws); a.status = status_word(ws);
+  return cuda_status(sv::launch_tree_attn(a, static_cast<cudaStream_t>(stream)), "sv_tree_attn");
+}
+
+sv_status sv_kv_accept(const sv_kv_layer* layers, int n_layers, const sv_seq_batch* seqs, int T, const int32_t* path,
+                       int P, const int32_t* n_path, void* ws, size_t ws_bytes, void* stream) {
+  sv_status s = check_layers(layers, n_layers, seqs);
+  if (s != SV_OK) return s;
+  if (T < 0 || P < 0 || P > T) return fail(SV_ERR_INVALID_ARG, "need 0 <= P <= T (P = %d, T = %d)", P, T);
+  if (P > 64) return fail(SV_ERR_UNSUPPORTED, "an accepted path has at most 64 tokens (P = %d)", P);
+  if (P > 0 && !path) return fail(SV_ERR_INVALID_ARG, "path must be non-NULL");
+  s = check_new_tokens(seqs, T);
+  if (s == SV_OK) s = check_ws(ws, ws_bytes, sv_evict_workspace_bytes());
+  if (s != SV_OK) return s;
+  for (int l0 = 0; l0 < n_layers; l0 += sv::kMaxLayers) {
+    const int n = n_layers - l0 < sv::kMaxLayers ? n_layers - l0 : sv::kMaxLayers;
+    const cudaError_t e = sv::launch_kv_accept(pools_of(layers + l0, n), n, layers->num_blocks, layers->n_kv_heads,
+                                               layers->head_dim, seqs->block_table, seqs->max_blocks, seqs->batch,
+                                               lens_of(seqs), seqs->n_vis, seqs->n_text, T, path, P, n_path,
+                                               status_word(ws), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_status(e, "sv_kv_accept");
+  }
+  return SV_OK;
+}
+
+size_t sv_pages_workspace_bytes(int batch, int max_blocks, int num_blocks) {
+  if (batch < 0 || max_blocks < 0 || num_blocks < 0) return kStatusBytes;
+  return kStatusBytes + round256(sv::pages_workspace_bytes(batch, max_blocks, num_blocks));
+}
+
+sv_status sv_pages_release(const sv_page_pool* pool, const sv_seq_batch* seqs, const int32_t* keep, void* ws,
+                           size_t ws_bytes, void* stream) {
+  sv::PagesArgs a;
+  sv_status s = check_pages(pool, seqs, ws, ws_bytes, a);
+  if (s != SV_OK) return s;
+  return cuda_status(sv::launch_pages_release(a, keep, static_cast<cudaStream_t>(stream)), "sv_pages_release");
+}
+
+sv_status sv_pages_fork(const sv_page_pool* pool, const sv_seq_batch* seqs, const int32_t* parent,
+                        const int32_t* child, int n, const int32_t* n_tok, void* ws, size_t ws_bytes, void* stream) {
+  sv::PagesArgs a;
+  sv_status s = check_pages(pool, seqs, ws, ws_bytes, a);
+  if (s != SV_OK) return s;
+  if (n < 0) return fail(SV_ERR_INVALID_ARG, "n must be >= 0");
+  if (n > 0 && (!parent || !child)) return fail(SV_ERR_INVALID_ARG, "parent and child must be non-NULL");
+  return cuda_status(sv::launch_pages_fork(a, parent, child, n, n_tok, static_cast<cudaStream_t>(stream)),
+                     "sv_pages_fork");
+}
+
+sv_status sv_pages_reserve(const sv_page_pool* pool, const sv_kv_layer* layers, int n_layers, const sv_seq_batch* seqs,
+                           int T, const int32_t* n_new, void* ws, size_t ws_bytes, void* stream) {
+  sv::PagesArgs a;
+  sv_status s = check_pages(pool, seqs, ws, ws_bytes, a);
+  if (s == SV_OK && n_layers != 0) s = check_layers(layers, n_layers, seqs);
+  if (s != SV_OK) return s;
+  if (n_layers > 0 && layers->num_blocks != pool->num_blocks)
+    return fail(SV_ERR_INVALID_ARG, "the layers have %d pages, the pool %d", layers->num_blocks, pool->num_blocks);
+  if (seqs->n_vis < 0 || seqs->n_text < 0 || T < 0) return fail(SV_ERR_INVALID_ARG, "negative length");
+  s = check_new_tokens(seqs, T);
+  if (s != SV_OK) return s;
+  constexpr int kGroups = 16;
+  if (n_layers > kGroups * sv::kMaxLayers)
+    return fail(SV_ERR_UNSUPPORTED, "more than %d layers", kGroups * sv::kMaxLayers);
+  sv::LayerPools pools[kGroups];
+  int count[kGroups], groups = 0;
+  for (int l0 = 0; l0 < n_layers; l0 += sv::kMaxLayers, ++groups) {
+    count[groups] = n_layers - l0 < sv::kMaxLayers ? n_layers - l0 : sv::kMaxLayers;
+    pools[groups] = pools_of(layers + l0, count[groups]);
+  }
+  const int page_bytes = n_layers > 0 ? layers->n_kv_heads * SV_BLOCK_TOKENS * layers->head_dim * 2 : 0;
+  return cuda_status(sv::launch_pages_reserve(a, lens_of(seqs), seqs->n_vis, seqs->n_text, T, n_new, pools, groups,
+                                              count, page_bytes, after_status(ws), num_sms(),
+                                              static_cast<cudaStream_t>(stream)),
+                     "sv_pages_reserve");
 }
 
 sv_status sv_read_device_status(void* ws, int clear, int32_t* status_out, void* stream) {

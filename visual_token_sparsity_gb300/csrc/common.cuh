@@ -12,6 +12,8 @@ constexpr int kBlockTokens = 16;
 constexpr int kStatusBadBlock = 0x1;
 constexpr int kStatusBadIndex = 0x2;
 constexpr int kStatusBadLength = 0x4;  // a per-sequence length outside its capacity
+constexpr int kStatusBadPosition = 0x8;  // a rotation position outside the table
+constexpr int kStatusNoPages = 0x20;     // fewer free pages than a reservation needs
 constexpr int kStatusTimeout = 0x10;   // a bounded wait inside a kernel gave up
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -120,6 +120,85 @@ cudaError_t launch_kv_append(void* k_pool, void* v_pool, int num_blocks, int Hkv
                              cudaStream_t stream, const SeqLens& lens = SeqLens{}, int n_vis = 0,
                              int n_text = 0);
 
+// ---- norm and rotation of queries and keys (norm_rope.cu).  Rows are
+// token-major, [B][T] tokens of a.*_stride elements; the outputs are
+// [B][heads][T][d] (encoder operands) or, with `append`, q_out [B][T][H][d]
+// and the K / V pools (a.k_out, a.v_out) of the paged cache.
+struct NormRopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long q_stride, k_stride, v_stride;
+  int B, T, H, Hk;
+  const uint16_t* q_weight;   // [d] or nullptr (no norm)
+  const uint16_t* k_weight;
+  float eps;
+  const float* cos_sin;       // [n_pos][rot / 2][2]
+  const int32_t* pos;         // [n_axes][B][T]
+  int n_pos, rot, interleaved, n_axes;
+  int sec_end[3];             // pairs [sec_end[x - 1], sec_end[x]) turn by axis x
+  uint16_t* q_out;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int* status;
+  // append: where the new tokens go
+  const int32_t* block_table;
+  int num_blocks, max_blocks, n_vis, n_text;
+  SeqLens lens;
+  const int32_t* n_new;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, cudaStream_t stream);
+
+// ---- attention of T drafted tokens over the paged cache (tree_attn.cu)
+struct TreeArgs {
+  const void* q;
+  int T, H;
+  float scale_log2;
+  const void* k_pool;
+  const void* v_pool;
+  int num_blocks, Hkv, D;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* vis_idx;
+  int k_vis, n_vis, n_text, batch;   // capacities with per-sequence lengths
+  SeqLens lens;
+  const uint64_t* tree_mask;         // [batch][T], or nullptr: each sees itself and the earlier ones
+  const int32_t* n_new;              // [batch] or nullptr
+  void* out;
+  float* lse;
+  void* ws;                          // tree_attn_workspace_bytes
+  int* status;
+};
+size_t tree_attn_workspace_bytes(int B, int T, int H, int Hkv, int D, int n_tokens);
+cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t stream);
+
+// ---- pages shared between branches (pages.cu)
+constexpr int kMaxLayers = 64;   // layers of one launch
+struct LayerPools {
+  void* k[kMaxLayers];
+  void* v[kMaxLayers];
+};
+struct PagesArgs {
+  int32_t* ref;          // [num_pages] block-table entries that hold each page
+  int32_t* n_pages;      // [batch] entries each sequence holds
+  int num_pages;
+  int32_t* block_table;  // [batch][max_blocks]
+  int batch, max_blocks;
+  int* status;
+};
+cudaError_t launch_pages_release(const PagesArgs& a, const int32_t* keep, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesArgs& a, const int32_t* parent, const int32_t* child, int n,
+                              const int32_t* n_tok, cudaStream_t stream);
+size_t pages_workspace_bytes(long long batch, long long max_blocks, long long num_pages);
+// pools: n_pools groups of layers[i] layers each
+cudaError_t launch_pages_reserve(const PagesArgs& a, const SeqLens& lens, int n_vis, int n_text, int T,
+                                 const int32_t* n_new, const LayerPools* pools, int n_pools, const int* layers,
+                                 int page_bytes, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_accept(const LayerPools& pools, int layers, int num_blocks, int Hkv, int D,
+                             const int32_t* block_table, int max_blocks, int batch, const SeqLens& lens, int n_vis,
+                             int n_text, int T, const int32_t* path, int P, const int32_t* n_path, int* status,
+                             cudaStream_t stream);
+
 // ---- prefill salience (salience.cu)
 cudaError_t launch_head_mean(const float* colsum, int B, int H, int N, float inv, float* out,
                              cudaStream_t stream);
