@@ -168,6 +168,11 @@ struct TreeArgs {
   float* lse;
   void* ws;                          // tree_attn_workspace_bytes
   int* status;
+  // set by launch_tree_attn: query heads per KV head, tiles of query rows,
+  // pieces of one row tile's work, partial results
+  int G, row_tiles, columns;
+  float* part_ml;
+  float* part_o;
 };
 size_t tree_attn_workspace_bytes(int B, int T, int H, int Hkv, int D, int n_tokens);
 cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t stream);

@@ -6,90 +6,862 @@
 //   z_i = scale q . K[tok(i)], seen(i) = i < k + n_text or bit (i - k - n_text)
 //   out = sum_seen exp(z_i - m) V[tok(i)] / sum_seen exp(z_i - m)
 //
-// One warp per query row: a lane holds D / 32 dims of q and of the output and
-// keeps the running maximum and sum of the softmax.
+// The R = T * G rows of a KV head (G query heads of each token) share its
+// keys and values, so both products are matrix products on the tcgen05
+// tensor cores: S = Q K^T (128 rows x 128 tokens), then O += P V with P as
+// the bf16 A operand in tensor memory and V read token-major from shared
+// memory.  One pass: running maximum and sum per row in fp32 registers, the
+// accumulator rescaled only when a row's maximum grows by more than 2^8 (P
+// then stays below 2^8, its relative rounding is the same).
+//
+// A CTA runs two streams, each with its own S, P, O in tensor memory and four
+// softmax warps, so that one's products run while the other's weights are
+// formed.  Up to 128 rows: the streams take alternate token tiles of the same
+// rows and their (m, l, O) are joined at the end (bound by the cache's bytes:
+// padding to 128 rows costs 1024 tensor cycles a tile against the 2800 that
+// its 64 KB take to arrive).  More rows: the streams take 128 rows each of
+// the same token tile, which halves the bytes per product.
+//
+// Work is cut evenly whatever the shapes: for each tile of rows the token
+// tiles of all (sequence, KV head) units form one line, cut into equal pieces,
+// one per CTA column; a unit that lies in several pieces leaves fp32 partials
+// that a second kernel joins in a fixed order.  CTAs of one piece and
+// different row tiles are neighbours, so they meet in L2.
+//
+// Warps: 0-7 softmax and epilogue (one row per thread), 8 MMA issue, 9 query
+// rows, 10-13 cache rows: cp.async gathers of 16 bytes into a ring of 128-row
+// K and V tiles in the 128-byte-swizzled layout the MMA reads, page-table and
+// index loads running two tiles ahead.  Rows that are not there (behind the
+// end, a bad page) are zero-filled and masked.
 #include "common.cuh"
+#include "fastmath.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace sv {
 
+namespace {
+
+constexpr int kTile = 128;                  // tokens of a tile, rows of a stream
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8, kQueryWarp = 9, kLoadWarp = 10;
+constexpr int kLoadWarps = 4;
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kTmemCols = 512;              // S0 | S1 | O0 | O1, 128 columns each
+constexpr int kCtas = 152;                  // one per SM
+constexpr int kMaxSlots = 12;
+constexpr int kValidRing = 16;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr size_t kMaxSmem = 232448;         // 227 KB
+constexpr float kRescale = 8.f;             // log2 growth of a maximum that rescales O
+static_assert(kLoadWarps * 32 == kTile, "one loader thread per token");
+
+// Ring slots (128 tokens of K or V) beside QT query rows.
+template <int D, int QT>
+struct Smem {
+  static constexpr int kSlotBytes = kTile * D * 2;
+  static constexpr int kQBytes = QT * D * 2;
+  static constexpr int kSlots = D == 128 ? (QT == 128 ? 6 : 5) : (QT == 128 ? 12 : 10);
+  static constexpr int kBytes = kQBytes + kSlots * kSlotBytes;
+  static constexpr int kLag = kSlots - 2 < 8 ? kSlots - 2 : 8;   // copies in flight per loader thread
+  static_assert(kSlots <= kMaxSlots && kSlots / 2 + 1 < kValidRing, "ring sizes");
+};
+
+struct Shared {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, done;
+  uint32_t tmem;
+  int abort;
+  int odd_values;                 // some drafted V held an infinity or NaN
+  int b0;                         // this CTA's piece: first sequence,
+  long long off0, count;          // first tile inside it, tiles
+  uint32_t valid[kValidRing][4];  // tokens of a tile that are there
+  float ml[2][kTile][2];          // the streams' maxima and sums
+};
+// 1 KB of alignment before the ring covers the static part
+static_assert(sizeof(Shared) <= 3072 && Smem<128, 128>::kBytes + 3072 <= kMaxSmem &&
+                  Smem<128, 256>::kBytes + 3072 <= kMaxSmem && Smem<64, 128>::kBytes + 3072 <= kMaxSmem &&
+                  Smem<64, 256>::kBytes + 3072 <= kMaxSmem,
+              "shared memory");
+
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Shared& sh) {
+  if (ptx::mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = ptx::global_timer();
+  for (;;) {
+    if (ptx::mbar_try_wait_sleep(bar, parity, 100000)) return;
+    if (*(volatile int*)&sh.abort) return;
+    if (ptx::global_timer() - t0 > kWaitLimitNs) {
+      *(volatile int*)&sh.abort = 1;
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], A bf16 pairs in 32-bit columns, B token-major.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ---- the line of tiles and its pieces
+
+struct Seq {
+  int nv, nt, kb, tn;   // visual, text, selected (or all visual), drafted tokens
+};
+
+// Sequence b's counts; a sequence with a count out of range has none.
+__device__ __forceinline__ bool seq_of(const TreeArgs& a, int b, Seq& s) {
+  bool ok = attn_lengths(a.lens, a.vis_idx != nullptr, b, a.n_vis, a.n_text, a.k_vis, false, a.status, s.nv, s.nt,
+                         s.kb);
+  s.tn = a.n_new ? __ldg(a.n_new + b) : a.T;
+  ok = ok && s.tn >= 0 && s.tn <= a.T;
+  if (!ok) s.nv = s.nt = s.kb = s.tn = 0;
+  return ok;
+}
+
+// Tokens that rows [row0, row0 + QT) of a sequence can see (0: no such rows).
+__device__ __forceinline__ int tokens_of(const TreeArgs& a, const Seq& s, int row0, int QT) {
+  const int rows = s.tn * a.G;
+  if (row0 >= rows) return 0;
+  const int last = min(row0 + QT, rows) - 1;
+  return s.kb + s.nt + (a.tree_mask ? s.tn : last / a.G + 1);
+}
+__device__ __forceinline__ int tiles_of(const TreeArgs& a, int b, int row0, int QT) {
+  Seq s;
+  seq_of(a, b, s);
+  return (tokens_of(a, s, row0, QT) + kTile - 1) / kTile;
+}
+
+// Tiles of sequences [0, b_end) for one row tile (whole warp).
+__device__ long long line_length(const TreeArgs& a, int row0, int QT, int b_end) {
+  if (!a.lens.any() && a.n_new == nullptr) return (long long)b_end * a.Hkv * tiles_of(a, 0, row0, QT);
+  long long n = 0;
+  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += tiles_of(a, b, row0, QT);
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
+  return n * a.Hkv;
+}
+
+__device__ __forceinline__ long long piece_begin(long long total, int c, int C) { return total * c / C; }
+
+// Consecutive tiles [t0, t1) of one (sequence, KV head) unit.
+struct Segment {
+  Seq s;
+  int b, g, t0, t1, tiles, tokens, rows;
+  __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// Walks a CTA's piece; every warp has its own and sees the same segments.
+struct Walk {
+  int b, row0, QT;
+  long long off, left;
+  Segment x;
+  __device__ void start(const Shared& sh, int row0_, int QT_) {
+    row0 = row0_;
+    QT = QT_;
+    b = sh.b0;
+    off = sh.off0;
+    left = sh.count;
+  }
+  __device__ bool next(const TreeArgs& a) {
+    while (left > 0 && b < a.batch) {
+      seq_of(a, b, x.s);
+      x.tokens = tokens_of(a, x.s, row0, QT);
+      x.tiles = (x.tokens + kTile - 1) / kTile;
+      if (off < (long long)x.tiles * a.Hkv) {
+        x.b = b;
+        x.g = (int)(off / x.tiles);
+        x.t0 = (int)(off - (long long)x.g * x.tiles);
+        x.t1 = (int)min((long long)x.tiles, x.t0 + left);
+        x.rows = min(QT, x.s.tn * a.G - row0);
+        off += x.t1 - x.t0;
+        left -= x.t1 - x.t0;
+        return true;
+      }
+      ++b;
+      off = 0;
+    }
+    return false;
+  }
+};
+
+// Partial results of a unit cut into pieces: slot 0 of a CTA continues a unit
+// that an earlier piece began, slot 1 begins one that goes on.
+__device__ __forceinline__ size_t part_row(int cta, bool begins, int row, int QT) {
+  return ((size_t)cta * 2 + (begins ? 1 : 0)) * QT + row;
+}
+
+}  // namespace
+
+template <int D, int QT>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attn_kernel(const __grid_constant__ TreeArgs a) {
+  using M = Smem<D, QT>;
+  constexpr int CPR = D / 8;                       // 16-byte chunks of a row
+  constexpr int S = M::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms are 1 KB
+  __shared__ Shared sh;
+  grid_dep_sync();
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) flag_status(a.status, kStatusTimeout);
+    return;
+  }
+  const uint32_t q_base = smem_u32(smem), ring = q_base + M::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x / a.row_tiles, row0 = (int)(blockIdx.x % a.row_tiles) * QT;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(&sh.full[i], kLoadWarps);
+      ptx::mbar_init(&sh.empty[i], 1);
+    }
+    ptx::mbar_init(&sh.q_full, 1);
+    ptx::mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh.s_full[i], 1);
+      ptx::mbar_init(&sh.p_full[i], 4);
+    }
+    ptx::mbar_init(&sh.o_full, 1);
+    ptx::mbar_init(&sh.done, 1);
+    sh.abort = 0;
+    sh.odd_values = 0;
+    ptx::mbar_fence_init();
+  }
+  if (warp == 0) ptx::tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == 1) {
+    // this CTA's piece of the line
+    const long long total = line_length(a, row0, QT, a.batch);
+    const long long begin = piece_begin(total, col, a.columns), end = piece_begin(total, col + 1, a.columns);
+    int b = 0;
+    long long before = 0;
+    if (begin < end) {
+      if (!a.lens.any() && a.n_new == nullptr) {
+        const long long per = (long long)a.Hkv * tiles_of(a, 0, row0, QT);
+        b = (int)(begin / per);
+        before = b * per;
+      } else {
+        // the first sequence whose tiles reach past `begin`
+        for (; b < a.batch; b += 32) {
+          const int mine = b + lane;
+          const long long n = mine < a.batch ? (long long)a.Hkv * tiles_of(a, mine, row0, QT) : 0;
+          long long inc = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, before + inc > begin);
+          if (past) {
+            const int f = __ffs(past) - 1;
+            before += __shfl_sync(0xffffffffu, inc - n, f);
+            b += f;
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+      }
+    }
+    if (lane == 0) {
+      sh.b0 = b;
+      sh.off0 = begin - before;
+      sh.count = end - begin;
+    }
+  }
+  // sequences whose counts are out of range: reported, their rows read 0 and -inf
+  if (a.lens.any() || a.n_new != nullptr) {
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+      Seq s;
+      if (seq_of(a, b, s)) continue;
+      if (threadIdx.x == 0) flag_status(a.status, kStatusBadLength);
+      const size_t n = (size_t)a.T * a.H;
+      for (size_t i = threadIdx.x; i < n * CPR; i += kThreads)
+        reinterpret_cast<uint4*>(a.out)[b * n * CPR + i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.lse != nullptr)
+        for (size_t i = threadIdx.x; i < n; i += kThreads) a.lse[b * n + i] = -INFINITY;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tbase = sh.tmem;
+  Walk w;
+  w.start(sh, row0, QT);
+
+  if (warp >= kLoadWarp) {
+    // ------------------------------------------------ cache rows
+    const int me = threadIdx.x - kLoadWarp * 32;   // this thread's token of every tile
+    uint32_t group = 0;                            // copies issued: K, V, K, V, ...
+    int pending = 0;                               // of them not yet handed over
+    uint32_t drafted = 0;                          // bit tile % 32: holds drafted tokens
+
+    // the 16-byte chunks this lane copies: (token of the warp, chunk, offset in a slot)
+    auto chunk_at = [&](int i, int& tok, int& c) {
+      const int j = lane + 32 * i;
+      tok = j / CPR;
+      c = j % CPR;
+      const int row = (warp - kLoadWarp) * 32 + tok;
+      return (uint32_t)((c >> 3) * kTile * 128 + row * 128 + ((c & 7) ^ (row & 7)) * 16);
+    };
+    auto hand_over = [&]() {
+      const uint32_t g = group - pending, slot = g % S;
+      switch (pending) {                           // the oldest copy has landed
+        case 1: cp_async_wait<0>(); break;
+        case 2: cp_async_wait<1>(); break;
+        case 3: cp_async_wait<2>(); break;
+        case 4: cp_async_wait<3>(); break;
+        case 5: cp_async_wait<4>(); break;
+        case 6: cp_async_wait<5>(); break;
+        case 7: cp_async_wait<6>(); break;
+        case 8: cp_async_wait<7>(); break;
+        default: cp_async_wait<8>(); break;
+      }
+      if ((g & 1) && ((drafted >> ((g >> 1) & 31)) & 1)) {
+        // A row that does not see a drafted token multiplies its V by 0: an
+        // infinity or NaN there is taken out of the product (0 instead) and
+        // added by the epilogue to the rows that see it.
+#pragma unroll 1
+        for (int i = 0; i < CPR; ++i) {
+          int tok, c;
+          const uint32_t at = chunk_at(i, tok, c);
+          uint4* p = reinterpret_cast<uint4*>(smem + M::kQBytes + slot * M::kSlotBytes + at);
+          uint4 v = *p;
+          uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((u[e] & 0x7f80u) == 0x7f80u) { u[e] &= 0xffff0000u; odd = true; }
+            if ((u[e] & 0x7f800000u) == 0x7f800000u) { u[e] &= 0xffffu; odd = true; }
+          }
+          if (odd) {
+            *p = v;
+            *(volatile int*)&sh.odd_values = 1;
+          }
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.full[slot]);
+      --pending;
+    };
+    auto copy = [&](const uint16_t* pool, uint32_t rid) {
+      const uint32_t slot = group % S;
+      if (group >= (uint32_t)S) {
+        const uint32_t parity = (group / S - 1) & 1;
+        bool is_free = __all_sync(0xffffffffu, ptx::mbar_try_wait(&sh.empty[slot], parity));
+        while (!is_free && pending > 0) {
+          hand_over();
+          is_free = __all_sync(0xffffffffu, ptx::mbar_try_wait(&sh.empty[slot], parity));
+        }
+        if (!is_free) wait_bar(&sh.empty[slot], parity, sh);
+        __syncwarp();
+      }
+      const uint32_t dst = ring + slot * M::kSlotBytes;
+#pragma unroll
+      for (int i = 0; i < CPR; ++i) {
+        int tok, c;
+        const uint32_t o = chunk_at(i, tok, c);
+        const uint32_t r = __shfl_sync(0xffffffffu, rid, tok);
+        const bool there = r != kNoRowId;
+        cp_async16(dst + o, pool + (there ? (size_t)r * D + c * 8 : 0), there ? 16u : 0u);
+      }
+      cp_async_commit();
+      ++group;
+      if (++pending > M::kLag) hand_over();
+    };
+
+    // Tiles pass three steps: their indices are loaded (two tiles ahead),
+    // their pages (one ahead), then their rows.
+    struct Ahead {
+      int pos, page, nv, g;
+      const int32_t* bt;
+      bool exists, visual, there, drafted;
+    };
+    Ahead A = {}, B = {};
+    int t = 0, t_end = 0;
+    auto load_index = [&](Ahead& n) {
+      n.exists = false;
+      if (t >= t_end) {
+        if (!w.next(a)) return;
+        t = w.x.t0;
+        t_end = w.x.t1;
+      }
+      const Segment& x = w.x;
+      const int i = t * kTile + me;
+      n.exists = true;
+      n.there = i < x.tokens;
+      n.visual = i < x.s.kb;
+      n.drafted = (t + 1) * kTile > x.s.kb + x.s.nt;
+      n.nv = x.s.nv;
+      n.g = x.g;
+      n.bt = a.block_table + (size_t)x.b * a.max_blocks;
+      n.pos = !n.visual              ? x.s.nv + i - x.s.kb
+              : a.vis_idx == nullptr ? i
+                                     : __ldg(a.vis_idx + ((size_t)x.b * a.Hkv + x.g) * a.k_vis + i);
+      ++t;
+    };
+    auto load_page = [&](Ahead& n) {
+      if (!n.exists || !n.there) return;
+      if (n.visual && (n.pos < 0 || n.pos >= n.nv)) {
+        flag_status(a.status, kStatusBadIndex);
+        n.there = false;
+        return;
+      }
+      n.page = __ldg(n.bt + (n.pos >> 4));
+    };
+    const uint16_t* k_pool = static_cast<const uint16_t*>(a.k_pool);
+    const uint16_t* v_pool = static_cast<const uint16_t*>(a.v_pool);
+    load_index(A);
+    load_page(A);
+    load_index(B);
+    for (uint32_t tile = 0; A.exists; ++tile) {
+      uint32_t rid = kNoRowId;
+      if (A.there) {
+        if (A.page >= 0 && A.page < a.num_blocks)
+          rid = (((uint32_t)A.page * (uint32_t)a.Hkv + (uint32_t)A.g) << 4) | (uint32_t)(A.pos & 15);
+        else
+          flag_status(a.status, kStatusBadBlock);
+      }
+      if (A.drafted) drafted |= 1u << (tile & 31);
+      else drafted &= ~(1u << (tile & 31));
+      A = B;
+      load_page(A);
+      load_index(B);
+      const uint32_t v = __ballot_sync(0xffffffffu, rid != kNoRowId);
+      if (lane == 0) sh.valid[tile % kValidRing][warp - kLoadWarp] = v;
+      copy(k_pool, rid);
+      copy(v_pool, rid);
+    }
+    while (pending > 0) hand_over();
+  } else if (warp == kQueryWarp) {
+    // ------------------------------------------------ query rows
+    uint32_t n = 0;
+    for (; w.next(a); ++n) {
+      if (n > 0) wait_bar(&sh.q_empty, (n - 1) & 1, sh);
+      __syncwarp();
+      const Segment& x = w.x;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q);
+      for (int j = lane; j < x.rows * CPR; j += 32) {
+        const int r = j / CPR, c = j % CPR, row = row0 + r;
+        const int tk = row / a.G, h = x.g * a.G + row - tk * a.G;
+        const uint32_t o = (uint32_t)((r >> 7) * kTile * D * 2 + (c >> 3) * kTile * 128 + (r & 127) * 128 +
+                                      ((c & 7) ^ (r & 7)) * 16);
+        cp_async16(q_base + o, q + (((size_t)x.b * a.T + tk) * a.H + h) * D + c * 8, 16u);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.q_full);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ products
+    const uint32_t id_qk = ptx::idesc_bf16_f32(kTile, kTile);
+    const uint32_t id_pv = ptx::idesc_bf16_f32(kTile, D) | (1u << 16);     // B token-major
+    const uint32_t hi = ptx::smem_desc_hi_sw128(1024);
+    uint32_t seg = 0, tile0 = 0;       // segments, tiles so far
+    uint32_t np[2] = {0, 0};           // weights waited for, per stream
+    for (; w.next(a); ++seg) {
+      const Segment& x = w.x;
+      const bool split = x.rows <= kTile;
+      const int nt = x.t1 - x.t0, steps = split ? nt : 2 * nt;
+      wait_bar(&sh.q_full, seg & 1, sh);
+      auto qk = [&](int j) {
+        const int s = j & 1;
+        const uint32_t grp = 2 * (tile0 + (split ? j : j >> 1)), slot = grp % S;
+        wait_bar(&sh.full[slot], (grp / S) & 1, sh);
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (ptx::elect_one() && !*(volatile int*)&sh.abort) {
+          const uint32_t qa = q_base + (split ? 0 : s) * kTile * D * 2, kb = ring + slot * M::kSlotBytes;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = (uint32_t)(k / 4) * kTile * 128 + (k % 4) * 32;
+            ptx::mma_bf16_split(tbase + s * 128, ptx::smem_desc_lo_sw128(qa + o), ptx::smem_desc_lo_sw128(kb + o), hi,
+                                id_qk, k > 0);
+          }
+          ptx::mma_commit(&sh.s_full[s]);
+          if (split || s) ptx::mma_commit(&sh.empty[slot]);
+          if (j == steps - 1) ptx::mma_commit(&sh.q_empty);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int j) {
+        const int s = j & 1;
+        const uint32_t grp = 2 * (tile0 + (split ? j : j >> 1)) + 1, slot = grp % S;
+        wait_bar(&sh.full[slot], (grp / S) & 1, sh);
+        wait_bar(&sh.p_full[s], np[s]++ & 1, sh);
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (ptx::elect_one() && !*(volatile int*)&sh.abort) {
+          const uint32_t vb = ring + slot * M::kSlotBytes;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) {
+            // 16 tokens a step; 64-dim column groups lie a whole tile apart
+            const uint32_t lo = (((vb + k * 2048) & 0x3FFFFu) >> 4) | ((uint32_t)(kTile * 128 / 16) << 16);
+            mma_ts(tbase + 256 + s * 128, tbase + s * 128 + k * 8, lo, hi, id_pv, j >= 2 || k > 0);
+          }
+          if (split || s) ptx::mma_commit(&sh.empty[slot]);
+          if (j == steps - 1) ptx::mma_commit(&sh.o_full);
+        }
+        __syncwarp();
+      };
+      qk(0);
+      if (steps > 1) qk(1);
+      for (int j = 0; j < steps; ++j) {
+        pv(j);
+        if (j + 2 < steps) qk(j + 2);
+      }
+      tile0 += nt;
+    }
+    // every product has landed before the CTA gives its tensor memory back
+    if (ptx::elect_one()) ptx::mma_commit(&sh.done);
+    __syncwarp();
+    const uint64_t t0 = ptx::global_timer();
+    while (!ptx::mbar_try_wait_sleep(&sh.done, 0, 100000) && ptx::global_timer() - t0 < kWaitLimitNs) {}
+  } else {
+    // ------------------------------------------------ softmax and epilogue
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane 32 * (warp % 4)
+    const uint32_t t_s = tbase + s * 128 + lanes;
+    uint32_t seg = 0, tile0 = 0, ns = 0;
+    const float sl2 = a.scale_log2;
+    for (; w.next(a); ++seg) {
+      const Segment& x = w.x;
+      const bool split = x.rows <= kTile;
+      const int nt = x.t1 - x.t0, steps = split ? nt : 2 * nt;
+      const int row = split ? r : s * kTile + r;          // of this tile of rows
+      const bool active = row - lane < x.rows;            // this warp has rows at all
+      const int tk = (row0 + row) / a.G;
+      const int ctx = x.s.kb + x.s.nt;
+      uint64_t tree = 0;
+      if (a.tree_mask != nullptr && row < x.rows) tree = a.tree_mask[(size_t)x.b * a.T + tk];
+      float m = -INFINITY, l = 0.f;
+      for (int j = s; j < steps; j += 2, ++ns) {
+        const int i = split ? j : j >> 1;
+        wait_bar(&sh.s_full[s], ns & 1, sh);
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (active) {
+          const volatile uint32_t* vw = sh.valid[(tile0 + i) % kValidRing];
+          uint32_t see[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) see[q] = vw[q];
+          const int base = (x.t0 + i) * kTile;
+          if (base + kTile > ctx) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int in = ctx - (base + 32 * q);       // context tokens of this word
+              if (in >= 32) continue;
+              if (a.tree_mask != nullptr) {
+                uint32_t bits = in > 0 ? (1u << in) - 1 : 0u;
+                bits |= in >= 0 ? (uint32_t)(tree << in) : in > -64 ? (uint32_t)(tree >> -in) : 0u;
+                see[q] &= bits;
+              } else {
+                const int vis = in + tk + 1;              // tokens of this word that the row sees
+                see[q] &= vis >= 32 ? 0xffffffffu : vis > 0 ? (1u << vis) - 1 : 0u;
+              }
+            }
+          }
+          const bool dense =
+              __all_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu);
+          // the tile's maximum
+          float mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t u[32];
+            ptx::tmem_ld32(t_s + 32 * q, u);
+            ptx::tmem_wait_ld(u);
+            if (dense) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx = fm::max3(mx, __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((see[q] >> e) & 1) mx = fmaxf(mx, __uint_as_float(u[e]));
+            }
+          }
+          const float mz = mx == -INFINITY ? -INFINITY : mx * sl2;
+          // O is rescaled only when a maximum outgrows the reference by 2^8
+          float alpha = 1.f;
+          if (mz > m + kRescale || (m == -INFINITY && mz > m)) {
+            if (m != -INFINITY) alpha = fast_exp2(m - mz);
+            m = mz;
+            l *= alpha;
+          }
+          if (j >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            const uint32_t t_o = tbase + 256 + s * 128 + lanes;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t u[32];
+              ptx::tmem_ld32(t_o + c, u);
+              ptx::tmem_wait_ld(u);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+              tmem_st16(t_o + c, u);
+              tmem_st16(t_o + c + 16, u + 16);
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : -m;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t u[32], p[16];
+            ptx::tmem_ld32(t_s + 32 * q, u);
+            ptx::tmem_wait_ld(u);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0 = fast_exp2(fmaf(__uint_as_float(u[e]), sl2, off));
+              float p1 = fast_exp2(fmaf(__uint_as_float(u[e + 1]), sl2, off));
+              if (!dense) {
+                if (!((see[q] >> e) & 1)) p0 = 0.f;
+                if (!((see[q] >> (e + 1)) & 1)) p1 = 0.f;
+              }
+              sum0 += p0;
+              sum1 += p1;
+              p[e / 2] = bf16x2(p0, p1);
+            }
+            // P's columns lie over those of S that have been read
+            tmem_st16(t_s + 16 * q, p);
+          }
+          l += sum0 + sum1;
+          tmem_wait_st();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[s]);
+      }
+      tile0 += nt;
+
+      // ---- this segment's rows
+      wait_bar(&sh.o_full, seg & 1, sh);
+      __syncwarp();
+      ptx::tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;
+      int c0 = 0, c1 = D;
+      if (split) {
+        // join the streams: both warps of a row's lane quarter, half the columns each
+        sh.ml[s][r][0] = m;
+        sh.ml[s][r][1] = l;
+        soft_bar();
+        const float ma = sh.ml[0][r][0], la = sh.ml[0][r][1], mb = sh.ml[1][r][0], lb = sh.ml[1][r][1];
+        m = fmaxf(ma, mb);
+        w0 = ma == -INFINITY ? 0.f : fast_exp2(ma - m);
+        w1 = mb == -INFINITY ? 0.f : fast_exp2(mb - m);
+        l = la * w0 + lb * w1;
+        if (la != la || lb != lb) l = la + lb;            // NaN stays
+        c0 = s * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      if (active) {
+        const bool live = row < x.rows, whole = x.whole();
+        const int h = x.g * a.G + (row0 + row) - tk * a.G;
+        const size_t orow = ((size_t)x.b * a.T + tk) * a.H + h;
+        const size_t prow = part_row(blockIdx.x, x.t0 == 0, row, QT);
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const bool odd = *(volatile int*)&sh.odd_values != 0;
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t u[32];
+          ptx::tmem_ld32(tbase + 256 + (split ? 0 : s * 128) + lanes + c, u);
+          ptx::tmem_wait_ld(u);
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+          if (split) {
+            ptx::tmem_ld32(tbase + 384 + lanes + c, u);
+            ptx::tmem_wait_ld(u);
+            // (an empty stream's columns hold nothing that may be read)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = (w0 == 0.f ? 0.f : o[e] * w0) + (w1 == 0.f ? 0.f : __uint_as_float(u[e]) * w1);
+          }
+          if (odd && live) {
+            // infinities and NaN of the drafted tokens that this row sees
+            const int d0 = max(0, x.t0 * kTile - ctx), d1 = min(x.s.tn, x.t1 * kTile - ctx);
+            for (int dt = d0; dt < d1; ++dt) {
+              if (a.tree_mask != nullptr ? !((tree >> dt) & 1) : dt > tk) continue;
+              const int pos = x.s.nv + x.s.nt + dt;
+              const int page = __ldg(a.block_table + (size_t)x.b * a.max_blocks + (pos >> 4));
+              if (page < 0 || page >= a.num_blocks) continue;
+              const uint16_t* v = static_cast<const uint16_t*>(a.v_pool) +
+                                  ((((size_t)page * a.Hkv + x.g) << 4) + (pos & 15)) * D + c;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t bits = __ldg(v + e);
+                if ((bits & 0x7f80u) == 0x7f80u) o[e] += __uint_as_float(bits << 16);
+              }
+            }
+          }
+          if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              dst[e / 8] = make_uint4(bf16x2(o[e] * inv, o[e + 1] * inv), bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                      bf16x2(o[e + 4] * inv, o[e + 5] * inv), bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+          } else if (live) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (live && c0 == 0) {
+          if (!whole) *reinterpret_cast<float2*>(a.part_ml + 2 * prow) = make_float2(m, l);
+          else if (a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      // the next segment's products overwrite what the other stream's warps read
+      ptx::tc_fence_before();
+      soft_bar();
+      ptx::tc_fence_after();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && sh.abort) flag_status(a.status, kStatusTimeout);
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+// Joins the partials of the units that were cut: one warp per query row,
+// pieces in order.
 template <int D>
 __global__ void __launch_bounds__(256)
-tree_attn_row_kernel(const __grid_constant__ TreeArgs a) {
+tree_merge_kernel(const __grid_constant__ TreeArgs a, int QT) {
   constexpr int E = D / 32;
   grid_dep_sync();
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= (long long)a.batch * a.T * a.H) return;
-  const int h = (int)(w % a.H);
-  const int t = (int)(w / a.H % a.T), b = (int)(w / a.H / a.T);
-  const int g = h / (a.H / a.Hkv);
-  int nv, nt, kb;
-  const bool report = lane == 0 && t == 0 && h == 0;
-  bool ok = attn_lengths(a.lens, a.vis_idx != nullptr, b, a.n_vis, a.n_text, a.k_vis, report, a.status, nv, nt, kb);
-  int tn = a.n_new ? __ldg(a.n_new + b) : a.T;
-  if (tn < 0 || tn > a.T) {
-    if (report) flag_status(a.status, kStatusBadLength);
-    ok = false;
-  }
-  if (!ok) kb = nt = tn = 0;
-  else if (t >= tn) return;
-  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
-  const int32_t* vrow = a.vis_idx ? a.vis_idx + ((size_t)b * a.Hkv + g) * a.k_vis : nullptr;
-  const uint64_t mask = a.tree_mask ? a.tree_mask[(size_t)b * a.T + t] : 0;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+  const long long wi = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (wi >= (long long)a.batch * a.T * a.H) return;
+  const int h = (int)(wi % a.H);
+  const int t = (int)(wi / a.H % a.T), b = (int)(wi / a.H / a.T);
+  const int g = h / a.G;
+  Seq s;
+  if (!seq_of(a, b, s) || t >= s.tn) return;
+  const int row = t * a.G + (h - g * a.G), rt = row / QT, row0 = rt * QT;
+  const int tiles = (tokens_of(a, s, row0, QT) + kTile - 1) / kTile;
+  const long long total = line_length(a, row0, QT, a.batch);
+  const long long first = line_length(a, row0, QT, b) + (long long)g * tiles;
+  // the piece that holds tile x is the last one that begins at or before it
+  auto piece_of = [&](long long x) { return (int)(((x + 1) * a.columns - 1) / total); };
+  const int p0 = piece_of(first), p1 = piece_of(first + tiles - 1);
+  if (p0 == p1) return;
+  auto slot_of = [&](int p) { return part_row(p * a.row_tiles + rt, p == p0, row - row0, QT); };
+  auto empty = [&](int p) { return piece_begin(total, p, a.columns) == piece_begin(total, p + 1, a.columns); };
+  float M = -INFINITY;
+  for (int p = p0 + lane; p <= p1; p += 32)
+    if (!empty(p)) M = fmaxf(M, __ldcg(a.part_ml + 2 * slot_of(p)));
+  M = warp_max(M);
+  float L = 0.f, acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.q)[(size_t)w * D + e * 32 + lane] << 16);
-    o[e] = 0.f;
-  }
-  for (int i = 0; i < kb + nt + tn; ++i) {
-    const int j = i - kb - nt;
-    if (j >= 0 && !(a.tree_mask ? (mask >> j) & 1 : j <= t)) continue;
-    int pos = i < kb ? (vrow ? __ldg(vrow + i) : i) : nv + (i - kb);
-    if (i < kb && (pos < 0 || pos >= nv)) {
-      flag_status(a.status, kStatusBadIndex);
-      continue;
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int p = p0; p <= p1; ++p) {
+    if (empty(p)) continue;
+    const size_t at = slot_of(p);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * at));
+    const float wgt = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+    L = ml.y != ml.y ? ml.y : fmaf(wgt, ml.y, L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float o = __ldcg(a.part_o + at * D + e * 32 + lane);
+      if (wgt != 0.f || o != o) acc[e] = fmaf(wgt, o, acc[e]);
     }
-    const int page = __ldg(bt + (pos >> 4));
-    if (page < 0 || page >= a.num_blocks) {
-      flag_status(a.status, kStatusBadBlock);
-      continue;
-    }
-    const size_t row = ((((size_t)page * a.Hkv + g) << 4) + (pos & 15)) * D + lane;
-    float z = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      z = fmaf(q[e], __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k_pool)[row + 32 * e] << 16), z);
-    z = warp_sum(z) * a.scale_log2;
-    const float mn = fmaxf(m, z);
-    const float old = m == -INFINITY ? 0.f : fast_exp2(m - mn);
-    const float p = fast_exp2(z - mn);
-    l = l * old + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(p, __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v_pool)[row + 32 * e] << 16),
-                  o[e] * old);
-    m = mn;
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    static_cast<uint16_t*>(a.out)[(size_t)w * D + e * 32 + lane] = (uint16_t)f32_to_bf16_bits(o[e] * inv);
+    static_cast<uint16_t*>(a.out)[(size_t)wi * D + e * 32 + lane] = (uint16_t)f32_to_bf16_bits(acc[e] * inv);
   if (a.lse != nullptr && lane == 0)
-    a.lse[w] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    a.lse[wi] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
+
+namespace {
+
+// Row tiles of 128 rows, or of 256 when there are more rows than that; as
+// many pieces as leave every SM one CTA, at most one per tile of tokens.
+struct Plan {
+  int QT, row_tiles, columns;
+  bool cut() const { return columns > 1; }
+  size_t rows() const { return cut() ? (size_t)columns * row_tiles * 2 * QT : 0; }
+};
+Plan plan_of(int B, int T, int G, int Hkv, int n_tokens) {
+  Plan p;
+  const long long rows = (long long)T * G;
+  p.QT = rows <= kTile ? kTile : 2 * kTile;
+  p.row_tiles = (int)((rows + p.QT - 1) / p.QT);
+  const long long tiles = (long long)B * Hkv * (((long long)n_tokens + kTile - 1) / kTile);
+  long long c = p.row_tiles > 0 ? kCtas / p.row_tiles : 1;
+  if (c > tiles) c = tiles;
+  p.columns = (int)(c < 1 ? 1 : c);
+  return p;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int D, int QT>
+cudaError_t launch_qt(const TreeArgs& a, cudaStream_t stream) {
+  auto kernel = tree_attn_kernel<D, QT>;
+  const size_t smem = Smem<D, QT>::kBytes;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  return launch_dependent(kernel, dim3((unsigned)(a.columns * a.row_tiles)), dim3(kThreads), smem, stream, a);
+}
+
+}  // namespace
 
 size_t tree_attn_workspace_bytes(int B, int T, int H, int Hkv, int D, int n_tokens) {
-  (void)B; (void)T; (void)H; (void)Hkv; (void)D; (void)n_tokens;
-  return 0;
+  const Plan p = plan_of(B, T, H / Hkv, Hkv, n_tokens);
+  // (m, l) of every partial row, then their O
+  return round256(p.rows() * 2 * sizeof(float)) + p.rows() * D * sizeof(float);
 }
 
-cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t stream) {
+cudaError_t launch_tree_attn(const TreeArgs& args, cudaStream_t stream) {
+  TreeArgs a = args;
+  a.G = a.H / a.Hkv;
+  const Plan p = plan_of(a.batch, a.T, a.G, a.Hkv, a.k_vis + a.n_text + a.T);
+  a.row_tiles = p.row_tiles;
+  a.columns = p.columns;
+  a.part_ml = static_cast<float*>(a.ws);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + round256(p.rows() * 2 * sizeof(float)));
+  cudaError_t e;
+  if (a.D == 128) e = p.QT == 128 ? launch_qt<128, 128>(a, stream) : launch_qt<128, 256>(a, stream);
+  else e = p.QT == 128 ? launch_qt<64, 128>(a, stream) : launch_qt<64, 256>(a, stream);
+  if (e != cudaSuccess || !p.cut()) return e;
   const long long rows = (long long)a.batch * a.T * a.H;
-  const dim3 grid((unsigned)((rows + 7) / 8));
-  return launch_dependent(a.D == 128 ? tree_attn_row_kernel<128> : tree_attn_row_kernel<64>, grid, dim3(256), 0,
-                          stream, a);
+  return launch_dependent(a.D == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>, dim3((unsigned)((rows + 7) / 8)),
+                          dim3(256), 0, stream, a, p.QT);
 }
 
 }  // namespace sv
