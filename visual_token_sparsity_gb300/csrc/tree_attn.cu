@@ -46,7 +46,11 @@ constexpr int kTile = 128;                  // tokens of a tile, rows of a strea
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kQueryWarp = 9, kLoadWarp = 10;
 constexpr int kLoadWarps = 4;
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kThreads = 512;               // (warps 14 and 15 fill a warpgroup)
+// Registers: 512 threads at 128 at launch; the softmax warps hold a whole row
+// of S (128 columns), the others give theirs up: 256 x 192 + 256 x 64.
+constexpr int kSoftRegs = 192, kOtherRegs = 64;
+static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 65536 && kLoadWarp + 4 <= kThreads / 32, "register split");
 constexpr int kTmemCols = 512;              // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kCtas = 152;                  // one per SM
 constexpr int kMaxSlots = 12;
@@ -63,7 +67,6 @@ struct Smem {
   static constexpr int kQBytes = QT * D * 2;
   static constexpr int kSlots = D == 128 ? (QT == 128 ? 6 : 5) : (QT == 128 ? 12 : 10);
   static constexpr int kBytes = kQBytes + kSlots * kSlotBytes;
-  static constexpr int kLag = kSlots - 2 < 8 ? kSlots - 2 : 8;   // copies in flight per loader thread
   static_assert(kSlots <= kMaxSlots && kSlots / 2 + 1 < kValidRing, "ring sizes");
 };
 
@@ -97,6 +100,8 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Shared&
   }
 }
 
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -126,6 +131,29 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
+// Replaces the infinities and NaN among 8 bf16 values by 0.
+__device__ __forceinline__ bool zero_odd(uint4* p) {
+  uint4 v = *p;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((u[e] & 0x7f80u) == 0x7f80u) { u[e] &= 0xffff0000u; odd = true; }
+    if ((u[e] & 0x7f800000u) == 0x7f800000u) { u[e] &= 0xffffu; odd = true; }
+  }
+  if (odd) *p = v;
+  return odd;
+}
+
+template <int V>
+struct Stream {
+  static constexpr int value = V;
+};
+// Tensor memory columns of a stream's S (and P) and O: the CTA holds all 512,
+// so its allocation begins at column 0 (checked at the start).
+__host__ __device__ constexpr uint32_t tmem_s(int s) { return s * 128; }
+__host__ __device__ constexpr uint32_t tmem_o(int s) { return 256 + s * 128; }
 
 // ---- the line of tiles and its pieces
 
@@ -180,8 +208,8 @@ struct Walk {
   int b, row0, QT;
   long long off, left;
   Segment x;
-  __device__ void start(const Shared& sh, int row0_, int QT_) {
-    row0 = row0_;
+  __device__ void start(const Shared& sh, int top, int QT_) {
+    row0 = top;
     QT = QT_;
     b = sh.b0;
     off = sh.off0;
@@ -236,7 +264,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(&sh.full[i], kLoadWarps);
+      ptx::mbar_init(&sh.full[i], kLoadWarps * 32);
       ptx::mbar_init(&sh.empty[i], 1);
     }
     ptx::mbar_init(&sh.q_full, 1);
@@ -307,98 +335,57 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tbase = sh.tmem;
   Walk w;
   w.start(sh, row0, QT);
+  if (sh.tmem != 0) w.left = 0;   // (cannot be; reported below)
 
-  if (warp >= kLoadWarp) {
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
     // ------------------------------------------------ cache rows
     const int me = threadIdx.x - kLoadWarp * 32;   // this thread's token of every tile
     uint32_t group = 0;                            // copies issued: K, V, K, V, ...
-    int pending = 0;                               // of them not yet handed over
-    uint32_t drafted = 0;                          // bit tile % 32: holds drafted tokens
-
-    // the 16-byte chunks this lane copies: (token of the warp, chunk, offset in a slot)
-    auto chunk_at = [&](int i, int& tok, int& c) {
-      const int j = lane + 32 * i;
-      tok = j / CPR;
-      c = j % CPR;
-      const int row = (warp - kLoadWarp) * 32 + tok;
-      return (uint32_t)((c >> 3) * kTile * 128 + row * 128 + ((c & 7) ^ (row & 7)) * 16);
-    };
-    auto hand_over = [&]() {
-      const uint32_t g = group - pending, slot = g % S;
-      switch (pending) {                           // the oldest copy has landed
-        case 1: cp_async_wait<0>(); break;
-        case 2: cp_async_wait<1>(); break;
-        case 3: cp_async_wait<2>(); break;
-        case 4: cp_async_wait<3>(); break;
-        case 5: cp_async_wait<4>(); break;
-        case 6: cp_async_wait<5>(); break;
-        case 7: cp_async_wait<6>(); break;
-        case 8: cp_async_wait<7>(); break;
-        default: cp_async_wait<8>(); break;
-      }
-      if ((g & 1) && ((drafted >> ((g >> 1) & 31)) & 1)) {
-        // A row that does not see a drafted token multiplies its V by 0: an
-        // infinity or NaN there is taken out of the product (0 instead) and
-        // added by the epilogue to the rows that see it.
-#pragma unroll 1
-        for (int i = 0; i < CPR; ++i) {
-          int tok, c;
-          const uint32_t at = chunk_at(i, tok, c);
-          uint4* p = reinterpret_cast<uint4*>(smem + M::kQBytes + slot * M::kSlotBytes + at);
-          uint4 v = *p;
-          uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-          bool odd = false;
+    // A warp instruction copies RPI rows of its 32: this lane's chunk of row
+    // first + i * RPI, at a swizzle that repeats every 8 rows.
+    constexpr int RPI = 32 / CPR, VAR = 8 / RPI;
+    const uint32_t c = lane % CPR, first = lane / CPR;
+    uint32_t to[VAR];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((u[e] & 0x7f80u) == 0x7f80u) { u[e] &= 0xffff0000u; odd = true; }
-            if ((u[e] & 0x7f800000u) == 0x7f800000u) { u[e] &= 0xffffu; odd = true; }
-          }
-          if (odd) {
-            *p = v;
-            *(volatile int*)&sh.odd_values = 1;
-          }
-        }
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.full[slot]);
-      --pending;
-    };
-    auto copy = [&](const uint16_t* pool, uint32_t rid) {
+    for (int i = 0; i < VAR; ++i)
+      to[i] = ring + (c >> 3) * kTile * 128 + ((warp - kLoadWarp) * 32 + first) * 128 +
+              (((c & 7) ^ ((first + i * RPI) & 7)) * 16);
+    auto copy = [&](const uint16_t* pool, uint32_t rid, uint32_t there) {
       const uint32_t slot = group % S;
-      if (group >= (uint32_t)S) {
-        const uint32_t parity = (group / S - 1) & 1;
-        bool is_free = __all_sync(0xffffffffu, ptx::mbar_try_wait(&sh.empty[slot], parity));
-        while (!is_free && pending > 0) {
-          hand_over();
-          is_free = __all_sync(0xffffffffu, ptx::mbar_try_wait(&sh.empty[slot], parity));
-        }
-        if (!is_free) wait_bar(&sh.empty[slot], parity, sh);
-        __syncwarp();
-      }
-      const uint32_t dst = ring + slot * M::kSlotBytes;
+      uint32_t r[CPR];               // every row id first: no copy waits for a shuffle
 #pragma unroll
-      for (int i = 0; i < CPR; ++i) {
-        int tok, c;
-        const uint32_t o = chunk_at(i, tok, c);
-        const uint32_t r = __shfl_sync(0xffffffffu, rid, tok);
-        const bool there = r != kNoRowId;
-        cp_async16(dst + o, pool + (there ? (size_t)r * D + c * 8 : 0), there ? 16u : 0u);
+      for (int i = 0; i < CPR; ++i) r[i] = __shfl_sync(0xffffffffu, rid, first + i * RPI);
+      if (group >= (uint32_t)S) wait_bar(&sh.empty[slot], (group / S - 1) & 1, sh);
+      __syncwarp();
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(pool + c * 8);
+      const uint32_t dst = slot * M::kSlotBytes;
+      if (there == 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < CPR; ++i)
+          cp_async16(dst + to[i % VAR] + i * RPI * 128, src + (size_t)r[i] * (D * 2), 16u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < CPR; ++i) {
+          const bool ok = (there >> (first + i * RPI)) & 1;
+          cp_async16(dst + to[i % VAR] + i * RPI * 128, src + (ok ? (size_t)r[i] * (D * 2) : 0), ok ? 16u : 0u);
+        }
       }
-      cp_async_commit();
+      // the barrier counts this thread once its copies have landed; the
+      // threads that read them fence the proxies
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[slot])) : "memory");
       ++group;
-      if (++pending > M::kLag) hand_over();
     };
 
     // Tiles pass three steps: their indices are loaded (two tiles ahead),
     // their pages (one ahead), then their rows.
     struct Ahead {
-      int pos, page, nv, g;
+      int index, pos, page, nv, g;
       const int32_t* bt;
-      bool exists, visual, there, drafted;
+      bool exists, visual, listed, there;
     };
     Ahead A = {}, B = {};
     int t = 0, t_end = 0;
@@ -414,17 +401,17 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       n.exists = true;
       n.there = i < x.tokens;
       n.visual = i < x.s.kb;
-      n.drafted = (t + 1) * kTile > x.s.kb + x.s.nt;
       n.nv = x.s.nv;
       n.g = x.g;
       n.bt = a.block_table + (size_t)x.b * a.max_blocks;
-      n.pos = !n.visual              ? x.s.nv + i - x.s.kb
-              : a.vis_idx == nullptr ? i
-                                     : __ldg(a.vis_idx + ((size_t)x.b * a.Hkv + x.g) * a.k_vis + i);
+      n.pos = n.visual ? i : x.s.nv + i - x.s.kb;
+      n.listed = n.visual && a.vis_idx != nullptr;
+      if (n.listed) n.index = __ldg(a.vis_idx + ((size_t)x.b * a.Hkv + x.g) * a.k_vis + i);
       ++t;
     };
     auto load_page = [&](Ahead& n) {
       if (!n.exists || !n.there) return;
+      if (n.listed) n.pos = n.index;
       if (n.visual && (n.pos < 0 || n.pos >= n.nv)) {
         flag_status(a.status, kStatusBadIndex);
         n.there = false;
@@ -445,17 +432,15 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
         else
           flag_status(a.status, kStatusBadBlock);
       }
-      if (A.drafted) drafted |= 1u << (tile & 31);
-      else drafted &= ~(1u << (tile & 31));
       A = B;
       load_page(A);
       load_index(B);
       const uint32_t v = __ballot_sync(0xffffffffu, rid != kNoRowId);
       if (lane == 0) sh.valid[tile % kValidRing][warp - kLoadWarp] = v;
-      copy(k_pool, rid);
-      copy(v_pool, rid);
+      copy(k_pool, rid, v);
+      copy(v_pool, rid, v);
     }
-    while (pending > 0) hand_over();
+    cp_async_wait_all();
   } else if (warp == kQueryWarp) {
     // ------------------------------------------------ query rows
     uint32_t n = 0;
@@ -479,74 +464,90 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ products
-    const uint32_t id_qk = ptx::idesc_bf16_f32(kTile, kTile);
-    const uint32_t id_pv = ptx::idesc_bf16_f32(kTile, D) | (1u << 16);     // B token-major
-    const uint32_t hi = ptx::smem_desc_hi_sw128(1024);
-    uint32_t seg = 0, tile0 = 0;       // segments, tiles so far
-    uint32_t np[2] = {0, 0};           // weights waited for, per stream
+    // The whole warp walks the schedule and one elected lane issues: with the
+    // operands uniform over the warp an instruction takes 25 cycles to issue,
+    // in a single lane's own branch it took 110.
+    constexpr uint32_t id_qk = ptx::idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t id_pv = ptx::idesc_bf16_f32(kTile, D) | (1u << 16);   // B token-major
+    constexpr uint32_t hi = ptx::smem_desc_hi_sw128(1024);
+    const uint32_t q_lo = ptx::smem_desc_lo_sw128(q_base), k_lo = ptx::smem_desc_lo_sw128(ring);
+    // V: 64-dim column groups lie a whole tile apart
+    const uint32_t v_lo = ((ring & 0x3FFFFu) >> 4) | ((uint32_t)(kTile * 128 / 16) << 16);
+    uint32_t seg = 0, slot = 0, parity = 0;    // segments; ring position of the next K tile to use
+    uint32_t v_slot = 1, v_parity = 0;         // and of the next V tile
+    uint32_t np[2] = {0, 0};                   // weights waited for, per stream
     for (; w.next(a); ++seg) {
-      const Segment& x = w.x;
-      const bool split = x.rows <= kTile;
-      const int nt = x.t1 - x.t0, steps = split ? nt : 2 * nt;
+      const bool split = w.x.rows <= kTile;
+      const int nt = w.x.t1 - w.x.t0, steps = split ? nt : 2 * nt;
       wait_bar(&sh.q_full, seg & 1, sh);
-      auto qk = [&](int j) {
-        const int s = j & 1;
-        const uint32_t grp = 2 * (tile0 + (split ? j : j >> 1)), slot = grp % S;
-        wait_bar(&sh.full[slot], (grp / S) & 1, sh);
+      auto qk = [&](int j, auto stream) {
+        constexpr int s = decltype(stream)::value;
+        const bool last_use = split || s;
+        const uint32_t at = __shfl_sync(0xffffffffu, slot, 0);    // (uniform)
+        wait_bar(&sh.full[at], parity, sh);
         __syncwarp();
         ptx::tc_fence_after();
-        if (ptx::elect_one() && !*(volatile int*)&sh.abort) {
-          const uint32_t qa = q_base + (split ? 0 : s) * kTile * D * 2, kb = ring + slot * M::kSlotBytes;
+        if (ptx::elect_one()) {
+          ptx::fence_proxy_async_smem();          // the rows came through cp.async
+          const uint32_t qa = q_lo + (split ? 0 : s) * (kTile * D * 2 / 16), kb = k_lo + at * (M::kSlotBytes / 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (uint32_t)(k / 4) * kTile * 128 + (k % 4) * 32;
-            ptx::mma_bf16_split(tbase + s * 128, ptx::smem_desc_lo_sw128(qa + o), ptx::smem_desc_lo_sw128(kb + o), hi,
-                                id_qk, k > 0);
+            constexpr uint32_t kBlock = kTile * 128 / 16;
+            const uint32_t o = (uint32_t)(k / 4) * kBlock + (k % 4) * 2;
+            ptx::mma_bf16_split(tmem_s(s), qa + o, kb + o, hi, id_qk, k > 0);
           }
           ptx::mma_commit(&sh.s_full[s]);
-          if (split || s) ptx::mma_commit(&sh.empty[slot]);
+          if (last_use) ptx::mma_commit(&sh.empty[at]);
           if (j == steps - 1) ptx::mma_commit(&sh.q_empty);
         }
-        __syncwarp();
+        if (last_use) {
+          slot += 2;
+          if (slot >= (uint32_t)S) { slot -= S; parity ^= 1; }
+        }
       };
-      auto pv = [&](int j) {
-        const int s = j & 1;
-        const uint32_t grp = 2 * (tile0 + (split ? j : j >> 1)) + 1, slot = grp % S;
-        wait_bar(&sh.full[slot], (grp / S) & 1, sh);
+      auto pv = [&](int j, auto stream) {
+        constexpr int s = decltype(stream)::value;
+        const bool last_use = split || s;
+        const uint32_t at = __shfl_sync(0xffffffffu, v_slot, 0);
+        wait_bar(&sh.full[at], v_parity, sh);
         wait_bar(&sh.p_full[s], np[s]++ & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
-        if (ptx::elect_one() && !*(volatile int*)&sh.abort) {
-          const uint32_t vb = ring + slot * M::kSlotBytes;
+        if (ptx::elect_one()) {
+          ptx::fence_proxy_async_smem();
+          const uint32_t vb = v_lo + at * (M::kSlotBytes / 16);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) {
-            // 16 tokens a step; 64-dim column groups lie a whole tile apart
-            const uint32_t lo = (((vb + k * 2048) & 0x3FFFFu) >> 4) | ((uint32_t)(kTile * 128 / 16) << 16);
-            mma_ts(tbase + 256 + s * 128, tbase + s * 128 + k * 8, lo, hi, id_pv, j >= 2 || k > 0);
-          }
-          if (split || s) ptx::mma_commit(&sh.empty[slot]);
+          for (int k = 0; k < kTile / 16; ++k)    // 16 tokens a step
+            mma_ts(tmem_o(s), tmem_s(s) + k * 8, vb + k * (2048 / 16), hi, id_pv, j >= 2 || k > 0);
+          if (last_use) ptx::mma_commit(&sh.empty[at]);
           if (j == steps - 1) ptx::mma_commit(&sh.o_full);
         }
-        __syncwarp();
+        if (last_use) {
+          v_slot += 2;
+          if (v_slot >= (uint32_t)S) { v_slot -= S; v_parity ^= 1; }
+        }
       };
-      qk(0);
-      if (steps > 1) qk(1);
-      for (int j = 0; j < steps; ++j) {
-        pv(j);
-        if (j + 2 < steps) qk(j + 2);
+      qk(0, Stream<0>());
+      if (steps > 1) qk(1, Stream<1>());
+      for (int j = 0; j < steps; j += 2) {
+        pv(j, Stream<0>());
+        if (j + 2 < steps) qk(j + 2, Stream<0>());
+        if (j + 1 < steps) pv(j + 1, Stream<1>());
+        if (j + 3 < steps) qk(j + 3, Stream<1>());
       }
-      tile0 += nt;
     }
     // every product has landed before the CTA gives its tensor memory back
     if (ptx::elect_one()) ptx::mma_commit(&sh.done);
     __syncwarp();
     const uint64_t t0 = ptx::global_timer();
     while (!ptx::mbar_try_wait_sleep(&sh.done, 0, 100000) && ptx::global_timer() - t0 < kWaitLimitNs) {}
+  }
   } else {
     // ------------------------------------------------ softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane 32 * (warp % 4)
-    const uint32_t t_s = tbase + s * 128 + lanes;
+    const uint32_t t_s = tmem_s(s) + lanes;
     uint32_t seg = 0, tile0 = 0, ns = 0;
     const float sl2 = a.scale_log2;
     for (; w.next(a); ++seg) {
@@ -586,26 +587,29 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
               }
             }
           }
-          const bool dense =
-              __all_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu);
-          // the tile's maximum
-          float mx = -INFINITY;
+          uint32_t u[kTile];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t u[32];
-            ptx::tmem_ld32(t_s + 32 * q, u);
-            ptx::tmem_wait_ld(u);
-            if (dense) {
+          for (int q = 0; q < 4; ++q) ptx::tmem_ld32(t_s + 32 * q, u + 32 * q);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mx = fm::max3(mx, __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
-            } else {
+          for (int q = 0; q < 4; ++q) ptx::tmem_wait_ld(u + 32 * q);
+          if (__any_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) != 0xffffffffu)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if ((see[q] >> e) & 1) mx = fmaxf(mx, __uint_as_float(u[e]));
-            }
+                if (!((see[q] >> e) & 1)) u[32 * q + e] = 0xff800000u;    // -inf: weight 0
           }
-          const float mz = mx == -INFINITY ? -INFINITY : mx * sl2;
+          // the tile's maximum
+          float mx[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            mx[q] = __uint_as_float(u[32 * q]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2)
+              mx[q] = fm::max3(mx[q], __uint_as_float(u[32 * q + e]), __uint_as_float(u[32 * q + e + 1]));
+            mx[q] = fmaxf(mx[q], __uint_as_float(u[32 * q + 31]));
+          }
+          const float mz = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
           // O is rescaled only when a maximum outgrows the reference by 2^8
           float alpha = 1.f;
           if (mz > m + kRescale || (m == -INFINITY && mz > m)) {
@@ -613,43 +617,53 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
             m = mz;
             l *= alpha;
           }
-          if (j >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            const uint32_t t_o = tbase + 256 + s * 128 + lanes;
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t u[32];
-              ptx::tmem_ld32(t_o + c, u);
-              ptx::tmem_wait_ld(u);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-              tmem_st16(t_o + c, u);
-              tmem_st16(t_o + c + 16, u + 16);
-            }
-          }
-          const float off = m == -INFINITY ? 0.f : -m;
-          float sum0 = 0.f, sum1 = 0.f;
+          const uint64_t sl2x2 = fm::splat2(sl2), off = fm::splat2(m == -INFINITY ? 0.f : -m);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t u[32], p[16];
-            ptx::tmem_ld32(t_s + 32 * q, u);
-            ptx::tmem_wait_ld(u);
+            uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0 = fast_exp2(fmaf(__uint_as_float(u[e]), sl2, off));
-              float p1 = fast_exp2(fmaf(__uint_as_float(u[e + 1]), sl2, off));
-              if (!dense) {
-                if (!((see[q] >> e) & 1)) p0 = 0.f;
-                if (!((see[q] >> (e + 1)) & 1)) p1 = 0.f;
-              }
-              sum0 += p0;
-              sum1 += p1;
-              p[e / 2] = bf16x2(p0, p1);
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t z =
+                  fm::fma2(fm::pack2(__uint_as_float(u[32 * q + 2 * e]), __uint_as_float(u[32 * q + 2 * e + 1])), sl2x2, off);
+              const uint64_t pp = fm::exp2_mufu2(z);
+              sum[e & 1] = fm::add2(sum[e & 1], pp);
+              float p0, p1;
+              fm::unpack2(pp, p0, p1);
+              p[e] = bf16x2(p0, p1);
             }
-            // P's columns lie over those of S that have been read
-            tmem_st16(t_s + 16 * q, p);
+            tmem_st16(t_s + 16 * q, p);                   // P lies over S
           }
-          l += sum0 + sum1;
+          float s0, s1;
+          fm::unpack2(fm::add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          if (j >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            const uint32_t t_o = tmem_o(s) + lanes;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              ptx::tmem_ld32(t_o + c, o);
+              ptx::tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(t_o + c, o);
+              tmem_st16(t_o + c + 16, o + 16);
+            }
+          }
           tmem_wait_st();
+        }
+        if ((x.t0 + i + 1) * kTile > ctx) {
+          // Drafted tokens: a row that does not see one multiplies its V by 0,
+          // so an infinity or NaN there is taken out of the product (0
+          // instead) and added by the epilogue to the rows that see it.
+          const uint32_t grp = 2 * (tile0 + i) + 1, slot = grp % S;
+          wait_bar(&sh.full[slot], (grp / S) & 1, sh);
+          uint4* v = reinterpret_cast<uint4*>(smem + M::kQBytes + slot * M::kSlotBytes);
+          bool odd = false;
+#pragma unroll 4
+          for (int k = r; k < kTile * CPR; k += kTile) odd |= zero_odd(v + k);
+          if (odd) *(volatile int*)&sh.odd_values = 1;
+          ptx::fence_proxy_async_smem();
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -686,13 +700,13 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
         const bool odd = *(volatile int*)&sh.odd_values != 0;
         for (int c = c0; c < c1; c += 32) {
           uint32_t u[32];
-          ptx::tmem_ld32(tbase + 256 + (split ? 0 : s * 128) + lanes + c, u);
+          ptx::tmem_ld32(tmem_o(split ? 0 : s) + lanes + c, u);
           ptx::tmem_wait_ld(u);
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
           if (split) {
-            ptx::tmem_ld32(tbase + 384 + lanes + c, u);
+            ptx::tmem_ld32(tmem_o(1) + lanes + c, u);
             ptx::tmem_wait_ld(u);
             // (an empty stream's columns hold nothing that may be read)
 #pragma unroll
@@ -741,10 +755,10 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && sh.abort) flag_status(a.status, kStatusTimeout);
+  if (threadIdx.x == 0 && (sh.abort || sh.tmem != 0)) flag_status(a.status, kStatusTimeout);
   if (warp == 0) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tbase, kTmemCols);
+    ptx::tmem_dealloc(sh.tmem, kTmemCols);
   }
 }
 
