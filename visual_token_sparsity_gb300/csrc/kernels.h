@@ -169,8 +169,9 @@ struct TreeArgs {
   void* ws;                          // tree_attn_workspace_bytes
   int* status;
   // set by launch_tree_attn: query heads per KV head, tiles of query rows,
-  // pieces of one row tile's work, partial results
+  // pieces of one row tile's work, cut units and their partial results
   int G, row_tiles, columns;
+  int* part_unit;
   float* part_ml;
   float* part_o;
 };

@@ -11,8 +11,7 @@
 // tensor cores: S = Q K^T (128 rows x 128 tokens), then O += P V with P as
 // the bf16 A operand in tensor memory and V read token-major from shared
 // memory.  One pass: running maximum and sum per row in fp32 registers, the
-// accumulator rescaled only when a row's maximum grows by more than 2^8 (P
-// then stays below 2^8, its relative rounding is the same).
+// accumulator rescaled only when a row's maximum grows far beyond it.
 //
 // A CTA runs two streams, each with its own S, P, O in tensor memory and four
 // softmax warps, so that one's products run while the other's weights are
@@ -44,20 +43,25 @@ namespace {
 
 constexpr int kTile = 128;                  // tokens of a tile, rows of a stream
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kQueryWarp = 9, kLoadWarp = 10;
-constexpr int kLoadWarps = 4;
-constexpr int kThreads = 512;               // (warps 14 and 15 fill a warpgroup)
+constexpr int kMmaWarp = 8;                 // and 9: one per stream
+constexpr int kLoadWarp = 10, kLoadWarps = 4;
+constexpr int kQueryWarp = 14, kQueryWarps = 2;
+constexpr int kThreads = 512;
 // Registers: 512 threads at 128 at launch; the softmax warps hold a whole row
 // of S (128 columns), the others give theirs up: 256 x 192 + 256 x 64.
 constexpr int kSoftRegs = 192, kOtherRegs = 64;
-static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 65536 && kLoadWarp + 4 <= kThreads / 32, "register split");
+static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 65536 && 32 * (kQueryWarp + kQueryWarps) == kThreads,
+              "register split");
 constexpr int kTmemCols = 512;              // S0 | S1 | O0 | O1, 128 columns each
-constexpr int kCtas = 152;                  // one per SM
+constexpr int kCtas = 152;                  // one per SM (fewer than 2^15)
 constexpr int kMaxSlots = 12;
 constexpr int kValidRing = 16;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr size_t kMaxSmem = 232448;         // 227 KB
-constexpr float kRescale = 8.f;             // log2 growth of a maximum that rescales O
+// A row's weights are taken relative to a reference that is raised, and O
+// rescaled, only when the maximum outgrows it by 2^32: bf16 and fp32 have the
+// exponents for it, and no rounding depends on it.
+constexpr float kRescale = 32.f;
 static_assert(kLoadWarps * 32 == kTile, "one loader thread per token");
 
 // Ring slots (128 tokens of K or V) beside QT query rows.
@@ -72,13 +76,13 @@ struct Smem {
 
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, done;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, done, turn[2];
   uint32_t tmem;
   int abort;
   int odd_values;                 // some drafted V held an infinity or NaN
   int b0;                         // this CTA's piece: first sequence,
-  long long off0, count;          // first tile inside it, tiles
-  uint32_t valid[kValidRing][4];  // tokens of a tile that are there
+  long long off0, count, total;   // first tile inside it, tiles; the whole line
+  alignas(16) uint32_t valid[kValidRing][4];  // tokens of a tile that are there
   float ml[2][kTile][2];          // the streams' maxima and sums
 };
 // 1 KB of alignment before the ring covers the static part
@@ -146,10 +150,6 @@ __device__ __forceinline__ bool zero_odd(uint4* p) {
   return odd;
 }
 
-template <int V>
-struct Stream {
-  static constexpr int value = V;
-};
 // Tensor memory columns of a stream's S (and P) and O: the CTA holds all 512,
 // so its allocation begins at column 0 (checked at the start).
 __host__ __device__ constexpr uint32_t tmem_s(int s) { return s * 128; }
@@ -182,16 +182,6 @@ __device__ __forceinline__ int tiles_of(const TreeArgs& a, int b, int row0, int 
   Seq s;
   seq_of(a, b, s);
   return (tokens_of(a, s, row0, QT) + kTile - 1) / kTile;
-}
-
-// Tiles of sequences [0, b_end) for one row tile (whole warp).
-__device__ long long line_length(const TreeArgs& a, int row0, int QT, int b_end) {
-  if (!a.lens.any() && a.n_new == nullptr) return (long long)b_end * a.Hkv * tiles_of(a, 0, row0, QT);
-  long long n = 0;
-  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += tiles_of(a, b, row0, QT);
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
-  return n * a.Hkv;
 }
 
 __device__ __forceinline__ long long piece_begin(long long total, int c, int C) { return total * c / C; }
@@ -238,10 +228,13 @@ struct Walk {
 };
 
 // Partial results of a unit cut into pieces: slot 0 of a CTA continues a unit
-// that an earlier piece began, slot 1 begins one that goes on.
-__device__ __forceinline__ size_t part_row(int cta, bool begins, int row, int QT) {
-  return ((size_t)cta * 2 + (begins ? 1 : 0)) * QT + row;
-}
+// that an earlier piece began, slot 1 begins one that goes on.  (m, l) are
+// [slot][row], O is [slot][dim / 4][row][4]: consecutive rows, which
+// neighbouring lanes hold, lie side by side.
+__device__ __forceinline__ size_t part_slot(int cta, bool begins) { return (size_t)cta * 2 + (begins ? 1 : 0); }
+
+// The piece that holds tile x of a line: the last one that begins at or before it.
+__device__ __forceinline__ int piece_of(long long x, long long total, int C) { return (int)(((x + 1) * C - 1) / total); }
 
 }  // namespace
 
@@ -262,61 +255,75 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = blockIdx.x / a.row_tiles, row0 = (int)(blockIdx.x % a.row_tiles) * QT;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(&sh.full[i], kLoadWarps * 32);
-      ptx::mbar_init(&sh.empty[i], 1);
-    }
-    ptx::mbar_init(&sh.q_full, 1);
-    ptx::mbar_init(&sh.q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sh.s_full[i], 1);
-      ptx::mbar_init(&sh.p_full[i], 4);
-    }
-    ptx::mbar_init(&sh.o_full, 1);
-    ptx::mbar_init(&sh.done, 1);
-    sh.abort = 0;
-    sh.odd_values = 0;
-    ptx::mbar_fence_init();
-  }
   if (warp == 0) ptx::tmem_alloc(&sh.tmem, kTmemCols);
   if (warp == 1) {
+    // barriers: a lane each
+    if (lane < S) {
+      ptx::mbar_init(&sh.full[lane], kLoadWarps * 32);
+      ptx::mbar_init(&sh.empty[lane], 2);            // both streams' products
+    } else if (lane < S + 2) {
+      ptx::mbar_init(&sh.s_full[lane - S], 1);
+      ptx::mbar_init(&sh.p_full[lane - S], 4);
+      ptx::mbar_init(&sh.turn[lane - S], 1);
+    } else if (lane == S + 2) {
+      ptx::mbar_init(&sh.q_full, kQueryWarps);
+      ptx::mbar_init(&sh.q_empty, 2);
+      ptx::mbar_init(&sh.o_full, 2);
+      ptx::mbar_init(&sh.done, 2);
+      sh.abort = 0;
+      sh.odd_values = 0;
+    }
+    ptx::mbar_fence_init();
+  }
+  if (warp == 2) {
     // this CTA's piece of the line
-    const long long total = line_length(a, row0, QT, a.batch);
-    const long long begin = piece_begin(total, col, a.columns), end = piece_begin(total, col + 1, a.columns);
     int b = 0;
-    long long before = 0;
-    if (begin < end) {
-      if (!a.lens.any() && a.n_new == nullptr) {
-        const long long per = (long long)a.Hkv * tiles_of(a, 0, row0, QT);
-        b = (int)(begin / per);
-        before = b * per;
-      } else {
-        // the first sequence whose tiles reach past `begin`
-        for (; b < a.batch; b += 32) {
-          const int mine = b + lane;
-          const long long n = mine < a.batch ? (long long)a.Hkv * tiles_of(a, mine, row0, QT) : 0;
-          long long inc = n;
+    long long before = 0, begin, end, total;
+    if (!a.lens.any() && a.n_new == nullptr) {
+      const long long per = (long long)a.Hkv * tiles_of(a, 0, row0, QT);
+      total = per * a.batch;
+      begin = piece_begin(total, col, a.columns);
+      end = piece_begin(total, col + 1, a.columns);
+      b = per > 0 ? (int)(begin / per) : 0;
+      before = b * per;
+    } else {
+      // tiles of sequences [b0, b0 + 32) up to this lane's
+      auto scan = [&](int b0, long long& n) {
+        n = b0 + lane < a.batch ? (long long)a.Hkv * tiles_of(a, b0 + lane, row0, QT) : 0;
+        long long inc = n;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-          }
-          const uint32_t past = __ballot_sync(0xffffffffu, before + inc > begin);
-          if (past) {
-            const int f = __ffs(past) - 1;
-            before += __shfl_sync(0xffffffffu, inc - n, f);
-            b += f;
-            break;
-          }
-          before += __shfl_sync(0xffffffffu, inc, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
         }
+        return inc;
+      };
+      long long n, inc = scan(0, n);
+      total = __shfl_sync(0xffffffffu, inc, 31);
+      for (int b0 = 32; b0 < a.batch; b0 += 32) {
+        long long n2;
+        total += __shfl_sync(0xffffffffu, scan(b0, n2), 31);
+      }
+      begin = piece_begin(total, col, a.columns);
+      end = piece_begin(total, col + 1, a.columns);
+      // the first sequence whose tiles reach past `begin`
+      for (; begin < end && b < a.batch; b += 32) {
+        if (b > 0) inc = scan(b, n);
+        const uint32_t past = __ballot_sync(0xffffffffu, before + inc > begin);
+        if (past) {
+          const int f = __ffs(past) - 1;
+          before += __shfl_sync(0xffffffffu, inc - n, f);
+          b += f;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
       }
     }
     if (lane == 0) {
       sh.b0 = b;
       sh.off0 = begin - before;
       sh.count = end - begin;
+      sh.total = total;
     }
   }
   // sequences whose counts are out of range: reported, their rows read 0 and -inf
@@ -406,7 +413,13 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       n.bt = a.block_table + (size_t)x.b * a.max_blocks;
       n.pos = n.visual ? i : x.s.nv + i - x.s.kb;
       n.listed = n.visual && a.vis_idx != nullptr;
-      if (n.listed) n.index = __ldg(a.vis_idx + ((size_t)x.b * a.Hkv + x.g) * a.k_vis + i);
+      if (n.listed) {
+        const size_t at = ((size_t)x.b * a.Hkv + x.g) * a.k_vis + i;
+        n.index = __ldg(a.vis_idx + at);
+        // the list's lines reach L1 eight tiles ahead (the next unit's rows follow)
+        if (at + 8 * kTile < (size_t)a.batch * a.Hkv * a.k_vis)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(a.vis_idx + at + 8 * kTile));
+      }
       ++t;
     };
     auto load_page = [&](Ahead& n) {
@@ -441,100 +454,121 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       copy(v_pool, rid, v);
     }
     cp_async_wait_all();
-  } else if (warp == kQueryWarp) {
-    // ------------------------------------------------ query rows
+  } else if (warp >= kQueryWarp) {
+    // ------------------------------------------------ query rows: 32 at a time
+    constexpr int RPI = 32 / CPR;
+    const uint32_t c = lane % CPR, first = lane / CPR;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + c * 8;
     uint32_t n = 0;
     for (; w.next(a); ++n) {
       if (n > 0) wait_bar(&sh.q_empty, (n - 1) & 1, sh);
       __syncwarp();
       const Segment& x = w.x;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q);
-      for (int j = lane; j < x.rows * CPR; j += 32) {
-        const int r = j / CPR, c = j % CPR, row = row0 + r;
-        const int tk = row / a.G, h = x.g * a.G + row - tk * a.G;
-        const uint32_t o = (uint32_t)((r >> 7) * kTile * D * 2 + (c >> 3) * kTile * 128 + (r & 127) * 128 +
-                                      ((c & 7) ^ (r & 7)) * 16);
-        cp_async16(q_base + o, q + (((size_t)x.b * a.T + tk) * a.H + h) * D + c * 8, 16u);
+      for (int r0 = 32 * (warp - kQueryWarp); r0 < x.rows; r0 += 32 * kQueryWarps) {
+        const int row = row0 + r0 + lane, tk = row / a.G;
+        // (a row past the last one reads the sequence's first: its results go nowhere)
+        const uint32_t mine = r0 + lane < x.rows ? (uint32_t)tk * a.H + (uint32_t)(x.g * a.G + row - tk * a.G) : 0u;
+        const uint16_t* src = q + (size_t)x.b * a.T * a.H * D;
+        const uint32_t dst = q_base + (r0 >> 7) * kTile * D * 2 + (c >> 3) * kTile * 128 + ((r0 & 127) + first) * 128;
+#pragma unroll
+        for (int i = 0; i < CPR; ++i) {
+          const uint32_t r = __shfl_sync(0xffffffffu, mine, first + i * RPI);
+          cp_async16(dst + i * RPI * 128 + (((c & 7) ^ ((first + i * RPI) & 7)) * 16), src + (size_t)r * D, 16u);
+        }
       }
-      cp_async_commit();
-      cp_async_wait<0>();
+      cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh.q_full);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kMmaWarp + 2) {
     // ------------------------------------------------ products
-    // The whole warp walks the schedule and one elected lane issues: with the
+    // One warp per stream, so that neither waits for the other's weights.  The
+    // whole warp walks the schedule and one elected lane issues: with the
     // operands uniform over the warp an instruction takes 25 cycles to issue,
     // in a single lane's own branch it took 110.
     constexpr uint32_t id_qk = ptx::idesc_bf16_f32(kTile, kTile);
     constexpr uint32_t id_pv = ptx::idesc_bf16_f32(kTile, D) | (1u << 16);   // B token-major
     constexpr uint32_t hi = ptx::smem_desc_hi_sw128(1024);
+    const uint32_t s = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);         // (uniform)
+    const uint32_t t_s = tmem_s(s), t_o = tmem_o(s);
     const uint32_t q_lo = ptx::smem_desc_lo_sw128(q_base), k_lo = ptx::smem_desc_lo_sw128(ring);
     // V: 64-dim column groups lie a whole tile apart
     const uint32_t v_lo = ((ring & 0x3FFFFu) >> 4) | ((uint32_t)(kTile * 128 / 16) << 16);
-    uint32_t seg = 0, slot = 0, parity = 0;    // segments; ring position of the next K tile to use
-    uint32_t v_slot = 1, v_parity = 0;         // and of the next V tile
-    uint32_t np[2] = {0, 0};                   // weights waited for, per stream
+    uint32_t seg = 0, tile0 = 0, np = 0;       // segments, tiles, weights so far
+    // In pairs the streams issue in turns, half a period apart: started
+    // together they would form their weights, and then queue for the tensor
+    // core, at the same time.
+    uint32_t turns = 0;
+    auto take_turn = [&]() {
+      if (s == 1) wait_bar(&sh.turn[1], turns & 1, sh);
+      else if (turns > 0) wait_bar(&sh.turn[0], (turns - 1) & 1, sh);
+      ++turns;
+    };
+    auto pass_turn = [&]() {
+      if (lane == 0) ptx::mbar_arrive(&sh.turn[s ^ 1]);
+    };
     for (; w.next(a); ++seg) {
       const bool split = w.x.rows <= kTile;
-      const int nt = w.x.t1 - w.x.t0, steps = split ? nt : 2 * nt;
+      const int nt = w.x.t1 - w.x.t0;
+      // this stream's tiles: every second one from s on, or all
+      const int step = split ? 2 : 1, begin = split ? (int)s : 0;
+      const uint32_t qa = q_lo + (split ? 0u : s) * (kTile * D * 2 / 16);
       wait_bar(&sh.q_full, seg & 1, sh);
-      auto qk = [&](int j, auto stream) {
-        constexpr int s = decltype(stream)::value;
-        const bool last_use = split || s;
-        const uint32_t at = __shfl_sync(0xffffffffu, slot, 0);    // (uniform)
-        wait_bar(&sh.full[at], parity, sh);
+      auto qk = [&](int i) {
+        const uint32_t grp = __shfl_sync(0xffffffffu, 2 * (tile0 + i), 0), slot = grp % S;
+        wait_bar(&sh.full[slot], (grp / S) & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           ptx::fence_proxy_async_smem();          // the rows came through cp.async
-          const uint32_t qa = q_lo + (split ? 0 : s) * (kTile * D * 2 / 16), kb = k_lo + at * (M::kSlotBytes / 16);
+          const uint32_t kb = k_lo + slot * (M::kSlotBytes / 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             constexpr uint32_t kBlock = kTile * 128 / 16;
             const uint32_t o = (uint32_t)(k / 4) * kBlock + (k % 4) * 2;
-            ptx::mma_bf16_split(tmem_s(s), qa + o, kb + o, hi, id_qk, k > 0);
+            ptx::mma_bf16_split(t_s, qa + o, kb + o, hi, id_qk, k > 0);
           }
           ptx::mma_commit(&sh.s_full[s]);
-          if (last_use) ptx::mma_commit(&sh.empty[at]);
-          if (j == steps - 1) ptx::mma_commit(&sh.q_empty);
-        }
-        if (last_use) {
-          slot += 2;
-          if (slot >= (uint32_t)S) { slot -= S; parity ^= 1; }
+          ptx::mma_commit(&sh.empty[slot]);
+          if (split) ptx::mma_commit(&sh.empty[slot]);    // (for the stream that does not use it)
+          if (i + step >= nt) ptx::mma_commit(&sh.q_empty);
         }
       };
-      auto pv = [&](int j, auto stream) {
-        constexpr int s = decltype(stream)::value;
-        const bool last_use = split || s;
-        const uint32_t at = __shfl_sync(0xffffffffu, v_slot, 0);
-        wait_bar(&sh.full[at], v_parity, sh);
-        wait_bar(&sh.p_full[s], np[s]++ & 1, sh);
+      auto pv = [&](int i) {
+        const uint32_t grp = __shfl_sync(0xffffffffu, 2 * (tile0 + i) + 1, 0), slot = grp % S;
+        wait_bar(&sh.full[slot], (grp / S) & 1, sh);
+        wait_bar(&sh.p_full[s], np++ & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           ptx::fence_proxy_async_smem();
-          const uint32_t vb = v_lo + at * (M::kSlotBytes / 16);
+          const uint32_t vb = v_lo + slot * (M::kSlotBytes / 16);
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)    // 16 tokens a step
-            mma_ts(tmem_o(s), tmem_s(s) + k * 8, vb + k * (2048 / 16), hi, id_pv, j >= 2 || k > 0);
-          if (last_use) ptx::mma_commit(&sh.empty[at]);
-          if (j == steps - 1) ptx::mma_commit(&sh.o_full);
-        }
-        if (last_use) {
-          v_slot += 2;
-          if (v_slot >= (uint32_t)S) { v_slot -= S; v_parity ^= 1; }
+            mma_ts(t_o, t_s + k * 8, vb + k * (2048 / 16), hi, id_pv, i > begin || k > 0);
+          ptx::mma_commit(&sh.empty[slot]);
+          if (split) ptx::mma_commit(&sh.empty[slot]);
+          if (i + step >= nt) ptx::mma_commit(&sh.o_full);
         }
       };
-      qk(0, Stream<0>());
-      if (steps > 1) qk(1, Stream<1>());
-      for (int j = 0; j < steps; j += 2) {
-        pv(j, Stream<0>());
-        if (j + 2 < steps) qk(j + 2, Stream<0>());
-        if (j + 1 < steps) pv(j + 1, Stream<1>());
-        if (j + 3 < steps) qk(j + 3, Stream<1>());
+      if (begin < nt) {
+        if (!split) take_turn();
+        qk(begin);
+        if (!split) pass_turn();
+        for (int i = begin; i < nt; i += step) {
+          if (!split) take_turn();
+          pv(i);
+          if (i + step < nt) qk(i + step);
+          __syncwarp();
+          if (!split) pass_turn();
+        }
+      } else if (ptx::elect_one()) {              // a stream without a tile
+        ptx::mma_commit(&sh.q_empty);
+        ptx::mma_commit(&sh.o_full);
       }
+      __syncwarp();
+      tile0 += nt;
     }
     // every product has landed before the CTA gives its tensor memory back
     if (ptx::elect_one()) ptx::mma_commit(&sh.done);
@@ -549,6 +583,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane 32 * (warp % 4)
     const uint32_t t_s = tmem_s(s) + lanes;
     uint32_t seg = 0, tile0 = 0, ns = 0;
+    bool cut = false;                  // the last unit goes on in the next piece
     const float sl2 = a.scale_log2;
     for (; w.next(a); ++seg) {
       const Segment& x = w.x;
@@ -567,10 +602,11 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
         __syncwarp();
         ptx::tc_fence_after();
         if (active) {
-          const volatile uint32_t* vw = sh.valid[(tile0 + i) % kValidRing];
           uint32_t see[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) see[q] = vw[q];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(see[0]), "=r"(see[1]), "=r"(see[2]), "=r"(see[3])
+                       : "r"(smem_u32(sh.valid[(tile0 + i) % kValidRing]))
+                       : "memory");
           const int base = (x.t0 + i) * kTile;
           if (base + kTile > ctx) {
 #pragma unroll
@@ -610,7 +646,6 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
             mx[q] = fmaxf(mx[q], __uint_as_float(u[32 * q + 31]));
           }
           const float mz = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          // O is rescaled only when a maximum outgrows the reference by 2^8
           float alpha = 1.f;
           if (mz > m + kRescale || (m == -INFINITY && mz > m)) {
             if (m != -INFINITY) alpha = fast_exp2(m - mz);
@@ -695,7 +730,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
         const bool live = row < x.rows, whole = x.whole();
         const int h = x.g * a.G + (row0 + row) - tk * a.G;
         const size_t orow = ((size_t)x.b * a.T + tk) * a.H + h;
-        const size_t prow = part_row(blockIdx.x, x.t0 == 0, row, QT);
+        const size_t slot = part_slot(blockIdx.x, x.t0 == 0);
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const bool odd = *(volatile int*)&sh.odd_values != 0;
         for (int c = c0; c < c1; c += 32) {
@@ -737,20 +772,29 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
               dst[e / 8] = make_uint4(bf16x2(o[e] * inv, o[e + 1] * inv), bf16x2(o[e + 2] * inv, o[e + 3] * inv),
                                       bf16x2(o[e + 4] * inv, o[e + 5] * inv), bf16x2(o[e + 6] * inv, o[e + 7] * inv));
           } else if (live) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c);
+            float4* dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + c / 4) * QT + row;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 4) dst[(e / 4) * QT] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         if (live && c0 == 0) {
-          if (!whole) *reinterpret_cast<float2*>(a.part_ml + 2 * prow) = make_float2(m, l);
+          if (!whole) reinterpret_cast<float2*>(a.part_ml)[slot * QT + row] = make_float2(m, l);
           else if (a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
       }
+      cut = x.t0 == 0 && x.t1 < x.tiles;
       // the next segment's products overwrite what the other stream's warps read
       ptx::tc_fence_before();
       soft_bar();
       ptx::tc_fence_after();
+    }
+    if (threadIdx.x == 0 && a.columns > 1) {
+      // the unit that begins here and goes on, for the merge: its sequence, KV
+      // head and last piece (-1: none), its rows and the line's length
+      const Segment& x = w.x;
+      const int last =
+          cut ? piece_of(piece_begin(sh.total, col + 1, a.columns) + x.tiles - x.t1 - 1, sh.total, a.columns) : -1;
+      reinterpret_cast<int4*>(a.part_unit)[blockIdx.x] = make_int4(x.b, x.g, last, x.rows | (int)min(sh.total, 0x7fffLL) << 16);
     }
   }
   ptx::tc_fence_before();
@@ -762,56 +806,41 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   }
 }
 
-// Joins the partials of the units that were cut: one warp per query row,
-// pieces in order.
-template <int D>
+// Joins the partials of the units that were cut, pieces in order: blocks of 32
+// rows x 32 dims of the unit that CTA blockIdx.x of the kernel above began, a
+// thread per row and four dims.
+template <int D, int QT>
 __global__ void __launch_bounds__(256)
-tree_merge_kernel(const __grid_constant__ TreeArgs a, int QT) {
-  constexpr int E = D / 32;
+tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   grid_dep_sync();
-  const int lane = threadIdx.x & 31;
-  const long long wi = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (wi >= (long long)a.batch * a.T * a.H) return;
-  const int h = (int)(wi % a.H);
-  const int t = (int)(wi / a.H % a.T), b = (int)(wi / a.H / a.T);
-  const int g = h / a.G;
-  Seq s;
-  if (!seq_of(a, b, s) || t >= s.tn) return;
-  const int row = t * a.G + (h - g * a.G), rt = row / QT, row0 = rt * QT;
-  const int tiles = (tokens_of(a, s, row0, QT) + kTile - 1) / kTile;
-  const long long total = line_length(a, row0, QT, a.batch);
-  const long long first = line_length(a, row0, QT, b) + (long long)g * tiles;
-  // the piece that holds tile x is the last one that begins at or before it
-  auto piece_of = [&](long long x) { return (int)(((x + 1) * a.columns - 1) / total); };
-  const int p0 = piece_of(first), p1 = piece_of(first + tiles - 1);
-  if (p0 == p1) return;
-  auto slot_of = [&](int p) { return part_row(p * a.row_tiles + rt, p == p0, row - row0, QT); };
-  auto empty = [&](int p) { return piece_begin(total, p, a.columns) == piece_begin(total, p + 1, a.columns); };
-  float M = -INFINITY;
-  for (int p = p0 + lane; p <= p1; p += 32)
-    if (!empty(p)) M = fmaxf(M, __ldcg(a.part_ml + 2 * slot_of(p)));
-  M = warp_max(M);
-  float L = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int p = p0; p <= p1; ++p) {
-    if (empty(p)) continue;
-    const size_t at = slot_of(p);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * at));
-    const float wgt = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-    L = ml.y != ml.y ? ml.y : fmaf(wgt, ml.y, L);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float o = __ldcg(a.part_o + at * D + e * 32 + lane);
-      if (wgt != 0.f || o != o) acc[e] = fmaf(wgt, o, acc[e]);
-    }
+  const int cta = blockIdx.x, row = blockIdx.y * 32 + (threadIdx.x & 31);
+  const int4 unit = __ldcg(reinterpret_cast<const int4*>(a.part_unit) + cta);
+  if (unit.z < 0 || row >= (unit.w & 0xffff)) return;
+  const int total = unit.w >> 16;           // exact where it is less than the pieces
+  const int rt = cta % a.row_tiles, p0 = cta / a.row_tiles, c4 = blockIdx.z * 8 + (threadIdx.x >> 5);
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = p0; p <= unit.z; ++p) {
+    if (total < a.columns && piece_begin(total, p, a.columns) == piece_begin(total, p + 1, a.columns)) continue;
+    const size_t slot = part_slot(p * a.row_tiles + rt, p == p0);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * QT + row);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (D / 4) + c4) * QT + row);
+    const float m = fmaxf(M, ml.x);
+    const float w0 = M == -INFINITY ? 0.f : fast_exp2(M - m), w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+    L = (L == 0.f ? 0.f : L * w0) + (ml.y == 0.f ? 0.f : ml.y * w1);
+    acc.x = acc.x * w0 + o.x * w1;
+    acc.y = acc.y * w0 + o.y * w1;
+    acc.z = acc.z * w0 + o.z * w1;
+    acc.w = acc.w * w0 + o.w * w1;
+    M = m;
   }
   const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    static_cast<uint16_t*>(a.out)[(size_t)wi * D + e * 32 + lane] = (uint16_t)f32_to_bf16_bits(acc[e] * inv);
-  if (a.lse != nullptr && lane == 0)
-    a.lse[wi] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  const int r = rt * QT + row, t = r / a.G, h = unit.y * a.G + r - t * a.G;
+  const size_t orow = ((size_t)unit.x * a.T + t) * a.H + h;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * c4) =
+      make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+  if (a.lse != nullptr && c4 == 0) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 namespace {
@@ -821,7 +850,8 @@ namespace {
 struct Plan {
   int QT, row_tiles, columns;
   bool cut() const { return columns > 1; }
-  size_t rows() const { return cut() ? (size_t)columns * row_tiles * 2 * QT : 0; }
+  size_t ctas() const { return (size_t)columns * row_tiles; }
+  size_t rows() const { return cut() ? ctas() * 2 * QT : 0; }
 };
 Plan plan_of(int B, int T, int G, int Hkv, int n_tokens) {
   Plan p;
@@ -855,27 +885,44 @@ cudaError_t launch_qt(const TreeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+// Workspace: left as it was (other calls keep counters there) | the cut units
+// | (m, l) of every partial row | their O.
+struct Layout {
+  size_t unit, ml, o, total;
+};
+static Layout layout_of(const Plan& p, int B, int Hkv, int D) {
+  Layout l;
+  l.unit = round256((size_t)B * Hkv * sizeof(int));
+  l.ml = l.unit + (p.cut() ? round256(p.ctas() * sizeof(int4)) : 0);
+  l.o = l.ml + round256(p.rows() * sizeof(float2));
+  l.total = l.o + p.rows() * D * sizeof(float);
+  return l;
+}
+
 size_t tree_attn_workspace_bytes(int B, int T, int H, int Hkv, int D, int n_tokens) {
-  const Plan p = plan_of(B, T, H / Hkv, Hkv, n_tokens);
-  // (m, l) of every partial row, then their O
-  return round256(p.rows() * 2 * sizeof(float)) + p.rows() * D * sizeof(float);
+  return layout_of(plan_of(B, T, H / Hkv, Hkv, n_tokens), B, Hkv, D).total;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& args, cudaStream_t stream) {
   TreeArgs a = args;
   a.G = a.H / a.Hkv;
   const Plan p = plan_of(a.batch, a.T, a.G, a.Hkv, a.k_vis + a.n_text + a.T);
+  const Layout l = layout_of(p, a.batch, a.Hkv, a.D);
+  char* ws = static_cast<char*>(a.ws);
   a.row_tiles = p.row_tiles;
   a.columns = p.columns;
-  a.part_ml = static_cast<float*>(a.ws);
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + round256(p.rows() * 2 * sizeof(float)));
+  a.part_unit = reinterpret_cast<int*>(ws + l.unit);
+  a.part_ml = reinterpret_cast<float*>(ws + l.ml);
+  a.part_o = reinterpret_cast<float*>(ws + l.o);
   cudaError_t e;
   if (a.D == 128) e = p.QT == 128 ? launch_qt<128, 128>(a, stream) : launch_qt<128, 256>(a, stream);
   else e = p.QT == 128 ? launch_qt<64, 128>(a, stream) : launch_qt<64, 256>(a, stream);
   if (e != cudaSuccess || !p.cut()) return e;
-  const long long rows = (long long)a.batch * a.T * a.H;
-  return launch_dependent(a.D == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>, dim3((unsigned)((rows + 7) / 8)),
-                          dim3(256), 0, stream, a, p.QT);
+  const long long rows = (long long)a.T * a.G;
+  const dim3 grid((unsigned)p.ctas(), (unsigned)(((rows < p.QT ? rows : p.QT) + 31) / 32), (unsigned)(a.D / 32));
+  auto merge = a.D == 128 ? (p.QT == 128 ? tree_merge_kernel<128, 128> : tree_merge_kernel<128, 256>)
+                          : (p.QT == 128 ? tree_merge_kernel<64, 128> : tree_merge_kernel<64, 256>);
+  return launch_dependent(merge, grid, dim3(256), 0, stream, a);
 }
 
 }  // namespace sv
