@@ -64,19 +64,23 @@ constexpr size_t kMaxSmem = 232448;         // 227 KB
 constexpr float kRescale = 32.f;
 static_assert(kLoadWarps * 32 == kTile, "one loader thread per token");
 
-// Ring slots (128 tokens of K or V) beside QT query rows.
+// Ring slots (128 tokens of K or V) beside the query rows.  The next segment's
+// queries are loaded while the last one runs where two sets fit (128 rows: many
+// short segments; a load takes the time of two tiles when HBM is busy).
 template <int D, int QT>
 struct Smem {
   static constexpr int kSlotBytes = kTile * D * 2;
-  static constexpr int kQBytes = QT * D * 2;
-  static constexpr int kSlots = D == 128 ? (QT == 128 ? 6 : 5) : (QT == 128 ? 12 : 10);
-  static constexpr int kBytes = kQBytes + kSlots * kSlotBytes;
+  static constexpr int kQBufs = QT == 128 ? 2 : 1;
+  static constexpr int kQBytes = QT * D * 2;            // one set
+  static constexpr int kSlots = D == 128 ? 5 : (QT == 128 ? 12 : 10);
+  static constexpr int kRing = kQBufs * kQBytes;        // where the ring begins
+  static constexpr int kBytes = kRing + kSlots * kSlotBytes;
   static_assert(kSlots <= kMaxSlots && kSlots / 2 + 1 < kValidRing, "ring sizes");
 };
 
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, done, turn[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full, done, turn[2];
   uint32_t tmem;
   int abort;
   int odd_values;                 // some drafted V held an infinity or NaN
@@ -122,6 +126,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 columns, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem], A bf16 pairs in 32-bit columns, B token-major.
@@ -154,6 +168,12 @@ __device__ __forceinline__ bool zero_odd(uint4* p) {
 // so its allocation begins at column 0 (checked at the start).
 __host__ __device__ constexpr uint32_t tmem_s(int s) { return s * 128; }
 __host__ __device__ constexpr uint32_t tmem_o(int s) { return 256 + s * 128; }
+
+// Ring positions of a CTA's K and V tiles: K0 K1 V0 K2 V1 K3 V2 ..., the order
+// in which they are used (V a softmax later than K; requested together, V
+// would hold its slot that much longer).
+__device__ __forceinline__ uint32_t ring_k(uint32_t tile) { return tile > 0 ? 2 * tile - 1 : 0; }
+__device__ __forceinline__ uint32_t ring_v(uint32_t tile) { return 2 * tile + 2; }
 
 // ---- the line of tiles and its pieces
 
@@ -246,12 +266,8 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int S = M::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms are 1 KB
   __shared__ Shared sh;
-  grid_dep_sync();
-  if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) flag_status(a.status, kStatusTimeout);
-    return;
-  }
-  const uint32_t q_base = smem_u32(smem), ring = q_base + M::kQBytes;
+  const uint32_t q_base = smem_u32(smem), ring = q_base + M::kRing;
+  constexpr uint32_t QB = M::kQBufs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = blockIdx.x / a.row_tiles, row0 = (int)(blockIdx.x % a.row_tiles) * QT;
 
@@ -265,9 +281,9 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       ptx::mbar_init(&sh.s_full[lane - S], 1);
       ptx::mbar_init(&sh.p_full[lane - S], 4);
       ptx::mbar_init(&sh.turn[lane - S], 1);
+      ptx::mbar_init(&sh.q_full[lane - S], kQueryWarps);
+      ptx::mbar_init(&sh.q_empty[lane - S], 2);
     } else if (lane == S + 2) {
-      ptx::mbar_init(&sh.q_full, kQueryWarps);
-      ptx::mbar_init(&sh.q_empty, 2);
       ptx::mbar_init(&sh.o_full, 2);
       ptx::mbar_init(&sh.done, 2);
       sh.abort = 0;
@@ -275,6 +291,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
     }
     ptx::mbar_fence_init();
   }
+  grid_dep_sync();                                    // (nothing before it touches global memory)
   if (warp == 2) {
     // this CTA's piece of the line
     int b = 0;
@@ -344,14 +361,14 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   ptx::tc_fence_after();
   Walk w;
   w.start(sh, row0, QT);
-  if (sh.tmem != 0) w.left = 0;   // (cannot be; reported below)
+  const bool misplaced = sh.tmem != 0 || (smem_u32(smem) & 1023u) != 0;   // (cannot be)
+  if (misplaced) w.left = 0;
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
     // ------------------------------------------------ cache rows
     const int me = threadIdx.x - kLoadWarp * 32;   // this thread's token of every tile
-    uint32_t group = 0;                            // copies issued: K, V, K, V, ...
     // A warp instruction copies RPI rows of its 32: this lane's chunk of row
     // first + i * RPI, at a swizzle that repeats every 8 rows.
     constexpr int RPI = 32 / CPR, VAR = 8 / RPI;
@@ -361,7 +378,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
     for (int i = 0; i < VAR; ++i)
       to[i] = ring + (c >> 3) * kTile * 128 + ((warp - kLoadWarp) * 32 + first) * 128 +
               (((c & 7) ^ ((first + i * RPI) & 7)) * 16);
-    auto copy = [&](const uint16_t* pool, uint32_t rid, uint32_t there) {
+    auto copy = [&](const uint16_t* pool, uint32_t group, uint32_t rid, uint32_t there) {
       const uint32_t slot = group % S;
       uint32_t r[CPR];               // every row id first: no copy waits for a shuffle
 #pragma unroll
@@ -376,15 +393,13 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
           cp_async16(dst + to[i % VAR] + i * RPI * 128, src + (size_t)r[i] * (D * 2), 16u);
       } else {
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          const bool ok = (there >> (first + i * RPI)) & 1;
-          cp_async16(dst + to[i % VAR] + i * RPI * 128, src + (ok ? (size_t)r[i] * (D * 2) : 0), ok ? 16u : 0u);
-        }
+        for (int i = 0; i < CPR; ++i)
+          cp_async16(dst + to[i % VAR] + i * RPI * 128, src + (size_t)r[i] * (D * 2),
+                     (there >> (first + i * RPI)) & 1 ? 16u : 0u);
       }
       // the barrier counts this thread once its copies have landed; the
       // threads that read them fence the proxies
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[slot])) : "memory");
-      ++group;
     };
 
     // Tiles pass three steps: their indices are loaded (two tiles ahead),
@@ -437,22 +452,24 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
     load_index(A);
     load_page(A);
     load_index(B);
-    for (uint32_t tile = 0; A.exists; ++tile) {
-      uint32_t rid = kNoRowId;
-      if (A.there) {
-        if (A.page >= 0 && A.page < a.num_blocks)
-          rid = (((uint32_t)A.page * (uint32_t)a.Hkv + (uint32_t)A.g) << 4) | (uint32_t)(A.pos & 15);
-        else
-          flag_status(a.status, kStatusBadBlock);
+    uint32_t tile = 0, rid = 0, there = 0;    // this tile's row (0: not there) and the warp's rows
+    for (; A.exists; ++tile) {
+      const uint32_t last_rid = rid, last_there = there;
+      bool ok = A.there;
+      if (ok && (A.page < 0 || A.page >= a.num_blocks)) {
+        flag_status(a.status, kStatusBadBlock);
+        ok = false;
       }
+      rid = ok ? (((uint32_t)A.page * (uint32_t)a.Hkv + (uint32_t)A.g) << 4) | (uint32_t)(A.pos & 15) : 0u;
       A = B;
       load_page(A);
       load_index(B);
-      const uint32_t v = __ballot_sync(0xffffffffu, rid != kNoRowId);
-      if (lane == 0) sh.valid[tile % kValidRing][warp - kLoadWarp] = v;
-      copy(k_pool, rid, v);
-      copy(v_pool, rid, v);
+      there = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) sh.valid[tile % kValidRing][warp - kLoadWarp] = there;
+      copy(k_pool, ring_k(tile), rid, there);
+      if (tile > 0) copy(v_pool, ring_v(tile - 1), last_rid, last_there);
     }
+    if (tile > 0) copy(v_pool, ring_v(tile - 1), rid, there);
     cp_async_wait_all();
   } else if (warp >= kQueryWarp) {
     // ------------------------------------------------ query rows: 32 at a time
@@ -461,15 +478,16 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + c * 8;
     uint32_t n = 0;
     for (; w.next(a); ++n) {
-      if (n > 0) wait_bar(&sh.q_empty, (n - 1) & 1, sh);
+      if (n >= QB) wait_bar(&sh.q_empty[n % QB], (n / QB - 1) & 1, sh);
       __syncwarp();
       const Segment& x = w.x;
+      const uint32_t base = q_base + (n % QB) * M::kQBytes;
       for (int r0 = 32 * (warp - kQueryWarp); r0 < x.rows; r0 += 32 * kQueryWarps) {
         const int row = row0 + r0 + lane, tk = row / a.G;
         // (a row past the last one reads the sequence's first: its results go nowhere)
         const uint32_t mine = r0 + lane < x.rows ? (uint32_t)tk * a.H + (uint32_t)(x.g * a.G + row - tk * a.G) : 0u;
         const uint16_t* src = q + (size_t)x.b * a.T * a.H * D;
-        const uint32_t dst = q_base + (r0 >> 7) * kTile * D * 2 + (c >> 3) * kTile * 128 + ((r0 & 127) + first) * 128;
+        const uint32_t dst = base + (r0 >> 7) * kTile * D * 2 + (c >> 3) * kTile * 128 + ((r0 & 127) + first) * 128;
 #pragma unroll
         for (int i = 0; i < CPR; ++i) {
           const uint32_t r = __shfl_sync(0xffffffffu, mine, first + i * RPI);
@@ -479,7 +497,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.q_full);
+      if (lane == 0) ptx::mbar_arrive(&sh.q_full[n % QB]);
     }
   } else if (warp < kMmaWarp + 2) {
     // ------------------------------------------------ products
@@ -513,10 +531,11 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       const int nt = w.x.t1 - w.x.t0;
       // this stream's tiles: every second one from s on, or all
       const int step = split ? 2 : 1, begin = split ? (int)s : 0;
-      const uint32_t qa = q_lo + (split ? 0u : s) * (kTile * D * 2 / 16);
-      wait_bar(&sh.q_full, seg & 1, sh);
+      const uint32_t qb = __shfl_sync(0xffffffffu, seg % QB, 0);
+      const uint32_t qa = q_lo + (qb * M::kQBytes + (split ? 0u : s) * kTile * D * 2) / 16;
+      wait_bar(&sh.q_full[qb], (seg / QB) & 1, sh);
       auto qk = [&](int i) {
-        const uint32_t grp = __shfl_sync(0xffffffffu, 2 * (tile0 + i), 0), slot = grp % S;
+        const uint32_t grp = __shfl_sync(0xffffffffu, ring_k(tile0 + i), 0), slot = grp % S;
         wait_bar(&sh.full[slot], (grp / S) & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
@@ -532,11 +551,11 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
           ptx::mma_commit(&sh.s_full[s]);
           ptx::mma_commit(&sh.empty[slot]);
           if (split) ptx::mma_commit(&sh.empty[slot]);    // (for the stream that does not use it)
-          if (i + step >= nt) ptx::mma_commit(&sh.q_empty);
+          if (i + step >= nt) ptx::mma_commit(&sh.q_empty[qb]);
         }
       };
       auto pv = [&](int i) {
-        const uint32_t grp = __shfl_sync(0xffffffffu, 2 * (tile0 + i) + 1, 0), slot = grp % S;
+        const uint32_t grp = __shfl_sync(0xffffffffu, ring_v(tile0 + i), 0), slot = grp % S;
         wait_bar(&sh.full[slot], (grp / S) & 1, sh);
         wait_bar(&sh.p_full[s], np++ & 1, sh);
         __syncwarp();
@@ -564,7 +583,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
           if (!split) pass_turn();
         }
       } else if (ptx::elect_one()) {              // a stream without a tile
-        ptx::mma_commit(&sh.q_empty);
+        ptx::mma_commit(&sh.q_empty[qb]);
         ptx::mma_commit(&sh.o_full);
       }
       __syncwarp();
@@ -675,14 +694,12 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
           if (j >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
             const uint32_t t_o = tmem_o(s) + lanes;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              ptx::tmem_ld32(t_o + c, o);
-              ptx::tmem_wait_ld(o);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(t_o + c, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
               tmem_st16(t_o + c, o);
-              tmem_st16(t_o + c + 16, o + 16);
             }
           }
           tmem_wait_st();
@@ -691,12 +708,17 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
           // Drafted tokens: a row that does not see one multiplies its V by 0,
           // so an infinity or NaN there is taken out of the product (0
           // instead) and added by the epilogue to the rows that see it.
-          const uint32_t grp = 2 * (tile0 + i) + 1, slot = grp % S;
+          const uint32_t grp = ring_v(tile0 + i), slot = grp % S;
           wait_bar(&sh.full[slot], (grp / S) & 1, sh);
-          uint4* v = reinterpret_cast<uint4*>(smem + M::kQBytes + slot * M::kSlotBytes);
+          uint8_t* v = smem + M::kRing + slot * M::kSlotBytes;
+          const int base = (x.t0 + i) * kTile, from = max(0, ctx - base);
+          const int chunks = (min(kTile, ctx + x.s.tn - base) - from) * CPR;
           bool odd = false;
-#pragma unroll 4
-          for (int k = r; k < kTile * CPR; k += kTile) odd |= zero_odd(v + k);
+#pragma unroll 1
+          for (int k = r; k < chunks; k += kTile) {
+            const int tok = from + k / CPR, ch = k % CPR;
+            odd |= zero_odd(reinterpret_cast<uint4*>(v + (ch >> 3) * kTile * 128 + tok * 128 + ((ch & 7) ^ (tok & 7)) * 16));
+          }
           if (odd) *(volatile int*)&sh.odd_values = 1;
           ptx::fence_proxy_async_smem();
         }
@@ -732,49 +754,56 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
         const size_t orow = ((size_t)x.b * a.T + tk) * a.H + h;
         const size_t slot = part_slot(blockIdx.x, x.t0 == 0);
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const bool odd = *(volatile int*)&sh.odd_values != 0;
-        for (int c = c0; c < c1; c += 32) {
-          uint32_t u[32];
-          ptx::tmem_ld32(tmem_o(split ? 0 : s) + lanes + c, u);
-          ptx::tmem_wait_ld(u);
-          float o[32];
+        // 16 columns at a time, rolled: this code runs once a segment, and
+        // fetching it unrolled took longer than the work
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 16) {
+          uint32_t u[16];
+          float o[16];
+          tmem_ld16(tmem_o(split ? 0 : s) + lanes + c, u);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(u[e]);
           if (split) {
-            ptx::tmem_ld32(tmem_o(1) + lanes + c, u);
-            ptx::tmem_wait_ld(u);
+            tmem_ld16(tmem_o(1) + lanes + c, u);
             // (an empty stream's columns hold nothing that may be read)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               o[e] = (w0 == 0.f ? 0.f : o[e] * w0) + (w1 == 0.f ? 0.f : __uint_as_float(u[e]) * w1);
-          }
-          if (odd && live) {
-            // infinities and NaN of the drafted tokens that this row sees
-            const int d0 = max(0, x.t0 * kTile - ctx), d1 = min(x.s.tn, x.t1 * kTile - ctx);
-            for (int dt = d0; dt < d1; ++dt) {
-              if (a.tree_mask != nullptr ? !((tree >> dt) & 1) : dt > tk) continue;
-              const int pos = x.s.nv + x.s.nt + dt;
-              const int page = __ldg(a.block_table + (size_t)x.b * a.max_blocks + (pos >> 4));
-              if (page < 0 || page >= a.num_blocks) continue;
-              const uint16_t* v = static_cast<const uint16_t*>(a.v_pool) +
-                                  ((((size_t)page * a.Hkv + x.g) << 4) + (pos & 15)) * D + c;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const uint32_t bits = __ldg(v + e);
-                if ((bits & 0x7f80u) == 0x7f80u) o[e] += __uint_as_float(bits << 16);
-              }
-            }
           }
           if (live && whole) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
+            for (int e = 0; e < 16; e += 8)
               dst[e / 8] = make_uint4(bf16x2(o[e] * inv, o[e + 1] * inv), bf16x2(o[e + 2] * inv, o[e + 3] * inv),
                                       bf16x2(o[e + 4] * inv, o[e + 5] * inv), bf16x2(o[e + 6] * inv, o[e + 7] * inv));
           } else if (live) {
             float4* dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + c / 4) * QT + row;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) dst[(e / 4) * QT] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; e += 4) dst[(e / 4) * QT] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (*(volatile int*)&sh.odd_values != 0 && live) {
+          // infinities and NaN of the drafted tokens that this row sees, added
+          // to what this thread has just written
+          const int d0 = max(0, x.t0 * kTile - ctx), d1 = min(x.s.tn, x.t1 * kTile - ctx);
+#pragma unroll 1
+          for (int dt = d0; dt < d1; ++dt) {
+            if (a.tree_mask != nullptr ? !((tree >> dt) & 1) : dt > tk) continue;
+            const int pos = x.s.nv + x.s.nt + dt;
+            const int page = __ldg(a.block_table + (size_t)x.b * a.max_blocks + (pos >> 4));
+            if (page < 0 || page >= a.num_blocks) continue;
+            const uint16_t* v =
+                static_cast<const uint16_t*>(a.v_pool) + ((((size_t)page * a.Hkv + x.g) << 4) + (pos & 15)) * D;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+              const uint32_t bits = __ldg(v + c);
+              if ((bits & 0x7f80u) != 0x7f80u) continue;
+              uint16_t* out = static_cast<uint16_t*>(a.out) + orow * D + c;
+              float* part = a.part_o + ((slot * (D / 4) + c / 4) * QT + row) * 4 + (c & 3);
+              const float sum = __uint_as_float(bits << 16) + (whole ? __uint_as_float((uint32_t)*out << 16) : *part);
+              if (whole) *out = (uint16_t)f32_to_bf16_bits(sum);
+              else *part = sum;
+            }
           }
         }
         if (live && c0 == 0) {
@@ -799,7 +828,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && (sh.abort || sh.tmem != 0)) flag_status(a.status, kStatusTimeout);
+  if (threadIdx.x == 0 && (sh.abort || misplaced)) flag_status(a.status, kStatusTimeout);
   if (warp == 0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(sh.tmem, kTmemCols);
