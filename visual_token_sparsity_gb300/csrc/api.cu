@@ -715,7 +715,8 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
   if (vis_idx && (k < 0 || k > seqs->n_vis)) return fail(SV_ERR_INVALID_ARG, "need 0 <= k <= n_vis");
   if ((long long)seqs->batch * T * H > 0x7fffffffLL) return fail(SV_ERR_INVALID_ARG, "batch * T * H too large");
   const long long n_tok = (long long)k_vis + seqs->n_text + T;   // <= max_blocks * 16
-  if (n_tok > 0x7fffffffLL - 1024) return fail(SV_ERR_UNSUPPORTED, "more than 2^31 tokens");
+  if (seqs->batch * (n_tok / 128 + 1) > 0x7fffffffLL / Hkv)
+    return fail(SV_ERR_UNSUPPORTED, "batch * n_kv_heads * tokens beyond 2^38");
   s = check_ws(ws, ws_bytes,
                sv_tree_attn_workspace_bytes(seqs->batch, T, H, Hkv, layer->head_dim, (int)n_tok));
   if (s != SV_OK) return s;

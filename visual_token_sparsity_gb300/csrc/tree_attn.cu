@@ -85,7 +85,7 @@ struct Shared {
   int abort;
   int odd_values;                 // some drafted V held an infinity or NaN
   int b0;                         // this CTA's piece: first sequence,
-  long long off0, count, total;   // first tile inside it, tiles; the whole line
+  int off0, count, total;         // first tile inside it, tiles; the whole line
   alignas(16) uint32_t valid[kValidRing][4];  // tokens of a tile that are there
   float ml[2][kTile][2];          // the streams' maxima and sums
 };
@@ -204,7 +204,12 @@ __device__ __forceinline__ int tiles_of(const TreeArgs& a, int b, int row0, int 
   return (tokens_of(a, s, row0, QT) + kTile - 1) / kTile;
 }
 
-__device__ __forceinline__ long long piece_begin(long long total, int c, int C) { return total * c / C; }
+// First tile of piece c of C: floor(total * c / C).  (32 bits throughout: a 64-bit
+// division is a hundred instructions, and code that runs once is mostly fetching.)
+__device__ __forceinline__ int piece_begin(int total, int c, int C) {
+  const int q = total / C;
+  return q * c + (total - q * C) * c / C;
+}
 
 // Consecutive tiles [t0, t1) of one (sequence, KV head) unit.
 struct Segment {
@@ -215,8 +220,7 @@ struct Segment {
 
 // Walks a CTA's piece; every warp has its own and sees the same segments.
 struct Walk {
-  int b, row0, QT;
-  long long off, left;
+  int b, row0, QT, off, left;
   Segment x;
   __device__ void start(const Shared& sh, int top, int QT_) {
     row0 = top;
@@ -230,11 +234,11 @@ struct Walk {
       seq_of(a, b, x.s);
       x.tokens = tokens_of(a, x.s, row0, QT);
       x.tiles = (x.tokens + kTile - 1) / kTile;
-      if (off < (long long)x.tiles * a.Hkv) {
+      if (off < x.tiles * a.Hkv) {
         x.b = b;
-        x.g = (int)(off / x.tiles);
-        x.t0 = (int)(off - (long long)x.g * x.tiles);
-        x.t1 = (int)min((long long)x.tiles, x.t0 + left);
+        x.g = off / x.tiles;
+        x.t0 = off - x.g * x.tiles;
+        x.t1 = min(x.tiles, x.t0 + left);
         x.rows = min(QT, x.s.tn * a.G - row0);
         off += x.t1 - x.t0;
         left -= x.t1 - x.t0;
@@ -252,9 +256,6 @@ struct Walk {
 // [slot][row], O is [slot][dim / 4][row][4]: consecutive rows, which
 // neighbouring lanes hold, lie side by side.
 __device__ __forceinline__ size_t part_slot(int cta, bool begins) { return (size_t)cta * 2 + (begins ? 1 : 0); }
-
-// The piece that holds tile x of a line: the last one that begins at or before it.
-__device__ __forceinline__ int piece_of(long long x, long long total, int C) { return (int)(((x + 1) * C - 1) / total); }
 
 }  // namespace
 
@@ -294,31 +295,30 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
   grid_dep_sync();                                    // (nothing before it touches global memory)
   if (warp == 2) {
     // this CTA's piece of the line
-    int b = 0;
-    long long before = 0, begin, end, total;
+    int b = 0, before = 0, begin, end, total;
     if (!a.lens.any() && a.n_new == nullptr) {
-      const long long per = (long long)a.Hkv * tiles_of(a, 0, row0, QT);
+      const int per = a.Hkv * tiles_of(a, 0, row0, QT);
       total = per * a.batch;
       begin = piece_begin(total, col, a.columns);
       end = piece_begin(total, col + 1, a.columns);
-      b = per > 0 ? (int)(begin / per) : 0;
+      b = per > 0 ? begin / per : 0;
       before = b * per;
     } else {
       // tiles of sequences [b0, b0 + 32) up to this lane's
-      auto scan = [&](int b0, long long& n) {
-        n = b0 + lane < a.batch ? (long long)a.Hkv * tiles_of(a, b0 + lane, row0, QT) : 0;
-        long long inc = n;
+      auto scan = [&](int b0, int& n) {
+        n = b0 + lane < a.batch ? a.Hkv * tiles_of(a, b0 + lane, row0, QT) : 0;
+        int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
           if (lane >= o) inc += y;
         }
         return inc;
       };
-      long long n, inc = scan(0, n);
+      int n, inc = scan(0, n);
       total = __shfl_sync(0xffffffffu, inc, 31);
       for (int b0 = 32; b0 < a.batch; b0 += 32) {
-        long long n2;
+        int n2;
         total += __shfl_sync(0xffffffffu, scan(b0, n2), 31);
       }
       begin = piece_begin(total, col, a.columns);
@@ -821,9 +821,13 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       // the unit that begins here and goes on, for the merge: its sequence, KV
       // head and last piece (-1: none), its rows and the line's length
       const Segment& x = w.x;
-      const int last =
-          cut ? piece_of(piece_begin(sh.total, col + 1, a.columns) + x.tiles - x.t1 - 1, sh.total, a.columns) : -1;
-      reinterpret_cast<int4*>(a.part_unit)[blockIdx.x] = make_int4(x.b, x.g, last, x.rows | (int)min(sh.total, 0x7fffLL) << 16);
+      int last = -1;
+      if (cut) {
+        // the last piece that begins before the unit's end
+        const int end = piece_begin(sh.total, col + 1, a.columns) + x.tiles - x.t1;
+        for (last = col + 1; last + 1 < a.columns && piece_begin(sh.total, last + 1, a.columns) < end; ++last) {}
+      }
+      reinterpret_cast<int4*>(a.part_unit)[blockIdx.x] = make_int4(x.b, x.g, last, x.rows | min(sh.total, 0x7fff) << 16);
     }
   }
   ptx::tc_fence_before();
@@ -875,7 +879,8 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a) {
 namespace {
 
 // Row tiles of 128 rows, or of 256 when there are more rows than that; as
-// many pieces as leave every SM one CTA, at most one per tile of tokens.
+// many pieces as leave every SM one CTA, of two token tiles at least (one for
+// each stream; pieces of one measured 2 % faster to 9 % slower).
 struct Plan {
   int QT, row_tiles, columns;
   bool cut() const { return columns > 1; }
@@ -889,7 +894,7 @@ Plan plan_of(int B, int T, int G, int Hkv, int n_tokens) {
   p.row_tiles = (int)((rows + p.QT - 1) / p.QT);
   const long long tiles = (long long)B * Hkv * (((long long)n_tokens + kTile - 1) / kTile);
   long long c = p.row_tiles > 0 ? kCtas / p.row_tiles : 1;
-  if (c > tiles) c = tiles;
+  if (c > tiles / 2) c = tiles / 2;
   p.columns = (int)(c < 1 ? 1 : c);
   return p;
 }
@@ -947,6 +952,13 @@ cudaError_t launch_tree_attn(const TreeArgs& args, cudaStream_t stream) {
   if (a.D == 128) e = p.QT == 128 ? launch_qt<128, 128>(a, stream) : launch_qt<128, 256>(a, stream);
   else e = p.QT == 128 ? launch_qt<64, 128>(a, stream) : launch_qt<64, 256>(a, stream);
   if (e != cudaSuccess || !p.cut()) return e;
+  if (!a.lens.any() && a.n_new == nullptr && (a.tree_mask != nullptr || p.row_tiles == 1)) {
+    // equal lengths: nothing to join when every piece ends with a unit
+    const int tiles = (a.k_vis + a.n_text + a.T + kTile - 1) / kTile, total = tiles * a.batch * a.Hkv;
+    bool whole = true;
+    for (int c = 1; c < p.columns; ++c) whole = whole && (long long)total * c / p.columns % tiles == 0;
+    if (whole) return e;
+  }
   const long long rows = (long long)a.T * a.G;
   const dim3 grid((unsigned)p.ctas(), (unsigned)(((rows < p.QT ? rows : p.QT) + 31) / 32), (unsigned)(a.D / 32));
   auto merge = a.D == 128 ? (p.QT == 128 ? tree_merge_kernel<128, 128> : tree_merge_kernel<128, 256>)
