@@ -171,6 +171,7 @@ struct TreeArgs {
   // set by launch_tree_attn: query heads per KV head, tiles of query rows,
   // pieces of one row tile's work, cut units and their partial results
   int G, row_tiles, columns;
+  bool by_unit;
   int* part_unit;
   float* part_ml;
   float* part_o;
