@@ -649,7 +649,7 @@ sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_
   a.B = B; a.T = N; a.H = H; a.Hk = Hk;
   a.q_out = static_cast<uint16_t*>(q_out); a.k_out = static_cast<uint16_t*>(k_out);
   a.status = status_word(ws);
-  return cuda_status(sv::launch_norm_rope(a, d, false, static_cast<cudaStream_t>(stream)), "sv_qk_norm_rope");
+  return cuda_status(sv::launch_norm_rope(a, d, false, num_sms(), static_cast<cudaStream_t>(stream)), "sv_qk_norm_rope");
 }
 
 sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -687,7 +687,7 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
   a.status = status_word(ws);
   a.block_table = seqs->block_table; a.num_blocks = layer->num_blocks; a.max_blocks = seqs->max_blocks;
   a.n_vis = seqs->n_vis; a.n_text = seqs->n_text; a.lens = lens_of(seqs); a.n_new = n_new;
-  return cuda_status(sv::launch_norm_rope(a, d, true, static_cast<cudaStream_t>(stream)), "sv_qk_norm_rope_append");
+  return cuda_status(sv::launch_norm_rope(a, d, true, num_sms(), static_cast<cudaStream_t>(stream)), "sv_qk_norm_rope_append");
 }
 
 size_t sv_tree_attn_workspace_bytes(int B, int T, int H, int n_kv_heads, int head_dim, int n_tokens) {

@@ -147,7 +147,8 @@ struct NormRopeArgs {
   SeqLens lens;
   const int32_t* n_new;
 };
-cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, int num_sms,
+                             cudaStream_t stream);
 
 // ---- attention of T drafted tokens over the paged cache (tree_attn.cu)
 struct TreeArgs {

@@ -15,6 +15,7 @@
 // rotated: 8 in a row), so no pair crosses lanes and the four (cos, sin) it
 // needs are loaded once per token and reused for the warp's rows.
 #include "common.cuh"
+#include "fastmath.cuh"
 #include "kernels.h"
 
 namespace sv {
@@ -22,40 +23,88 @@ namespace sv {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;     // row groups in flight per warp
+constexpr int kUnroll = 4;       // row groups in flight per warp
+constexpr int kWarpsPerSm = 64;  // warps that a launch spreads over before they take more rows each
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t bf16x2(uint64_t v) {
+  float lo, hi;
+  fm::unpack2(v, lo, hi);
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void unpack4(uint2 u, float* x) {
-  x[0] = bf16_lo(u.x);
-  x[1] = bf16_hi(u.x);
-  x[2] = bf16_lo(u.y);
-  x[3] = bf16_hi(u.y);
-}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) { return bf16x2(fm::pack2(lo, hi)); }
+
+// A lane's 8 elements of a row as the first (p) and second (y) members of
+// four pairs, two pairs per register pair.  INTER: 8 in a row, pairs (2e, 2e + 1);
+// else 4 at off0 and 4 at off1, pairs (e, e + 4).
+template <bool INTER>
+struct Lane8 {
+  uint4 u;
+  __device__ __forceinline__ void load(const uint16_t* row, int off0, int off1) {
+    if (INTER) {
+      u = *reinterpret_cast<const uint4*>(row + off0);
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(row + off0), b = *reinterpret_cast<const uint2*>(row + off1);
+      u = make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* row, int off0, int off1) const {
+    if (INTER) {
+      *reinterpret_cast<uint4*>(row + off0) = u;
+    } else {
+      *reinterpret_cast<uint2*>(row + off0) = make_uint2(u.x, u.y);
+      *reinterpret_cast<uint2*>(row + off1) = make_uint2(u.z, u.w);
+    }
+  }
+  __device__ __forceinline__ void unpack(uint64_t* p, uint64_t* y) const {
+    if (INTER) {
+      p[0] = fm::pack2(bf16_lo(u.x), bf16_lo(u.y));
+      y[0] = fm::pack2(bf16_hi(u.x), bf16_hi(u.y));
+      p[1] = fm::pack2(bf16_lo(u.z), bf16_lo(u.w));
+      y[1] = fm::pack2(bf16_hi(u.z), bf16_hi(u.w));
+    } else {
+      p[0] = fm::pack2(bf16_lo(u.x), bf16_hi(u.x));
+      p[1] = fm::pack2(bf16_lo(u.y), bf16_hi(u.y));
+      y[0] = fm::pack2(bf16_lo(u.z), bf16_hi(u.z));
+      y[1] = fm::pack2(bf16_lo(u.w), bf16_hi(u.w));
+    }
+  }
+  __device__ __forceinline__ void pack(const uint64_t* p, const uint64_t* y) {
+    if (INTER) {
+      float a, b, c, d;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fm::unpack2(p[e], a, b);
+        fm::unpack2(y[e], c, d);
+        (e ? u.z : u.x) = bf16x2(a, c);
+        (e ? u.w : u.y) = bf16x2(b, d);
+      }
+    } else {
+      u = make_uint4(bf16x2(p[0]), bf16x2(p[1]), bf16x2(y[0]), bf16x2(y[1]));
+    }
+  }
+};
 
 }  // namespace
 
-// One warp: kUnroll * (32 / L) consecutive rows of one token, where a token's
-// rows are its H queries, Hk keys and (append) Hk values.
-template <int L, bool APPEND>
+// A warp takes `chunks` chunks of kUnroll * (32 / L) consecutive rows of one
+// token, where a token's rows are its H queries, Hk keys and (append) Hk values.
+template <int L, bool APPEND, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kWarps * 32)
-norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t warps_per_token) {
   constexpr int D = 8 * L;
   constexpr int RPG = 32 / L;                 // rows side by side
-  constexpr int RPW = RPG * kUnroll;
+  constexpr int RPC = RPG * kUnroll;
   grid_dep_sync();
   const int lane = threadIdx.x & 31;
   const int sub = lane / L, j = lane - sub * L;
-  const int rows = a.H + (APPEND ? 2 : 1) * a.Hk;
-  const int wpt = (rows + RPW - 1) / RPW;     // warps per token
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long tok = w / wpt;
-  if (tok >= (long long)a.B * a.T) return;
-  const int r0 = (int)(w - tok * wpt) * RPW;
-  const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
+  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const uint32_t tok = w / warps_per_token;
+  if (tok >= (uint32_t)a.B * a.T) return;
+  const int b = (int)(tok / (uint32_t)a.T), t = (int)(tok - (uint32_t)b * a.T);
+  const int r0 = (int)(w - tok * warps_per_token) * chunks * RPC, r1 = r0 + chunks * RPC;
+  const bool first = r0 == 0 && lane == 0;    // reports for the token
 
   // where the token goes in the cache, and whether it is there at all
   int page = 0, slot = 0;
@@ -66,7 +115,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     const bool ok = seq_lengths(l, b, a.n_vis, a.n_text, 0, nv, nt, kb);
     const int tn = a.n_new ? __ldg(a.n_new + b) : a.T;
     if (!ok || tn < 0 || tn > a.T) {
-      if (r0 == 0 && t == 0 && lane == 0) flag_status(a.status, kStatusBadLength);
+      if (first && t == 0) flag_status(a.status, kStatusBadLength);
       return;
     }
     if (t >= tn) return;
@@ -74,20 +123,18 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     page = __ldg(a.block_table + (size_t)b * a.max_blocks + (pos >> 4));
     slot = pos & 15;
     if (page < 0 || page >= a.num_blocks) {
-      if (r0 == 0 && lane == 0) flag_status(a.status, kStatusBadBlock);
+      if (first) flag_status(a.status, kStatusBadBlock);
       page = -1;                              // the queries are still written
     }
   }
 
-  // this lane's elements off0.. and off1.. and the four turns between them
+  // this lane's elements off0.. and off1.. and the four turns between them,
+  // two to a register pair
   const int half = a.rot >> 1;
-  const bool turned = 4 * j < half;
-  const bool split = turned && !a.interleaved;
+  const bool turned = 4 * j < half, split = !INTER && turned;
   const int off0 = split ? 4 * j : 8 * j;
   const int off1 = split ? half + 4 * j : 8 * j + 4;
-  float cs[4], sn[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
+  uint64_t cs[2] = {fm::splat2(1.f), fm::splat2(1.f)}, sn[2] = {0, 0};
   if (half > 0) {
     int p[3] = {0, 0, 0};
     bool bad = false;
@@ -98,118 +145,134 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         bad |= p[x] < 0 || p[x] >= a.n_pos;
       }
     if (bad) {
-      if (r0 == 0 && lane == 0) flag_status(a.status, kStatusBadPosition);
+      if (first) flag_status(a.status, kStatusBadPosition);
       return;
     }
     if (turned) {
+      float2 f[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int pr = 4 * j + i;
         const int px = pr < a.sec_end[0] ? p[0] : pr < a.sec_end[1] ? p[1] : p[2];
-        const float2 v = __ldg(reinterpret_cast<const float2*>(a.cos_sin) + (size_t)px * half + pr);
-        cs[i] = v.x;
-        sn[i] = v.y;
+        f[i] = __ldg(reinterpret_cast<const float2*>(a.cos_sin) + (size_t)px * half + pr);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        cs[i] = fm::pack2(f[2 * i].x, f[2 * i + 1].x);
+        sn[i] = fm::pack2(f[2 * i].y, f[2 * i + 1].y);
       }
     }
   }
+  const uint64_t ns[2] = {sn[0] ^ 0x8000000080000000ull, sn[1] ^ 0x8000000080000000ull};
 
-  uint2 u0[kUnroll], u1[kUnroll];
-#pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int r = r0 + i * RPG + sub;
-    u0[i] = u1[i] = make_uint2(0u, 0u);
-    if (sub < RPG && r < rows) {
-      const uint16_t* src = r < a.H          ? a.q + tok * a.q_stride + (size_t)r * D
-                            : r < a.H + a.Hk ? a.k + tok * a.k_stride + (size_t)(r - a.H) * D
-                                             : a.v + tok * a.v_stride + (size_t)(r - a.H - a.Hk) * D;
-      u0[i] = *reinterpret_cast<const uint2*>(src + off0);
-      u1[i] = *reinterpret_cast<const uint2*>(src + off1);
+  // rows [n0, n1) of one kind: at src + row * D, to dst + row * stride
+  auto rows = [&](const uint16_t* src, int n0, int n1, const uint16_t* weight, uint16_t* dst, size_t stride) {
+    uint64_t gp[2], gy[2];
+    if (NORM && weight != nullptr) {
+      Lane8<INTER> g;
+      g.load(weight, off0, off1);
+      g.unpack(gp, gy);
     }
-  }
+    const int mine = n0 + sub;
+    const uint16_t* from = src + (size_t)mine * D;
+    uint16_t* to = dst + (size_t)mine * stride;
+    const int left = sub < RPG ? n1 - mine : 0;       // of this lane's rows, RPG apart
+    for (int done = 0; done < n1 - n0; done += RPC, from += RPC * D, to += RPC * stride) {
+      Lane8<INTER> x[kUnroll];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int r = r0 + i * RPG + sub;
-    const bool live = sub < RPG && r < rows;
-    const bool is_q = r < a.H, is_v = r >= a.H + a.Hk;
-    float x[8];
-    unpack4(u0[i], x);
-    unpack4(u1[i], x + 4);
-    const uint16_t* wgt = is_q ? a.q_weight : a.k_weight;
-    // the reduction is warp-wide: every lane takes part
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
-      if (o >= L) continue;
-      const float y = __shfl_down_sync(0xffffffffu, s, o);
-      if (j + o < L) s += y;
-    }
-    s = __shfl_sync(0xffffffffu, s, sub < RPG ? sub * L : lane);
-    if (!live) continue;
-    if (!is_v) {
-      if (wgt != nullptr) {
-        const float inv = rsqrtf(s * (1.f / D) + a.eps);
-        float g[8];
-        unpack4(__ldg(reinterpret_cast<const uint2*>(wgt + off0)), g);
-        unpack4(__ldg(reinterpret_cast<const uint2*>(wgt + off1)), g + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e];
+      for (int i = 0; i < kUnroll; ++i) {
+        x[i].u = make_uint4(0u, 0u, 0u, 0u);
+        if (done + i * RPG < left) x[i].load(from + i * RPG * D, off0, off1);
       }
-      if (turned) {
-        // rotate-half: pairs (e, e + 4); interleaved: pairs (2e, 2e + 1)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (split) {
-            const float p = x[e], q = x[e + 4];
-            x[e] = p * cs[e] - q * sn[e];
-            x[e + 4] = p * sn[e] + q * cs[e];
-          } else {
-            const float p = x[2 * e], q = x[2 * e + 1];
-            x[2 * e] = p * cs[e] - q * sn[e];
-            x[2 * e + 1] = p * sn[e] + q * cs[e];
+      for (int i = 0; i < kUnroll; ++i) {
+        uint64_t p[2], y[2];
+        x[i].unpack(p, y);
+        if (NORM && weight != nullptr) {
+          uint64_t s2 = fm::mul2(p[0], p[0]);
+          s2 = fm::fma2(p[1], p[1], s2);
+          s2 = fm::fma2(y[0], y[0], s2);
+          s2 = fm::fma2(y[1], y[1], s2);
+          float s, s_hi;
+          fm::unpack2(s2, s, s_hi);
+          s += s_hi;
+          // the reduction is warp-wide: every lane takes part
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) {
+            if (o >= L) continue;
+            const float z = __shfl_down_sync(0xffffffffu, s, o);
+            if (j + o < L) s += z;
+          }
+          s = __shfl_sync(0xffffffffu, s, sub < RPG ? sub * L : lane);
+          const uint64_t inv = fm::splat2(rsqrtf(s * (1.f / D) + a.eps));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            p[e] = fm::mul2(fm::mul2(p[e], inv), gp[e]);
+            y[e] = fm::mul2(fm::mul2(y[e], inv), gy[e]);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t re = fm::fma2(p[e], cs[e], fm::mul2(y[e], ns[e]));
+          y[e] = fm::fma2(p[e], sn[e], fm::mul2(y[e], cs[e]));
+          p[e] = re;
+        }
+        x[i].pack(p, y);
+        if (done + i * RPG < left) x[i].store(to + (size_t)(i * RPG) * stride, off0, off1);
       }
-      u0[i] = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
-      u1[i] = make_uint2(bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
     }
-    uint16_t* dst;
-    if (APPEND) {
-      if (is_q) {
-        dst = a.q_out + ((size_t)tok * a.H + r) * D;
-      } else {
-        if (page < 0) continue;
-        const int g = is_v ? r - a.H - a.Hk : r - a.H;
-        dst = (is_v ? a.v_out : a.k_out) + ((((size_t)page * a.Hk + g) << 4) + slot) * D;
-      }
-    } else {
-      dst = is_q ? a.q_out + (((size_t)b * a.H + r) * a.T + t) * D
-                 : a.k_out + (((size_t)b * a.Hk + (r - a.H)) * a.T + t) * D;
-    }
-    *reinterpret_cast<uint2*>(dst + off0) = u0[i];
-    *reinterpret_cast<uint2*>(dst + off1) = u1[i];
+  };
+  if (r0 < a.H) {
+    const uint16_t* q = a.q + tok * (size_t)a.q_stride;
+    if (APPEND) rows(q, r0, min(r1, a.H), a.q_weight, a.q_out + (size_t)tok * a.H * D, D);
+    else rows(q, r0, min(r1, a.H), a.q_weight, a.q_out + ((size_t)b * a.H * a.T + t) * D, (size_t)a.T * D);
+  }
+  if (page < 0) return;
+  if (r1 > a.H && r0 < a.H + a.Hk) {
+    const uint16_t* k = a.k + tok * (size_t)a.k_stride;
+    const int n0 = max(0, r0 - a.H), n1 = min(a.Hk, r1 - a.H);
+    if (APPEND) rows(k, n0, n1, a.k_weight, a.k_out + ((size_t)page * a.Hk * 16 + slot) * D, 16 * D);
+    else rows(k, n0, n1, a.k_weight, a.k_out + ((size_t)b * a.Hk * a.T + t) * D, (size_t)a.T * D);
+  }
+  if (APPEND && r1 > a.H + a.Hk) {
+    // values: 16 bytes a lane, L lanes a row
+    const uint16_t* v = a.v + tok * (size_t)a.v_stride;
+    uint16_t* to = a.v_out + ((size_t)page * a.Hk * 16 + slot) * D;
+    const int n0 = max(0, r0 - a.H - a.Hk), n1 = min(a.Hk, r1 - a.H - a.Hk);
+    if (sub < RPG)
+      for (int g = n0 + sub; g < n1; g += RPG)
+        *reinterpret_cast<uint4*>(to + (size_t)g * 16 * D + 8 * j) = *reinterpret_cast<const uint4*>(v + (size_t)g * D + 8 * j);
   }
 }
 
+// Chunks per warp: one when there are few tokens (latency), up to a whole
+// token's when there are enough to fill the SMs several times over.
 template <int L>
-static cudaError_t launch_l(const NormRopeArgs& a, bool append, cudaStream_t stream) {
-  const int rpw = 32 / L * kUnroll;
-  const int rows = a.H + (append ? 2 : 1) * a.Hk;
-  const long long warps = (long long)a.B * a.T * ((rows + rpw - 1) / rpw);
-  const long long blocks = (warps + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_dependent(append ? norm_rope_kernel<L, true> : norm_rope_kernel<L, false>, dim3((unsigned)blocks),
-                          dim3(kWarps * 32), 0, stream, a);
+static cudaError_t launch_l(const NormRopeArgs& a, bool append, int num_sms, cudaStream_t stream) {
+  const int rpc = 32 / L * kUnroll;
+  const int rows = a.H + (append ? 2 : 1) * a.Hk, all = (rows + rpc - 1) / rpc;
+  const long long tokens = (long long)a.B * a.T;
+  long long chunks = tokens * all / ((long long)num_sms * kWarpsPerSm);
+  chunks = chunks < 1 ? 1 : chunks > all ? all : chunks;
+  const long long per_token = (all + chunks - 1) / chunks;
+  const long long blocks = (tokens * per_token + kWarps - 1) / kWarps;
+  if (blocks * kWarps > 0xffffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
+  auto kernel = append ? (a.interleaved ? (norm ? norm_rope_kernel<L, true, true, true> : norm_rope_kernel<L, true, true, false>)
+                                        : (norm ? norm_rope_kernel<L, true, false, true> : norm_rope_kernel<L, true, false, false>))
+                       : (a.interleaved ? (norm ? norm_rope_kernel<L, false, true, true> : norm_rope_kernel<L, false, true, false>)
+                                        : (norm ? norm_rope_kernel<L, false, false, true> : norm_rope_kernel<L, false, false, false>));
+  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a, (int)chunks,
+                          (uint32_t)per_token);
 }
 
-cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, cudaStream_t stream) {
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, int num_sms, cudaStream_t stream) {
   if ((long long)a.B * a.T == 0) return cudaSuccess;
   switch (d) {
-    case 64: return launch_l<8>(a, append, stream);
-    case 72: return launch_l<9>(a, append, stream);
-    case 80: return launch_l<10>(a, append, stream);
-    case 128: return launch_l<16>(a, append, stream);
+    case 64: return launch_l<8>(a, append, num_sms, stream);
+    case 72: return launch_l<9>(a, append, num_sms, stream);
+    case 80: return launch_l<10>(a, append, num_sms, stream);
+    case 128: return launch_l<16>(a, append, num_sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -47,9 +47,11 @@ constexpr int kMmaWarp = 8;                 // and 9: one per stream
 constexpr int kLoadWarp = 10, kLoadWarps = 4;
 constexpr int kQueryWarp = 14, kQueryWarps = 2;
 constexpr int kThreads = 512;
-// Registers: 512 threads at 128 at launch; the softmax warps hold a whole row
-// of S (128 columns), the others give theirs up: 256 x 192 + 256 x 64.
-constexpr int kSoftRegs = 192, kOtherRegs = 64;
+// Registers: 512 threads at 128 at launch; the softmax warps, which hold a
+// whole row of S (128 columns), take some of the others'.  The cache-row warps
+// need 80: with 64 they spill, and the LLaVA-NeXT batch took 81 us, not 77 (160 /
+// 96, where the softmax warps spill: 79).
+constexpr int kSoftRegs = 176, kOtherRegs = 80;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 65536 && 32 * (kQueryWarp + kQueryWarps) == kThreads,
               "register split");
 constexpr int kTmemCols = 512;              // S0 | S1 | O0 | O1, 128 columns each
