@@ -22,8 +22,15 @@ namespace sv {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kUnroll = 4;       // row groups in flight per warp
+constexpr int kWarps = 4;
+// Row groups in flight per warp (and as many more on their way) and the CTAs per
+// SM that the registers leave: of 1 to 4 groups and 3 to 5 CTAs of 8 warps, 8 and
+// 9 of 4, these were the fastest (16384 vision tokens 28 us, 28 to 43; a
+// prefill of 11540 tokens 34 us, 34 to 51).
+template <bool APPEND>
+struct Shape {
+  static constexpr int kUnroll = APPEND ? 2 : 3, kCtas = APPEND ? 9 : 8;
+};
 constexpr int kWarpsPerSm = 64;  // warps that a launch spreads over before they take more rows each
 
 __device__ __forceinline__ uint32_t bf16x2(uint64_t v) {
@@ -88,14 +95,14 @@ struct Lane8 {
 
 }  // namespace
 
-// A warp takes `chunks` chunks of kUnroll * (32 / L) consecutive rows of one
-// token, where a token's rows are its H queries, Hk keys and (append) Hk values.
+// A warp takes `per_warp` consecutive rows of one token, where a token's rows
+// are its H queries, Hk keys and (append) Hk values.
 template <int L, bool APPEND, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32)
-norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t warps_per_token) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<APPEND>::kCtas)
+norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t warps_per_token) {
   constexpr int D = 8 * L;
   constexpr int RPG = 32 / L;                 // rows side by side
-  constexpr int RPC = RPG * kUnroll;
+  constexpr int kUnroll = Shape<APPEND>::kUnroll, RPC = RPG * kUnroll;
   grid_dep_sync();
   const int lane = threadIdx.x & 31;
   const int sub = lane / L, j = lane - sub * L;
@@ -103,8 +110,30 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t wa
   const uint32_t tok = w / warps_per_token;
   if (tok >= (uint32_t)a.B * a.T) return;
   const int b = (int)(tok / (uint32_t)a.T), t = (int)(tok - (uint32_t)b * a.T);
-  const int r0 = (int)(w - tok * warps_per_token) * chunks * RPC, r1 = r0 + chunks * RPC;
+  const int r0 = (int)(w - tok * warps_per_token) * per_warp, r1 = r0 + per_warp;
   const bool first = r0 == 0 && lane == 0;    // reports for the token
+
+  // this lane's elements: off0.. and off1..
+  const int half = a.rot >> 1;
+  const bool turned = 4 * j < half, split = !INTER && turned;
+  const int off0 = split ? 4 * j : 8 * j;
+  const int off1 = split ? half + 4 * j : 8 * j + 4;
+  // one chunk, of which this lane has the rows i * RPG < left
+  Lane8<INTER> x[kUnroll];
+  auto load = [&](Lane8<INTER>* to, const uint16_t* from, int left) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      to[i].u = make_uint4(0u, 0u, 0u, 0u);
+      if (i * RPG < left) to[i].load(from + i * RPG * D, off0, off1);
+    }
+  };
+  const uint16_t* q = a.q + tok * (size_t)a.q_stride;
+  const uint16_t* k = a.k + tok * (size_t)a.k_stride;
+  // (the first rows are on their way before anything waits for a length or a position)
+  const bool has_q = r0 < a.H;
+  const int k0 = max(0, r0 - a.H), k1 = min(a.Hk, r1 - a.H);
+  if (has_q) load(x, q + (size_t)(r0 + sub) * D, sub < RPG ? min(r1, a.H) - r0 - sub : 0);
+  else if (k0 < k1) load(x, k + (size_t)(k0 + sub) * D, sub < RPG ? k1 - k0 - sub : 0);
 
   // where the token goes in the cache, and whether it is there at all
   int page = 0, slot = 0;
@@ -128,12 +157,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t wa
     }
   }
 
-  // this lane's elements off0.. and off1.. and the four turns between them,
-  // two to a register pair
-  const int half = a.rot >> 1;
-  const bool turned = 4 * j < half, split = !INTER && turned;
-  const int off0 = split ? 4 * j : 8 * j;
-  const int off1 = split ? half + 4 * j : 8 * j + 4;
+  // the four turns between this lane's elements, two to a register pair
   uint64_t cs[2] = {fm::splat2(1.f), fm::splat2(1.f)}, sn[2] = {0, 0};
   if (half > 0) {
     int p[3] = {0, 0, 0};
@@ -165,7 +189,8 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t wa
   }
   const uint64_t ns[2] = {sn[0] ^ 0x8000000080000000ull, sn[1] ^ 0x8000000080000000ull};
 
-  // rows [n0, n1) of one kind: at src + row * D, to dst + row * stride
+  // rows [n0, n1) of one kind: at src + row * D (the first chunk is in x
+  // already), to dst + row * stride
   auto rows = [&](const uint16_t* src, int n0, int n1, const uint16_t* weight, uint16_t* dst, size_t stride) {
     uint64_t gp[2], gy[2];
     if (NORM && weight != nullptr) {
@@ -178,12 +203,8 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t wa
     uint16_t* to = dst + (size_t)mine * stride;
     const int left = sub < RPG ? n1 - mine : 0;       // of this lane's rows, RPG apart
     for (int done = 0; done < n1 - n0; done += RPC, from += RPC * D, to += RPC * stride) {
-      Lane8<INTER> x[kUnroll];
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        x[i].u = make_uint4(0u, 0u, 0u, 0u);
-        if (done + i * RPG < left) x[i].load(from + i * RPG * D, off0, off1);
-      }
+      Lane8<INTER> next[kUnroll];
+      if (done + RPC < n1 - n0) load(next, from + RPC * D, left - done - RPC);
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         uint64_t p[2], y[2];
@@ -219,20 +240,19 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t wa
         }
         x[i].pack(p, y);
         if (done + i * RPG < left) x[i].store(to + (size_t)(i * RPG) * stride, off0, off1);
+        x[i] = next[i];
       }
     }
   };
-  if (r0 < a.H) {
-    const uint16_t* q = a.q + tok * (size_t)a.q_stride;
+  if (has_q) {
     if (APPEND) rows(q, r0, min(r1, a.H), a.q_weight, a.q_out + (size_t)tok * a.H * D, D);
     else rows(q, r0, min(r1, a.H), a.q_weight, a.q_out + ((size_t)b * a.H * a.T + t) * D, (size_t)a.T * D);
   }
   if (page < 0) return;
-  if (r1 > a.H && r0 < a.H + a.Hk) {
-    const uint16_t* k = a.k + tok * (size_t)a.k_stride;
-    const int n0 = max(0, r0 - a.H), n1 = min(a.Hk, r1 - a.H);
-    if (APPEND) rows(k, n0, n1, a.k_weight, a.k_out + ((size_t)page * a.Hk * 16 + slot) * D, 16 * D);
-    else rows(k, n0, n1, a.k_weight, a.k_out + ((size_t)b * a.Hk * a.T + t) * D, (size_t)a.T * D);
+  if (k0 < k1) {
+    if (has_q) load(x, k + (size_t)(k0 + sub) * D, sub < RPG ? k1 - k0 - sub : 0);
+    if (APPEND) rows(k, k0, k1, a.k_weight, a.k_out + ((size_t)page * a.Hk * 16 + slot) * D, 16 * D);
+    else rows(k, k0, k1, a.k_weight, a.k_out + ((size_t)b * a.Hk * a.T + t) * D, (size_t)a.T * D);
   }
   if (APPEND && r1 > a.H + a.Hk) {
     // values: 16 bytes a lane, L lanes a row
@@ -245,16 +265,16 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int chunks, uint32_t wa
   }
 }
 
-// Chunks per warp: one when there are few tokens (latency), up to a whole
-// token's when there are enough to fill the SMs several times over.
+// Rows per warp: one group side by side when there are few tokens (latency), up
+// to a whole token's when there are enough to fill the SMs several times over.
 template <int L>
 static cudaError_t launch_l(const NormRopeArgs& a, bool append, int num_sms, cudaStream_t stream) {
-  const int rpc = 32 / L * kUnroll;
-  const int rows = a.H + (append ? 2 : 1) * a.Hk, all = (rows + rpc - 1) / rpc;
+  constexpr int RPG = 32 / L;
+  const int rows = a.H + (append ? 2 : 1) * a.Hk, all = (rows + RPG - 1) / RPG;
   const long long tokens = (long long)a.B * a.T;
-  long long chunks = tokens * all / ((long long)num_sms * kWarpsPerSm);
-  chunks = chunks < 1 ? 1 : chunks > all ? all : chunks;
-  const long long per_token = (all + chunks - 1) / chunks;
+  long long groups = tokens * all / ((long long)num_sms * kWarpsPerSm);
+  groups = groups < 1 ? 1 : groups > all ? all : groups;
+  const long long per_token = (all + groups - 1) / groups;
   const long long blocks = (tokens * per_token + kWarps - 1) / kWarps;
   if (blocks * kWarps > 0xffffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
@@ -262,8 +282,8 @@ static cudaError_t launch_l(const NormRopeArgs& a, bool append, int num_sms, cud
                                         : (norm ? norm_rope_kernel<L, true, false, true> : norm_rope_kernel<L, true, false, false>))
                        : (a.interleaved ? (norm ? norm_rope_kernel<L, false, true, true> : norm_rope_kernel<L, false, true, false>)
                                         : (norm ? norm_rope_kernel<L, false, false, true> : norm_rope_kernel<L, false, false, false>));
-  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a, (int)chunks,
-                          (uint32_t)per_token);
+  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a,
+                          (int)groups * RPG, (uint32_t)per_token);
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, int num_sms, cudaStream_t stream) {
