@@ -355,6 +355,74 @@ def test_tree_attention_in_place_and_without_lse(lib):
     assert torch.equal(a, b)
 
 
+def test_tree_attention_with_an_empty_list(lib):
+    """k = 0 with a list is text alone, not every visual token."""
+    c = Cache(1, 2, 64, 200, seed=91)
+    q = synth.normal_bf16((1, 5, 4, 64), 5)
+    args = (0, [150], [30], [0], [5], None, 0.125)
+    out, lse, status = run_tree(c, q, np.zeros((1, 2, 0), np.int32), *args)
+    assert status == 0
+    assert_tree_close(out, lse, *oracle_tree(q, c, np.zeros((1, 2, 0), int), *args[1:]))
+
+
+def test_calls_share_a_workspace_with_the_decode_attention(lib):
+    """In one workspace, between tree attention and page calls, the decode
+    attention finds its counters as it left them."""
+    from visual_token_sparsity_gb300 import binding as sv
+    B, H, Hkv, d, T, n_vis, n_text = 3, 8, 8, 64, 30, 700, 40
+    c = Cache(B, Hkv, d, n_vis + n_text + T, seed=95)
+    layer, bt = c.layer(), c.bt.to(DEV)
+    seqs, after = sv.SeqBatch(bt, n_vis, n_text), sv.SeqBatch(bt, n_vis, n_text + T)
+    pool = sv.PagePool(torch.ones(c.blocks, dtype=torch.int32, device=DEV), i32([c.per] * B))
+    n = n_vis + n_text + T
+    ws = sv.workspace(max(sv.sv_tree_attn_workspace_bytes(B, T, H, Hkv, d, n),
+                          sv.sv_attn_workspace_bytes(B, H, Hkv, d, n),
+                          sv.sv_pages_workspace_bytes(B, c.per, c.blocks)))
+    q = synth.normal_bf16((B, T, H, d), 5).to(DEV)
+    q1 = q[:, -1].contiguous()
+    outs = []
+    for _ in range(3):
+        out, one = torch.empty_like(q), torch.empty_like(q1)
+        sv.sv_tree_attn(q, 0.125, layer, seqs, None, 0, None, out, None, ws)
+        sv.sv_pages_reserve(pool, [layer], seqs, T, ws)
+        sv.sv_sparse_decode_attn(q1, 0.125, layer, after, None, 0, one, None, ws)
+        outs.append((out, one))
+    assert sv.sv_read_device_status(ws) == 0
+    for out, one in outs:
+        assert torch.equal(out, outs[0][0]) and torch.equal(one, outs[0][1])
+        # the last drafted token of a chain attends to what the decode token does
+        assert (out[:, -1].float() - one.float()).abs().max() <= 0.02
+
+
+def test_binding_refuses_what_the_kernels_could_not_read(lib):
+    from visual_token_sparsity_gb300 import binding as sv
+    c = Cache(2, 2, 64, 60, seed=3)
+    layer, seqs = c.layer(), sv.SeqBatch(c.bt.to(DEV), 20, 10)
+    q = synth.normal_bf16((2, 4, 4, 64), 5).to(DEV)
+    out, ws = torch.empty_like(q), sv.workspace(sv.sv_tree_attn_workspace_bytes(2, 4, 4, 2, 64, 34))
+    good = dict(q=q, scale=0.1, layer=layer, seqs=seqs, vis_idx=None, k=0, tree_mask=None, out=out, lse=None, ws=ws)
+    sv.sv_tree_attn(**good)
+    for change in (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:1]), dict(out=out[:, :3]), dict(ws=ws.cpu()),
+                   dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(lse=out),
+                   dict(tree_mask=torch.zeros(2, 4, dtype=torch.int32, device=DEV)),
+                   dict(tree_mask=torch.zeros(2, 3, dtype=torch.int64, device=DEV)),
+                   dict(vis_idx=i32(np.zeros((2, 2, 5))), k=4), dict(n_new=i32([1, 2, 3]))):
+        with pytest.raises(ValueError):
+            sv.sv_tree_attn(**{**good, **change})
+    rot = sv.Rotation(None, None)
+    k = synth.normal_bf16((2, 4, 2, 64), 6).to(DEV)
+    with pytest.raises(ValueError, match="evenly"):
+        sv.sv_qk_norm_rope_append(q, k.transpose(0, 1).contiguous().transpose(0, 1), k, rot, layer, seqs, out, ws)
+    with pytest.raises(ValueError, match="tokens"):
+        cs = torch.zeros(9, 32, 2, device=DEV)
+        sv.sv_qk_norm_rope_append(q, k, k, sv.Rotation(cs, i32(np.zeros((2, 3)))), layer, seqs, out, ws)
+    with pytest.raises(sv.SvError, match="overflow"):
+        sv.sv_tree_attn(**{**good, "seqs": sv.SeqBatch(c.bt.to(DEV), 20, 41)})
+    with pytest.raises(sv.SvError) as e:
+        sv.sv_tree_attn(**{**good, "ws": ws[:128]})
+    assert e.value.status == 4
+
+
 def test_tree_attention_is_deterministic_on_streams_and_in_graphs(lib):
     """The same bits eager, on another stream, and captured; two graphs over
     one workspace replay in turn."""

@@ -167,6 +167,14 @@ def workspace(nbytes, device="cuda"):
     return torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
 
 
+def _one_device(*tensors):
+    """Index of the device that all these tensors are on (None: no tensor)."""
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(devs)}")
+    return devs.pop() if devs else None
+
+
 # ------------------------------------------------------------------ descriptors
 
 class KvLayer:
@@ -177,6 +185,7 @@ class KvLayer:
         self.k_pool, self.v_pool = k_pool, v_pool
         self.c = sv_kv_layer(_ptr(k_pool, torch.bfloat16, "k_pool"), _ptr(v_pool, torch.bfloat16, "v_pool"),
                              k_pool.shape[0], k_pool.shape[1], k_pool.shape[3])
+        self.device = _one_device(k_pool, v_pool)
 
 
 class SeqBatch:
@@ -199,6 +208,7 @@ class SeqBatch:
         self.c = sv_seq_batch(_ptr(block_table, torch.int32, "block_table"), B,
                               block_table.shape[1], int(n_vis), int(n_text), opt(n_vis_seq, "n_vis_seq"),
                               opt(n_text_seq, "n_text_seq"), opt(k_seq, "k_seq"))
+        self.device = _one_device(block_table, n_vis_seq, n_text_seq, k_seq)
 
     @property
     def n_vis(self):
@@ -246,6 +256,7 @@ class Rotation:
                              _ptr(pos if cos_sin is not None else None, torch.int32, "pos"), n_axes,
                              (ctypes.c_int32 * 3)(*sec), _ptr(q_weight, torch.bfloat16, "q_weight"),
                              _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps))
+        self.device = _one_device(cos_sin, pos if cos_sin is not None else None, q_weight, k_weight)
 
     def check(self, B, T, d):
         """The call's tokens and head dim are the descriptor's."""
@@ -265,37 +276,59 @@ class PagePool:
             raise ValueError("ref must be [num_blocks], n_pages [batch]")
         self.ref, self.n_pages = ref, n_pages
         self.c = sv_page_pool(_ptr(ref, torch.int32, "ref"), _ptr(n_pages, torch.int32, "n_pages"), ref.shape[0])
+        self.device = _one_device(ref, n_pages)
 
 
-def _rows(t, dtype, name):
-    """Pointer and token stride of a [B][T][heads][d] tensor whose tokens lie
-    evenly apart (a slice of a fused projection, for instance)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    B, T, h, d = t.shape
-    sb, st, sh, sd = t.stride()
-    ptr = ctypes.c_void_p(t.data_ptr())
-    if t.numel() == 0:
-        return ptr, h * d
-    stride = st if T > 1 else sb if B > 1 else h * d
-    if (sd != 1 and d > 1) or (sh != d and h > 1) or (B > 1 and T > 1 and sb != T * st):
-        raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, strides {t.stride()}")
-    return ptr, stride
+class _Call:
+    """Pointers of one call's tensors, checked: on the current device (the
+    launch goes there), of the given type and shape, contiguous.  These calls
+    are made many times per decoded token, so the checks are lean."""
 
+    def __init__(self, ws, stream, *descriptors):
+        self.dev = dev = torch._C._cuda_getDevice()
+        for d in descriptors:
+            if d.device not in (dev, None):
+                raise ValueError(f"descriptor on cuda:{d.device}, current device is cuda:{dev}")
+        if ws.dtype != torch.uint8:
+            raise ValueError(f"ws must be {torch.uint8}, got {ws.dtype}")
+        self.ws = self.device_ptr(ws, "ws"), ws.numel()
+        if stream is None:
+            self.stream = torch._C._cuda_getCurrentRawStream(dev)
+        else:
+            self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-def _here(*tensors):
-    """The launch goes to the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
+    def device_ptr(self, t, name):
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{self.dev}, is on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
 
+    def ptr(self, t, dtype, shape, name):
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        return self.device_ptr(t, name)
 
-def _want(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    def rows(self, t, shape, name):
+        """Pointer and token stride of a bf16 [B][T][heads][d] tensor whose
+        tokens lie evenly apart (a slice of a fused projection, for instance)."""
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{self.dev}, is on {t.device}")
+        B, T, h, d = shape
+        if B * T * h * d == 0:
+            return t.data_ptr(), h * d
+        sb, st, sh, sd = t.stride()
+        if (sd != 1 and d > 1) or (sh != d and h > 1) or (B > 1 and T > 1 and sb != T * st):
+            raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, strides {t.stride()}")
+        return t.data_ptr(), st if T > 1 else sb if B > 1 else h * d
 
 
 # ------------------------------------------------------------------ sizes
@@ -483,14 +516,11 @@ def sv_qk_norm_rope(q, k, rot, q_out, k_out, ws, stream=None):
     lib = load()
     B, N, H, d = q.shape
     Hk = k.shape[2]
-    _want(k, (B, N, Hk, d), "k")
-    _want(q_out, (B, H, N, d), "q_out")
-    _want(k_out, (B, Hk, N, d), "k_out")
+    c = _Call(ws, stream, rot)
     rot.check(B, N, d)
-    _here(q, k, q_out, k_out, ws, rot.cos_sin, rot.pos, rot.q_weight, rot.k_weight)
-    _check(lib.sv_qk_norm_rope(*_rows(q, torch.bfloat16, "q"), *_rows(k, torch.bfloat16, "k"), B, N, H, Hk, d,
-                               ctypes.byref(rot.c), _ptr(q_out, torch.bfloat16, "q_out"),
-                               _ptr(k_out, torch.bfloat16, "k_out"), *_ws(ws), _stream(stream)))
+    _check(lib.sv_qk_norm_rope(*c.rows(q, (B, N, H, d), "q"), *c.rows(k, (B, N, Hk, d), "k"), B, N, H, Hk, d,
+                               ctypes.byref(rot.c), c.ptr(q_out, torch.bfloat16, (B, H, N, d), "q_out"),
+                               c.ptr(k_out, torch.bfloat16, (B, Hk, N, d), "k_out"), *c.ws, c.stream))
 
 
 def sv_qk_norm_rope_append(q, k, v, rot, layer, seqs, q_out, ws, n_new=None, stream=None):
@@ -499,19 +529,13 @@ def sv_qk_norm_rope_append(q, k, v, rot, layer, seqs, q_out, ws, n_new=None, str
     n_text unchanged (the caller adds T or n_new).  n_new int32 [B]: new tokens of each sequence, or None."""
     lib = load()
     B, T, H, d = q.shape
-    Hkv = layer.c.n_kv_heads
-    _want(q, (seqs.c.batch, T, H, layer.c.head_dim), "q")
-    _want(k, (B, T, Hkv, d), "k")
-    _want(v, (B, T, Hkv, d), "v")
-    _want(q_out, (B, T, H, d), "q_out")
-    _want(n_new, (B,), "n_new")
+    kv = (B, T, layer.c.n_kv_heads, d)
+    c = _Call(ws, stream, rot, layer, seqs)
     rot.check(B, T, d)
-    _here(q, k, v, q_out, ws, n_new, layer.k_pool, layer.v_pool, seqs.block_table, rot.cos_sin, rot.pos, rot.q_weight,
-          rot.k_weight)
-    _check(lib.sv_qk_norm_rope_append(*_rows(q, torch.bfloat16, "q"), *_rows(k, torch.bfloat16, "k"),
-                                      *_rows(v, torch.bfloat16, "v"), T, H, ctypes.byref(rot.c),
-                                      ctypes.byref(layer.c), ctypes.byref(seqs.c), _ptr(n_new, torch.int32, "n_new"),
-                                      _ptr(q_out, torch.bfloat16, "q_out"), *_ws(ws), _stream(stream)))
+    _check(lib.sv_qk_norm_rope_append(*c.rows(q, (seqs.c.batch, T, H, layer.c.head_dim), "q"), *c.rows(k, kv, "k"),
+                                      *c.rows(v, kv, "v"), T, H, ctypes.byref(rot.c), ctypes.byref(layer.c),
+                                      ctypes.byref(seqs.c), c.ptr(n_new, torch.int32, (B,), "n_new"),
+                                      c.ptr(q_out, torch.bfloat16, q.shape, "q_out"), *c.ws, c.stream))
 
 
 def sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens):
@@ -524,22 +548,19 @@ def sv_tree_attn(q, scale, layer, seqs, vis_idx, k, tree_mask, out, lse, ws, n_n
     s, or None: causal; lse fp32 [B][T][H] or None; n_new int32 [B]: drafted tokens of each sequence, or None."""
     lib = load()
     B, T, H, d = q.shape
-    _want(q, (seqs.c.batch, T, H, layer.c.head_dim), "q")
-    if vis_idx is not None:
-        _want(vis_idx, (B, layer.c.n_kv_heads, k), "vis_idx")
+    c = _Call(ws, stream, layer, seqs)
+    vis = c.ptr(vis_idx, torch.int32, (B, layer.c.n_kv_heads, k), "vis_idx")
+    if vis_idx is not None and k == 0:
+        vis = c.ws[0]            # an empty list, not "all visual tokens": any address, nothing is read
+    mask = None
     if tree_mask is not None:
-        _want(tree_mask, (B, T), "tree_mask")
         if tree_mask.dtype not in (torch.int64, torch.uint64):
             raise ValueError(f"tree_mask must be 64-bit integers, got {tree_mask.dtype}")
-    _want(out, (B, T, H, d), "out")
-    _want(lse, (B, T, H), "lse")
-    _want(n_new, (B,), "n_new")
-    _here(q, out, lse, ws, n_new, vis_idx, tree_mask, layer.k_pool, layer.v_pool, seqs.block_table)
-    _check(lib.sv_tree_attn(_ptr(q, torch.bfloat16, "q"), T, H, float(scale), ctypes.byref(layer.c),
-                            ctypes.byref(seqs.c), _ptr(vis_idx, torch.int32, "vis_idx"), int(k),
-                            _ptr(tree_mask, None, "tree_mask"), _ptr(n_new, torch.int32, "n_new"),
-                            _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"), *_ws(ws),
-                            _stream(stream)))
+        mask = c.ptr(tree_mask, tree_mask.dtype, (B, T), "tree_mask")
+    _check(lib.sv_tree_attn(c.ptr(q, torch.bfloat16, (seqs.c.batch, T, H, layer.c.head_dim), "q"), T, H, scale,
+                            ctypes.byref(layer.c), ctypes.byref(seqs.c), vis, k, mask,
+                            c.ptr(n_new, torch.int32, (B,), "n_new"), c.ptr(out, torch.bfloat16, q.shape, "out"),
+                            c.ptr(lse, torch.float32, (B, T, H), "lse"), *c.ws, c.stream))
 
 
 def _layer_array(layers):
@@ -551,26 +572,28 @@ def sv_kv_accept(layers, seqs, T, path, ws, n_path=None, stream=None):
     indices (the first n_path[b] of a row, or all); n_text unchanged (the caller adds the accepted count)."""
     lib = load()
     B, P = path.shape
-    _want(path, (seqs.c.batch, P), "path")
-    _want(n_path, (B,), "n_path")
-    _here(path, n_path, ws, seqs.block_table, *(x for l in layers for x in (l.k_pool, l.v_pool)))
-    _check(lib.sv_kv_accept(_layer_array(layers), len(layers), ctypes.byref(seqs.c), int(T),
-                            _ptr(path, torch.int32, "path"), P, _ptr(n_path, torch.int32, "n_path"), *_ws(ws),
-                            _stream(stream)))
+    c = _Call(ws, stream, seqs, *layers)
+    _check(lib.sv_kv_accept(_layer_array(layers), len(layers), ctypes.byref(seqs.c), T,
+                            c.ptr(path, torch.int32, (seqs.c.batch, P), "path"), P,
+                            c.ptr(n_path, torch.int32, (B,), "n_path"), *c.ws, c.stream))
 
 
 def sv_pages_workspace_bytes(batch, max_blocks, num_blocks):
     return load().sv_pages_workspace_bytes(batch, max_blocks, num_blocks)
 
 
+def _pages(pool, seqs, ws, stream, *layers):
+    if pool.n_pages.shape != (seqs.c.batch,):
+        raise ValueError(f"n_pages must have shape ({seqs.c.batch},), got {tuple(pool.n_pages.shape)}")
+    return _Call(ws, stream, pool, seqs, *layers)
+
+
 def sv_pages_release(pool, seqs, keep, ws, stream=None):
     """Drops every sequence's pages behind its first keep[b] tokens (int32 [B]; -1: leave it; None: drop all)."""
     lib = load()
-    _want(pool.n_pages, (seqs.c.batch,), "n_pages")
-    _want(keep, (seqs.c.batch,), "keep")
-    _here(pool.ref, pool.n_pages, seqs.block_table, keep, ws)
-    _check(lib.sv_pages_release(ctypes.byref(pool.c), ctypes.byref(seqs.c), _ptr(keep, torch.int32, "keep"),
-                                *_ws(ws), _stream(stream)))
+    c = _pages(pool, seqs, ws, stream)
+    _check(lib.sv_pages_release(ctypes.byref(pool.c), ctypes.byref(seqs.c),
+                                c.ptr(keep, torch.int32, (seqs.c.batch,), "keep"), *c.ws, c.stream))
 
 
 def sv_pages_fork(pool, seqs, parent, child, ws, n_tok=None, stream=None):
@@ -578,24 +601,19 @@ def sv_pages_fork(pool, seqs, parent, child, ws, n_tok=None, stream=None):
     n_tok[i] tokens."""
     lib = load()
     n, = parent.shape
-    _want(pool.n_pages, (seqs.c.batch,), "n_pages")
-    _want(child, (n,), "child")
-    _want(n_tok, (n,), "n_tok")
-    _here(pool.ref, pool.n_pages, seqs.block_table, parent, child, n_tok, ws)
-    _check(lib.sv_pages_fork(ctypes.byref(pool.c), ctypes.byref(seqs.c), _ptr(parent, torch.int32, "parent"),
-                             _ptr(child, torch.int32, "child"), n, _ptr(n_tok, torch.int32, "n_tok"), *_ws(ws),
-                             _stream(stream)))
+    c = _pages(pool, seqs, ws, stream)
+    _check(lib.sv_pages_fork(ctypes.byref(pool.c), ctypes.byref(seqs.c),
+                             c.ptr(parent, torch.int32, (n,), "parent"), c.ptr(child, torch.int32, (n,), "child"), n,
+                             c.ptr(n_tok, torch.int32, (n,), "n_tok"), *c.ws, c.stream))
 
 
 def sv_pages_reserve(pool, layers, seqs, T, ws, n_new=None, stream=None):
     """Makes the T (or n_new[b], int32 [B]) positions behind each sequence's tokens writable: fresh pages, and
     private copies, in every layer, of the shared pages among them."""
     lib = load()
-    _want(pool.n_pages, (seqs.c.batch,), "n_pages")
-    _want(n_new, (seqs.c.batch,), "n_new")
-    _here(pool.ref, pool.n_pages, seqs.block_table, n_new, ws, *(x for l in layers for x in (l.k_pool, l.v_pool)))
-    _check(lib.sv_pages_reserve(ctypes.byref(pool.c), _layer_array(layers), len(layers), ctypes.byref(seqs.c),
-                                int(T), _ptr(n_new, torch.int32, "n_new"), *_ws(ws), _stream(stream)))
+    c = _pages(pool, seqs, ws, stream, *layers)
+    _check(lib.sv_pages_reserve(ctypes.byref(pool.c), _layer_array(layers), len(layers), ctypes.byref(seqs.c), T,
+                                c.ptr(n_new, torch.int32, (seqs.c.batch,), "n_new"), *c.ws, c.stream))
 
 
 def sv_read_device_status(ws, clear=False, stream=None):
