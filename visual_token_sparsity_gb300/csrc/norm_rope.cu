@@ -225,11 +225,15 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
             if (j + o < L) s += z;
           }
           s = __shfl_sync(0xffffffffu, s, sub < RPG ? sub * L : lane);
-          const uint64_t inv = fm::splat2(rsqrtf(s * (1.f / D) + a.eps));
+          // x * w is exact (8 bits times 8), so x' carries the error of the
+          // root, which one step of Newton's method makes small, and one rounding
+          const float mean = s * (1.f / D) + a.eps, r0 = rsqrtf(mean);
+          const float step = fmaf(-mean * r0, r0, 1.f);
+          const uint64_t inv = fm::splat2(isfinite(step) ? fmaf(0.5f * r0, step, r0) : r0);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            p[e] = fm::mul2(fm::mul2(p[e], inv), gp[e]);
-            y[e] = fm::mul2(fm::mul2(y[e], inv), gy[e]);
+            p[e] = fm::mul2(fm::mul2(p[e], gp[e]), inv);
+            y[e] = fm::mul2(fm::mul2(y[e], gy[e]), inv);
           }
         }
 #pragma unroll
