@@ -488,8 +488,8 @@ sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_
  *           (n_vis_seq[b] + n_text_seq[b] + t), as by sv_kv_append; the caller
  *           then adds T (or n_new[b]) to n_text.
  * n_new   : optional DEVICE int32 [B]: only the first n_new[b] tokens of
- *           sequence b are there; the rows behind them are neither read nor
- *           written.  A count outside [0, T] sets SV_DEV_BAD_LENGTH and the
+ *           sequence b are there; the rows behind them are not used, and
+ *           q_out and the cache stay as they were.  A count outside [0, T] sets SV_DEV_BAD_LENGTH and the
  *           sequence is skipped.
  * q_out   : out bf16 [B][T][H][d]; q itself (with q_stride == H * d) or apart
  *           from q, k and v.
