@@ -279,7 +279,7 @@ kv_accept_kernel(const __grid_constant__ LayerPools pools, int num_blocks, int H
                  const int32_t* __restrict__ block_table, int max_blocks, SeqLens lens, int n_vis, int n_text, int T,
                  const int32_t* __restrict__ path, int P, const int32_t* __restrict__ n_path, int* status) {
   grid_dep_sync();
-  const int g = blockIdx.x, b = blockIdx.y, layer = blockIdx.z;
+  const int b = blockIdx.x, g = blockIdx.y, layer = blockIdx.z;
   const bool report = threadIdx.x == 0 && g == 0 && layer == 0;
   SeqLens l = lens;
   l.k = nullptr;
@@ -380,7 +380,7 @@ cudaError_t launch_kv_accept(const LayerPools& pools, int layers, int num_blocks
                              int n_text, int T, const int32_t* path, int P, const int32_t* n_path, int* status,
                              cudaStream_t stream) {
   if (batch == 0 || layers == 0 || P == 0) return cudaSuccess;
-  return launch_dependent(kv_accept_kernel, dim3(Hkv, batch, layers), dim3(256), 0, stream, pools, num_blocks, Hkv,
+  return launch_dependent(kv_accept_kernel, dim3(batch, Hkv, layers), dim3(256), 0, stream, pools, num_blocks, Hkv,
                           D / 8, block_table, max_blocks, lens, n_vis, n_text, T, path, P, n_path, status);
 }
 

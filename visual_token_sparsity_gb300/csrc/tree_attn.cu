@@ -27,11 +27,11 @@
 // that a second kernel joins in a fixed order.  CTAs of one piece and
 // different row tiles are neighbours, so they meet in L2.
 //
-// Warps: 0-7 softmax and epilogue (one row per thread), 8 MMA issue, 9 query
-// rows, 10-13 cache rows: cp.async gathers of 16 bytes into a ring of 128-row
-// K and V tiles in the 128-byte-swizzled layout the MMA reads, page-table and
-// index loads running two tiles ahead.  Rows that are not there (behind the
-// end, a bad page) are zero-filled and masked.
+// Warps: 0-7 softmax and epilogue (one row per thread), 8-9 MMA issue (one per
+// stream), 10-13 cache rows: cp.async gathers of 16 bytes into a ring of
+// 128-row K and V tiles in the 128-byte-swizzled layout the MMA reads,
+// page-table and index loads running two tiles ahead, 14-15 query rows.  Rows
+// that are not there (behind the end, a bad page) are zero-filled and masked.
 #include "common.cuh"
 #include "fastmath.cuh"
 #include "kernels.h"
@@ -91,10 +91,12 @@ struct Shared {
   alignas(16) uint32_t valid[kValidRing][4];  // tokens of a tile that are there
   float ml[2][kTile][2];          // the streams' maxima and sums
 };
-// 1 KB of alignment before the ring covers the static part
-static_assert(sizeof(Shared) <= 3072 && Smem<128, 128>::kBytes + 3072 <= kMaxSmem &&
-                  Smem<128, 256>::kBytes + 3072 <= kMaxSmem && Smem<64, 128>::kBytes + 3072 <= kMaxSmem &&
-                  Smem<64, 256>::kBytes + 3072 <= kMaxSmem,
+// the static part lies before the ring, which begins at a multiple of 1 KB
+constexpr int kStaticSmem = 3 * 1024;
+static_assert(sizeof(Shared) <= kStaticSmem && Smem<128, 128>::kBytes + kStaticSmem <= kMaxSmem &&
+                  Smem<128, 256>::kBytes + kStaticSmem <= kMaxSmem &&
+                  Smem<64, 128>::kBytes + kStaticSmem <= kMaxSmem &&
+                  Smem<64, 256>::kBytes + kStaticSmem <= kMaxSmem,
               "shared memory");
 
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Shared& sh) {
