@@ -250,6 +250,14 @@ def test_tree_attention_of_many_short_sequences(lib):
     check_tree(2, 1, 64, 75, 4, 40, 10, 9, "tree", seed=8, ragged=True)
 
 
+@pytest.mark.parametrize("H,Hkv,d,B,T,n_text", [(14, 2, 128, 80, 18, 108), (28, 4, 128, 40, 9, 50), (32, 32, 64, 12, 20, 90)])
+def test_tree_attention_of_units_of_one_tile(lib, H, Hkv, d, B, T, n_text):
+    """Several (sequence, KV head) units per CTA, each with a tile for one of
+    its two streams only."""
+    for seed in range(3):
+        check_tree(H, Hkv, d, B, T, 0, None, n_text, "tree", seed=seed)
+
+
 @pytest.mark.parametrize("std,scale", [(4.0, 0.5), (16.0, 0.7), (1.0, 0.0)])
 def test_tree_attention_with_peaked_and_flat_weights(lib, std, scale):
     check_tree(8, 2, 128, 1, 20, 500, 250, 30, "tree", seed=5, std=std, scale=scale)

@@ -586,9 +586,16 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
           __syncwarp();
           if (!split) pass_turn();
         }
-      } else if (ptx::elect_one()) {              // a stream without a tile
-        ptx::mma_commit(&sh.q_empty[qb]);
-        ptx::mma_commit(&sh.o_full);
+      } else {
+        // A stream without a tile has nothing that holds it back: it must not
+        // count for this unit's O while the last unit's still misses the
+        // other stream's count.
+        if (seg > 0) wait_bar(&sh.o_full, (seg - 1) & 1, sh);
+        __syncwarp();
+        if (ptx::elect_one()) {
+          ptx::mma_commit(&sh.q_empty[qb]);
+          ptx::mma_commit(&sh.o_full);
+        }
       }
       __syncwarp();
       tile0 += nt;
