@@ -938,7 +938,12 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a) {
 
 namespace {
 
-// Row tiles of 128 rows, or of 256 when there are more rows than that; as
+// Row tiles of 128 rows, or of 256 when there are more rows than that and at
+// least eight tiles of 256 rows x 128 tokens for each CTA: the paired streams
+// read the cache half as often, but a piece of theirs starts and ends with
+// twice the rows.  128 against 256, 8 sequences of 4 KV heads, d 128: 224 rows
+// 23.2 / 26.3 us at 2 such tiles a CTA, 28.3 / 30.5 at 4, 37.7 / 38.2 at 8, 72.3 /
+// 67.7 at 24; 448 rows 32.5 / 35.1 at 4, 41.7 / 42.6 at 8, 59.8 / 57.1 at 16.  As
 // many pieces as leave every SM one CTA, of two token tiles at least (one for
 // each stream; pieces of one measured 2 % faster to 9 % slower).
 struct Plan {
@@ -950,9 +955,10 @@ struct Plan {
 Plan plan_of(int B, int T, int G, int Hkv, int n_tokens) {
   Plan p;
   const long long rows = (long long)T * G;
-  p.QT = rows <= kTile ? kTile : 2 * kTile;
-  p.row_tiles = (int)((rows + p.QT - 1) / p.QT);
   const long long tiles = (long long)B * Hkv * (((long long)n_tokens + kTile - 1) / kTile);
+  const long long pairs = (rows + 2 * kTile - 1) / (2 * kTile);
+  p.QT = rows <= kTile || tiles < (8 * kCtas + pairs - 1) / (pairs > 0 ? pairs : 1) ? kTile : 2 * kTile;
+  p.row_tiles = (int)((rows + p.QT - 1) / p.QT);
   long long c = p.row_tiles > 0 ? kCtas / p.row_tiles : 1;
   if (c > tiles / 2) c = tiles / 2;
   p.columns = (int)(c < 1 ? 1 : c);
