@@ -93,6 +93,36 @@ struct Lane8 {
   }
 };
 
+// The sum over a row's L lanes, in each of them: 8 and 16 by halves, 9 and 10
+// around the row's circle by lanes 1, 2 and 4 further on, and the one or two
+// that are left.  (Every lane takes part; those beside the rows add up to
+// nothing that is used.)
+template <int L>
+struct RowLanes {
+  static constexpr bool kCircle = (L & (L - 1)) != 0;
+  uint32_t to = 0;     // the four lanes, a byte each (a shuffle uses five bits)
+  __device__ __forceinline__ void set(int sub, int j, int lane) {
+#pragma unroll
+    for (int i = 0; i < (kCircle ? 4 : 0); ++i) {
+      const int n = j + (1 << i);
+      to |= (uint32_t)(sub < 32 / L ? sub * L + (n < L ? n : n - L) : lane) << (8 * i);
+    }
+  }
+};
+template <int L>
+__device__ __forceinline__ float row_sum(float s, const RowLanes<L>& next) {
+  if constexpr (RowLanes<L>::kCircle) {
+    const float two = s + __shfl_sync(0xffffffffu, s, next.to);
+    const float four = two + __shfl_sync(0xffffffffu, two, next.to >> 8);
+    const float eight = four + __shfl_sync(0xffffffffu, four, next.to >> 16);
+    return eight + __shfl_sync(0xffffffffu, L == 9 ? s : two, next.to >> 24);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+}
+
 }  // namespace
 
 // A warp takes `per_warp` consecutive rows of one token, where a token's rows
@@ -112,6 +142,8 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
   const int b = (int)(tok / (uint32_t)a.T), t = (int)(tok - (uint32_t)b * a.T);
   const int r0 = (int)(w - tok * warps_per_token) * per_warp, r1 = r0 + per_warp;
   const bool first = r0 == 0 && lane == 0;    // reports for the token
+  RowLanes<L> next_lane;
+  if (NORM) next_lane.set(sub, j, lane);
 
   // this lane's elements: off0.. and off1..
   const int half = a.rot >> 1;
@@ -217,14 +249,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
           float s, s_hi;
           fm::unpack2(s2, s, s_hi);
           s += s_hi;
-          // the reduction is warp-wide: every lane takes part
-#pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) {
-            if (o >= L) continue;
-            const float z = __shfl_down_sync(0xffffffffu, s, o);
-            if (j + o < L) s += z;
-          }
-          s = __shfl_sync(0xffffffffu, s, sub < RPG ? sub * L : lane);
+          s = row_sum<L>(s, next_lane);
           // x * w is exact (8 bits times 8), so x' carries the error of the
           // root, which one step of Newton's method makes small, and one rounding
           const float mean = s * (1.f / D) + a.eps, r0 = rsqrtf(mean);
