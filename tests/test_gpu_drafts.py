@@ -46,6 +46,43 @@ def weights(d, seed):
     return tuple((1 + 0.2 * synth.normal_bf16((d,), seed + i).float()).to(torch.bfloat16).to(DEV) for i in range(2))
 
 
+@pytest.mark.parametrize("d,rot_dim", [(128, 64), (80, 40), (72, 0)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_elements_behind_the_rotation_stay(lib, d, rot_dim, inter):
+    """Infinities and NaN behind rot_dim are passed on, each to its own place only."""
+    from visual_token_sparsity_gb300 import binding as sv
+    rot, ref = rotation(rot_dim, 1, 1, 9, 50, 4, None, inter)
+    x = synth.normal_bf16((1, 9, 3, d), 5)
+    x[0, :, :, rot_dim + 1::5] = float("inf")
+    x[0, ::2, :, rot_dim + 3::7] = float("nan")
+    x = x.to(DEV)
+    qo, ko = (torch.empty(1, h, 9, d, dtype=torch.bfloat16, device=DEV) for h in (2, 1))
+    sv.sv_qk_norm_rope(x[:, :, :2], x[:, :, 2:], rot, qo, ko, sv.workspace(256))
+    torch.cuda.synchronize()
+    got = torch.cat([qo, ko], 1).transpose(1, 2)
+    assert torch.equal(got[..., rot_dim:].view(torch.int16), x[..., rot_dim:].view(torch.int16))
+    clean = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    assert_rows_close(got[..., :rot_dim], ref(clean, None)[..., :rot_dim], "turned part")
+
+
+@pytest.mark.parametrize("d,rot_dim,inter", [(128, 64, False), (72, 32, True), (80, 0, False)])
+def test_an_infinity_behind_the_rotation_of_normed_rows(lib, d, rot_dim, inter):
+    """It becomes NaN and the rest of its row 0, as in the formula."""
+    from visual_token_sparsity_gb300 import binding as sv
+    rot, ref = rotation(rot_dim, 1, 1, 6, 50, 4, weights(d, 2), inter)
+    x = synth.normal_bf16((1, 6, 2, d), 8)
+    x[0, :3, :, rot_dim + 6] = float("-inf")
+    x = x.to(DEV)
+    qo, ko = (torch.empty(1, 1, 6, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    sv.sv_qk_norm_rope(x[:, :, :1], x[:, :, 1:], rot, qo, ko, sv.workspace(256))
+    torch.cuda.synchronize()
+    for got in (qo[0, 0], ko[0, 0]):
+        assert got[:3, rot_dim + 6].isnan().all()
+        rest = torch.cat([got[:3, :rot_dim + 6], got[:3, rot_dim + 7:]], 1)
+        assert (rest == 0).all()
+        assert got[3:].isfinite().all()
+
+
 @pytest.mark.parametrize("d,H,Hk,B,N,axes,sections,inter,norm", [
     (80, 16, 16, 1, 37, 2, [20, 20], False, False),
     (72, 5, 5, 2, 19, 1, None, True, True),

@@ -126,8 +126,11 @@ __device__ __forceinline__ float row_sum(float s, const RowLanes<L>& next) {
 }  // namespace
 
 // A warp takes `per_warp` consecutive rows of one token, where a token's rows
-// are its H queries, Hk keys and (append) Hk values.
-template <int L, bool APPEND, bool INTER, bool NORM>
+// are its H queries, Hk keys and (append) Hk values.  PARTLY: rot_dim
+// ends inside the row, and the elements behind it are not turned (by a sine of
+// 0 an infinity would reach its partner; told apart in the one kernel, the
+// encoder's 16384 tokens took 29 us, not 28).
+template <int L, bool APPEND, bool INTER, bool NORM, bool PARTLY>
 __global__ void __launch_bounds__(kWarps * 32, Shape<APPEND>::kCtas)
 norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t warps_per_token) {
   constexpr int D = 8 * L;
@@ -263,11 +266,12 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          if (PARTLY && !turned) break;
           const uint64_t re = fm::fma2(p[e], cs[e], fm::mul2(y[e], ns[e]));
           y[e] = fm::fma2(p[e], sn[e], fm::mul2(y[e], cs[e]));
           p[e] = re;
         }
-        x[i].pack(p, y);
+        if (!PARTLY || turned || (NORM && weight != nullptr)) x[i].pack(p, y);
         if (done + i * RPG < left) x[i].store(to + (size_t)(i * RPG) * stride, off0, off1);
         x[i] = next[i];
       }
@@ -294,6 +298,13 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
   }
 }
 
+template <int L, bool APPEND, bool INTER>
+static auto pick(bool norm, int rot) {
+  if (rot < 8 * L)
+    return norm ? norm_rope_kernel<L, APPEND, INTER, true, true> : norm_rope_kernel<L, APPEND, INTER, false, true>;
+  return norm ? norm_rope_kernel<L, APPEND, INTER, true, false> : norm_rope_kernel<L, APPEND, INTER, false, false>;
+}
+
 // Rows per warp: one group side by side when there are few tokens (latency), up
 // to a whole token's when there are enough to fill the SMs several times over.
 template <int L>
@@ -307,10 +318,8 @@ static cudaError_t launch_l(const NormRopeArgs& a, bool append, int num_sms, cud
   const long long blocks = (tokens * per_token + kWarps - 1) / kWarps;
   if (blocks * kWarps > 0xffffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
-  auto kernel = append ? (a.interleaved ? (norm ? norm_rope_kernel<L, true, true, true> : norm_rope_kernel<L, true, true, false>)
-                                        : (norm ? norm_rope_kernel<L, true, false, true> : norm_rope_kernel<L, true, false, false>))
-                       : (a.interleaved ? (norm ? norm_rope_kernel<L, false, true, true> : norm_rope_kernel<L, false, true, false>)
-                                        : (norm ? norm_rope_kernel<L, false, false, true> : norm_rope_kernel<L, false, false, false>));
+  auto kernel = append ? (a.interleaved ? pick<L, true, true>(norm, a.rot) : pick<L, true, false>(norm, a.rot))
+                       : (a.interleaved ? pick<L, false, true>(norm, a.rot) : pick<L, false, false>(norm, a.rot));
   return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a,
                           (int)groups * RPG, (uint32_t)per_token);
 }
