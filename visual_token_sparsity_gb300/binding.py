@@ -56,6 +56,9 @@ class sv_page_pool(ctypes.Structure):
     _fields_ = [("ref", ctypes.c_void_p), ("n_pages", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
 
 
+# (module constants and fields of their own: the calls of a decode step look them
+# up a dozen times each)
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _VP, _SZ, _I, _F, _I64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float, ctypes.c_int64
 _SIGS = {
     "sv_status_string": (ctypes.c_char_p, [_I]),
@@ -185,6 +188,7 @@ class KvLayer:
         self.k_pool, self.v_pool = k_pool, v_pool
         self.c = sv_kv_layer(_ptr(k_pool, torch.bfloat16, "k_pool"), _ptr(v_pool, torch.bfloat16, "v_pool"),
                              k_pool.shape[0], k_pool.shape[1], k_pool.shape[3])
+        self.by_ref, self.n_kv_heads, self.head_dim = ctypes.byref(self.c), k_pool.shape[1], k_pool.shape[3]
         self.device = _one_device(k_pool, v_pool)
 
 
@@ -208,6 +212,7 @@ class SeqBatch:
         self.c = sv_seq_batch(_ptr(block_table, torch.int32, "block_table"), B,
                               block_table.shape[1], int(n_vis), int(n_text), opt(n_vis_seq, "n_vis_seq"),
                               opt(n_text_seq, "n_text_seq"), opt(k_seq, "k_seq"))
+        self.by_ref, self.batch = ctypes.byref(self.c), B
         self.device = _one_device(block_table, n_vis_seq, n_text_seq, k_seq)
 
     @property
@@ -256,6 +261,7 @@ class Rotation:
                              _ptr(pos if cos_sin is not None else None, torch.int32, "pos"), n_axes,
                              (ctypes.c_int32 * 3)(*sec), _ptr(q_weight, torch.bfloat16, "q_weight"),
                              _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps))
+        self.by_ref = ctypes.byref(self.c)
         self.device = _one_device(cos_sin, pos if cos_sin is not None else None, q_weight, k_weight)
 
     def check(self, B, T, d):
@@ -276,6 +282,7 @@ class PagePool:
             raise ValueError("ref must be [num_blocks], n_pages [batch]")
         self.ref, self.n_pages = ref, n_pages
         self.c = sv_page_pool(_ptr(ref, torch.int32, "ref"), _ptr(n_pages, torch.int32, "n_pages"), ref.shape[0])
+        self.by_ref = ctypes.byref(self.c)
         self.device = _one_device(ref, n_pages)
 
 
@@ -289,8 +296,8 @@ class _Call:
         for d in descriptors:
             if d.device not in (dev, None):
                 raise ValueError(f"descriptor on cuda:{d.device}, current device is cuda:{dev}")
-        if ws.dtype != torch.uint8:
-            raise ValueError(f"ws must be {torch.uint8}, got {ws.dtype}")
+        if ws.dtype != _U8:
+            raise ValueError(f"ws must be {_U8}, got {ws.dtype}")
         self.ws = self.device_ptr(ws, "ws"), ws.numel()
         if stream is None:
             self.stream = torch._C._cuda_getCurrentRawStream(dev)
@@ -316,8 +323,8 @@ class _Call:
     def rows(self, t, shape, name):
         """Pointer and token stride of a bf16 [B][T][heads][d] tensor whose
         tokens lie evenly apart (a slice of a fused projection, for instance)."""
-        if t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.dtype != _BF16:
+            raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.get_device() != self.dev:
@@ -519,8 +526,8 @@ def sv_qk_norm_rope(q, k, rot, q_out, k_out, ws, stream=None):
     c = _Call(ws, stream, rot)
     rot.check(B, N, d)
     _check(lib.sv_qk_norm_rope(*c.rows(q, (B, N, H, d), "q"), *c.rows(k, (B, N, Hk, d), "k"), B, N, H, Hk, d,
-                               ctypes.byref(rot.c), c.ptr(q_out, torch.bfloat16, (B, H, N, d), "q_out"),
-                               c.ptr(k_out, torch.bfloat16, (B, Hk, N, d), "k_out"), *c.ws, c.stream))
+                               rot.by_ref, c.ptr(q_out, _BF16, (B, H, N, d), "q_out"),
+                               c.ptr(k_out, _BF16, (B, Hk, N, d), "k_out"), *c.ws, c.stream))
 
 
 def sv_qk_norm_rope_append(q, k, v, rot, layer, seqs, q_out, ws, n_new=None, stream=None):
@@ -529,13 +536,13 @@ def sv_qk_norm_rope_append(q, k, v, rot, layer, seqs, q_out, ws, n_new=None, str
     n_text unchanged (the caller adds T or n_new).  n_new int32 [B]: new tokens of each sequence, or None."""
     lib = load()
     B, T, H, d = q.shape
-    kv = (B, T, layer.c.n_kv_heads, d)
+    kv = (B, T, layer.n_kv_heads, d)
     c = _Call(ws, stream, rot, layer, seqs)
     rot.check(B, T, d)
-    _check(lib.sv_qk_norm_rope_append(*c.rows(q, (seqs.c.batch, T, H, layer.c.head_dim), "q"), *c.rows(k, kv, "k"),
-                                      *c.rows(v, kv, "v"), T, H, ctypes.byref(rot.c), ctypes.byref(layer.c),
-                                      ctypes.byref(seqs.c), c.ptr(n_new, torch.int32, (B,), "n_new"),
-                                      c.ptr(q_out, torch.bfloat16, q.shape, "q_out"), *c.ws, c.stream))
+    _check(lib.sv_qk_norm_rope_append(*c.rows(q, (seqs.batch, T, H, layer.head_dim), "q"), *c.rows(k, kv, "k"),
+                                      *c.rows(v, kv, "v"), T, H, rot.by_ref, layer.by_ref,
+                                      seqs.by_ref, c.ptr(n_new, _I32, (B,), "n_new"),
+                                      c.ptr(q_out, _BF16, q.shape, "q_out"), *c.ws, c.stream))
 
 
 def sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens):
@@ -549,7 +556,7 @@ def sv_tree_attn(q, scale, layer, seqs, vis_idx, k, tree_mask, out, lse, ws, n_n
     lib = load()
     B, T, H, d = q.shape
     c = _Call(ws, stream, layer, seqs)
-    vis = c.ptr(vis_idx, torch.int32, (B, layer.c.n_kv_heads, k), "vis_idx")
+    vis = c.ptr(vis_idx, _I32, (B, layer.n_kv_heads, k), "vis_idx")
     if vis_idx is not None and k == 0:
         vis = c.ws[0]            # an empty list, not "all visual tokens": any address, nothing is read
     mask = None
@@ -557,10 +564,10 @@ def sv_tree_attn(q, scale, layer, seqs, vis_idx, k, tree_mask, out, lse, ws, n_n
         if tree_mask.dtype not in (torch.int64, torch.uint64):
             raise ValueError(f"tree_mask must be 64-bit integers, got {tree_mask.dtype}")
         mask = c.ptr(tree_mask, tree_mask.dtype, (B, T), "tree_mask")
-    _check(lib.sv_tree_attn(c.ptr(q, torch.bfloat16, (seqs.c.batch, T, H, layer.c.head_dim), "q"), T, H, scale,
-                            ctypes.byref(layer.c), ctypes.byref(seqs.c), vis, k, mask,
-                            c.ptr(n_new, torch.int32, (B,), "n_new"), c.ptr(out, torch.bfloat16, q.shape, "out"),
-                            c.ptr(lse, torch.float32, (B, T, H), "lse"), *c.ws, c.stream))
+    _check(lib.sv_tree_attn(c.ptr(q, _BF16, (seqs.batch, T, H, layer.head_dim), "q"), T, H, scale,
+                            layer.by_ref, seqs.by_ref, vis, k, mask,
+                            c.ptr(n_new, _I32, (B,), "n_new"), c.ptr(out, _BF16, q.shape, "out"),
+                            c.ptr(lse, _F32, (B, T, H), "lse"), *c.ws, c.stream))
 
 
 def _layer_array(layers):
@@ -573,9 +580,9 @@ def sv_kv_accept(layers, seqs, T, path, ws, n_path=None, stream=None):
     lib = load()
     B, P = path.shape
     c = _Call(ws, stream, seqs, *layers)
-    _check(lib.sv_kv_accept(_layer_array(layers), len(layers), ctypes.byref(seqs.c), T,
-                            c.ptr(path, torch.int32, (seqs.c.batch, P), "path"), P,
-                            c.ptr(n_path, torch.int32, (B,), "n_path"), *c.ws, c.stream))
+    _check(lib.sv_kv_accept(_layer_array(layers), len(layers), seqs.by_ref, T,
+                            c.ptr(path, _I32, (seqs.batch, P), "path"), P,
+                            c.ptr(n_path, _I32, (B,), "n_path"), *c.ws, c.stream))
 
 
 def sv_pages_workspace_bytes(batch, max_blocks, num_blocks):
@@ -583,8 +590,8 @@ def sv_pages_workspace_bytes(batch, max_blocks, num_blocks):
 
 
 def _pages(pool, seqs, ws, stream, *layers):
-    if pool.n_pages.shape != (seqs.c.batch,):
-        raise ValueError(f"n_pages must have shape ({seqs.c.batch},), got {tuple(pool.n_pages.shape)}")
+    if pool.n_pages.shape != (seqs.batch,):
+        raise ValueError(f"n_pages must have shape ({seqs.batch},), got {tuple(pool.n_pages.shape)}")
     return _Call(ws, stream, pool, seqs, *layers)
 
 
@@ -592,8 +599,8 @@ def sv_pages_release(pool, seqs, keep, ws, stream=None):
     """Drops every sequence's pages behind its first keep[b] tokens (int32 [B]; -1: leave it; None: drop all)."""
     lib = load()
     c = _pages(pool, seqs, ws, stream)
-    _check(lib.sv_pages_release(ctypes.byref(pool.c), ctypes.byref(seqs.c),
-                                c.ptr(keep, torch.int32, (seqs.c.batch,), "keep"), *c.ws, c.stream))
+    _check(lib.sv_pages_release(pool.by_ref, seqs.by_ref,
+                                c.ptr(keep, _I32, (seqs.batch,), "keep"), *c.ws, c.stream))
 
 
 def sv_pages_fork(pool, seqs, parent, child, ws, n_tok=None, stream=None):
@@ -602,9 +609,9 @@ def sv_pages_fork(pool, seqs, parent, child, ws, n_tok=None, stream=None):
     lib = load()
     n, = parent.shape
     c = _pages(pool, seqs, ws, stream)
-    _check(lib.sv_pages_fork(ctypes.byref(pool.c), ctypes.byref(seqs.c),
-                             c.ptr(parent, torch.int32, (n,), "parent"), c.ptr(child, torch.int32, (n,), "child"), n,
-                             c.ptr(n_tok, torch.int32, (n,), "n_tok"), *c.ws, c.stream))
+    _check(lib.sv_pages_fork(pool.by_ref, seqs.by_ref,
+                             c.ptr(parent, _I32, (n,), "parent"), c.ptr(child, _I32, (n,), "child"), n,
+                             c.ptr(n_tok, _I32, (n,), "n_tok"), *c.ws, c.stream))
 
 
 def sv_pages_reserve(pool, layers, seqs, T, ws, n_new=None, stream=None):
@@ -612,8 +619,8 @@ def sv_pages_reserve(pool, layers, seqs, T, ws, n_new=None, stream=None):
     private copies, in every layer, of the shared pages among them."""
     lib = load()
     c = _pages(pool, seqs, ws, stream, *layers)
-    _check(lib.sv_pages_reserve(ctypes.byref(pool.c), _layer_array(layers), len(layers), ctypes.byref(seqs.c), T,
-                                c.ptr(n_new, torch.int32, (seqs.c.batch,), "n_new"), *c.ws, c.stream))
+    _check(lib.sv_pages_reserve(pool.by_ref, _layer_array(layers), len(layers), seqs.by_ref, T,
+                                c.ptr(n_new, _I32, (seqs.batch,), "n_new"), *c.ws, c.stream))
 
 
 def sv_read_device_status(ws, clear=False, stream=None):
