@@ -7,8 +7,12 @@
 // column) order.  There is no free list to keep in step, and the same state
 // always gives the same tables.  The counts and the tables are a few KB to a
 // few hundred KB and bound by latency: one launch each, one CTA where the
-// order of the pages matters.  The row and page copies are bound by memory
-// and run over every layer in one launch.
+// order of the pages matters.  The row and page copies run over every layer in
+// one launch.  Measured, replayed in a graph: release, fork and reserve of 2
+// branches in a pool of 80 pages 7.8 us for the four kernels, of 32 branches of
+// 211 pages each 13 us, with copies of 32 pages in 8 layers (17 MB read and
+// written).  ncu, each alone with cold caches: 5.0, 5.4, 9.4 (plan) and 6.5 us
+// (copies).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -273,7 +277,9 @@ pages_copy_kernel(const int4* __restrict__ plan, const __grid_constant__ LayerPo
 
 // Accepted path of a draft: row base + path[i] -> row base + i, for one
 // (layer, KV head, sequence) per CTA.  path ascends, so rows only move down;
-// every row is loaded before any is stored.
+// every row is loaded before any is stored.  At most 64 KB a CTA, bound by its
+// dependent loads (lengths, path, page table, row): 6.0 us alone with cold
+// caches for 8 sequences, 4 layers, 4 KV heads.
 __global__ void __launch_bounds__(256)
 kv_accept_kernel(const __grid_constant__ LayerPools pools, int num_blocks, int Hkv, int vecs,
                  const int32_t* __restrict__ block_table, int max_blocks, SeqLens lens, int n_vis, int n_text, int T,

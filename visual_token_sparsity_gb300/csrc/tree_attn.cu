@@ -32,6 +32,12 @@
 // 128-row K and V tiles in the 128-byte-swizzled layout the MMA reads,
 // page-table and index loads running two tiles ahead, 14-15 query rows.  Rows
 // that are not there (behind the end, a bad page) are zero-filled and masked.
+//
+// Measured (d 128): 16 sequences x 32 heads x 1584 tokens, 16 rows, 77.8 us =
+// 5.4 TB/s of cache rows; 8 x 4 KV heads of up to 12827 tokens, 189 rows, 51 us =
+// 3.1 TB/s; 1351 rows x 4 KV heads x 50392 tokens 132 us = 1.06 PFLOP/s, where a
+// tile takes a CTA 3800 cycles, 2048 of them in the products: each stream's
+// chain of S, weights and O is longer than what the other's hides.
 #include "common.cuh"
 #include "fastmath.cuh"
 #include "kernels.h"
@@ -872,7 +878,8 @@ __device__ __forceinline__ float4 join4(float4 a, float w0, float4 b, float w1) 
 // of one that a CTA of the kernel above began.  Its warps take
 // every eighth piece each (a unit may lie in two or in a hundred; one after the
 // other they took 14 us for 38), then the eight results are joined, always in
-// the same order.
+// the same order.  Bound by latency (ncu, alone and with cold caches: 11.4 us
+// for 152 pieces of 189 rows, 32 MB of L2 traffic, 15 MB of them from memory).
 template <int D, int QT>
 __global__ void __launch_bounds__(256)
 tree_merge_kernel(const __grid_constant__ TreeArgs a) {
