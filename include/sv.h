@@ -489,8 +489,8 @@ sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_
  *           then adds T (or n_new[b]) to n_text.
  * n_new   : optional DEVICE int32 [B]: only the first n_new[b] tokens of
  *           sequence b are there; the rows behind them are not used, and
- *           q_out and the cache stay as they were.  A count outside [0, T] sets SV_DEV_BAD_LENGTH and the
- *           sequence is skipped.
+ *           q_out and the cache stay as they were.  A count outside [0, T]
+ *           sets SV_DEV_BAD_LENGTH and the sequence is skipped.
  * q_out   : out bf16 [B][T][H][d]; q itself (with q_stride == H * d) or apart
  *           from q, k and v.
  * A page outside the pool sets SV_DEV_BAD_BLOCK; the token's queries are
@@ -512,7 +512,7 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
  *
  * The T tokens' own K / V have been appended at positions n_vis + n_text + s
  * (sv_kv_append or sv_qk_norm_rope_append) and are not yet in n_text.
- * tree_mask : DEVICE uint64 [B][T], T <= 64: token t sees drafted token s iff
+ * tree_mask : DEVICE uint64 [B][T], 8-byte aligned, T <= 64: token t sees drafted token s iff
  *             bit s is set (its own bit included; bits from T or n_new[b] on
  *             are ignored).  NULL: token t sees drafted tokens 0 .. t (any
  *             T up to 65536), e.g. a question's prefill; lse then serves as
@@ -524,7 +524,8 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
  * vis_idx, k, seqs : as for sv_sparse_decode_attn (a skipped sequence's rows
  *             read 0 and -inf; tokens of a page outside the pool are not
  *             attended).
- * q, out    : bf16 [B][T][H][d], 16-byte aligned; out may be q.
+ * q, out    : bf16 [B][T][H][d], 16-byte aligned; out may be q itself, or apart
+ *             from it.
  * lse       : optional out fp32 [B][T][H].  A row that sees no token at all
  *             has out 0 and lse -inf.
  * A drafted token that a row does not see has no part in it, whatever its K

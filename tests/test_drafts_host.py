@@ -116,6 +116,17 @@ def test_tree_arguments(lib):
     assert call(T=0) == call(S=seqs(batch=0)) == 0
 
 
+def test_tree_mask_and_output_addresses(lib):
+    def call(mask=None, out=P(0x2000000), T=5):
+        return lib.sv_tree_attn(P(0x1000000), T, 4, 0.1, ctypes.byref(layer()), ctypes.byref(seqs(0, 10)), None, 0,
+                                mask, None, out, None, P(0x3000000), 255, None)
+    assert call() == call(mask=P(0x10008)) == WORKSPACE                  # (nothing before it is wrong)
+    assert call(mask=P(0x10004)) == INVALID
+    rows = 2 * 5 * 4 * 64 * 2                                           # bytes of q
+    assert call(out=P(0x1000000 + rows - 16)) == call(out=P(0x1000000 - rows + 16)) == INVALID
+    assert call(out=P(0x1000000 + rows)) == call(out=P(0x1000000 - rows)) == call(out=P(0x1000000)) == WORKSPACE
+
+
 def test_accept_arguments(lib):
     from visual_token_sparsity_gb300 import binding as sv
     def call(layers=(layer(),), S=None, T=9, path=P(), n=4, ws=P(), nb=256):

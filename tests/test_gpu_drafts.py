@@ -295,6 +295,36 @@ def test_tree_attention_of_units_of_one_tile(lib, H, Hkv, d, B, T, n_text):
         check_tree(H, Hkv, d, B, T, 0, None, n_text, "tree", seed=seed)
 
 
+def test_more_row_tiles_than_a_gpu_has_places(lib):
+    check_tree(16, 1, 64, 1, 2450, 30, 20, 3, "chain")
+
+
+def test_a_batch_of_70000_sequences(lib):
+    """Reserve, append, attend and accept with one token of context each."""
+    from visual_token_sparsity_gb300 import binding as sv
+    B, T, d = 70000, 2, 64
+    kp, vp = (torch.zeros(B, 1, 16, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    layer = sv.KvLayer(kp, vp)
+    table = torch.full((B, 1), -1, dtype=torch.int32, device=DEV)
+    pool = sv.PagePool(torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV))
+    seqs = sv.SeqBatch(table, 0, 0)
+    ws = sv.workspace(max(sv.sv_pages_workspace_bytes(B, 1, B), sv.sv_tree_attn_workspace_bytes(B, T, 1, 1, d, T)))
+    sv.sv_pages_reserve(pool, [layer], seqs, T, ws)
+    x = synth.normal_bf16((3, B, T, 1, d), 4).to(DEV)
+    q, out = torch.empty_like(x[0]), torch.empty_like(x[0])
+    sv.sv_qk_norm_rope_append(x[0], x[1], x[2], sv.Rotation(None, None), layer, seqs, q, ws)
+    # token 0 sees itself, token 1 only itself
+    mask = torch.tensor([1, 2], dtype=torch.int64, device=DEV).repeat(B, 1)
+    sv.sv_tree_attn(q, 0.125, layer, seqs, None, 0, mask, out, None, ws)
+    path = torch.ones(B, 1, dtype=torch.int32, device=DEV)
+    sv.sv_kv_accept([layer], seqs, T, path, ws)
+    torch.cuda.synchronize()
+    assert sv.sv_read_device_status(ws) == 0
+    assert torch.equal(table[:, 0], torch.arange(B, dtype=torch.int32, device=DEV))
+    assert torch.equal(q, x[0]) and torch.equal(out, x[2])
+    assert torch.equal(kp[:, 0, 0], x[1][:, 1, 0]) and torch.equal(vp[:, 0, 0], x[2][:, 1, 0])
+
+
 @pytest.mark.parametrize("std,scale", [(4.0, 0.5), (16.0, 0.7), (1.0, 0.0)])
 def test_tree_attention_with_peaked_and_flat_weights(lib, std, scale):
     check_tree(8, 2, 128, 1, 20, 500, 250, 30, "tree", seed=5, std=std, scale=scale)

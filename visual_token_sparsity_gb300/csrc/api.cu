@@ -703,6 +703,7 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
   if (s != SV_OK) return s;
   if (!q || !out) return fail(SV_ERR_INVALID_ARG, "q and out must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(SV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(tree_mask) % 8) return fail(SV_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
   const int Hkv = layer->n_kv_heads;
   if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
   if (H / Hkv > 16) return fail(SV_ERR_UNSUPPORTED, "query heads per KV head %d > 16", H / Hkv);
@@ -714,6 +715,9 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
   const int k_vis = vis_idx ? k : seqs->n_vis;
   if (vis_idx && (k < 0 || k > seqs->n_vis)) return fail(SV_ERR_INVALID_ARG, "need 0 <= k <= n_vis");
   if ((long long)seqs->batch * T * H > 0x7fffffffLL) return fail(SV_ERR_INVALID_ARG, "batch * T * H too large");
+  const size_t out_bytes = (size_t)seqs->batch * T * H * layer->head_dim * 2;
+  if (out != q && overlap(out, out_bytes, q, out_bytes))
+    return fail(SV_ERR_INVALID_ARG, "out must be q itself or not overlap it");
   const long long n_tok = (long long)k_vis + seqs->n_text + T;   // <= max_blocks * 16
   if (seqs->batch * (n_tok / 128 + 1) > 0x7fffffffLL / Hkv)
     return fail(SV_ERR_UNSUPPORTED, "batch * n_kv_heads * tokens beyond 2^38");
