@@ -482,7 +482,9 @@ sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_
 
 /*
  * Decoder form: sv_kv_append of T new tokens whose queries and keys are
- * normalised and rotated on the way; values are copied.
+ * normalised and rotated on the way; values are copied.  Results next to a
+ * bf16 rounding boundary are formed with more than fp32, so that (almost) every
+ * element is the 64-bit result's, rounded to fp32 and then to bf16.
  * q, k, v : bf16 [B][T][H][d], [B][T][Hkv][d] twice, with token strides as
  *           above.  Keys and values go to positions n_vis + n_text + t
  *           (n_vis_seq[b] + n_text_seq[b] + t), as by sv_kv_append; the caller

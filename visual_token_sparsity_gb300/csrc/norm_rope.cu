@@ -7,9 +7,16 @@
 // Pair p turns by cos_sin[pos[axis(p)]][p]: one position per token, or up to
 // three (time, row, column) that own consecutive sections of the pairs.
 // Everything is fp32 between the bf16 load and the one rounding at the end.
+// Rows on their way into the cache are rounded as the 64-bit result would be,
+// by way of fp32: a query element that falls on the other side of a bf16
+// rounding boundary moves its row's log-sum-exp by some 1e-4, so results next to
+// a boundary are formed again with twice the bits (the step's lse is then
+// within 2e-7 of 64 bits, relative; with fp32 alone up to 9e-6).
 //
 // Bound by memory: every row is read once and written once, a dozen
-// operations per element.  A row is d / 8 lanes of 8 elements, 32 / (d / 8)
+// operations per element.  16384 tokens of 16 + 16 heads, d 80: 28 us, 6.0 TB/s; a
+// prefill of 8770 tokens of 36 heads with a norm 40 us, 4.5 TB/s, bound by
+// instructions (34 us without the second forming of results in doubt).  A row is d / 8 lanes of 8 elements, 32 / (d / 8)
 // rows side by side in a warp; a lane's elements are the two halves of four
 // pairs (rotate-half: 4 at 4j and 4 at rot/2 + 4j; interleaved or not
 // rotated: 8 in a row), so no pair crosses lanes and the four (cos, sin) it
@@ -24,13 +31,15 @@ namespace {
 
 constexpr int kWarps = 4;
 // Row groups in flight per warp (and as many more on their way) and the CTAs per
-// SM that the registers leave: of 1 to 4 groups and 3 to 5 CTAs of 8 warps, 8 and
-// 9 of 4, these were the fastest (16384 vision tokens 28 us, 28 to 43; a
-// prefill of 11540 tokens 34 us, 34 to 51).
+// SM that the registers leave: of 1 to 4 groups and 3 to 5 CTAs of 8 warps, 5 to
+// 10 of 4, these were the fastest (16384 vision tokens 28 us, 28 to 43; the
+// prefill 40 us, 40 to 49).
 template <bool APPEND>
 struct Shape {
-  static constexpr int kUnroll = APPEND ? 2 : 3, kCtas = APPEND ? 9 : 8;
+  static constexpr int kUnroll = APPEND ? 2 : 3, kCtas = APPEND ? 7 : 8;
 };
+// fp32's error is 0.6 of the last bit of a pair's larger member (rms)
+constexpr uint32_t kDoubt = 4;
 constexpr int kWarpsPerSm = 64;  // warps that a launch spreads over before they take more rows each
 
 __device__ __forceinline__ uint32_t bf16x2(uint64_t v) {
@@ -121,6 +130,85 @@ __device__ __forceinline__ float row_sum(float s, const RowLanes<L>& next) {
     for (int o = L / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
   }
+}
+
+// a c + b d, times (ih + il), from about 48 bits of each.
+__device__ __forceinline__ float exact_turn(float a, float b, float c, float d, float ih, float il) {
+  const float h1 = __fmul_rn(a, c), h2 = __fmul_rn(b, d);
+  const float s = __fadd_rn(h1, h2), t = __fadd_rn(s, -h1);
+  const float e = __fadd_rn(__fadd_rn(h1, -__fadd_rn(s, -t)), __fadd_rn(h2, -t));    // of the sum
+  const float lo = e + (fmaf(a, c, -h1) + fmaf(b, d, -h2));                          // and of the products
+  const float r = __fmul_rn(s, ih);
+  return __fadd_rn(r, fmaf(s, il, fmaf(lo, ih, fmaf(s, ih, -r))));
+}
+
+// (hi, lo) += (x, y), hi + lo holding about 48 bits.
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float x, float y) {
+  const float s = __fadd_rn(hi, x), t = __fadd_rn(s, -hi);
+  lo += __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -t)), __fadd_rn(x, -t)) + y;
+  hi = s;
+}
+
+// A lane's 8 results formed again with twice the bits (one group of rows in
+// thirty comes here).  The whole warp takes part.
+template <int L, bool INTER>
+__device__ __forceinline__ uint4 exact_row(uint4 raw, uint4 fast, const uint16_t* weight, int off0, int off1, float eps,
+                                        uint64_t c0, uint64_t c1, uint64_t s0, uint64_t s1) {
+  float x[8], w[8], c[4], n[4];
+  auto split = [&](uint4 u, float* to) {     // first members 0-3, second 4-7
+    Lane8<INTER> l;
+    l.u = u;
+    uint64_t p[2], y[2];
+    l.unpack(p, y);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      fm::unpack2(p[e], to[2 * e], to[2 * e + 1]);
+      fm::unpack2(y[e], to[4 + 2 * e], to[5 + 2 * e]);
+    }
+  };
+  split(raw, x);
+  fm::unpack2(c0, c[0], c[1]);
+  fm::unpack2(c1, c[2], c[3]);
+  fm::unpack2(s0, n[0], n[1]);
+  fm::unpack2(s1, n[2], n[3]);
+  float ih = 1.f, il = 0.f;
+  if (weight != nullptr) {
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add_exact(hi, lo, __fmul_rn(x[e], x[e]), 0.f);     // (the squares are exact)
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi, o), z = __shfl_xor_sync(0xffffffffu, lo, o);
+      add_exact(hi, lo, h, z);
+    }
+    hi *= 1.f / (8 * L);                     // (a power of two)
+    lo *= 1.f / (8 * L);
+    add_exact(hi, lo, eps, 0.f);
+    ih = rsqrtf(hi);
+    const float q = __fmul_rn(ih, ih), a = __fmul_rn(hi, q);
+    const float rest = __fadd_rn(1.f, -a) - fmaf(hi, q, -a) - fmaf(hi, fmaf(ih, ih, -q), lo * q);
+    il = 0.5f * ih * rest;
+    Lane8<INTER> g;
+    g.load(weight, off0, off1);
+    split(g.u, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], w[e]);                      // (exact)
+  }
+  float re[4], im[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    re[e] = exact_turn(x[e], x[4 + e], c[e], -n[e], ih, il);
+    im[e] = exact_turn(x[e], x[4 + e], n[e], c[e], ih, il);
+  }
+  // infinities and NaN, and what overflows in between, as the short way has them
+  bool fine = true;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) fine = fine && isfinite(re[e]) && isfinite(im[e]);
+  if (!fine) return fast;
+  Lane8<INTER> l;
+  uint64_t p[2] = {fm::pack2(re[0], re[1]), fm::pack2(re[2], re[3])}, y[2] = {fm::pack2(im[0], im[1]), fm::pack2(im[2], im[3])};
+  l.pack(p, y);
+  return l.u;
 }
 
 }  // namespace
@@ -240,6 +328,8 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
     for (int done = 0; done < n1 - n0; done += RPC, from += RPC * D, to += RPC * stride) {
       Lane8<INTER> next[kUnroll];
       if (done + RPC < n1 - n0) load(next, from + RPC * D, left - done - RPC);
+      Lane8<INTER> y8[kUnroll];               // the results
+      uint32_t near[kUnroll];
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         uint64_t p[2], y[2];
@@ -271,9 +361,46 @@ norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int per_warp, uint32_t 
           y[e] = fm::fma2(p[e], sn[e], fm::mul2(y[e], cs[e]));
           p[e] = re;
         }
-        if (!PARTLY || turned || (NORM && weight != nullptr)) x[i].pack(p, y);
-        if (done + i * RPG < left) x[i].store(to + (size_t)(i * RPG) * stride, off0, off1);
-        x[i] = next[i];
+        if constexpr (!APPEND) {
+          if (!PARTLY || turned || (NORM && weight != nullptr)) x[i].pack(p, y);
+          if (done + i * RPG < left) x[i].store(to + (size_t)(i * RPG) * stride, off0, off1);
+          x[i] = next[i];
+        } else {
+          near[i] = 0xffffffffu;
+          y8[i] = x[i];
+          if (!PARTLY || turned || (NORM && weight != nullptr)) {
+            y8[i].pack(p, y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              constexpr uint32_t kOff = (0x8000u + kDoubt) * 0x10001u;
+              near[i] = __viaddmin_u16x2(__byte_perm((uint32_t)p[e], (uint32_t)(p[e] >> 32), 0x5410), kOff, near[i]);
+              near[i] = __viaddmin_u16x2(__byte_perm((uint32_t)y[e], (uint32_t)(y[e] >> 32), 0x5410), kOff, near[i]);
+            }
+          }
+        }
+      }
+      if constexpr (APPEND) {
+        // What goes on to the cache is rounded as from 64 bits: where fp32's
+        // last bits could decide the rounding to bf16 (a result within kDoubt of
+        // them of a tie), the warp forms the row again with twice the bits.
+        auto doubt = [](uint32_t n) { return min(n & 0xffffu, n >> 16) <= 2 * kDoubt; };
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) any = any || doubt(near[i]);
+        if (__any_sync(0xffffffffu, any)) {
+          const bool keep = PARTLY && !turned && !(NORM && weight != nullptr);
+#pragma unroll
+          for (int i = 0; i < kUnroll; ++i)
+            if (__any_sync(0xffffffffu, doubt(near[i]))) {
+              const uint4 u = exact_row<L, INTER>(x[i].u, y8[i].u, NORM ? weight : nullptr, off0, off1, a.eps, cs[0], cs[1], sn[0], sn[1]);
+              if (!keep) y8[i].u = u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+          if (done + i * RPG < left) y8[i].store(to + (size_t)(i * RPG) * stride, off0, off1);
+          x[i] = next[i];
+        }
       }
     }
   };
@@ -318,8 +445,12 @@ static cudaError_t launch_l(const NormRopeArgs& a, bool append, int num_sms, cud
   const long long blocks = (tokens * per_token + kWarps - 1) / kWarps;
   if (blocks * kWarps > 0xffffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
-  auto kernel = append ? (a.interleaved ? pick<L, true, true>(norm, a.rot) : pick<L, true, false>(norm, a.rot))
-                       : (a.interleaved ? pick<L, false, true>(norm, a.rot) : pick<L, false, false>(norm, a.rot));
+  auto kernel = a.interleaved ? pick<L, false, true>(norm, a.rot) : pick<L, false, false>(norm, a.rot);
+  if constexpr (L == 8 || L == 16) {         // head dims of the cache
+    if (append) kernel = a.interleaved ? pick<L, true, true>(norm, a.rot) : pick<L, true, false>(norm, a.rot);
+  } else if (append) {
+    return cudaErrorInvalidValue;
+  }
   return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a,
                           (int)groups * RPG, (uint32_t)per_token);
 }
