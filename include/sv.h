@@ -450,6 +450,9 @@ sv_status sv_decode_append_attn(const void* q, int H, float scale, const sv_kv_l
  *               up to rot_dim / 2 (n_axes 1: section is not read).  Positions
  *               of an axis whose section is empty are not read.
  * q_weight, k_weight : bf16 [head dim], 16-byte aligned, or NULL: no norm.
+ * In this and the following calls a call without tokens (B, N or T 0) does
+ * nothing, and the tensors that hold a row per token (pos among them) may
+ * then be NULL.
  */
 typedef struct {
   const float* cos_sin;

@@ -217,3 +217,22 @@ def test_binding_refuses_before_the_library(lib):
         sv.Rotation(torch.zeros(4, 8, 2), torch.zeros(1, 2, dtype=torch.int32), sections=[4])
     with pytest.raises(ValueError, match="weight"):
         sv.Rotation(None, None, q_weight=torch.zeros(2, 8))
+
+
+def test_calls_without_tokens_take_null_tensors(lib):
+    """An empty tensor has no address: a step that drafted nothing is no error."""
+    r = rot(pos=None)
+    L, S = ctypes.byref(layer()), ctypes.byref(seqs())
+    for B, N in ((1, 0), (0, 8)):
+        assert lib.sv_qk_norm_rope(None, 256, None, 256, B, N, 4, 4, 64, ctypes.byref(r), None, None, P(), 256, None) == 0
+    assert lib.sv_qk_norm_rope_append(None, 256, None, 128, None, 128, 0, 4, ctypes.byref(r), L, S, None, None, P(), 256,
+                                      None) == 0
+    assert lib.sv_tree_attn(None, 0, 4, 0.1, L, S, None, 0, None, None, None, None, P(), 1 << 26, None) == 0
+    assert lib.sv_kv_accept(L, 1, S, 0, None, 0, None, P(), 256, None) == 0
+    # with tokens they are still refused
+    assert lib.sv_qk_norm_rope(None, 256, None, 256, 1, 8, 4, 4, 64, ctypes.byref(rot()), None, None, P(), 256, None) == INVALID
+    assert lib.sv_qk_norm_rope(P(0x1000000), 256, P(0x2000000), 256, 1, 8, 4, 4, 64, ctypes.byref(r), P(0x3000000),
+                               P(0x4000000), P(), 256, None) == INVALID
+    assert lib.sv_qk_norm_rope_append(None, 256, None, 128, None, 128, 1, 4, ctypes.byref(rot()), L, S, None, None, P(),
+                                      256, None) == INVALID
+    assert lib.sv_tree_attn(None, 1, 4, 0.1, L, S, None, 0, None, None, None, None, P(), 1 << 26, None) == INVALID

@@ -734,3 +734,24 @@ def test_speculative_step(lib):
     assert sv.sv_read_device_status(ws) == 0 and sv.sv_read_device_status(wa) == 0
     sv.sv_pages_release(pool, both, i32([-1, 0]), ws)
     assert torch.equal(pool.ref.cpu(), ref) and pool.n_pages.tolist() == [held, 0]
+
+
+def test_a_step_without_drafted_tokens(lib):
+    """T = 0 through the whole step: nothing is launched, nothing is refused."""
+    from visual_token_sparsity_gb300 import binding as sv
+    c = Cache(2, 2, 64, 60, seed=3)
+    layer, seqs, ws = c.layer(), sv.SeqBatch(c.bt.to(DEV), 20, 10), sv.workspace(1 << 20)
+    keep = layer.k_pool.clone()
+    none = lambda *s, t=torch.bfloat16: torch.empty(*s, dtype=t, device=DEV)
+    cs = torch.zeros(9, 32, 2, device=DEV)
+    rot = sv.Rotation(cs, none(2, 0, t=torch.int32))
+    q, kv = none(2, 0, 4, 64), none(2, 0, 2, 64)
+    sv.sv_qk_norm_rope(q, kv, rot, none(2, 4, 0, 64), none(2, 2, 0, 64), ws)
+    sv.sv_pages_reserve(sv.PagePool(torch.ones(c.blocks, dtype=torch.int32, device=DEV), i32([c.per] * 2)), [layer], seqs,
+                        0, sv.workspace(sv.sv_pages_workspace_bytes(2, c.per, c.blocks)))
+    sv.sv_qk_norm_rope_append(q, kv, kv, rot, layer, seqs, none(2, 0, 4, 64), ws)
+    sv.sv_tree_attn(q, 0.1, layer, seqs, None, 0, none(2, 0, t=torch.int64), none(2, 0, 4, 64), none(2, 0, 4, t=torch.float32),
+                    ws)
+    sv.sv_kv_accept([layer], seqs, 0, none(2, 0, t=torch.int32), ws)
+    assert sv.sv_read_device_status(ws) == 0
+    assert torch.equal(layer.k_pool, keep)

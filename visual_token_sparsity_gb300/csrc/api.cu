@@ -152,7 +152,7 @@ sv_status check_rotation(const sv_rotation* r, int d, long long n_tok) {
     return fail(SV_ERR_INVALID_ARG, "norm weights must be 16-byte aligned");
   if (n_tok > 0x7fffffffLL) return fail(SV_ERR_INVALID_ARG, "more than 2^31 tokens");
   if (r->rot_dim == 0) return SV_OK;
-  if (!r->cos_sin || !r->pos) return fail(SV_ERR_INVALID_ARG, "cos_sin and pos must be non-NULL");
+  if (!r->cos_sin || (!r->pos && n_tok > 0)) return fail(SV_ERR_INVALID_ARG, "cos_sin and pos must be non-NULL");
   if (!aligned16(r->cos_sin)) return fail(SV_ERR_INVALID_ARG, "cos_sin must be 16-byte aligned");
   if (r->n_pos <= 0) return fail(SV_ERR_INVALID_ARG, "n_pos must be positive");
   if (r->n_axes < 1 || r->n_axes > 3) return fail(SV_ERR_UNSUPPORTED, "n_axes = %d (1 to 3)", r->n_axes);
@@ -625,10 +625,11 @@ sv_status sv_kv_append(const sv_kv_layer* layer, const sv_seq_batch* seqs, const
 sv_status sv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int B, int N, int H,
                           int Hk, int d, const sv_rotation* rot, void* q_out, void* k_out, void* ws,
                           size_t ws_bytes, void* stream) {
-  if (!q || !k || !q_out || !k_out) return fail(SV_ERR_INVALID_ARG, "q, k, q_out and k_out must be non-NULL");
   if (B < 0 || N < 0 || H <= 0 || Hk <= 0) return fail(SV_ERR_INVALID_ARG, "need B >= 0, N >= 0, H > 0, Hk > 0");
-  if (!sv::salience_head_dim_supported(d)) return fail(SV_ERR_UNSUPPORTED, "head_dim %d (64, 72, 80 or 128)", d);
   const long long n_tok = (long long)B * N, qr = (long long)H * d, kr = (long long)Hk * d;
+  if (n_tok > 0 && (!q || !k || !q_out || !k_out))
+    return fail(SV_ERR_INVALID_ARG, "q, k, q_out and k_out must be non-NULL");
+  if (!sv::salience_head_dim_supported(d)) return fail(SV_ERR_UNSUPPORTED, "head_dim %d (64, 72, 80 or 128)", d);
   sv_status s = check_rows("q", q, q_stride, qr);
   if (s == SV_OK) s = check_rows("k", k, k_stride, kr);
   if (s == SV_OK) s = check_rotation(rot, d, n_tok);
@@ -658,9 +659,10 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
                                  size_t ws_bytes, void* stream) {
   sv_status s = check_cache(layer, seqs, true);
   if (s != SV_OK) return s;
-  if (!q || !k || !v || !q_out) return fail(SV_ERR_INVALID_ARG, "q, k, v and q_out must be non-NULL");
   const int Hkv = layer->n_kv_heads, d = layer->head_dim;
   if (T < 0) return fail(SV_ERR_INVALID_ARG, "T must be >= 0");
+  if (T > 0 && seqs->batch > 0 && (!q || !k || !v || !q_out))
+    return fail(SV_ERR_INVALID_ARG, "q, k, v and q_out must be non-NULL");
   if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
   s = check_new_tokens(seqs, T);
   const long long n_tok = (long long)seqs->batch * T, qr = (long long)H * d, kv = (long long)Hkv * d;
@@ -701,7 +703,7 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
                        float* lse, void* ws, size_t ws_bytes, void* stream) {
   sv_status s = check_cache(layer, seqs, true);
   if (s != SV_OK) return s;
-  if (!q || !out) return fail(SV_ERR_INVALID_ARG, "q and out must be non-NULL");
+  if (T > 0 && seqs->batch > 0 && (!q || !out)) return fail(SV_ERR_INVALID_ARG, "q and out must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(SV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(tree_mask) % 8) return fail(SV_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
   const int Hkv = layer->n_kv_heads;
