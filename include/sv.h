@@ -537,6 +537,8 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
  * and V hold (infinities and NaN included).
  * ws        : sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, d, n_tokens),
  *             n_tokens = k + n_text + T (k = n_vis when vis_idx is NULL).
+ *             The size never shrinks as B, T or n_tokens grow: sized for the
+ *             largest, a workspace serves every smaller call of the same heads.
  * scale     : finite, >= 0.  Supported: d in {64, 128}, G = H / Hkv <= 16.
  */
 size_t sv_tree_attn_workspace_bytes(int B, int T, int H, int n_kv_heads, int head_dim, int n_tokens);

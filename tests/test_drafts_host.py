@@ -236,3 +236,22 @@ def test_calls_without_tokens_take_null_tensors(lib):
     assert lib.sv_qk_norm_rope_append(None, 256, None, 128, None, 128, 1, 4, ctypes.byref(rot()), L, S, None, None, P(),
                                       256, None) == INVALID
     assert lib.sv_tree_attn(None, 1, 4, 0.1, L, S, None, 0, None, None, None, None, P(), 1 << 26, None) == INVALID
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(28, 4, 128), (4, 2, 64), (32, 32, 128), (16, 1, 64), (1, 1, 64)])
+def test_tree_workspace_serves_every_smaller_call(lib, H, Hkv, d):
+    """Never larger for fewer sequences, drafted tokens or context tokens,
+    whatever tiles and pieces the sizes are cut into."""
+    size = lambda B, T, ctx: lib.sv_tree_attn_workspace_bytes(B, T, H, Hkv, d, ctx + T)
+    Ts = list(range(1, 301)) + list(range(301, 4000, 37)) + [5600, 9728, 20000, 65535, 65536]
+    for B in (1, 2, 8, 33):
+        for ctx in (0, 100, 500, 1000, 3392, 12800, 50199):
+            sizes = [size(B, T, ctx) for T in Ts]
+            drop = [(T, a, b) for T, a, b in zip(Ts[1:], sizes, sizes[1:]) if b < a]
+            assert not drop, (B, ctx, drop[0])
+    for T in (1, 9, 33, 73, 74, 193, 2000):
+        for ctx in (0, 300, 3000, 50000):
+            by_batch = [size(B, T, ctx) for B in range(1, 160)]
+            assert by_batch == sorted(by_batch), (T, ctx)
+    # an index per (sequence, KV head) and partial results for a GPU of CTAs, no more
+    assert size(8, 65536, 50000) <= 256 + 8 * Hkv * 4 + 4 * 256 + 152 * 2 * 256 * (4 * d + 8) + 152 * 16
