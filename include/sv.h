@@ -17,9 +17,11 @@
  *     call (except sv_retrieve_topk_noalloc) takes a caller-owned device
  *     workspace `ws` of at least the size the matching
  *     sv_*_workspace_bytes() returns.  The first 256 bytes of every
- *     workspace hold the device status word (see sv_read_device_status); a
- *     fresh workspace must be zero-filled once before first use.  Calls that
- *     share a workspace must be ordered on one stream.
+ *     workspace hold the device status word (see sv_read_device_status), the
+ *     next 16 KB (where the size is more than 256 bytes) counters that every
+ *     call leaves at zero; a fresh workspace must be zero-filled once before
+ *     first use.  Any calls, of whatever shapes, may share a workspace of the
+ *     largest of their sizes; they must be ordered on one stream.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Work is enqueued asynchronously; nothing synchronises except
  *     sv_read_device_status and, for non-tail spans, nothing in

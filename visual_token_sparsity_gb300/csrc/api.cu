@@ -28,6 +28,7 @@ int topk_max_smem_keys();
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+constexpr size_t kHeadBytes = kStatusBytes + sv::kWorkspaceCounters * sizeof(int);
 constexpr size_t kMaxSmemPerBlock = 232448;  // 227 KB opt-in on sm_100-family parts
 thread_local char g_err[512] = "";
 
@@ -54,7 +55,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int* status_word(void* ws) { return static_cast<int*>(ws); }
 
-char* after_status(void* ws) { return static_cast<char*>(ws) + kStatusBytes; }
+// the zeroed counters, and what follows them: the calls' data
+int* counters_of(void* ws) { return reinterpret_cast<int*>(static_cast<char*>(ws) + kStatusBytes); }
+char* data_of(void* ws) { return static_cast<char*>(ws) + kHeadBytes; }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -256,7 +259,7 @@ const char* sv_version(void) { return "sv 0.1 sm_103a"; }
 
 size_t sv_salience_workspace_bytes(int B, int H, int N, int d) {
   if (B < 0 || H < 0 || N <= 0 || !sv::salience_head_dim_supported(d)) return kStatusBytes;
-  return kStatusBytes + round256(sv::salience_workspace_bytes(B, H, N, d));
+  return kHeadBytes + round256(sv::salience_workspace_bytes(B, H, N, d));
 }
 
 int sv_salience_kernel_count(int N, int d) {
@@ -277,9 +280,8 @@ size_t sv_prune_workspace_bytes(int B, int N, int k) {
 size_t sv_retrieve_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n_vis, int k) {
   (void)H; (void)head_dim; (void)k;
   if (B < 0 || n_kv_heads < 0 || n_vis < 0) return kStatusBytes;
-  // status | per-row completion counters [B][Hkv] | scores [B][Hkv][n_vis]
-  return kStatusBytes + round256((size_t)B * n_kv_heads * sizeof(int)) +
-         round256((size_t)B * n_kv_heads * n_vis * sizeof(float));
+  // status | counters | scores [B][Hkv][n_vis]
+  return kHeadBytes + round256((size_t)B * n_kv_heads * n_vis * sizeof(float));
 }
 
 size_t sv_attn_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n_tokens) {
@@ -288,9 +290,8 @@ size_t sv_attn_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n
   const int G = H / n_kv_heads;
   const sv::AttnPlan p = sv::attn_plan(B, n_kv_heads, G, n_tokens);
   const size_t parts = (size_t)B * n_kv_heads * p.nsplit_max * G;
-  // status | per-(sequence, KV head) split counters | (m, l) partials | o partials
-  return kStatusBytes + round256((size_t)B * n_kv_heads * sizeof(int)) + round256(parts * 2 * sizeof(float)) +
-         round256(parts * head_dim * sizeof(float));
+  // status | counters | (m, l) partials | o partials
+  return kHeadBytes + round256(parts * 2 * sizeof(float)) + round256(parts * head_dim * sizeof(float));
 }
 
 size_t sv_evict_workspace_bytes(void) { return kStatusBytes; }
@@ -320,8 +321,8 @@ sv_status sv_salience_prefill(const void* q, const void* k, int B, int H, int N,
   sv_status s = check_ws(ws, ws_bytes, sv_salience_workspace_bytes(B, H, N, d));
   if (s != SV_OK) return s;
   if (B == 0) return SV_OK;
-  cudaError_t e = sv::launch_salience(q, k, B, H, N, d, scale, salience, after_status(ws),
-                                      status_word(ws), num_sms(), static_cast<cudaStream_t>(stream));
+  cudaError_t e = sv::launch_salience(q, k, B, H, N, d, scale, salience, data_of(ws),
+                                      counters_of(ws), status_word(ws), num_sms(), static_cast<cudaStream_t>(stream));
   if (e == cudaErrorInvalidValue)
     return fail(SV_ERR_CUDA, "tensor-map encoding or launch rejected the salience operands");
   return cuda_status(e, "sv_salience_prefill");
@@ -331,7 +332,7 @@ size_t sv_salience_summary_workspace_bytes(int B, int H, int N, int d, int R) {
   (void)d;
   (void)R;
   if (B < 0 || H < 0 || N < 0) return kStatusBytes;
-  return kStatusBytes + round256((size_t)B * H * N * sizeof(float));
+  return kHeadBytes + round256((size_t)B * H * N * sizeof(float));
 }
 
 sv_status sv_salience_summary(const void* q, const void* k, int B, int H, int N, int d, int R, float scale,
@@ -349,7 +350,7 @@ sv_status sv_salience_summary(const void* q, const void* k, int B, int H, int N,
   if (s != SV_OK) return s;
   if (B == 0) return SV_OK;
   cudaError_t e = sv::launch_summary_salience(q, k, B, H, N, d, R, scale, salience,
-                                              reinterpret_cast<float*>(after_status(ws)),
+                                              reinterpret_cast<float*>(data_of(ws)),
                                               static_cast<cudaStream_t>(stream));
   return cuda_status(e, "sv_salience_summary");
 }
@@ -421,12 +422,10 @@ sv_status sv_retrieve_topk(const void* q, int R, int H, const sv_kv_layer* layer
   if (s != SV_OK) return s;
   if (seqs->batch == 0) return SV_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t rows = (size_t)seqs->batch * Hkv;
-  int* row_done = reinterpret_cast<int*>(after_status(ws));
-  float* sc = scores ? scores : reinterpret_cast<float*>(after_status(ws) + round256(rows * sizeof(int)));
+  float* sc = scores ? scores : reinterpret_cast<float*>(data_of(ws));
   cudaError_t e = sv::launch_retrieve(q, R, H, H / Hkv, layer->k_pool, layer->num_blocks, Hkv,
                                       layer->head_dim, seqs->block_table, seqs->max_blocks, seqs->n_vis,
-                                      seqs->batch, sc, status_word(ws), num_sms(), row_done, k, vis_idx, st,
+                                      seqs->batch, sc, status_word(ws), num_sms(), counters_of(ws), k, vis_idx, st,
                                       lens_of(seqs), seqs->n_text);
   return cuda_status(e, "sv_retrieve_topk");
 }
@@ -434,7 +433,7 @@ sv_status sv_retrieve_topk(const void* q, int R, int H, const sv_kv_layer* layer
 size_t sv_retrieve_softmax_workspace_bytes(int B, int R, int H, int n_kv_heads, int head_dim, int n_vis,
                                            int n_text) {
   if (B < 0 || R <= 0 || H <= 0 || n_kv_heads <= 0 || H % n_kv_heads || n_vis < 0 || n_text < 0) return kStatusBytes;
-  return kStatusBytes + sv::retrieve_softmax_workspace_bytes(B, R, H, n_kv_heads, head_dim, n_vis, n_text);
+  return kHeadBytes + sv::retrieve_softmax_workspace_bytes(B, R, H, n_kv_heads, head_dim, n_vis, n_text);
 }
 
 sv_status sv_retrieve_topk_softmax(const void* q, int R, int H, float scale, const sv_kv_layer* layer,
@@ -460,7 +459,7 @@ sv_status sv_retrieve_topk_softmax(const void* q, int R, int H, float scale, con
   if (seqs->batch == 0) return SV_OK;
   cudaError_t e = sv::launch_retrieve_softmax(q, R, H, scale, layer->k_pool, layer->num_blocks, Hkv, layer->head_dim,
                                               seqs->block_table, seqs->max_blocks, seqs->n_vis, seqs->n_text,
-                                              seqs->batch, lse, k, vis_idx, scores, after_status(ws), status_word(ws),
+                                              seqs->batch, lse, k, vis_idx, scores, data_of(ws), status_word(ws),
                                               static_cast<cudaStream_t>(stream));
   return cuda_status(e, "sv_retrieve_topk_softmax");
 }
@@ -507,12 +506,9 @@ static sv_status decode_attn(const char* name, const void* q, int H, float scale
   a.batch = seqs->batch; a.out = out; a.lse = lse;
   a.lens = lens_of(seqs);
   a.k_new = k_new; a.v_new = v_new;
-  // the counters' offset depends only on the batch shape, so a workspace
-  // reused with other token counts finds them where the last call zeroed them
-  const size_t cnt_bytes = round256((size_t)seqs->batch * Hkv * sizeof(int));
-  a.split_done = reinterpret_cast<int*>(after_status(ws));
-  a.part_ml = reinterpret_cast<float*>(after_status(ws) + cnt_bytes);
-  a.part_o = reinterpret_cast<float*>(after_status(ws) + cnt_bytes + round256(parts * 2 * sizeof(float)));
+  a.split_done = counters_of(ws);
+  a.part_ml = reinterpret_cast<float*>(data_of(ws));
+  a.part_o = reinterpret_cast<float*>(data_of(ws) + round256(parts * 2 * sizeof(float)));
   a.status = status_word(ws);
   return cuda_status(sv::launch_sparse_attn(a, static_cast<cudaStream_t>(stream)), name);
 }
@@ -695,7 +691,7 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
 size_t sv_tree_attn_workspace_bytes(int B, int T, int H, int n_kv_heads, int head_dim, int n_tokens) {
   if (B < 0 || T < 0 || H <= 0 || n_kv_heads <= 0 || H % n_kv_heads || head_dim <= 0 || n_tokens < 0)
     return kStatusBytes;
-  return kStatusBytes + round256(sv::tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens));
+  return kHeadBytes + round256(sv::tree_attn_workspace_bytes(B, T, H, n_kv_heads, head_dim, n_tokens));
 }
 
 sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_layer* layer, const sv_seq_batch* seqs,
@@ -738,7 +734,7 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
   a.lens = lens_of(seqs);
   a.tree_mask = tree_mask; a.n_new = n_new;
   a.out = out; a.lse = lse;
-  a.ws = after_status(ws); a.status = status_word(ws);
+  a.ws = data_of(ws); a.status = status_word(ws);
   return cuda_status(sv::launch_tree_attn(a, static_cast<cudaStream_t>(stream)), "sv_tree_attn");
 }
 
@@ -765,7 +761,7 @@ sv_status sv_kv_accept(const sv_kv_layer* layers, int n_layers, const sv_seq_bat
 
 size_t sv_pages_workspace_bytes(int batch, int max_blocks, int num_blocks) {
   if (batch < 0 || max_blocks < 0 || num_blocks < 0) return kStatusBytes;
-  return kStatusBytes + round256(sv::pages_workspace_bytes(batch, max_blocks, num_blocks));
+  return kHeadBytes + round256(sv::pages_workspace_bytes(batch, max_blocks, num_blocks));
 }
 
 sv_status sv_pages_release(const sv_page_pool* pool, const sv_seq_batch* seqs, const int32_t* keep, void* ws,
@@ -809,7 +805,7 @@ sv_status sv_pages_reserve(const sv_page_pool* pool, const sv_kv_layer* layers, 
   }
   const int page_bytes = n_layers > 0 ? layers->n_kv_heads * SV_BLOCK_TOKENS * layers->head_dim * 2 : 0;
   return cuda_status(sv::launch_pages_reserve(a, lens_of(seqs), seqs->n_vis, seqs->n_text, T, n_new, pools, groups,
-                                              count, page_bytes, after_status(ws), num_sms(),
+                                              count, page_bytes, data_of(ws), num_sms(),
                                               static_cast<cudaStream_t>(stream)),
                      "sv_pages_reserve");
 }

@@ -141,6 +141,10 @@ AttnPlan attn_plan(int B, int Hkv, int G, int n_tokens) {
   return p;
 }
 
+// A unit with more than one split counts its finished splits: there are fewer
+// such units than warps in the plan.
+static_assert(kAttnTargetWarps <= kWorkspaceCounters && kMmaTargetWarps <= kWorkspaceCounters, "counters");
+
 static bool attn_fused_merge(const AttnPlan& p, int G) {
   if (p.nsplit > kFusedMergeMaxSplits) return false;
   return !attn_uses_mma(G) || (long long)G * p.nsplit <= kMmaFusedMergeMax;
@@ -347,7 +351,7 @@ sparse_attn_split_kernel(const uint16_t* __restrict__ q, int H,
   __threadfence();
   __syncwarp();
   int last = 0;
-  if (lane == 0) last = atomicAdd(split_done + bg, 1) == nsplit - 1;
+  if (lane == 0) last = nsplit == 1 || atomicAdd(split_done + bg, 1) == nsplit - 1;
   if (!__shfl_sync(0xffffffffu, last, 0)) return;
   __threadfence();
   constexpr int DPL = D / 32;   // output dims per lane
@@ -389,7 +393,7 @@ sparse_attn_split_kernel(const uint16_t* __restrict__ q, int H,
     if (lse != nullptr && lane == 0)
       lse[(size_t)b * H + g * G + hh] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
   }
-  if (lane == 0) split_done[bg] = 0;   // ready for the next call
+  if (lane == 0 && nsplit > 1) split_done[bg] = 0;   // ready for the next call
 }
 
 template <int D, int G, int TILE>

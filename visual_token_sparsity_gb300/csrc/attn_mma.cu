@@ -352,7 +352,7 @@ sparse_attn_mma_kernel(const uint16_t* __restrict__ q, int H, int G,
   __threadfence();
   __syncwarp();
   int last = 0;
-  if (lane == 0) last = atomicAdd(split_done + bg, 1) == nsplit - 1;
+  if (lane == 0) last = nsplit == 1 || atomicAdd(split_done + bg, 1) == nsplit - 1;
   if (!__shfl_sync(0xffffffffu, last, 0)) return;
   __threadfence();
   constexpr int DPL = D / 32;
@@ -380,7 +380,7 @@ sparse_attn_mma_kernel(const uint16_t* __restrict__ q, int H, int G,
     if (lse != nullptr && lane == 0)
       lse[(size_t)b * H + g * G + hh] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
   }
-  if (lane == 0) split_done[bg] = 0;
+  if (lane == 0 && nsplit > 1) split_done[bg] = 0;
 }
 
 size_t attn_mma_smem_bytes(int D) { return (size_t)kMmaWarps * kMmaStages * 2 * kSubTile * D * 2; }

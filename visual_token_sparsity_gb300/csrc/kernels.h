@@ -7,6 +7,14 @@
 
 namespace sv {
 
+// Zeroed counters behind the status word of every workspace that holds more
+// than it: completion counts that each call leaves at zero.  They lie at one
+// place, which nothing else uses, whatever the call and its shapes, so that
+// calls may share a workspace: a count that another call's data had run over
+// would never be reached.  Enough for one per (sequence, KV head) that has
+// more than one split.
+constexpr int kWorkspaceCounters = 4096;
+
 // Optional per-sequence lengths of a decode batch: device int32 arrays of
 // `batch` entries, nullptr = the batch-wide value for every sequence.  With
 // any of them set, the batch-wide n_vis / n_text / k are capacities: strides
@@ -88,7 +96,7 @@ struct AttnArgs {
   float* lse;
   float* part_ml;
   float* part_o;
-  int* split_done;   // zeroed int per (sequence, KV head); left zeroed after the call
+  int* split_done;   // zeroed int per (sequence, KV head) with splits; left zeroed after the call
   int* status;
   // fused append: one new token per (sequence, KV head), bf16 [batch][Hkv][D],
   // stored at text position n_text and attended as the last token (n_text
@@ -221,7 +229,7 @@ bool salience_uses_long_schedule(int N, int d);
 int salience_kernel_count(int N, int d);
 size_t salience_workspace_bytes(int B, int H, int N, int d);
 cudaError_t launch_salience(const void* q, const void* k, int B, int H, int N, int d, float scale,
-                            float* salience, void* ws, int* status, int num_sms,
+                            float* salience, void* ws, int* counters, int* status, int num_sms,
                             cudaStream_t stream);
 
 }  // namespace sv

@@ -348,14 +348,10 @@ cudaError_t launch_pages_fork(const PagesArgs& a, const int32_t* parent, const i
   return launch_dependent(pages_fork_kernel, dim3(n), dim3(256), 0, stream, a, parent, child, n, n_tok);
 }
 
-// The workspace's first part, where other calls keep a zeroed counter per
-// (sequence, KV head), is left as it is (up to 256 KV heads).
-static size_t counters_bytes(long long batch) { return (size_t)batch * 256 * sizeof(int); }
-
 size_t pages_workspace_bytes(long long batch, long long max_blocks, long long num_pages) {
   const long long entries = batch * max_blocks < num_pages ? batch * max_blocks : num_pages;
-  // others' counters | plan | counts [batch] | free ids
-  return counters_bytes(batch) + (size_t)(1 + entries) * sizeof(int4) + ((size_t)batch + 3) / 4 * 16 + (size_t)entries * sizeof(int32_t);
+  // plan | counts [batch] | free ids
+  return (size_t)(1 + entries) * sizeof(int4) + ((size_t)batch + 3) / 4 * 16 + (size_t)entries * sizeof(int32_t);
 }
 
 cudaError_t launch_pages_reserve(const PagesArgs& a, const SeqLens& lens, int n_vis, int n_text, int T,
@@ -364,7 +360,7 @@ cudaError_t launch_pages_reserve(const PagesArgs& a, const SeqLens& lens, int n_
   if (a.batch == 0 || T == 0) return cudaSuccess;
   const long long all = (long long)a.batch * a.max_blocks;
   const long long entries = all < a.num_pages ? all : a.num_pages;
-  int4* plan = reinterpret_cast<int4*>(static_cast<char*>(ws) + counters_bytes(a.batch));
+  int4* plan = static_cast<int4*>(ws);
   int32_t* counts = reinterpret_cast<int32_t*>(plan + 1 + entries);
   int32_t* free_ids = counts + ((size_t)a.batch + 3) / 4 * 4;
   cudaError_t e = launch_dependent(pages_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, lens, n_vis, n_text,

@@ -738,10 +738,10 @@ Plan make_plan(int N) {
   return p;
 }
 
-// Workspace after the status word: colsum [B*H][N] | fail counters (256 B) |
-// fail list [units] | long schedule: fold records [B*H][Nf].
+// Workspace: colsum [B*H][N] | fail list [units] | long schedule: fold records
+// [B*H][Nf].  The list's length is one of the zeroed counters.
 struct WsLayout {
-  size_t colsum, counters, list, fold, total;
+  size_t colsum, list, fold, total;
 };
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 WsLayout ws_layout(int B, int H, int N, const Plan& p) {
@@ -749,8 +749,7 @@ WsLayout ws_layout(int B, int H, int N, const Plan& p) {
   const size_t bh = (size_t)B * H;
   const size_t units = p.sched == kShort ? bh : bh * p.nt;
   w.colsum = 0;
-  w.counters = round256(bh * N * sizeof(float));
-  w.list = w.counters + 256;
+  w.list = round256(bh * N * sizeof(float));
   w.fold = w.list + round256(units * sizeof(int));
   w.total = w.fold + (p.sched == kShort ? 0 : round256(bh * p.Nf * 16));
   return w;
@@ -779,7 +778,7 @@ Plan plan_of(int N, int d) {
 
 template <int MB, int TD>
 cudaError_t run_salience(const void* q, const void* k, int B, int H, int N, int d, float scale, float* salience,
-                         void* ws, int* status, int num_sms, cudaStream_t stream) {
+                         void* ws, int* counters, int* status, int num_sms, cudaStream_t stream) {
   const Plan p = make_plan<MB, TD>(N);
   const WsLayout w = ws_layout(B, H, N, p);
   char* base = static_cast<char*>(ws);
@@ -806,7 +805,7 @@ cudaError_t run_salience(const void* q, const void* k, int B, int H, int N, int 
   a.inv_sl2 = 1.0f / a.sl2;
   a.colsum = reinterpret_cast<float*>(base + w.colsum);
   a.fold = reinterpret_cast<uint4*>(base + w.fold);
-  a.fail_count = reinterpret_cast<int*>(base + w.counters);
+  a.fail_count = counters;
   a.fail_done = a.fail_count + 1;
   a.fail_list = reinterpret_cast<int*>(base + w.list);
   a.status = status;
@@ -868,12 +867,13 @@ size_t salience_workspace_bytes(int B, int H, int N, int d) {
 }
 
 cudaError_t launch_salience(const void* q, const void* k, int B, int H, int N, int d, float scale,
-                            float* salience, void* ws, int* status, int num_sms, cudaStream_t stream) {
+                            float* salience, void* ws, int* counters, int* status, int num_sms,
+                            cudaStream_t stream) {
   switch (d) {
-    case 64: return run_salience<1, 0>(q, k, B, H, N, d, scale, salience, ws, status, num_sms, stream);
-    case 72: return run_salience<1, 1>(q, k, B, H, N, d, scale, salience, ws, status, num_sms, stream);
-    case 80: return run_salience<1, 2>(q, k, B, H, N, d, scale, salience, ws, status, num_sms, stream);
-    case 128: return run_salience<2, 0>(q, k, B, H, N, d, scale, salience, ws, status, num_sms, stream);
+    case 64: return run_salience<1, 0>(q, k, B, H, N, d, scale, salience, ws, counters, status, num_sms, stream);
+    case 72: return run_salience<1, 1>(q, k, B, H, N, d, scale, salience, ws, counters, status, num_sms, stream);
+    case 80: return run_salience<1, 2>(q, k, B, H, N, d, scale, salience, ws, counters, status, num_sms, stream);
+    case 128: return run_salience<2, 0>(q, k, B, H, N, d, scale, salience, ws, counters, status, num_sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -991,8 +991,7 @@ cudaError_t launch_qt(const TreeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Workspace: left as it was (other calls keep counters there) | the cut units
-// | (m, l) of every partial row | their O.
+// Workspace: the cut units | (m, l) of every partial row | their O.
 // The rows of partials are those of the plan, or for the size that a caller
 // asks for a bound that no call with fewer sequences, tokens or rows exceeds: a
 // plan has at most one CTA per SM and at most one per two token tiles of each
@@ -1000,13 +999,12 @@ cudaError_t launch_qt(const TreeArgs& a, cudaStream_t stream) {
 // ones.  (The plan itself is no such bound: 74 rows take less than 73, and with
 // more row tiles than half the SMs nothing is cut.)
 struct Layout {
-  size_t unit, ml, o, total;
+  size_t ml, o, total;
 };
-static Layout layout_of(size_t ctas, int QT, int B, int Hkv, int D) {
+static Layout layout_of(size_t ctas, int QT, int D) {
   const size_t rows = ctas * 2 * QT;
   Layout l;
-  l.unit = round256((size_t)B * Hkv * sizeof(int));
-  l.ml = l.unit + round256(ctas * sizeof(int4));
+  l.ml = round256(ctas * sizeof(int4));
   l.o = l.ml + round256(rows * sizeof(float2));
   l.total = l.o + rows * D * sizeof(float);
   return l;
@@ -1016,19 +1014,19 @@ size_t tree_attn_workspace_bytes(int B, int T, int H, int Hkv, int D, int n_toke
   const Plan p = plan_of(B, T, H / Hkv, Hkv, n_tokens);
   const long long tiles = (long long)B * Hkv * (((long long)n_tokens + kTile - 1) / kTile);
   const long long most = tiles / 2 > 1 ? p.row_tiles * (tiles / 2) : 0;
-  return layout_of((size_t)(most < kCtas ? most : kCtas), p.QT, B, Hkv, D).total;
+  return layout_of((size_t)(most < kCtas ? most : kCtas), p.QT, D).total;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& args, cudaStream_t stream) {
   TreeArgs a = args;
   a.G = a.H / a.Hkv;
   const Plan p = plan_of(a.batch, a.T, a.G, a.Hkv, a.k_vis + a.n_text + a.T);
-  const Layout l = layout_of(p.cut() ? p.ctas() : 0, p.QT, a.batch, a.Hkv, a.D);
+  const Layout l = layout_of(p.cut() ? p.ctas() : 0, p.QT, a.D);
   char* ws = static_cast<char*>(a.ws);
   a.row_tiles = p.row_tiles;
   a.columns = p.columns;
   a.by_unit = (long long)a.batch * a.Hkv * p.row_tiles <= (long long)p.ctas();
-  a.part_unit = reinterpret_cast<int*>(ws + l.unit);
+  a.part_unit = reinterpret_cast<int*>(ws);
   a.part_ml = reinterpret_cast<float*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   cudaError_t e;
