@@ -755,3 +755,24 @@ def test_a_step_without_drafted_tokens(lib):
     sv.sv_kv_accept([layer], seqs, 0, none(2, 0, t=torch.int32), ws)
     assert sv.sv_read_device_status(ws) == 0
     assert torch.equal(layer.k_pool, keep)
+
+
+@pytest.mark.parametrize("d,H,T", [(64, 4, 9), (128, 14, 30)])
+def test_scale_zero_whatever_the_products(lib, d, H, T):
+    """Every token weighs the same: products near fp32's largest value count
+    0, hidden tokens stay hidden, and 0 times an infinity is NaN."""
+    n_vis, n_text, std = 140, 9, 1.2e18 / math.sqrt(d / 64)
+    c = Cache(1, 2, d, n_vis + n_text + T, seed=61, std=std)
+    q = synth.normal_bf16((1, T, H, d), 4, std=std)
+    mask = [random_tree(T, np.random.default_rng(3))]
+    args = ([n_vis], [n_text], [0], [T], mask, 0.0)
+    out, lse, status = run_tree(c, q, None, 0, *args)
+    assert status == 0
+    ref = oracle_tree(q, c, None, *args)
+    assert_tree_close(out, lse, *ref)
+    q[0, 2, 1, 7], q[0, 4, 0, d - 1] = math.inf, math.nan
+    out, lse, _ = run_tree(c, q, None, 0, *args)
+    for t, h in ((2, 1), (4, 0)):
+        assert out[0, t, h].isnan().all() and lse[0, t, h].isnan()
+        out[0, t, h], lse[0, t, h] = torch.from_numpy(ref[0][0, t, h]), float(ref[1][0, t, h])
+    assert_tree_close(out, lse, *ref)

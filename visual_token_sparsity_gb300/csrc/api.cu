@@ -725,8 +725,10 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
   if (seqs->batch == 0 || T == 0) return SV_OK;
   sv::TreeArgs a = {};
   // hidden logits are -inf, which a factor of 0 would turn into NaN: the
-  // smallest factor in place of 0 leaves every finite logit below 2^-20
-  a.q = q; a.T = T; a.H = H; a.scale_log2 = std::fmax(scale * 1.4426950408889634f, 1e-37f);
+  // kernel takes 0 times the queries instead
+  a.q = q; a.T = T; a.H = H;
+  a.zero_scale = scale == 0.f;
+  a.scale_log2 = a.zero_scale ? 1.f : scale * 1.4426950408889634f;
   a.k_pool = layer->k_pool; a.v_pool = layer->v_pool;
   a.num_blocks = layer->num_blocks; a.Hkv = Hkv; a.D = layer->head_dim;
   a.block_table = seqs->block_table; a.max_blocks = seqs->max_blocks;

@@ -162,7 +162,8 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, bool append, int num_
 struct TreeArgs {
   const void* q;
   int T, H;
-  float scale_log2;
+  float scale_log2;                  // > 0
+  bool zero_scale;                   // the queries count as 0 times what they are
   const void* k_pool;
   const void* v_pool;
   int num_blocks, Hkv, D;

@@ -174,6 +174,16 @@ __device__ __forceinline__ bool zero_odd(uint4* p) {
   return odd;
 }
 
+// 8 bf16 values times 0: infinities and NaN give NaN.
+__device__ __forceinline__ void times_zero(uint4* p) {
+  uint4 v = *p;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    u[e] = ((u[e] & 0x7f80u) == 0x7f80u ? 0x7fc0u : 0u) | ((u[e] & 0x7f800000u) == 0x7f800000u ? 0x7fc00000u : 0u);
+  *p = v;
+}
+
 // Tensor memory columns of a stream's S (and P) and O: the CTA holds all 512,
 // so its allocation begins at column 0 (checked at the start).
 __host__ __device__ constexpr uint32_t tmem_s(int s) { return s * 128; }
@@ -505,6 +515,17 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
         }
       }
       cp_async_wait_all();
+      if (a.zero_scale) {
+        // (each lane on the chunks that it copied itself)
+#pragma unroll 1
+        for (int r0 = 32 * (warp - kQueryWarp); r0 < x.rows; r0 += 32 * kQueryWarps)
+#pragma unroll 1
+          for (int i = 0; i < CPR; ++i) {
+            const uint32_t r = first + i * RPI;
+            times_zero(reinterpret_cast<uint4*>(smem + (n % QB) * M::kQBytes + (r0 >> 7) * kTile * D * 2 +
+                                                (c >> 3) * kTile * 128 + ((r0 & 127) + r) * 128 + (((c & 7) ^ (r & 7)) * 16)));
+          }
+      }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh.q_full[n % QB]);
