@@ -255,3 +255,22 @@ def test_tree_workspace_serves_every_smaller_call(lib, H, Hkv, d):
             assert by_batch == sorted(by_batch), (T, ctx)
     # counters, and partial results for a GPU of CTAs: no more
     assert size(8, 65536, 50000) <= 256 + 4 * 4096 + 4 * 256 + 152 * 2 * 256 * (4 * d + 8) + 152 * 16
+
+
+def test_the_plan_cases_take_the_plans_they_name(lib):
+    """The GPU cases of test_gpu_tree_plans.py name the row tile and pieces that
+    they were made for.  The rule, written again, has to give both those and the
+    library's workspace size, which tells the row tile: (m, l) and O of two
+    units' rows per CTA."""
+    from test_gpu_tree_plans import CASES
+    up = lambda a, b: -(-a // b)
+    for name, (H, Hkv, d, B, T, n_vis, k, n_text, _, _, tile, row_tiles, pieces, by_unit) in CASES.items():
+        rows, n = T * (H // Hkv), (n_vis if k is None else k) + n_text + T
+        tiles = B * Hkv * up(n, 128)
+        qt = 256 if rows > 128 and tiles >= up(8 * 152, up(rows, 256)) else 128
+        rt = up(rows, qt)
+        cols = max(1, min(152 // rt, tiles // 2))
+        assert (qt, rt, cols, B * Hkv * rt <= cols * rt) == (tile, row_tiles, pieces, by_unit), name
+        ctas = min(152, rt * (tiles // 2))
+        size = up(ctas * 16, 256) * 256 + up(ctas * 2 * qt * 8, 256) * 256 + ctas * 2 * qt * d * 4
+        assert lib.sv_tree_attn_workspace_bytes(B, T, H, Hkv, d, n) == 256 + 4 * 4096 + up(size, 256) * 256, name

@@ -776,3 +776,17 @@ def test_scale_zero_whatever_the_products(lib, d, H, T):
         assert out[0, t, h].isnan().all() and lse[0, t, h].isnan()
         out[0, t, h], lse[0, t, h] = torch.from_numpy(ref[0][0, t, h]), float(ref[1][0, t, h])
     assert_tree_close(out, lse, *ref)
+
+
+@pytest.mark.parametrize("H,Hkv,d,B,T", [(32, 32, 128, 2, 150), (28, 4, 128, 2, 150), (28, 4, 128, 4, 1), (8, 2, 64, 2, 150),
+                                         (8, 8, 64, 3, 2)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_append_of_plain_rotate_half_heads(lib, H, Hkv, d, B, T, ragged):
+    """The whole head rotated by halves, one position, no norm: a prefill and
+    single tokens as most decoders have them."""
+    test_append(lib, H, Hkv, d, d, B, T, 1, None, False, False, ragged)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_plain_rotate_half_rows_are_rounded_as_from_64_bits(lib, d):
+    test_appended_rows_are_rounded_as_from_64_bits(lib, d, False, False)
