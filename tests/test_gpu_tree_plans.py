@@ -205,3 +205,19 @@ def test_hidden_infinities_in_paired_streams(lib, name, bad):
         assert torch.equal(odd[b, :n][..., ~dims], out[b, :n][..., ~dims])
         if at >= n:
             assert torch.equal(odd[b, :n], out[b, :n])
+
+
+@pytest.mark.parametrize("name", ["draft_ragged", "draft_d64", "question_d64", "by_cta_ragged", "by_cta_paired"])
+def test_tokens_that_are_not_there_in_every_tile(lib, name):
+    """Each 128 entries of the lists have their own indices outside the
+    visual tokens, tile after tile: none counts, every other one does."""
+    from visual_token_sparsity_gb300 import binding as sv
+    w = Work(*CASES[name], seed=9)
+    g = np.random.default_rng(4)
+    w.vis[g.random(w.vis.shape) < 0.03] = -1
+    for g in range(5):
+        w.vis[:, :, g::1024] = -1
+    w.count_tokens()
+    out, lse, status = w.run()
+    assert status == sv.SV_DEV_BAD_INDEX
+    w.check_counts(out, lse, name)

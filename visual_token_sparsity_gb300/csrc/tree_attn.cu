@@ -89,6 +89,7 @@ struct Smem {
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full, done, turn[2];
+  uint64_t valid_full[kValidRing];
   uint32_t tmem;
   int abort;
   int odd_values;                 // some drafted V held an infinity or NaN
@@ -310,6 +311,7 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       sh.abort = 0;
       sh.odd_values = 0;
     }
+    if (lane < kValidRing) ptx::mbar_init(&sh.valid_full[lane], kLoadWarps);
     ptx::mbar_fence_init();
   }
   grid_dep_sync();                                    // (nothing before it touches global memory)
@@ -485,7 +487,12 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       load_page(A);
       load_index(B);
       there = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) sh.valid[tile % kValidRing][warp - kLoadWarp] = there;
+      // (a barrier of their own: the one that the copies arrive at orders no
+      // ordinary store)
+      if (lane == 0) {
+        sh.valid[tile % kValidRing][warp - kLoadWarp] = there;
+        ptx::mbar_arrive(&sh.valid_full[tile % kValidRing]);
+      }
       copy(k_pool, ring_k(tile), rid, there);
       if (tile > 0) copy(v_pool, ring_v(tile - 1), last_rid, last_there);
     }
@@ -655,15 +662,21 @@ tree_attn_kernel(const __grid_constant__ TreeArgs a) {
       float m = -INFINITY, l = 0.f;
       for (int j = s; j < steps; j += 2, ++ns) {
         const int i = split ? j : j >> 1;
+        uint32_t see[4];
+        if (active) {
+          // (written before the tile's copies began, and rewritten only when
+          // its slots have long been given back)
+          const uint32_t v = (tile0 + i) % kValidRing;
+          wait_bar(&sh.valid_full[v], ((tile0 + i) / kValidRing) & 1, sh);
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(see[0]), "=r"(see[1]), "=r"(see[2]), "=r"(see[3])
+                       : "r"(smem_u32(sh.valid[v]))
+                       : "memory");
+        }
         wait_bar(&sh.s_full[s], ns & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
         if (active) {
-          uint32_t see[4];
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(see[0]), "=r"(see[1]), "=r"(see[2]), "=r"(see[3])
-                       : "r"(smem_u32(sh.valid[(tile0 + i) % kValidRing]))
-                       : "memory");
           const int base = (x.t0 + i) * kTile;
           if (base + kTile > ctx) {
 #pragma unroll
