@@ -454,7 +454,7 @@ sv_status sv_decode_append_attn(const void* q, int H, float scale, const sv_kv_l
  * q_weight, k_weight : bf16 [head dim], 16-byte aligned, or NULL: no norm.
  * In this and the following calls a call without tokens (B, N or T 0) does
  * nothing, and the tensors that hold a row per token (pos among them) may
- * then be NULL.
+ * then be NULL.  A sequence has at most 2^30 tokens, the new ones included.
  */
 typedef struct {
   const float* cos_sin;

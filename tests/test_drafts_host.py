@@ -274,3 +274,22 @@ def test_the_plan_cases_take_the_plans_they_name(lib):
         ctas = min(152, rt * (tiles // 2))
         size = up(ctas * 16, 256) * 256 + up(ctas * 2 * qt * 8, 256) * 256 + ctas * 2 * qt * d * 4
         assert lib.sv_tree_attn_workspace_bytes(B, T, H, Hkv, d, n) == 256 + 4 * 4096 + up(size, 256) * 256, name
+
+
+def test_positions_stay_within_32_bits(lib):
+    """A block table may have room for more positions than int32 counts; the
+    calls whose kernels count them in 32 bits refuse such lengths."""
+    from visual_token_sparsity_gb300 import binding as sv
+    L = ctypes.byref(layer())
+    for n_vis, n_text in ((2 ** 31 - 9, 4), (2 ** 30 - 4, 0), (2 ** 30, 2 ** 30)):
+        S = seqs(n_vis, n_text, batch=1, per=2 ** 29)
+        s = ctypes.byref(S)
+        tree = lambda T: lib.sv_tree_attn(P(0x1000000), T, 4, 0.1, L, s, None, 0, None, None, P(0x2000000), None,
+                                          P(0x3000000), 1 << 40, None)
+        append = lambda T: lib.sv_qk_norm_rope_append(P(0x1000000), 256, P(0x2000000), 128, P(0x3000000), 128, T, 4,
+                                                      ctypes.byref(rot()), L, s, None, P(0x4000000), P(), 256, None)
+        accept = lambda T: lib.sv_kv_accept(L, 1, s, T, P(), 1, None, P(), 256, None)
+        pool = sv.sv_page_pool(P(), P(), 100)
+        reserve = lambda T: lib.sv_pages_reserve(ctypes.byref(pool), None, 0, s, T, None, P(), 1 << 40, None)
+        assert tree(5) == append(5) == accept(5) == reserve(5) == UNSUPPORTED, (n_vis, n_text)
+        assert b"2^30" in lib.sv_last_error()

@@ -184,10 +184,13 @@ void fill_rotation(sv::NormRopeArgs& a, const sv_rotation* r) {
   }
 }
 
-// T more tokens behind n_vis + n_text fit the block table
+// T more tokens behind n_vis + n_text fit the block table, and their positions
+// (rounded up to tiles) 32 bits
 sv_status check_new_tokens(const sv_seq_batch* S, int T) {
-  if ((long long)S->n_vis + S->n_text + T > (long long)S->max_blocks * SV_BLOCK_TOKENS)
+  const long long end = (long long)S->n_vis + S->n_text + T;
+  if (end > (long long)S->max_blocks * SV_BLOCK_TOKENS)
     return fail(SV_ERR_INVALID_ARG, "%d new tokens overflow the block table", T);
+  if (end > (1 << 30)) return fail(SV_ERR_UNSUPPORTED, "%lld tokens of a sequence: more than 2^30", end);
   return SV_OK;
 }
 
