@@ -536,7 +536,10 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
  * lse       : optional out fp32 [B][T][H].  A row that sees no token at all
  *             has out 0 and lse -inf.
  * A drafted token that a row does not see has no part in it, whatever its K
- * and V hold (infinities and NaN included).
+ * and V hold (infinities and NaN included).  Finite values of V beyond 2^70 in
+ * magnitude may overflow (the running sums carry weights of up to 2^32).
+ * The weights are rounded to bf16 for the product with V, as by
+ * sv_sparse_decode_attn from three query heads per KV head on.
  * ws        : sv_tree_attn_workspace_bytes(B, T, H, n_kv_heads, d, n_tokens),
  *             n_tokens = k + n_text + T (k = n_vis when vis_idx is NULL).
  *             The size never shrinks as B, T or n_tokens grow: sized for the

@@ -181,7 +181,8 @@ def _one_device(*tensors):
 # ------------------------------------------------------------------ descriptors
 
 class KvLayer:
-    """One layer's paged cache: bf16 pools [num_blocks][Hkv][16][d]."""
+    """One layer's paged cache: bf16 pools [num_blocks][Hkv][16][d], both on one
+    device (ValueError otherwise, as for the descriptors below)."""
 
     def __init__(self, k_pool, v_pool):
         assert k_pool.shape == v_pool.shape and k_pool.shape[2] == BLOCK_TOKENS

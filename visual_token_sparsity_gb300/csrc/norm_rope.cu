@@ -7,16 +7,19 @@
 // Pair p turns by cos_sin[pos[axis(p)]][p]: one position per token, or up to
 // three (time, row, column) that own consecutive sections of the pairs.
 // Everything is fp32 between the bf16 load and the one rounding at the end.
-// Rows on their way into the cache are rounded as the 64-bit result would be,
-// by way of fp32: a query element that falls on the other side of a bf16
-// rounding boundary moves its row's log-sum-exp by some 1e-4, so results next to
-// a boundary are formed again with twice the bits (the step's lse is then
-// within 2e-7 of 64 bits, relative; with fp32 alone up to 9e-6).
+// Rows on their way into the cache are rounded more closely: a query element
+// that falls on the other side of a bf16 rounding boundary moves its row's
+// log-sum-exp by some 1e-4, so results next to a boundary are formed again with
+// twice the bits (the step's lse is then within 2e-7 of 64 bits, relative; with
+// fp32 alone up to 9e-6).  "Next to" is measured in last bits of the result: a
+// pair's larger member is then rounded as the 64-bit result, a smaller one
+// whose fp32 error is many of its own last bits may still fall on the other side.
 //
 // Bound by memory: every row is read once and written once, a dozen
 // operations per element.  16384 tokens of 16 + 16 heads, d 80: 28 us, 6.0 TB/s; a
-// prefill of 8770 tokens of 36 heads with a norm 40 us, 4.5 TB/s, bound by
-// instructions (34 us without the second forming of results in doubt).  A row is d / 8 lanes of 8 elements, 32 / (d / 8)
+// prefill of 9808 tokens of 36 heads with a norm 40 us, 4.5 TB/s, where issue
+// slots are 60 % used and half of the warps resident: chains of shuffles, root
+// and turns per row (34 us without the second forming of results in doubt).  A row is d / 8 lanes of 8 elements, 32 / (d / 8)
 // rows side by side in a warp; a lane's elements are the two halves of four
 // pairs (rotate-half: 4 at 4j and 4 at rot/2 + 4j; interleaved or not
 // rotated: 8 in a row), so no pair crosses lanes and the four (cos, sin) it

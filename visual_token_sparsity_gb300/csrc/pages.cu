@@ -9,7 +9,7 @@
 // few hundred KB and bound by latency: one launch each, one CTA where the
 // order of the pages matters.  The row and page copies run over every layer in
 // one launch.  Measured, replayed in a graph: release, fork and reserve of 2
-// branches in a pool of 80 pages 7.8 us for the four kernels, of 32 branches of
+// branches in a pool of 80 pages 9.4 us for the four kernels, of 32 branches of
 // 211 pages each 13 us, with copies of 32 pages in 8 layers (17 MB read and
 // written).  ncu, each alone with cold caches: 5.0, 5.4, 9.4 (plan) and 6.5 us
 // (copies).

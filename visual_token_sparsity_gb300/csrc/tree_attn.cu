@@ -21,11 +21,14 @@
 // its 64 KB take to arrive).  More rows: the streams take 128 rows each of
 // the same token tile, which halves the bytes per product.
 //
-// Work is cut evenly whatever the shapes: for each tile of rows the token
-// tiles of all (sequence, KV head) units form one line, cut into equal pieces,
-// one per CTA column; a unit that lies in several pieces leaves fp32 partials
-// that a second kernel joins in a fixed order.  CTAs of one piece and
-// different row tiles are neighbours, so they meet in L2.
+// Within a tile of rows the work is cut evenly: the token tiles of all
+// (sequence, KV head) units form one line, cut into equal pieces, one per CTA
+// column; a unit that lies in several pieces leaves fp32 partials that a second
+// kernel joins in a fixed order.  CTAs of one piece and different row tiles are
+// neighbours, so they meet in L2.  Every row tile gets the same whole number of
+// columns, so with many row tiles SMs are left over, half of them from 77 on
+// (28 / 4 heads, 50176 + T tokens: T 2770, 76 row tiles of 2 columns, 1.34
+// PFLOP/s; T 2800, 77 of one, 0.69).
 //
 // Warps: 0-7 softmax and epilogue (one row per thread), 8-9 MMA issue (one per
 // stream), 10-13 cache rows: cp.async gathers of 16 bytes into a ring of
@@ -33,9 +36,14 @@
 // page-table and index loads running two tiles ahead, 14-15 query rows.  Rows
 // that are not there (behind the end, a bad page) are zero-filled and masked.
 //
-// Measured (d 128): 16 sequences x 32 heads x 1584 tokens, 16 rows, 77.8 us =
-// 5.4 TB/s of cache rows; 8 x 4 KV heads of up to 12827 tokens, 189 rows, 51 us =
-// 3.1 TB/s; 1351 rows x 4 KV heads x 50392 tokens 132 us = 1.06 PFLOP/s, where a
+// The weights enter the value product as bf16, the type of V that the tensor
+// core asks for, while the sum l takes them unrounded, which lse needs: at most
+// 2^-8 of sum p |v| beside the output's own 2^-8.  (Measured against 64 bits,
+// relative: 2.3e-3, where fp32 weights give 1.7e-3.)
+//
+// Measured (d 128): 16 sequences x 32 heads x 1584 tokens, 16 rows, 78 us =
+// 5.4 TB/s of cache rows; 8 x 4 KV heads of up to 12827 tokens, 189 rows, 51.6 us =
+// 3.1 TB/s; 1351 rows x 4 KV heads x 50392 tokens 133 us = 1.05 PFLOP/s, where a
 // tile takes a CTA 3800 cycles, 2048 of them in the products: each stream's
 // chain of S, weights and O is longer than what the other's hides.
 #include "common.cuh"
@@ -68,7 +76,8 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr size_t kMaxSmem = 232448;         // 227 KB
 // A row's weights are taken relative to a reference that is raised, and O
 // rescaled, only when the maximum outgrows it by 2^32: bf16 and fp32 have the
-// exponents for it, and no rounding depends on it.
+// exponents for it (as long as the values stay below 2^70 in magnitude, and the
+// tokens below 2^25), and no rounding depends on it.
 constexpr float kRescale = 32.f;
 static_assert(kLoadWarps * 32 == kTile, "one loader thread per token");
 
@@ -984,9 +993,11 @@ namespace {
 // read the cache half as often, but a piece of theirs starts and ends with
 // twice the rows.  128 against 256, 8 sequences of 4 KV heads, d 128: 224 rows
 // 23.2 / 26.3 us at 2 such tiles a CTA, 28.3 / 30.5 at 4, 37.7 / 38.2 at 8, 72.3 /
-// 67.7 at 24; 448 rows 32.5 / 35.1 at 4, 41.7 / 42.6 at 8, 59.8 / 57.1 at 16.  As
-// many pieces as leave every SM one CTA, of two token tiles at least (one for
-// each stream; pieces of one measured 2 % faster to 9 % slower).
+// 67.7 at 24; 448 rows 32.5 / 35.1 at 4, 41.7 / 42.6 at 8, 59.8 / 57.1 at 16: at
+// eight the two are within 2 % of one another, and 256 win somewhere between
+// there and 16.  As many pieces of each row tile as SMs divided by the row
+// tiles, rounded down, of two token tiles at least (one for each stream; pieces
+// of one measured 2 % faster to 9 % slower).
 struct Plan {
   int QT, row_tiles, columns;
   bool cut() const { return columns > 1; }
