@@ -544,7 +544,7 @@ sv_status sv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
  *             n_tokens = k + n_text + T (k = n_vis when vis_idx is NULL).
  *             The size never shrinks as B, T or n_tokens grow: sized for the
  *             largest, a workspace serves every smaller call of the same heads.
- * scale     : finite, >= 0.  Supported: d in {64, 128}, G = H / Hkv <= 16.
+ * scale     : >= 0 and finite, times log2(e) too.  Supported: d in {64, 128}, G = H / Hkv <= 16.
  */
 size_t sv_tree_attn_workspace_bytes(int B, int T, int H, int n_kv_heads, int head_dim, int n_tokens);
 sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_layer* layer,

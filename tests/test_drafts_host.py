@@ -293,3 +293,12 @@ def test_positions_stay_within_32_bits(lib):
         reserve = lambda T: lib.sv_pages_reserve(ctypes.byref(pool), None, 0, s, T, None, P(), 1 << 40, None)
         assert tree(5) == append(5) == accept(5) == reserve(5) == UNSUPPORTED, (n_vis, n_text)
         assert b"2^30" in lib.sv_last_error()
+
+
+def test_tree_scale_stays_finite_in_base_two(lib):
+    """The kernel works with scale * log2(e): where that is infinite, products
+    of 0 would be NaN."""
+    call = lambda scale: lib.sv_tree_attn(P(0x1000000), 5, 4, scale, ctypes.byref(layer()), ctypes.byref(seqs()), None, 0,
+                                          None, None, P(0x2000000), None, P(0x3000000), 255, None)
+    assert call(2.3e38) == call(0.0) == call(1e-45) == WORKSPACE          # (nothing before it is wrong)
+    assert call(2.4e38) == call(3.4e38) == call(float("inf")) == INVALID

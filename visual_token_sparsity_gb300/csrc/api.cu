@@ -708,7 +708,8 @@ sv_status sv_tree_attn(const void* q, int T, int H, float scale, const sv_kv_lay
   const int Hkv = layer->n_kv_heads;
   if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
   if (H / Hkv > 16) return fail(SV_ERR_UNSUPPORTED, "query heads per KV head %d > 16", H / Hkv);
-  if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(SV_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (!(scale >= 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+    return fail(SV_ERR_INVALID_ARG, "scale must be >= 0 and finite, times log2(e) too");
   if (T < 0 || T > 65536) return fail(SV_ERR_INVALID_ARG, "need 0 <= T <= 65536 (T = %d)", T);
   if (tree_mask && T > 64) return fail(SV_ERR_UNSUPPORTED, "a tree mask holds at most 64 drafted tokens (T = %d)", T);
   s = check_new_tokens(seqs, T);
