@@ -107,8 +107,9 @@ typedef struct {
  * skipped (its indices read -1, its attention output 0).
  * Accepted by sv_retrieve_topk, sv_retrieve_topk_noalloc,
  * sv_sparse_decode_attn, sv_decode_append_attn, sv_kv_append,
- * sv_qk_norm_rope_append, sv_tree_attn, sv_kv_accept and sv_pages_reserve
- * (sv_pages_fork and sv_pages_release read no lengths); the other calls taking
+ * sv_qk_norm_rope_append, sv_tree_attn, sv_kv_accept, sv_pages_reserve
+ * (sv_pages_fork and sv_pages_release read no lengths), sv_kv8_append,
+ * sv_kv8_retrieve_topk and sv_kv8_decode_attn; the other calls taking
  * a batch return SV_ERR_UNSUPPORTED when any of the arrays is set.
  * Zero-initialise the struct so that the arrays default to NULL.
  */
@@ -636,6 +637,127 @@ sv_status sv_pages_fork(const sv_page_pool* pool, const sv_seq_batch* seqs, cons
 sv_status sv_pages_reserve(const sv_page_pool* pool, const sv_kv_layer* layers, int n_layers,
                            const sv_seq_batch* seqs, int T, const int32_t* n_new, void* ws, size_t ws_bytes,
                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * Causal attention of whole prompts.  (No counterpart on the SparseVILA pages:
+ * their prefill brings its own; lse serves as the lse of
+ * sv_retrieve_topk_softmax.)
+ *
+ *   out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h] . k[j][g]) v[j][g],  g = h / G,
+ *   i and j of one sequence
+ *
+ * q, k, v   : bf16 [N][H][d], [N][Hkv][d] twice, after norm and rotation: the
+ *             packed tokens of all sequences, which lie *_stride elements apart
+ *             (slices of a fused projection are read in place).  Strides:
+ *             multiples of 8, at least a token's row.
+ * seq_start : DEVICE int32 [batch + 1], ascending within [0, N]: sequence b's
+ *             tokens are [seq_start[b], seq_start[b + 1]); it may have none.
+ *             Entries that do not ascend set SV_DEV_BAD_LENGTH, and nothing is
+ *             computed.
+ * out       : out bf16 [N][H][d], apart from q, k and v.
+ * lse       : optional out fp32 [N][H], natural log.
+ * Rows of out and lse that belong to no sequence are left as they were.
+ * A token that a row does not see has no part in it, whatever its K and V hold
+ * (infinities and NaN included).  The weights are rounded to bf16 for the
+ * product with V, as by sv_tree_attn.
+ * scale     : > 0 and finite, times log2(e) too.  Supported: d in {64, 128},
+ *             G = H / Hkv <= 16, N * H < 2^31.
+ * ws        : sv_prompt_attn_workspace_bytes(N, batch, H, Hkv, d).
+ */
+size_t sv_prompt_attn_workspace_bytes(int N, int batch, int H, int n_kv_heads, int head_dim);
+sv_status sv_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, int N, int H, int n_kv_heads, int head_dim, float scale,
+                         const int32_t* seq_start, int batch, void* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
+ * The paged cache in 8 bits.  (No counterpart on the SparseVILA pages, whose
+ * decode is bound by the bytes of the cache: these calls read half of them.)
+ *
+ * k_pool, v_pool : e4m3 [num_blocks][n_kv_heads][16][head_dim] (4 exponent bits,
+ *                  3 mantissa bits, largest value 448, no infinities), 16-byte
+ *                  aligned.
+ * scales         : fp32 [num_blocks][n_kv_heads][2], 8-byte aligned: the factor
+ *                  of the page's keys and of its values.  A row's value is its
+ *                  e4m3 value times the factor.
+ * Pages, block table and logical positions are those of sv_kv_layer.  The page
+ * calls (sv_pages_*) serve this cache with n_layers 0; sv_pages_reserve then
+ * makes no private copies, so a page that is shared must be full (fork at
+ * multiples of 16 tokens).  A tail of the text is evicted by lowering n_text.
+ */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* scales;
+  int32_t num_blocks;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} sv_kv8_layer;
+
+/*
+ * New tokens into the 8-bit cache: queries and keys are normalised and rotated
+ * as by sv_qk_norm_rope_append (results rounded to bf16 from more than fp32),
+ * keys and values then rounded to e4m3.
+ *
+ * q, k, v   : bf16 [N][H][d], [N][Hkv][d] twice, packed, with token strides as
+ *             above.
+ * rot       : as for sv_qk_norm_rope_append, pos: DEVICE int32 [n_axes][N].
+ * seq_start : DEVICE int32 [batch + 1], ascending within [0, N]: tokens
+ *             [seq_start[b], seq_start[b + 1]) go to positions n_vis + n_text + i
+ *             (n_vis_seq[b] + n_text_seq[b] + i) of sequence b; the caller then
+ *             adds their number to n_text.  NULL: N / batch tokens each.
+ * q_out     : out bf16 [N][H][d]; q itself (with q_stride == H * d) or apart
+ *             from the inputs.
+ * k_out     : optional out bf16 [N][Hkv][d]: the keys before they are rounded to
+ *             8 bits, e.g. for sv_prompt_attn; k itself (with k_stride ==
+ *             Hkv * d) or apart from the inputs.
+ * The factor of a page, KV head and pool: the smallest power of two, at least
+ * 2^-126, with |x| <= 448 * factor for every finite x of the rows that the call
+ * brings; where the page holds earlier rows (slots before the first new one) it
+ * is at least its old factor, and when it grows those rows are rounded again.
+ * Infinities become the largest value of their sign, NaN stays.  The outcome
+ * does not depend on the order in which the GPU runs.
+ * A sequence whose entries of seq_start do not ascend within [0, N], whose
+ * lengths are out of range or whose tokens overflow the block table sets
+ * SV_DEV_BAD_LENGTH and nothing of it enters the cache (where the entries of
+ * seq_start do not ascend, sequences behind it may be skipped too).  A page
+ * outside the pool sets SV_DEV_BAD_BLOCK and its tokens are not cached; in both
+ * cases q_out and k_out of tokens that lie in a sequence may still be written.
+ * A position outside the table sets SV_DEV_BAD_POSITION and that token's
+ * outputs and cache rows are left as they were.
+ * Pages that are written must not be shared.  d: 64 or 128.
+ * ws        : sv_evict_workspace_bytes().
+ */
+sv_status sv_kv8_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int N, int H, const sv_rotation* rot, const sv_kv8_layer* layer,
+                        const sv_seq_batch* seqs, const int32_t* seq_start, void* q_out, void* k_out, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * sv_retrieve_topk from the 8-bit cache (the scores are of the keys' values).
+ * The selection is that of the scores in 64 bits: tokens whose fp32 scores are
+ * too near to the k-th one to tell are scored again.  Exact ties go to the lower
+ * index.  scores (optional out) are the fp32 ones.  With scores that are not
+ * finite the choice is unspecified (but valid).
+ * ws : sv_kv8_retrieve_workspace_bytes(B, H, n_kv_heads, head_dim, n_vis, k);
+ *      sized for the largest B and n_vis it serves every smaller call.
+ */
+size_t sv_kv8_retrieve_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n_vis, int k);
+sv_status sv_kv8_retrieve_topk(const void* q, int R, int H, const sv_kv8_layer* layer, const sv_seq_batch* seqs,
+                               int k, int32_t* vis_idx, float* scores, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sv_sparse_decode_attn over the 8-bit cache; arguments, per-sequence lengths
+ * and skipped loads as there.  A row that attends to no token has out 0 and
+ * lse -inf.  out: 16-byte aligned, apart from q.
+ * ws : sv_kv8_attn_workspace_bytes(B, H, n_kv_heads, head_dim, n_tokens),
+ *      n_tokens = k + n_text (k = n_vis when vis_idx is NULL); the size never
+ *      shrinks as B or n_tokens grow.
+ */
+size_t sv_kv8_attn_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n_tokens);
+sv_status sv_kv8_decode_attn(const void* q, int H, float scale, const sv_kv8_layer* layer,
+                             const sv_seq_batch* seqs, const int32_t* vis_idx, int k, void* out, float* lse,
+                             void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Read (and optionally clear) the device status word of a workspace.

@@ -46,3 +46,12 @@ from .drafts import (  # noqa: F401
     tree_attention,
     tree_sees,
 )
+from .kv8 import (  # noqa: F401
+    E4M3,
+    attend,
+    kv8_append,
+    kv8_rows,
+    page_scale,
+    prompt_attention,
+    to_e4m3,
+)

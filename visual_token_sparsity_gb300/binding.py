@@ -56,6 +56,11 @@ class sv_page_pool(ctypes.Structure):
     _fields_ = [("ref", ctypes.c_void_p), ("n_pages", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
 
 
+class sv_kv8_layer(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 # (module constants and fields of their own: the calls of a decode step look them
 # up a dozen times each)
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -112,6 +117,16 @@ _SIGS = {
                            _VP]),
     "sv_pages_reserve": (_I, [ctypes.POINTER(sv_page_pool), ctypes.POINTER(sv_kv_layer), _I,
                               ctypes.POINTER(sv_seq_batch), _I, _VP, _VP, _SZ, _VP]),
+    "sv_prompt_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "sv_prompt_attn": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _I, _I, _I, _I, _F, _VP, _I, _VP, _VP, _VP, _SZ, _VP]),
+    "sv_kv8_append": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _I, _I, ctypes.POINTER(sv_rotation),
+                           ctypes.POINTER(sv_kv8_layer), ctypes.POINTER(sv_seq_batch), _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "sv_kv8_retrieve_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "sv_kv8_retrieve_topk": (_I, [_VP, _I, _I, ctypes.POINTER(sv_kv8_layer), ctypes.POINTER(sv_seq_batch), _I, _VP,
+                                  _VP, _VP, _SZ, _VP]),
+    "sv_kv8_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "sv_kv8_decode_attn": (_I, [_VP, _I, _F, ctypes.POINTER(sv_kv8_layer), ctypes.POINTER(sv_seq_batch), _VP, _I, _VP,
+                                _VP, _VP, _SZ, _VP]),
     "sv_read_device_status": (_I, [_VP, _I, ctypes.POINTER(ctypes.c_int32), _VP]),
 }
 EXPORTED = tuple(_SIGS)
@@ -193,6 +208,26 @@ class KvLayer:
         self.device = _one_device(k_pool, v_pool)
 
 
+class Kv8Layer:
+    """One layer's cache in 8 bits: e4m3 pools [num_blocks][Hkv][16][d] (torch.float8_e4m3fn, or its
+    bytes as torch.uint8) and fp32 scales [num_blocks][Hkv][2], of keys and of values."""
+
+    def __init__(self, k_pool, v_pool, scales):
+        if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.shape[2] != BLOCK_TOKENS:
+            raise ValueError(f"pools must be [num_blocks][Hkv][{BLOCK_TOKENS}][d], got {tuple(k_pool.shape)}, "
+                             f"{tuple(v_pool.shape)}")
+        for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+            if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise ValueError(f"{name} must be torch.float8_e4m3fn or torch.uint8, got {t.dtype}")
+        if scales.shape != (k_pool.shape[0], k_pool.shape[1], 2):
+            raise ValueError(f"scales must be [num_blocks][Hkv][2], got {tuple(scales.shape)}")
+        self.k_pool, self.v_pool, self.scales = k_pool, v_pool, scales
+        self.c = sv_kv8_layer(_ptr(k_pool, None, "k_pool"), _ptr(v_pool, None, "v_pool"),
+                              _ptr(scales, torch.float32, "scales"), k_pool.shape[0], k_pool.shape[1], k_pool.shape[3])
+        self.by_ref, self.n_kv_heads, self.head_dim = ctypes.byref(self.c), k_pool.shape[1], k_pool.shape[3]
+        self.device = _one_device(k_pool, v_pool, scales)
+
+
 class SeqBatch:
     """Block table (int32 [batch][max_blocks]) plus lengths: uniform n_vis /
     n_text, or -- with the optional int32 [batch] device tensors n_vis_seq,
@@ -269,6 +304,15 @@ class Rotation:
         """The call's tokens and head dim are the descriptor's."""
         if self.tokens is not None and self.tokens != (B, T):
             raise ValueError(f"pos is for {self.tokens} tokens, the call has {(B, T)}")
+        self._check_weights(d)
+
+    def check_packed(self, N, d):
+        """The same for N packed tokens: pos [1][N], or [B][T] with B * T = N."""
+        if self.tokens is not None and self.tokens[0] * self.tokens[1] != N:
+            raise ValueError(f"pos is for {self.tokens} tokens, the call has {N}")
+        self._check_weights(d)
+
+    def _check_weights(self, d):
         for w, name in ((self.q_weight, "q_weight"), (self.k_weight, "k_weight")):
             if w is not None and w.shape[0] != d:
                 raise ValueError(f"{name} has {w.shape[0]} elements, head_dim is {d}")
@@ -337,6 +381,20 @@ class _Call:
         if (sd != 1 and d > 1) or (sh != d and h > 1) or (B > 1 and T > 1 and sb != T * st):
             raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, strides {t.stride()}")
         return t.data_ptr(), st if T > 1 else sb if B > 1 else h * d
+
+
+    def packed(self, t, heads, d, name):
+        """Pointer and token stride of bf16 [N][heads][d] rows that lie evenly apart."""
+        if t.dtype != _BF16:
+            raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+            raise ValueError(f"{name} must have shape (N, {heads}, {d}), got {tuple(t.shape)}")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{self.dev}, is on {t.device}")
+        st, sh, sd = t.stride()
+        if t.numel() and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
+            raise ValueError(f"{name}: heads must be contiguous, strides {t.stride()}")
+        return t.data_ptr(), st if t.shape[0] > 1 else heads * d
 
 
 # ------------------------------------------------------------------ sizes
@@ -622,6 +680,78 @@ def sv_pages_reserve(pool, layers, seqs, T, ws, n_new=None, stream=None):
     c = _pages(pool, seqs, ws, stream, *layers)
     _check(lib.sv_pages_reserve(pool.by_ref, _layer_array(layers), len(layers), seqs.by_ref, T,
                                 c.ptr(n_new, _I32, (seqs.batch,), "n_new"), *c.ws, c.stream))
+
+
+def sv_prompt_attn_workspace_bytes(N, batch, H, n_kv_heads, head_dim):
+    return load().sv_prompt_attn_workspace_bytes(N, batch, H, n_kv_heads, head_dim)
+
+
+def sv_prompt_attn(q, k, v, seq_start, scale, out, lse, ws, stream=None):
+    """Causal attention of packed prompts: q bf16 [N][H][d], k, v bf16 [N][Hkv][d] (tokens may be strided: slices of
+    a fused projection), seq_start int32 [B + 1] ascending; out bf16 [N][H][d] and lse fp32 [N][H] or None (written)."""
+    lib = load()
+    N, H, d = q.shape
+    Hkv, B = k.shape[1], seq_start.shape[0] - 1
+    if k.shape[0] != N or v.shape != k.shape:
+        raise ValueError(f"k and v must have {N} tokens and one shape, got {tuple(k.shape)}, {tuple(v.shape)}")
+    if B < 0:
+        raise ValueError("seq_start must have batch + 1 entries")
+    c = _Call(ws, stream)
+    _check(lib.sv_prompt_attn(*c.packed(q, H, d, "q"), *c.packed(k, Hkv, d, "k"), *c.packed(v, Hkv, d, "v"), N, H, Hkv,
+                              d, scale, c.ptr(seq_start, _I32, (B + 1,), "seq_start"), B,
+                              c.ptr(out, _BF16, (N, H, d), "out"), c.ptr(lse, _F32, (N, H), "lse"), *c.ws, c.stream))
+
+
+def sv_kv8_append(q, k, v, rot, layer, seqs, q_out, ws, seq_start=None, k_out=None, stream=None):
+    """Packed new tokens into the 8-bit cache: q bf16 [N][H][d], k, v bf16 [N][Hkv][d] (tokens may be strided); q
+    normalised and rotated -> q_out [N][H][d]; k likewise -> k_out [N][Hkv][d] (or None) and, with v, rounded to e4m3
+    -> the cache at n_vis + n_text + i.  seq_start int32 [B + 1]: tokens [seq_start[b], seq_start[b + 1]) are sequence
+    b's; None: N / B each.  n_text unchanged (the caller adds the new tokens)."""
+    lib = load()
+    N, H, d = q.shape
+    Hkv = layer.n_kv_heads
+    if k.shape[0] != N or v.shape[0] != N:
+        raise ValueError(f"k and v must have {N} tokens, got {k.shape[0]}, {v.shape[0]}")
+    c = _Call(ws, stream, rot, layer, seqs)
+    rot.check_packed(N, d)
+    _check(lib.sv_kv8_append(*c.packed(q, H, layer.head_dim, "q"), *c.packed(k, Hkv, d, "k"),
+                             *c.packed(v, Hkv, d, "v"), N, H, rot.by_ref, layer.by_ref, seqs.by_ref,
+                             c.ptr(seq_start, _I32, (seqs.batch + 1,), "seq_start"),
+                             c.ptr(q_out, _BF16, q.shape, "q_out"), c.ptr(k_out, _BF16, (N, Hkv, d), "k_out"), *c.ws,
+                             c.stream))
+
+
+def sv_kv8_retrieve_workspace_bytes(B, H, n_kv_heads, head_dim, n_vis, k):
+    return load().sv_kv8_retrieve_workspace_bytes(B, H, n_kv_heads, head_dim, n_vis, k)
+
+
+def sv_kv8_retrieve_topk(q, layer, seqs, k, vis_idx, scores, ws, stream=None):
+    """sv_retrieve_topk from the 8-bit cache: q bf16 [B][R][H][d]; vis_idx int32 [B][Hkv][k] (the selection of the
+    exact scores); scores fp32 [B][Hkv][n_vis] or None."""
+    lib = load()
+    B, R, H, d = q.shape
+    c = _Call(ws, stream, layer, seqs)
+    _check(lib.sv_kv8_retrieve_topk(c.ptr(q, _BF16, (seqs.batch, R, H, layer.head_dim), "q"), R, H, layer.by_ref,
+                                    seqs.by_ref, k, c.ptr(vis_idx, _I32, (B, layer.n_kv_heads, k), "vis_idx"),
+                                    c.ptr(scores, _F32, (B, layer.n_kv_heads, seqs.n_vis), "scores"), *c.ws, c.stream))
+
+
+def sv_kv8_attn_workspace_bytes(B, H, n_kv_heads, head_dim, n_tokens):
+    return load().sv_kv8_attn_workspace_bytes(B, H, n_kv_heads, head_dim, n_tokens)
+
+
+def sv_kv8_decode_attn(q, scale, layer, seqs, vis_idx, k, out, lse, ws, stream=None):
+    """sv_sparse_decode_attn over the 8-bit cache: q, out bf16 [B][H][d]; vis_idx int32 [B][Hkv][k] or None (all
+    visual tokens); lse fp32 [B][H] or None."""
+    lib = load()
+    B, H, d = q.shape
+    c = _Call(ws, stream, layer, seqs)
+    vis = c.ptr(vis_idx, _I32, (B, layer.n_kv_heads, k), "vis_idx")
+    if vis_idx is not None and k == 0:
+        vis = c.ws[0]            # an empty list, not "all visual tokens": any address, nothing is read
+    _check(lib.sv_kv8_decode_attn(c.ptr(q, _BF16, (seqs.batch, H, layer.head_dim), "q"), H, scale, layer.by_ref,
+                                  seqs.by_ref, vis, k, c.ptr(out, _BF16, (B, H, d), "out"),
+                                  c.ptr(lse, _F32, (B, H), "lse"), *c.ws, c.stream))
 
 
 def sv_read_device_status(ws, clear=False, stream=None):

@@ -171,7 +171,8 @@ sv_status check_rotation(const sv_rotation* r, int d, long long n_tok) {
   return SV_OK;
 }
 
-void fill_rotation(sv::NormRopeArgs& a, const sv_rotation* r) {
+template <typename Args>
+void fill_rotation(Args& a, const sv_rotation* r) {
   a.q_weight = static_cast<const uint16_t*>(r->q_weight);
   a.k_weight = static_cast<const uint16_t*>(r->k_weight);
   a.eps = r->eps;
@@ -234,6 +235,16 @@ sv_status check_pages(const sv_page_pool* pool, const sv_seq_batch* seqs, void* 
   a.max_blocks = seqs->max_blocks;
   a.status = status_word(ws);
   return check_ws(ws, ws_bytes, sv_pages_workspace_bytes(seqs->batch, seqs->max_blocks, pool->num_blocks));
+}
+
+// ---- checks of the 8-bit cache
+
+sv_status check_cache8(const sv_kv8_layer* L, const sv_seq_batch* S, bool need_v) {
+  if (!L || !S) return fail(SV_ERR_INVALID_ARG, "layer or batch descriptor is NULL");
+  if (!L->scales || reinterpret_cast<uintptr_t>(L->scales) % 8)
+    return fail(SV_ERR_INVALID_ARG, "scales must be non-NULL and 8-byte aligned");
+  const sv_kv_layer as = {L->k_pool, L->v_pool, L->num_blocks, L->n_kv_heads, L->head_dim};
+  return sv::check_cache(&as, S, need_v);
 }
 
 }  // namespace
@@ -814,6 +825,172 @@ sv_status sv_pages_reserve(const sv_page_pool* pool, const sv_kv_layer* layers, 
                                               count, page_bytes, data_of(ws), num_sms(),
                                               static_cast<cudaStream_t>(stream)),
                      "sv_pages_reserve");
+}
+
+// ------------------------------------------------------------------ prompts and the 8-bit cache
+
+size_t sv_prompt_attn_workspace_bytes(int N, int batch, int H, int n_kv_heads, int head_dim) {
+  (void)N; (void)batch; (void)H; (void)n_kv_heads; (void)head_dim;
+  return kHeadBytes;
+}
+
+sv_status sv_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, int N, int H, int n_kv_heads, int head_dim, float scale,
+                         const int32_t* seq_start, int batch, void* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream) {
+  if (N < 0 || batch < 0) return fail(SV_ERR_INVALID_ARG, "need N >= 0 and batch >= 0");
+  if (H <= 0 || n_kv_heads <= 0 || H % n_kv_heads)
+    return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
+  if (H / n_kv_heads > 16) return fail(SV_ERR_UNSUPPORTED, "query heads per KV head %d > 16", H / n_kv_heads);
+  if (head_dim != 64 && head_dim != 128) return fail(SV_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", head_dim);
+  if ((long long)N * H > 0x7fffffffLL) return fail(SV_ERR_UNSUPPORTED, "N * H = %lld: 2^31 or more", (long long)N * H);
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+    return fail(SV_ERR_INVALID_ARG, "scale must be > 0 and finite, times log2(e) too");
+  if (N > 0 && batch > 0 && (!q || !k || !v || !out || !seq_start))
+    return fail(SV_ERR_INVALID_ARG, "q, k, v, seq_start and out must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(seq_start) % 4) return fail(SV_ERR_INVALID_ARG, "seq_start must be 4-byte aligned");
+  const long long qr = (long long)H * head_dim, kv = (long long)n_kv_heads * head_dim;
+  sv_status s = check_rows("q", q, q_stride, qr);
+  if (s == SV_OK) s = check_rows("k", k, k_stride, kv);
+  if (s == SV_OK) s = check_rows("v", v, v_stride, kv);
+  if (s == SV_OK) s = check_ws(ws, ws_bytes, sv_prompt_attn_workspace_bytes(N, batch, H, n_kv_heads, head_dim));
+  if (s != SV_OK) return s;
+  if (!aligned16(out)) return fail(SV_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (N == 0 || batch == 0) return SV_OK;
+  const size_t ob = (size_t)N * qr * 2;
+  if (overlap(out, ob, q, row_extent(N, q_stride, qr)) || overlap(out, ob, k, row_extent(N, k_stride, kv)) ||
+      overlap(out, ob, v, row_extent(N, v_stride, kv)))
+    return fail(SV_ERR_INVALID_ARG, "out must not overlap q, k and v");
+  sv::PromptArgs a = {};
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.N = N; a.H = H; a.Hkv = n_kv_heads; a.batch = batch;
+  a.seq_start = seq_start;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out; a.lse = lse;
+  a.counters = counters_of(ws); a.status = status_word(ws);
+  return cuda_status(sv::launch_prompt_attn(a, head_dim, static_cast<cudaStream_t>(stream)), "sv_prompt_attn");
+}
+
+sv_status sv_kv8_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int N, int H, const sv_rotation* rot, const sv_kv8_layer* layer,
+                        const sv_seq_batch* seqs, const int32_t* seq_start, void* q_out, void* k_out, void* ws,
+                        size_t ws_bytes, void* stream) {
+  sv_status s = check_cache8(layer, seqs, true);
+  if (s != SV_OK) return s;
+  const int Hkv = layer->n_kv_heads, d = layer->head_dim, B = seqs->batch;
+  if (N < 0) return fail(SV_ERR_INVALID_ARG, "N must be >= 0");
+  const bool some = N > 0 && B > 0;
+  if (some && (!q || !k || !v || !q_out)) return fail(SV_ERR_INVALID_ARG, "q, k, v and q_out must be non-NULL");
+  if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
+  if (reinterpret_cast<uintptr_t>(seq_start) % 4) return fail(SV_ERR_INVALID_ARG, "seq_start must be 4-byte aligned");
+  if (!seq_start && B > 0 && N % B)
+    return fail(SV_ERR_INVALID_ARG, "N = %d is no multiple of the batch %d (and there is no seq_start)", N, B);
+  s = check_new_tokens(seqs, !seq_start && B > 0 ? N / B : 0);
+  const long long qr = (long long)H * d, kv = (long long)Hkv * d;
+  if (s == SV_OK) s = check_rows("q", q, q_stride, qr);
+  if (s == SV_OK) s = check_rows("k", k, k_stride, kv);
+  if (s == SV_OK) s = check_rows("v", v, v_stride, kv);
+  if (s == SV_OK) s = check_rotation(rot, d, N);
+  if (s == SV_OK) s = check_ws(ws, ws_bytes, sv_evict_workspace_bytes());
+  if (s != SV_OK) return s;
+  if (!aligned16(q_out) || !aligned16(k_out))
+    return fail(SV_ERR_INVALID_ARG, "q_out and k_out must be 16-byte aligned");
+  if ((long long)N * H + (N / 16 + 2ll * B) * 2 * Hkv > 0x7fffffffLL)
+    return fail(SV_ERR_UNSUPPORTED, "N * H and the touched pages: 2^31 rows or more");
+  if (!some) return SV_OK;
+  const size_t qb = (size_t)N * qr * 2, kb = (size_t)N * kv * 2;
+  const size_t qe = row_extent(N, q_stride, qr), ke = row_extent(N, k_stride, kv), ve = row_extent(N, v_stride, kv);
+  const bool q_in_place = q_out == q && q_stride == qr, k_in_place = k_out != nullptr && k_out == k && k_stride == kv;
+  if ((!q_in_place && overlap(q_out, qb, q, qe)) || overlap(q_out, qb, k, ke) || overlap(q_out, qb, v, ve))
+    return fail(SV_ERR_INVALID_ARG, "q_out must be q itself or not overlap q, k and v");
+  if (k_out && ((!k_in_place && overlap(k_out, kb, k, ke)) || overlap(k_out, kb, q, qe) || overlap(k_out, kb, v, ve) ||
+                overlap(k_out, kb, q_out, qb)))
+    return fail(SV_ERR_INVALID_ARG, "k_out must be k itself or not overlap q, k, v and q_out");
+  sv::Kv8AppendArgs a = {};
+  fill_rotation(a, rot);
+  a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k); a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.N = N; a.H = H; a.Hkv = Hkv;
+  a.seq_start = seq_start; a.per_seq = N / B;
+  a.q_out = static_cast<uint16_t*>(q_out); a.k_out = static_cast<uint16_t*>(k_out);
+  a.k_pool = static_cast<uint8_t*>(layer->k_pool); a.v_pool = static_cast<uint8_t*>(layer->v_pool);
+  a.scales = layer->scales;
+  a.block_table = seqs->block_table; a.num_blocks = layer->num_blocks; a.max_blocks = seqs->max_blocks;
+  a.batch = B; a.n_vis = seqs->n_vis; a.n_text = seqs->n_text; a.lens = lens_of(seqs);
+  a.status = status_word(ws);
+  return cuda_status(sv::launch_kv8_append(a, d, num_sms(), static_cast<cudaStream_t>(stream)), "sv_kv8_append");
+}
+
+size_t sv_kv8_retrieve_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n_vis, int k) {
+  (void)H; (void)k;
+  if (B < 0 || n_kv_heads <= 0 || head_dim <= 0 || n_vis < 0) return kStatusBytes;
+  return kHeadBytes + sv::kv8_retrieve_workspace_bytes(B, n_kv_heads, head_dim, n_vis);
+}
+
+sv_status sv_kv8_retrieve_topk(const void* q, int R, int H, const sv_kv8_layer* layer, const sv_seq_batch* seqs,
+                               int k, int32_t* vis_idx, float* scores, void* ws, size_t ws_bytes, void* stream) {
+  sv_status s = check_cache8(layer, seqs, false);
+  if (s != SV_OK) return s;
+  const sv_kv_layer as = {layer->k_pool, nullptr, layer->num_blocks, layer->n_kv_heads, layer->head_dim};
+  s = sv::check_retrieve_args(q, R, H, &as, seqs, k, vis_idx);
+  if (s != SV_OK) return s;
+  s = check_ws(ws, ws_bytes, sv_kv8_retrieve_workspace_bytes(seqs->batch, H, layer->n_kv_heads, layer->head_dim,
+                                                             seqs->n_vis, k));
+  if (s != SV_OK) return s;
+  if (seqs->batch == 0) return SV_OK;
+  sv::Kv8RetrieveArgs a = {};
+  a.q = q; a.R = R; a.H = H;
+  a.k_pool = static_cast<const uint8_t*>(layer->k_pool); a.scales = layer->scales;
+  a.num_blocks = layer->num_blocks; a.Hkv = layer->n_kv_heads;
+  a.block_table = seqs->block_table; a.max_blocks = seqs->max_blocks;
+  a.n_vis = seqs->n_vis; a.n_text = seqs->n_text; a.k = k; a.batch = seqs->batch; a.lens = lens_of(seqs);
+  a.vis_idx = vis_idx; a.scores = scores;
+  a.ws = data_of(ws); a.status = status_word(ws);
+  return cuda_status(sv::launch_kv8_retrieve(a, layer->head_dim, num_sms(), static_cast<cudaStream_t>(stream)),
+                     "sv_kv8_retrieve_topk");
+}
+
+size_t sv_kv8_attn_workspace_bytes(int B, int H, int n_kv_heads, int head_dim, int n_tokens) {
+  if (B < 0 || H <= 0 || n_kv_heads <= 0 || H % n_kv_heads || head_dim <= 0 || n_tokens < 0) return kStatusBytes;
+  return kHeadBytes + round256(sv::kv8_attn_workspace_bytes(B, H, n_kv_heads, head_dim, n_tokens));
+}
+
+sv_status sv_kv8_decode_attn(const void* q, int H, float scale, const sv_kv8_layer* layer, const sv_seq_batch* seqs,
+                             const int32_t* vis_idx, int k, void* out, float* lse, void* ws, size_t ws_bytes,
+                             void* stream) {
+  sv_status s = check_cache8(layer, seqs, true);
+  if (s != SV_OK) return s;
+  if (seqs->batch > 0 && (!q || !out)) return fail(SV_ERR_INVALID_ARG, "q and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(SV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const int Hkv = layer->n_kv_heads;
+  if (H <= 0 || H % Hkv) return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
+  if (H / Hkv > 16) return fail(SV_ERR_UNSUPPORTED, "query heads per KV head %d > 16", H / Hkv);
+  if (!std::isfinite(scale * 1.4426950408889634f))
+    return fail(SV_ERR_INVALID_ARG, "scale must be finite, times log2(e) too");
+  const int k_vis = vis_idx ? k : seqs->n_vis;
+  if (vis_idx && (k < 0 || k > seqs->n_vis)) return fail(SV_ERR_INVALID_ARG, "need 0 <= k <= n_vis");
+  const int n_tok = k_vis + seqs->n_text;
+  if (n_tok <= 0) return fail(SV_ERR_INVALID_ARG, "the attended token set is empty");
+  if (n_tok > (1 << 30) || seqs->n_vis + (long long)seqs->n_text > (1 << 30))
+    return fail(SV_ERR_UNSUPPORTED, "a sequence of more than 2^30 tokens");
+  if ((long long)seqs->batch * H > 0x7fffffffLL / 128) return fail(SV_ERR_UNSUPPORTED, "batch * H too large");
+  const size_t bytes = (size_t)seqs->batch * H * layer->head_dim * 2;
+  if (overlap(out, bytes, q, bytes)) return fail(SV_ERR_INVALID_ARG, "out must not overlap q");
+  s = check_ws(ws, ws_bytes, sv_kv8_attn_workspace_bytes(seqs->batch, H, Hkv, layer->head_dim, n_tok));
+  if (s != SV_OK) return s;
+  if (seqs->batch == 0) return SV_OK;
+  sv::Kv8AttnArgs a = {};
+  a.q = q; a.H = H; a.scale_log2 = scale * 1.4426950408889634f;
+  a.k_pool = static_cast<const uint8_t*>(layer->k_pool); a.v_pool = static_cast<const uint8_t*>(layer->v_pool);
+  a.scales = layer->scales;
+  a.num_blocks = layer->num_blocks; a.Hkv = Hkv;
+  a.block_table = seqs->block_table; a.max_blocks = seqs->max_blocks;
+  a.vis_idx = vis_idx; a.k_vis = k_vis; a.n_vis = seqs->n_vis; a.n_text = seqs->n_text; a.batch = seqs->batch;
+  a.lens = lens_of(seqs);
+  a.out = out; a.lse = lse;
+  a.ws = data_of(ws); a.counters = counters_of(ws); a.status = status_word(ws);
+  return cuda_status(sv::launch_kv8_attn(a, layer->head_dim, static_cast<cudaStream_t>(stream)), "sv_kv8_decode_attn");
 }
 
 sv_status sv_read_device_status(void* ws, int clear, int32_t* status_out, void* stream) {

@@ -189,6 +189,90 @@ struct TreeArgs {
 size_t tree_attn_workspace_bytes(int B, int T, int H, int Hkv, int D, int n_tokens);
 cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t stream);
 
+// ---- the cache in 8 bits: e4m3 pools [num_blocks][Hkv][16][D] and fp32 factors
+// [num_blocks][Hkv][2], of K and of V (kv8_append.cu, kv8_retrieve.cu, kv8_attn.cu)
+struct Kv8AppendArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long q_stride, k_stride, v_stride;
+  int N, H, Hkv;                   // packed new tokens
+  const int32_t* seq_start;        // [batch + 1], or nullptr: per_seq tokens each
+  int per_seq;
+  const uint16_t* q_weight;        // norm and rotation as in NormRopeArgs, pos [n_axes][N]
+  const uint16_t* k_weight;
+  float eps;
+  const float* cos_sin;
+  const int32_t* pos;
+  int n_pos, rot, interleaved, n_axes;
+  int sec_end[3];
+  uint16_t* q_out;                 // [N][H][D]
+  uint16_t* k_out;                 // [N][Hkv][D] or nullptr
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* scales;
+  const int32_t* block_table;
+  int num_blocks, max_blocks, batch, n_vis, n_text;
+  SeqLens lens;
+  int* status;
+};
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int d, int num_sms, cudaStream_t stream);
+
+struct Kv8RetrieveArgs {
+  const void* q;
+  int R, H;
+  const uint8_t* k_pool;
+  const float* scales;
+  int num_blocks, Hkv;
+  const int32_t* block_table;
+  int max_blocks, n_vis, n_text, k, batch;   // capacities with per-sequence lengths
+  SeqLens lens;
+  int32_t* vis_idx;
+  float* scores;                   // [batch][Hkv][n_vis] or nullptr
+  void* ws;                        // kv8_retrieve_workspace_bytes
+  int* status;
+};
+size_t kv8_retrieve_workspace_bytes(int B, int Hkv, int D, int n_vis);
+cudaError_t launch_kv8_retrieve(const Kv8RetrieveArgs& a, int D, int num_sms, cudaStream_t stream);
+
+struct Kv8AttnArgs {
+  const void* q;
+  int H;
+  float scale_log2;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* scales;
+  int num_blocks, Hkv;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* vis_idx;
+  int k_vis, n_vis, n_text, batch;
+  SeqLens lens;
+  void* out;
+  float* lse;
+  void* ws;                        // kv8_attn_workspace_bytes
+  int* counters;
+  int* status;
+};
+size_t kv8_attn_workspace_bytes(int B, int H, int Hkv, int D, int n_tokens);
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int D, cudaStream_t stream);
+
+// ---- causal attention of packed prompts (prompt_attn.cu)
+struct PromptArgs {
+  const void* q;                   // token-major rows, strides in elements
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  int N, H, Hkv, batch;
+  const int32_t* seq_start;        // [batch + 1]
+  float scale_log2;                // > 0
+  void* out;                       // [N][H][D]
+  float* lse;                      // [N][H] or nullptr
+  int* counters;
+  int* status;
+};
+cudaError_t launch_prompt_attn(const PromptArgs& a, int D, cudaStream_t stream);
+
 // ---- pages shared between branches (pages.cu)
 constexpr int kMaxLayers = 64;   // layers of one launch
 struct LayerPools {
