@@ -661,7 +661,7 @@ sv_status sv_pages_reserve(const sv_page_pool* pool, const sv_kv_layer* layers, 
  * (infinities and NaN included).  The weights are rounded to bf16 for the
  * product with V, as by sv_tree_attn.
  * scale     : > 0 and finite, times log2(e) too.  Supported: d in {64, 128},
- *             G = H / Hkv <= 16, N * H < 2^31.
+ *             G = H / Hkv <= 16, N <= 2^30, N * H < 2^31.
  * ws        : sv_prompt_attn_workspace_bytes(N, batch, H, Hkv, d).
  */
 size_t sv_prompt_attn_workspace_bytes(int N, int batch, int H, int n_kv_heads, int head_dim);

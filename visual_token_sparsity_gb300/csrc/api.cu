@@ -843,7 +843,8 @@ sv_status sv_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t
     return fail(SV_ERR_INVALID_ARG, "H must be a positive multiple of n_kv_heads");
   if (H / n_kv_heads > 16) return fail(SV_ERR_UNSUPPORTED, "query heads per KV head %d > 16", H / n_kv_heads);
   if (head_dim != 64 && head_dim != 128) return fail(SV_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", head_dim);
-  if ((long long)N * H > 0x7fffffffLL) return fail(SV_ERR_UNSUPPORTED, "N * H = %lld: 2^31 or more", (long long)N * H);
+  if (N > (1 << 30) || (long long)N * H > 0x7fffffffLL)
+    return fail(SV_ERR_UNSUPPORTED, "N = %d, H = %d: more than 2^30 tokens, or 2^31 rows", N, H);
   if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
     return fail(SV_ERR_INVALID_ARG, "scale must be > 0 and finite, times log2(e) too");
   if (N > 0 && batch > 0 && (!q || !k || !v || !out || !seq_start))
@@ -869,7 +870,7 @@ sv_status sv_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out; a.lse = lse;
   a.counters = counters_of(ws); a.status = status_word(ws);
-  return cuda_status(sv::launch_prompt_attn(a, head_dim, static_cast<cudaStream_t>(stream)), "sv_prompt_attn");
+  return cuda_status(sv::launch_prompt_attn(a, head_dim, num_sms(), static_cast<cudaStream_t>(stream)), "sv_prompt_attn");
 }
 
 sv_status sv_kv8_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

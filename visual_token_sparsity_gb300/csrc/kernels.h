@@ -271,7 +271,7 @@ struct PromptArgs {
   int* counters;
   int* status;
 };
-cudaError_t launch_prompt_attn(const PromptArgs& a, int D, cudaStream_t stream);
+cudaError_t launch_prompt_attn(const PromptArgs& a, int D, int num_sms, cudaStream_t stream);
 
 // ---- pages shared between branches (pages.cu)
 constexpr int kMaxLayers = 64;   // layers of one launch

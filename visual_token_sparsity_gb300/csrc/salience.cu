@@ -59,6 +59,7 @@
 #include "kernels.h"
 #include "fastmath.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace sv {
 
@@ -675,12 +676,9 @@ salience_kernel(const __grid_constant__ CUtensorMap tq_main, const __grid_consta
   }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
-EncodeTiledFn encode_fn() {
+EncodeTiledFn tensor_map_encoder() {
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -693,9 +691,11 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+namespace {
+
 // bf16 [units][rows][cols] tensor, box {box_cols, 128, 1}.
 bool make_map(CUtensorMap* map, const void* base, int cols, int rows, int units, int box_cols, bool swizzle128) {
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)units};
   cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)rows * cols * 2};
