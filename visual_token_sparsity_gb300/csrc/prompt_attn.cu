@@ -17,9 +17,9 @@
 // sequence's longest first, to one CTA per SM; a stream goes on to its next
 // unit's products while its softmax warps still write the last one's rows.
 //
-// Warps: 0-7 softmax and epilogue (one row per thread), 8 MMA issue, in turns
-// between the streams, 9 the units and the TMA loads (10 and 11 make the group of
-// four whole that gives registers up).
+// Warps: 0-7 softmax and epilogue (one row per thread), 8-9 MMA issue (one per
+// stream), 10 the units and the TMA loads (11 makes the group of four whole that
+// gives registers up).
 //
 // A token that a row does not see has weight 0, which an infinity or NaN of its
 // V (or a row of the next sequence's) turns into NaN.  Such rows show in the
@@ -36,7 +36,7 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;                 // rows of a stream, tokens of a tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 10;
 constexpr int kThreads = 384;              // at 168 registers at launch
 // A softmax thread holds a row of S (128 columns).
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
@@ -199,7 +199,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       ptx::mbar_init(&sh.unit_full[lane - S - 2], 1);
       ptx::mbar_init(&sh.unit_empty[lane - S - 2], kSoftWarps + 2);
     } else if (lane == S + 2 + kUnits) {
-      ptx::mbar_init(&sh.done, 1);
+      ptx::mbar_init(&sh.done, 2);
       sh.abort = sh.progress = 0;
     }
     ptx::mbar_fence_init();
@@ -316,77 +316,70 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         a.counters[1] = 0;
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kMmaWarp + 2) {
     // ------------------------------------------------ products
-    // The streams take turns, each the value product of its last tile and the
-    // logits of its next.  The whole warp walks the schedule and one elected lane
-    // issues (operands uniform over the warp).
+    // One warp per stream: waits, issue and commits of a tile take a warp 1400
+    // cycles, so that one for both streams was the bound.  The whole warp walks
+    // the schedule and one elected lane issues (operands uniform over the warp).
     constexpr uint32_t id_qk = ptx::idesc_bf16_f32(kTile, kTile);
     constexpr uint32_t id_pv = ptx::idesc_bf16_f32(kTile, D) | (1u << 16);   // B token-major
     constexpr uint32_t hi = ptx::smem_desc_hi_sw128(1024);
-    const uint32_t q_lo = ptx::smem_desc_lo_sw128(q_base), k_lo = ptx::smem_desc_lo_sw128(ring);
+    const int s = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);              // (uniform)
+    const uint32_t t_s = tmem_s(s), t_o = tmem_o(s);
+    const uint32_t qa = ptx::smem_desc_lo_sw128(q_base) + s * (TB / 16), k_lo = ptx::smem_desc_lo_sw128(ring);
     // V: 64-dim column groups lie a whole tile apart
     const uint32_t v_lo = ((ring & 0x3FFFFu) >> 4) | ((uint32_t)(kTile * 128 / 16) << 16);
-    struct Cursor {
-      int j = -1, n = 0, most = 0;     // tile, this stream's tiles, the unit's tiles
-      uint32_t unit = 0, kv0 = 0;      // units taken, ring position of the unit's first tile
-      uint32_t units = 0, items = 0;   // units with rows, products of weights so far
-      bool pending = false, more = true;
-    } x0, x1;
-    auto step = [&](Cursor& x, const int s) {
-      const uint32_t t_s = tmem_s(s), t_o = tmem_o(s);
-      if (x.pending) {
-        const uint32_t grp = __shfl_sync(0xffffffffu, x.kv0 + 2 * (uint32_t)x.j + 1, 0), slot = grp % S;
-        wait_bar(&sh.kv_full[slot], (grp / S) & 1, sh);
-        if (x.j == 0 && x.units > 1) wait_bar(&sh.o_empty[s], x.units & 1, sh);      // (the unit before: units - 2)
-        const uint32_t vb = v_lo + slot * (TB / 16);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          wait_bar(&sh.p_full[s][half], x.items & 1, sh);
-          __syncwarp();
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) {
-#pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)          // 16 tokens a step
-              ptx::mma_ts(t_o, t_s + k * 8, vb + k * (2048 / 16), hi, id_pv, x.j > 0 || k > 0);
-            if (half == 1) {
-              ptx::mma_commit(&sh.kv_empty[slot]);
-              if (x.j == x.n - 1) ptx::mma_commit(&sh.o_full[s]);
-            }
-          }
-          __syncwarp();
-        }
-        ++x.items;
-        x.pending = false;
+    uint32_t slot = 0, phase = 0;      // of the next tile in the ring
+    auto advance = [&]() {
+      if (++slot == (uint32_t)S) {
+        slot = 0;
+        phase ^= 1;
       }
-      if (!x.more) return;
-      if (++x.j >= x.most) {
-        const uint32_t us = x.unit % kUnits;
-        wait_bar(&sh.unit_full[us], (x.unit / kUnits) & 1, sh);
-        const Unit y = sh.unit[us];
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.unit_empty[us]);
-        x.kv0 += 2 * (uint32_t)x.most;
-        ++x.unit;
-        if (y.len < 0 || aborted(sh)) {
-          x.more = false;
-          return;
-        }
-        x.n = tiles_of(y, s, tpt);
-        x.most = max(tiles_of(y, 0, tpt), tiles_of(y, 1, tpt));
-        x.j = 0;
-      }
-      const uint32_t grp = __shfl_sync(0xffffffffu, x.kv0 + 2 * (uint32_t)x.j, 0), slot = grp % S;
-      if (x.j < x.n) {
-        if (x.j == 0) {
-          wait_bar(&sh.q_full[s], x.units & 1, sh);
-          ++x.units;
-        }
-        wait_bar(&sh.kv_full[slot], (grp / S) & 1, sh);
+    };
+    uint32_t vslot = 0, vphase = 0;    // of the V tile that a pending value product reads
+    uint32_t units = 0, items = 0;     // with rows, products of weights so far
+    bool pending = false, first = false, last = false;
+    auto value_product = [&]() {
+      wait_bar(&sh.kv_full[vslot], vphase, sh);
+      if (first && units > 1) wait_bar(&sh.o_empty[s], units & 1, sh);       // (the unit before: units - 2)
+      const uint32_t vb = v_lo + vslot * (TB / 16);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        wait_bar(&sh.p_full[s][half], items & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint32_t qa = q_lo + s * (TB / 16), kb = k_lo + slot * (TB / 16);
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k)                      // 16 tokens a step
+            ptx::mma_ts(t_o, t_s + k * 8, vb + k * (2048 / 16), hi, id_pv, !first || k > 0);
+          if (half == 1) {
+            ptx::mma_commit(&sh.kv_empty[vslot]);
+            if (last) ptx::mma_commit(&sh.o_full[s]);
+          }
+        }
+        __syncwarp();
+      }
+      ++items;
+      pending = false;
+    };
+    for (uint32_t unit = 0;; ++unit) {
+      const uint32_t us = unit % kUnits;
+      wait_bar(&sh.unit_full[us], (unit / kUnits) & 1, sh);
+      const Unit x = sh.unit[us];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.unit_empty[us]);
+      if (x.len < 0 || aborted(sh)) break;
+      const int n = tiles_of(x, s, tpt), most = max(tiles_of(x, 0, tpt), tiles_of(x, 1, tpt));
+      for (int j = 0; j < n; ++j) {
+        // the value product of the tile before (the last unit's, too), then the
+        // logits of this one, which take the place of its weights
+        if (pending) value_product();
+        if (j == 0) wait_bar(&sh.q_full[s], units++ & 1, sh);
+        wait_bar(&sh.kv_full[slot], phase, sh);
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t kb = k_lo + slot * (TB / 16);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             constexpr uint32_t kBlock = kTile * 128 / 16;
@@ -395,26 +388,28 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
           }
           ptx::mma_commit(&sh.s_full[s]);
           ptx::mma_commit(&sh.kv_empty[slot]);
-          if (x.j == x.n - 1) ptx::mma_commit(&sh.q_empty[s]);
+          if (j == n - 1) ptx::mma_commit(&sh.q_empty[s]);
         }
-        x.pending = true;
-      } else {
-        // a tile that this stream's rows do not see: given back as soon as it is there
-        const uint32_t next = grp + 1, vslot = next % S;
-        wait_bar(&sh.kv_full[slot], (grp / S) & 1, sh);
-        wait_bar(&sh.kv_full[vslot], (next / S) & 1, sh);
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&sh.kv_empty[slot]);
-          ptx::mbar_arrive(&sh.kv_empty[vslot]);
-        }
+        advance();
+        vslot = slot;
+        vphase = phase;
+        advance();
+        first = j == 0;
+        last = j == n - 1;
+        pending = true;
       }
-      __syncwarp();
-    };
-    while (x0.more || x1.more || x0.pending || x1.pending) {
-      step(x0, 0);
-      step(x1, 1);
+      // Tiles that this stream's rows do not see: given back when they are there
+      // (the pending product first, so that nothing waits for a slot that it holds).
+      if (n < most && pending) value_product();
+      for (int j = 2 * n; j < 2 * most; ++j) {
+        wait_bar(&sh.kv_full[slot], phase, sh);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.kv_empty[slot]);
+        advance();
+      }
     }
+    if (pending && !aborted(sh)) value_product();
     // every product has landed before the CTA gives its tensor memory back
     if (ptx::elect_one()) ptx::mma_commit(&sh.done);
     __syncwarp();
