@@ -63,7 +63,7 @@ struct Unit {
 
 struct Shared {
   uint64_t kv_full[10], kv_empty[10];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
   uint64_t unit_full[kUnits], unit_empty[kUnits], done;
   uint32_t tmem;
   int abort, progress;
@@ -100,6 +100,19 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// 32 bytes, in one store where the address is a multiple of 32: a lane's rows lie
+// in lines of their own, and each store visits all of them.
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t* w, bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 __host__ __device__ constexpr uint32_t tmem_s(int s) { return s * 128; }
@@ -194,7 +207,6 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       ptx::mbar_init(&sh.p_full[s][0], 4);
       ptx::mbar_init(&sh.p_full[s][1], 4);
       ptx::mbar_init(&sh.o_full[s], 1);
-      ptx::mbar_init(&sh.o_empty[s], 4);
     } else if (lane < S + 2 + kUnits) {
       ptx::mbar_init(&sh.unit_full[lane - S - 2], 1);
       ptx::mbar_init(&sh.unit_empty[lane - S - 2], kSoftWarps + 2);
@@ -341,7 +353,6 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     bool pending = false, first = false, last = false;
     auto value_product = [&]() {
       wait_bar(&sh.kv_full[vslot], vphase, sh);
-      if (first && units > 1) wait_bar(&sh.o_empty[s], units & 1, sh);       // (the unit before: units - 2)
       const uint32_t vb = v_lo + vslot * (TB / 16);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -424,6 +435,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     const uint32_t t_s = tmem_s(s) + lanes, t_o = tmem_o(s) + lanes;
     const float sl2 = a.scale_log2;
     const int rt = r / G, rh = r - rt * G;                // this row's token and head of the tile
+    const bool whole_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     uint32_t unit = 0, ns = 0, units = 0;
     for (;; ++unit) {
       const uint32_t us = unit % kUnits;
@@ -439,17 +451,28 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         wait_bar(&sh.s_full[s], ns & 1, sh);
         __syncwarp();
         ptx::tc_fence_after();
+        if (j * kTile + kTile - 1 > first) {
+          // Some row does not see all columns: those are set to -inf (weight 0) in
+          // tensor memory, 16 at a time from the first that any row of the warp does
+          // not see (rolled: code beside the loop's costs the loop its fetches).
+          const int vis = tk - j * kTile;                 // columns 0 .. vis are seen
+          const int from = max(0, __reduce_min_sync(0xffffffffu, vis) + 1) & ~15;
+#pragma unroll 1
+          for (int c = from; c < kTile; c += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(t_s + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e > vis) o[e] = 0xff800000u;
+            ptx::tmem_st16(t_s + c, o);
+          }
+          ptx::tmem_wait_st();
+        }
         uint32_t u[kTile];
 #pragma unroll
         for (int q = 0; q < 4; ++q) ptx::tmem_ld32(t_s + 32 * q, u + 32 * q);
 #pragma unroll
         for (int q = 0; q < 4; ++q) ptx::tmem_wait_ld(u + 32 * q);
-        if (j * kTile + kTile - 1 > first) {
-          const int vis = tk - j * kTile;                 // columns 0 .. vis are seen
-#pragma unroll
-          for (int e = 0; e < kTile; ++e)
-            if (e > vis) u[e] = 0xff800000u;              // -inf: weight 0
-        }
         float mx[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -516,24 +539,23 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       bool odd = false;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        uint32_t o[16], w[8];
-        ptx::tmem_ld16(t_o + c, o);
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld32(t_o + c, o);
+        ptx::tmem_wait_ld(o);
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + orow * D + c;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[e] = bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          odd = odd || (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-        }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[e] = bf16x2(__uint_as_float(o[16 * q + 2 * e]) * inv, __uint_as_float(o[16 * q + 2 * e + 1]) * inv);
+            odd = odd || (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+          }
+          if (live) store32(dst + 16 * q, w, whole_sectors);
         }
       }
       if (live && a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
       // rows that are not finite, over exactly the tokens that they see
       uint32_t again = __ballot_sync(0xffffffffu, odd && live);
       while (again) {
