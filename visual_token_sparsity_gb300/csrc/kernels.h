@@ -105,6 +105,9 @@ struct AttnArgs {
   const void* v_new = nullptr;
 };
 cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t stream);
+// joins nsplit partials per (sequence, query head), [batch][Hkv][nsplit][G]
+cudaError_t launch_attn_merge(const float* part_ml, const float* part_o, int batch, int H, int Hkv, int D, int nsplit,
+                              void* out, float* lse, cudaStream_t stream);
 cudaError_t launch_sparse_attn_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
 
 // ---- compaction gather (prune.cu)
@@ -253,6 +256,11 @@ struct Kv8AttnArgs {
   void* ws;                        // kv8_attn_workspace_bytes
   int* counters;
   int* status;
+  // set by launch_kv8_attn: partial results of the splits and their counters
+  // (nullptr: the merge kernel joins them)
+  float* part_ml;
+  float* part_o;
+  int* split_done;
 };
 size_t kv8_attn_workspace_bytes(int B, int H, int Hkv, int D, int n_tokens);
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int D, cudaStream_t stream);
