@@ -976,6 +976,8 @@ sv_status sv_kv8_decode_attn(const void* q, int H, float scale, const sv_kv8_lay
   if (n_tok > (1 << 30) || seqs->n_vis + (long long)seqs->n_text > (1 << 30))
     return fail(SV_ERR_UNSUPPORTED, "a sequence of more than 2^30 tokens");
   if ((long long)seqs->batch * H > 0x7fffffffLL / 128) return fail(SV_ERR_UNSUPPORTED, "batch * H too large");
+  if (seqs->batch * (n_tok / 32 + 1ll) > 0x7fffffffLL / Hkv)
+    return fail(SV_ERR_UNSUPPORTED, "batch * n_kv_heads * tokens beyond 2^36");
   const size_t bytes = (size_t)seqs->batch * H * layer->head_dim * 2;
   if (overlap(out, bytes, q, bytes)) return fail(SV_ERR_INVALID_ARG, "out must not overlap q");
   s = check_ws(ws, ws_bytes, sv_kv8_attn_workspace_bytes(seqs->batch, H, Hkv, layer->head_dim, n_tok));

@@ -256,8 +256,10 @@ struct Kv8AttnArgs {
   void* ws;                        // kv8_attn_workspace_bytes
   int* counters;
   int* status;
-  // set by launch_kv8_attn: partial results of the splits and their counters
-  // (nullptr: the merge kernel joins them)
+  // set by launch_kv8_attn: pieces that the work is cut into, their partial
+  // results and the counters of the units that they share (nullptr: the merge
+  // kernel joins them)
+  int pieces;
   float* part_ml;
   float* part_o;
   int* split_done;

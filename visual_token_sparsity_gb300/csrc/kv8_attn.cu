@@ -12,16 +12,24 @@
 //   S [16 tokens x 8 heads] = K (A) Q^T (B),   O [16 dims x 8 heads] += V^T (A) P^T (B)
 //
 // The order of the 16 elements that a tile sums over is free as long as both
-// operands have it, and so are the tile's rows, so every lane loads 16 bytes in
+// operands have it, and so are the tile's rows, so every lane takes 16 bytes in
 // a row of its token and turns them in registers: as K, bytes (4i, 4i + 1 | 4i + 2,
 // 4i + 3) are a tile's two pairs; as V, the bytes of two tokens are interleaved.
-// S comes out token-major and goes back in as P^T by way of movmatrix.  Nothing
-// passes through shared memory until a CTA's warps are joined.
+// S comes out token-major and goes back in as P^T by way of movmatrix.
+//
+// Rows are gathered by cp.async into a ring per warp, three steps of 16 tokens
+// ahead (six of half the bytes at head dim 64); the indices, pages and factors
+// that lead to them run two blocks of 32 tokens before that.
 //
 // The weights carry the factor s_v of their page relative to the largest so far
 // (and 2^6), the scores a reference that is raised only when one outgrows it by
 // 2^8, so that most steps need no maximum.  A weight keeps its eleven bits down to
 // 2^-20 of the reference and vanishes below 2^-30.
+//
+// Work is cut evenly: the blocks of 32 tokens of all (sequence, KV head) units
+// form one line, cut into equal pieces, one per warp.  A unit that lies in several
+// pieces leaves fp32 partials, which the last of its warps joins (few pieces) or a
+// second kernel (many), always in the order of the pieces.
 #include "kernels.h"
 #include "kv8.cuh"
 
@@ -29,10 +37,33 @@ namespace sv {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kCtas = 3;      // per CTA, and CTAs per SM (shared memory and 168 registers)
+constexpr int kSms = 152;
 constexpr int kBlock = 32;               // tokens whose rows a warp looks up at a time
+constexpr int kStep = 16;                // tokens of a step
 constexpr float kRaise = 8.f;            // log2: a reference is raised when a score outgrows it by more
-constexpr int kFusedMerge = 16;          // splits that the last CTA joins itself
+constexpr int kMinBlocks = 2;            // of a piece
+constexpr int kFusedPieces = 16;         // of a unit of at most two heads that its last warp joins itself
+
+// A warp's ring: per stage K and V rows of 16 tokens, the blocks' factors beside.
+template <int D>
+struct Ring {
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kPool = kStep * D, kStage = 2 * kPool;
+  static constexpr int kFactors = kStages * kStage;             // a stage: 16 (s_k, s_v)
+  static constexpr int kThere = kFactors + kStages * kStep * 8;  // a stage: which of the 16 tokens are there
+  static constexpr int kBytes = kThere + kStages * 4 + (kStages * 4 % 128 ? 128 - kStages * 4 % 128 : 0);
+};
+
+// Where 16-byte unit `u` of row `t` of a stage's K or V lies.  Lanes that read
+// together (as K: two neighbouring rows, four units; as V: four rows of one
+// parity, two units) meet eight different units of a 128-byte line.
+template <int D>
+__device__ __forceinline__ uint32_t unit_at(uint32_t t, uint32_t u) {
+  const uint32_t turn = ((t >> 1) & 3) << 1;
+  if (D == 128) return t * 128 + ((u ^ turn ^ ((t & 1) << 2)) << 4);
+  return (t >> 1) * 128 + (((((t & 1) << 2) | u) ^ turn) << 4);
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -58,35 +89,175 @@ __device__ __forceinline__ uint32_t exponent_of(float x, float y) {
   return min(max(__float_as_uint(fmaxf(fabsf(x), fabsf(y))) & 0x7f800000u, 0x00800000u), 253u << 23);
 }
 
-// 16 bytes of a row: D = 128 has two such pieces per lane of K, 64 bytes apart.
-template <int D>
-struct Rows {
-  static constexpr int KC = D / 64;          // pieces of K per token and lane
-  static constexpr int VB = D / 8;           // bytes of V per token and lane
-  uint4 k[2][KC];                            // tokens r and r + 8
-  uint32_t v[4][VB / 4];                     // tokens 2q, 2q + 1, 2q + 8, 2q + 9
+// First block of piece c of C: floor(total * c / C), in 32 bits.
+__host__ __device__ __forceinline__ uint32_t piece_begin(uint32_t total, uint32_t c, uint32_t C) {
+  const uint32_t q = total / C;
+  return q * c + (total - q * C) * c / C;
+}
+// The piece that block s lies in.
+__device__ __forceinline__ int piece_of(uint32_t total, uint32_t s, uint32_t C) {
+  return (int)(((unsigned long long)(s + 1) * C - 1) / total);
+}
+
+struct Seq {
+  int nv, nt, kb;       // visual, text, attended visual tokens
+  __device__ int blocks() const { return (kb + nt + kBlock - 1) / kBlock; }
 };
+__device__ __forceinline__ bool seq_of(const Kv8AttnArgs& a, int b, Seq& s) {
+  return attn_lengths(a.lens, a.vis_idx != nullptr, b, a.n_vis, a.n_text, a.k_vis, false, a.status, s.nv, s.nt, s.kb);
+}
+
+// Blocks of sequences [b0, b0 + 32) up to this lane's (and its own), by a whole warp.
+__device__ __forceinline__ uint32_t scan_blocks(const Kv8AttnArgs& a, int b0, int lane, uint32_t& mine) {
+  Seq s;
+  mine = 0;
+  if (b0 + lane < a.batch) {
+    seq_of(a, b0 + lane, s);
+    mine = (uint32_t)s.blocks() * (uint32_t)a.Hkv;
+  }
+  uint32_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  return inc;
+}
+__device__ __forceinline__ uint32_t line_total(const Kv8AttnArgs& a, int lane) {
+  if (!a.lens.any()) {
+    Seq s;
+    seq_of(a, 0, s);
+    return (uint32_t)s.blocks() * (uint32_t)a.Hkv * (uint32_t)a.batch;
+  }
+  uint32_t total = 0, mine;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) total += __shfl_sync(0xffffffffu, scan_blocks(a, b0, lane, mine), 31);
+  return total;
+}
+// The sequence that block `at` of the line lies in, and the blocks before it.
+__device__ __forceinline__ void line_find(const Kv8AttnArgs& a, uint32_t at, int lane, int& b, uint32_t& before) {
+  if (!a.lens.any()) {
+    Seq s;
+    seq_of(a, 0, s);
+    const uint32_t per = (uint32_t)s.blocks() * (uint32_t)a.Hkv;
+    b = (int)(at / per);
+    before = (uint32_t)b * per;
+    return;
+  }
+  before = 0;
+  for (b = 0; b < a.batch; b += 32) {
+    uint32_t mine;
+    const uint32_t inc = scan_blocks(a, b, lane, mine);
+    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > at);
+    if (past) {
+      const int f = __ffs(past) - 1;
+      before += __shfl_sync(0xffffffffu, inc - mine, f);
+      b += f;
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
+
+// (m, l) and O of a piece's part of a unit: slot 0 of a piece continues a unit,
+// slot 1 begins one that goes on.
+__device__ __forceinline__ size_t part_slot(int piece, bool begins) { return (size_t)piece * 2 + (begins ? 1 : 0); }
+
+// (M, L, O) of head h of a unit over pieces p0 + w0, + step, ... < p0 + n, by a warp:
+// D / 32 dims a lane, eight pieces in flight.
+template <int D>
+__device__ __forceinline__ void gather_pieces(const Kv8AttnArgs& a, int p0, int n, int w0, int step, int lane, int h,
+                                              float& M, float& L, float (&acc)[D / 32]) {
+  constexpr int E = D / 32, kBatch = 8;
+  const int G = a.H / a.Hkv;
+  M = -INFINITY;
+  L = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int s0 = w0; s0 < n; s0 += kBatch * step) {
+    float x[kBatch][E];
+    float2 ml[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i * step;
+      const size_t at = part_slot(p0 + s, s == 0) * G + h;
+      ml[i] = s < n ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 y = s < n ? __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D + lane * E + e)) : make_float2(0.f, 0.f);
+        x[i][e] = y.x;
+        x[i][e + 1] = y.y;
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+    const float old = M == -INFINITY ? 0.f : fast_exp2(M - top);
+    L *= old;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= old;
+    M = top;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = ml[i].x == -INFINITY ? 0.f : fast_exp2(ml[i].x - top);
+      L = fmaf(ml[i].y, w, L);                              // (a NaN stays)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+    }
+  }
+}
 
 }  // namespace
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 5 : 4)
-kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a, int nsplit, int chunk) {
-  using R = Rows<D>;
-  constexpr int KS = D / 16, VW = R::VB / 4;
-  extern __shared__ __align__(16) float joined[];        // [warps][G][D], then (m, l)
-  __shared__ int s_last;
+__global__ void __launch_bounds__(kWarps * 32, kCtas)
+kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
+  using R = Ring<D>;
+  constexpr int KS = D / 16, KC = D / 64, VB = D / 8, VW = VB / 4, S = R::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
   grid_dep_sync();
   const int G = a.H / a.Hkv;
-  const int unit = blockIdx.x / nsplit, split = blockIdx.x - unit * nsplit;
-  const int b = unit / a.Hkv, g = unit - b * a.Hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q4 = lane & 3;
-  int nv, nt, kb;
-  attn_lengths(a.lens, a.vis_idx != nullptr, b, a.n_vis, a.n_text, a.k_vis, threadIdx.x == 0 && g == 0 && split == 0,
-               a.status, nv, nt, kb);
-  const int total = kb + nt, begin = split * chunk, end = min(total, begin + chunk);
+  // sequences without a token (or with a length out of range): 0 and -inf
+  if (a.lens.any()) {
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+      Seq s;
+      const bool ok = seq_of(a, b, s);
+      if (!ok && threadIdx.x == 0) flag_status(a.status, kStatusBadLength);
+      if (s.kb + s.nt > 0) continue;
+      for (int i = threadIdx.x; i < a.H * (D / 8); i += kWarps * 32)
+        reinterpret_cast<uint4*>(a.out)[(size_t)b * a.H * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.lse != nullptr)
+        for (int i = threadIdx.x; i < a.H; i += kWarps * 32) a.lse[(size_t)b * a.H + i] = -INFINITY;
+    }
+  }
+  const uint32_t total = line_total(a, lane);
+  const uint32_t C = min((uint32_t)a.pieces, total);
+  uint8_t* ring = smem + warp * R::kBytes;
+  const uint32_t ring_at = smem_u32(ring);
+  const int piece = blockIdx.x * kWarps + warp;
+  if (piece >= (int)C) return;
+  const uint32_t from = piece_begin(total, piece, C);
+  int left = (int)(piece_begin(total, piece + 1, C) - from), b;
+  uint32_t before;
+  line_find(a, from, lane, b, before);
+  uint32_t off = from - before;
+
+#pragma unroll 1
+  for (; left > 0; ++b, off = 0) {
+  Seq sq;
+  seq_of(a, b, sq);
+  const int nv = sq.nv, kb = sq.kb, total_tok = sq.kb + sq.nt, per_unit = sq.blocks();
+  const uint32_t in_seq = (uint32_t)per_unit * (uint32_t)a.Hkv;
+#pragma unroll 1
+  while (left > 0 && off < in_seq) {
+  const int g = (int)(off / (uint32_t)per_unit), blk0 = (int)off - g * per_unit, blk1 = min(per_unit, blk0 + left);
+  off += blk1 - blk0;
+  left -= blk1 - blk0;
   const int32_t* list = a.vis_idx != nullptr ? a.vis_idx + ((size_t)b * a.Hkv + g) * a.k_vis : nullptr;
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+  const int first = blk0 * kBlock, end = min(total_tok, blk1 * kBlock);
+  constexpr int stride = kBlock;
 
   // ---- a block's tokens, a lane each, in three steps: position (two blocks
   // ahead), page (one ahead), row and factors
@@ -108,19 +279,46 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a, int nsplit, int chunk) {
     n.page = n.there ? __ldg(bt + (n.pos >> 4)) : -1;
   };
   uint32_t rid, there;
-  float2 sc;
   auto load_row = [&](const Ahead& n) {
     const bool ok = n.there && n.page >= 0 && n.page < a.num_blocks;
     if (n.there && !ok) flag_status(a.status, kStatusBadBlock);
-    const uint32_t u = ok ? (uint32_t)n.page * (uint32_t)a.Hkv + (uint32_t)g : 0u;
-    rid = u * 16u + (uint32_t)(n.pos & 15);
-    sc = ok ? __ldg(reinterpret_cast<const float2*>(a.scales) + u) : make_float2(0.f, 0.f);
+    rid = ok ? ((uint32_t)n.page * (uint32_t)a.Hkv + (uint32_t)g) * 16u + (uint32_t)(n.pos & 15) : 0u;
     there = __ballot_sync(0xffffffffu, ok);
   };
-  const int first = begin + warp * kBlock, stride = kWarps * kBlock;
   Ahead n1, n2;
   load_pos(first, n1);
   load_pos(first + stride, n2);
+  load_page(first, n1);
+  // Requests the rows and factors of step `i` (its tokens' ids are looked up with
+  // the first of a block's two steps); tokens that are not there read as zeros.
+  int t_ahead = first;
+  auto request = [&](int i) {
+    if ((i & 1) == 0) {
+      load_row(n1);
+      n1 = n2;
+      load_page(t_ahead + stride, n1);
+      load_pos(t_ahead + 2 * stride, n2);
+      t_ahead += stride;
+    }
+    const int h = (i & 1) * 16;
+    const uint32_t stage = (uint32_t)i % S;
+    constexpr int U = D / 16, RPI = 32 / U;                 // 16-byte units of a row, rows of an instruction
+    const uint32_t u = lane % U, t0 = lane / U;
+#pragma unroll
+    for (int c = 0; c < kStep / RPI; ++c) {
+      const uint32_t t = t0 + c * RPI, row = __shfl_sync(0xffffffffu, rid, h + t), n = (there >> (h + t)) & 1 ? 16u : 0u;
+      const uint32_t to = ring_at + stage * R::kStage + unit_at<D>(t, u);
+      cp_async16(to, a.k_pool + (size_t)row * D + u * 16, n);
+      cp_async16(to + R::kPool, a.v_pool + (size_t)row * D + u * 16, n);
+    }
+    const uint32_t mine = __shfl_sync(0xffffffffu, rid, h + (lane & 15));
+    if (lane < 16)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(ring_at + R::kFactors + (stage * kStep + lane) * 8),
+                   "l"(a.scales + (size_t)(mine >> 4) * 2), "r"((there >> (h + lane)) & 1 ? 8u : 0u)
+                   : "memory");
+    if (lane == 0) reinterpret_cast<uint32_t*>(ring + R::kThere)[stage] = there >> h;
+    cp_async_commit();
+  };
 
   // ---- the queries: each head's elements over 2^e, so that the largest lies in
   // [2^14, 2^15); those that are not finite stay what they are
@@ -176,48 +374,26 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a, int nsplit, int chunk) {
   }
   uint32_t vtop = 0x00800000u;      // the largest factor of V so far, rounded down to a power of two (bits)
 
-  R x;
-  auto load_k = [&](uint32_t rows, int h) {      // rows: this step's row ids, 16 h on
+  const int steps = (end - first + kStep - 1) / kStep;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t row = __shfl_sync(0xffffffffu, rows, 16 * h + 8 * i + r);
-      const bool ok = (there >> (16 * h + 8 * i + r)) & 1;
+  for (int i = 0; i < S - 1; ++i) request(i);
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      request(i + S - 1);
+      const uint32_t stage = (uint32_t)i % S;
+      const uint8_t* at = ring + stage * R::kStage;
+      const float2* fac = reinterpret_cast<const float2*>(ring + R::kFactors + stage * kStep * 8);
+      const float2 f0 = fac[r], f1 = fac[r + 8];
+      const float sk0 = f0.x, sv0 = f0.y, sk1 = f1.x, sv1 = f1.y;
+      const uint32_t seen = reinterpret_cast<const uint32_t*>(ring + R::kThere)[stage];
+      const bool ok0 = (seen >> r) & 1, ok1 = (seen >> (8 + r)) & 1;
+      uint4 xk[2][KC];
 #pragma unroll
-      for (int c = 0; c < R::KC; ++c)
-        x.k[i][c] = ok ? ld_stream16(a.k_pool + (size_t)row * D + c * 64 + q4 * 16) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  auto load_v = [&](uint32_t rows, int h) {
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 16 * h + 2 * q4 + (i & 1) + (i >> 1) * 8;
-      const uint32_t row = __shfl_sync(0xffffffffu, rows, tok);
-      const bool ok = (there >> tok) & 1;
-      const uint8_t* src = a.v_pool + (size_t)row * D + r * R::VB;
-      if constexpr (VW == 4) {
-        const uint4 y = ok ? ld_stream16(src) : make_uint4(0u, 0u, 0u, 0u);
-        x.v[i][0] = y.x; x.v[i][1] = y.y; x.v[i][2] = y.z; x.v[i][3] = y.w;
-      } else {
-        const uint2 y = ok ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
-        x.v[i][0] = y.x; x.v[i][1] = y.y;
-      }
-    }
-  };
-
-  load_page(first, n1);
-  for (int t0 = first; t0 < end; t0 += stride) {
-    load_row(n1);
-    n1 = n2;
-    load_page(t0 + stride, n1);
-    load_pos(t0 + 2 * stride, n2);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && t0 + 16 >= end) break;
-      load_k(rid, h);
-      load_v(rid, h);
-      const float sk0 = __shfl_sync(0xffffffffu, sc.x, 16 * h + r), sk1 = __shfl_sync(0xffffffffu, sc.x, 16 * h + 8 + r);
-      const float sv0 = __shfl_sync(0xffffffffu, sc.y, 16 * h + r), sv1 = __shfl_sync(0xffffffffu, sc.y, 16 * h + 8 + r);
-      const bool ok0 = (there >> (16 * h + r)) & 1, ok1 = (there >> (16 * h + 8 + r)) & 1;
+        for (int c = 0; c < KC; ++c) xk[n][c] = *reinterpret_cast<const uint4*>(at + unit_at<D>(r + 8 * n, 4 * c + q4));
       float z[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -226,8 +402,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a, int nsplit, int chunk) {
       }
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&x.k[0][k >> 2]);
-        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&x.k[1][k >> 2]);
+        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&xk[0][k >> 2]);
+        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&xk[1][k >> 2]);
         const uint32_t y0 = w0[k & 3], y1 = w1[k & 3];
         const uint32_t a0 = kv8::e4m3x2_to_half2((uint16_t)y0), a1 = kv8::e4m3x2_to_half2((uint16_t)y1);
         const uint32_t a2 = kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), a3 = kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16));
@@ -282,23 +458,37 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a, int nsplit, int chunk) {
         p[t][0] = transposed(half2_of(y[0] * w0, y[1] * w0));
         p[t][1] = transposed(half2_of(y[2] * w1, y[3] * w1));
       }
+      uint32_t xv[4][VW];                         // tokens 2 q4, + 1, + 8, + 9
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t t = 2 * q4 + (n & 1) + (n >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 y = *reinterpret_cast<const uint4*>(at + R::kPool + unit_at<D>(t, r));
+          xv[n][0] = y.x; xv[n][1] = y.y; xv[n][2] = y.z; xv[n][3] = y.w;
+        } else {
+          const uint2 y = *reinterpret_cast<const uint2*>(at + R::kPool + unit_at<D>(t, r >> 1) + (r & 1) * 8);
+          xv[n][0] = y.x; xv[n][1] = y.y;
+        }
+      }
 #pragma unroll
       for (int w = 0; w < VW; ++w)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t sel = i ? 0x7362u : 0x5140u;       // (token, next token) x two bytes
-          const uint32_t lo = __byte_perm(x.v[0][w], x.v[1][w], sel), hi = __byte_perm(x.v[2][w], x.v[3][w], sel);
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const uint32_t sel = i2 ? 0x7362u : 0x5140u;      // (token, next token) x two bytes
+          const uint32_t lo = __byte_perm(xv[0][w], xv[1][w], sel), hi = __byte_perm(xv[2][w], xv[3][w], sel);
           const uint32_t a0 = kv8::e4m3x2_to_half2((uint16_t)lo), a1 = kv8::e4m3x2_to_half2((uint16_t)(lo >> 16));
           const uint32_t a2 = kv8::e4m3x2_to_half2((uint16_t)hi), a3 = kv8::e4m3x2_to_half2((uint16_t)(hi >> 16));
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + i], a0, a1, a2, a3, p[t][0], p[t][1]);
+          for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + i2], a0, a1, a2, a3, p[t][0], p[t][1]);
         }
-    }
   }
+  cp_async_wait<0>();
+  __syncwarp();                                             // (the ring is free for the next unit)
 
-  // ---- the CTA's warps joined
+  // ---- this part of the unit
   const float back = __uint_as_float(vtop) * (1.f / 64.f);
-  float* ml = joined + kWarps * G * D;
+  const bool whole = blk0 == 0 && blk1 == per_unit;
+  const size_t slot = part_slot(piece, blk0 == 0);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -308,143 +498,171 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a, int nsplit, int chunk) {
       s += __shfl_xor_sync(0xffffffffu, s, 4);
       s += __shfl_xor_sync(0xffffffffu, s, 8);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
-      if (h < G) {
-        if (r == 0) {
-          ml[(warp * G + h) * 2] = m[t][i];
-          ml[(warp * G + h) * 2 + 1] = s;
-        }
-        float* dst = joined + (warp * G + h) * D + r * R::VB;
+      if (h >= G) continue;
+      if (whole) {
+        const float inv = s > 0.f ? 1.f / s : (s == 0.f ? 0.f : s);
+        const size_t row = (size_t)b * a.H + (size_t)g * G + h;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + r * VB);
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+          dst[j] = f32_to_bf16_bits(o[t][j][i] * back * inv) | f32_to_bf16_bits(o[t][j][i + 2] * back * inv) << 16;
+        if (r == 0 && a.lse != nullptr)
+          a.lse[row] = s == 0.f ? -INFINITY : (m[t][i] + log2f(s)) * 0.6931471805599453f;
+      } else {
+        float* dst = a.part_o + (slot * G + h) * D + r * VB;
 #pragma unroll
         for (int j = 0; j < KS; ++j)
           *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back, o[t][j][i + 2] * back);
+        if (r == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(m[t][i], s);
       }
     }
-  __syncthreads();
-  const size_t part = ((size_t)unit * nsplit + split) * G;
-  float* part_ml = reinterpret_cast<float*>(a.part_ml);
-  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
-    const int h = i / D, e = i - h * D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[(w * G + h) * 2]);
-    float L = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = ml[(w * G + h) * 2], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-      // (a NaN of the sum stays even where the maximum knows nothing of it)
-      L += mw == -INFINITY ? ml[(w * G + h) * 2 + 1] * 0.f : f * ml[(w * G + h) * 2 + 1];
-      acc += f * joined[(w * G + h) * D + e];
-    }
-    if (nsplit == 1) {
-      const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-      const size_t row = (size_t)b * a.H + (size_t)g * G + h;
-      static_cast<uint16_t*>(a.out)[row * D + e] = (uint16_t)f32_to_bf16_bits(acc * inv);
-      if (e == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-    } else {
-      a.part_o[part * D + i] = acc;
-      if (e == 0) {
-        part_ml[(part + h) * 2] = M;
-        part_ml[(part + h) * 2 + 1] = L;
-      }
-    }
-  }
-  if (nsplit == 1 || a.split_done == nullptr) return;
+  if (whole || a.split_done == nullptr) continue;
 
-  // ---- the last CTA of a (sequence, KV head) joins its splits
+  // ---- the last warp of a unit joins its pieces
+  const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
+  const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
+  const int unit = b * a.Hkv + g;
   __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(a.split_done + unit, 1) == nsplit - 1;
-  __syncthreads();
-  if (!s_last) return;
+  __syncwarp();
+  int last = 0;
+  if (lane == 0) last = atomicAdd(a.split_done + unit, 1) == n - 1;
+  if (!__shfl_sync(0xffffffffu, last, 0)) continue;
   __threadfence();
-  if (threadIdx.x == 0) a.split_done[unit] = 0;           // ready for the next call
-  const size_t base = (size_t)unit * nsplit * G;
-  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
-    const int h = i / D, e = i - h * D;
-    float M = -INFINITY;
-    for (int s = 0; s < nsplit; ++s) M = fmaxf(M, __ldcg(part_ml + (base + s * G + h) * 2));
-    float L = 0.f, acc = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < nsplit; ++s) {
-      const float2 x2 = __ldcg(reinterpret_cast<const float2*>(part_ml) + base + s * G + h);
-      const float v = __ldcg(a.part_o + (base + s * G) * D + i);
-      const float f = x2.x == -INFINITY ? 0.f : fast_exp2(x2.x - M);
-      L += x2.x == -INFINITY ? x2.y * 0.f : f * x2.y;
-      acc += f * v;
-    }
+  if (lane == 0) a.split_done[unit] = 0;                  // ready for the next call
+#pragma unroll 1
+  for (int h = 0; h < G; ++h) {
+    constexpr int E = D / 32;
+    float M, L, acc[E];
+    gather_pieces<D>(a, p0, n, 0, 1, lane, h, M, L, acc);
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     const size_t row = (size_t)b * a.H + (size_t)g * G + h;
-    static_cast<uint16_t*>(a.out)[row * D + e] = (uint16_t)f32_to_bf16_bits(acc * inv);
-    if (e == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = f32_to_bf16_bits(acc[e] * inv) | f32_to_bf16_bits(acc[e + 1] * inv) << 16;
+    if (lane == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
+  }
+  before += in_seq;
+  }
+}
+
+// Joins the units that were cut: a CTA per (unit, head), whose warps take every
+// eighth piece each.
+constexpr int kMergeWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
+  constexpr int E = D / 32;
+  __shared__ float part[kMergeWarps][D];
+  __shared__ float2 part_ml[kMergeWarps];
+  grid_dep_sync();
+  const int G = a.H / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, g = h / G;
+  const uint32_t total = line_total(a, lane), C = min((uint32_t)a.pieces, total);
+  Seq s;
+  seq_of(a, b, s);
+  const int per_unit = s.blocks();
+  if (per_unit == 0) return;
+  uint32_t before = 0;
+  if (!a.lens.any()) {
+    before = (uint32_t)b * (uint32_t)per_unit * (uint32_t)a.Hkv;
+  } else {
+    for (int b0 = 0; b0 <= b; b0 += 32) {
+      uint32_t mine;
+      const uint32_t inc = scan_blocks(a, b0, lane, mine);
+      before += b - b0 < 32 ? __shfl_sync(0xffffffffu, inc - mine, b - b0) : __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
+  const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
+  if (n == 1) return;
+  float M, L, acc[E];
+  gather_pieces<D>(a, p0, n, warp, kMergeWarps, lane, h - g * G, M, L, acc);
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+  if (lane == 0) part_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, part_ml[w].x);
+  L = 0.f;
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = part_ml[w].x == -INFINITY ? 0.f : fast_exp2(part_ml[w].x - M);
+    L += part_ml[w].y * f;
+    v += part[w][threadIdx.x] * f;
+  }
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  const size_t row = (size_t)b * a.H + h;
+  static_cast<uint16_t*>(a.out)[row * D + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v * inv);
+  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 namespace {
 
-// Splits of a (sequence, KV head): as many CTAs as are resident at once (152 SMs
-// times 5, or 4 with more than 8 heads), so that what varies is how full the
-// last round is; each split costs about three steps beside its tokens.
-constexpr int kSms = 152;
-constexpr int kMaxSplits = 128;
-int resident(int G) { return kSms * (G <= 8 ? 5 : 4); }
-struct Plan {
-  int nsplit, chunk;
-};
-Plan plan_of(long long units, int G, int n_tokens) {
-  const int block = kWarps * kBlock;
-  const int blocks = n_tokens > 0 ? (n_tokens + block - 1) / block : 1;
-  const long long cap = resident(G);
-  Plan best = {1, blocks * block};
-  long long best_cost = -1;
-  for (int s = 1; s <= blocks && s <= kMaxSplits; ++s) {
-    if (s > 1 && (units * s > 2 * cap || units > kWorkspaceCounters)) break;
-    const int per = (blocks + s - 1) / s;
-    const long long ctas = units * ((blocks + per - 1) / per), rounds = (ctas + cap - 1) / cap;
-    const long long cost = rounds * (per * 2 + 3);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = {(blocks + per - 1) / per, per * block};
-    }
-  }
-  return best;
+// Pieces of the line: one per resident warp, of kMinBlocks blocks at least.  Where
+// that is four or more to a unit, the same number to each, so that none lies across
+// two units (a warp's second unit begins with the whole chain of lookups).
+int pieces_of(long long units, long long blocks) {
+  const long long most = (long long)kSms * kCtas * kWarps;
+  long long each = blocks / kMinBlocks;
+  each = each > 1 ? each : 1;
+  if (units * each <= most) return (int)(units * each > 1 ? units * each : 1);
+  each = units > 0 ? most / units : 0;
+  return (int)(each >= 4 ? units * each : most);
+}
+// No fewer pieces, for any smaller call.
+long long pieces_bound(long long units, long long blocks) {
+  const long long most = (long long)kSms * kCtas * kWarps, c = units * (blocks / kMinBlocks > 1 ? blocks / kMinBlocks : 1);
+  return c < 1 ? 1 : c < most ? c : most;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// (m, l) | O of every split: a bound that no smaller call exceeds
+// (m, l) | O of two parts of every piece: a bound that no smaller call exceeds
 size_t kv8_attn_workspace_bytes(int B, int H, int Hkv, int D, int n_tokens) {
   const int G = H / Hkv;
-  const long long units = (long long)B * Hkv, most = 2ll * resident(G);
-  long long splits = (n_tokens + kWarps * kBlock - 1) / (kWarps * kBlock);
-  splits = splits < kMaxSplits ? splits : kMaxSplits;
-  long long parts = units * splits;
-  parts = parts < most ? parts : most;
-  return up256((size_t)parts * G * 2 * sizeof(float)) + up256((size_t)parts * G * D * sizeof(float));
+  const size_t parts = 2 * (size_t)pieces_bound((long long)B * Hkv, ((long long)n_tokens + kBlock - 1) / kBlock);
+  return up256(parts * G * 2 * sizeof(float)) + up256(parts * G * D * sizeof(float));
 }
 
 template <int D, int NT>
-static cudaError_t launch_nt(const Kv8AttnArgs& a, const Plan& p, cudaStream_t stream) {
-  const int G = a.H / a.Hkv;
-  const size_t smem = (size_t)kWarps * G * (D + 2) * sizeof(float);
-  return launch_dependent(kv8_attn_kernel<D, NT>, dim3((unsigned)((long long)a.batch * a.Hkv * p.nsplit)),
-                          dim3(kWarps * 32), smem, stream, a, p.nsplit, p.chunk);
+static cudaError_t launch_nt(const Kv8AttnArgs& a, cudaStream_t stream) {
+  auto kernel = kv8_attn_kernel<D, NT>;
+  const int smem = kWarps * Ring<D>::kBytes;
+  static_assert(kCtas * (kWarps * Ring<D>::kBytes + 1024) <= 228 * 1024, "shared memory");
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  e = launch_dependent(kernel, dim3((unsigned)((a.pieces + kWarps - 1) / kWarps)), dim3(kWarps * 32), (size_t)smem, stream, a);
+  if (e != cudaSuccess || a.split_done != nullptr) return e;
+  return launch_dependent(kv8_merge_kernel<D>, dim3((unsigned)((long long)a.batch * a.H)), dim3(kMergeWarps * 32), 0,
+                          stream, a);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int D, cudaStream_t stream) {
   Kv8AttnArgs a = args;
   const int G = a.H / a.Hkv;
-  const Plan p = plan_of((long long)a.batch * a.Hkv, G, a.k_vis + a.n_text);
+  const long long units = (long long)a.batch * a.Hkv, blocks = (a.k_vis + a.n_text + kBlock - 1) / kBlock;
+  a.pieces = pieces_of(units, blocks);
   a.part_ml = static_cast<float*>(a.ws);
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
-                                      up256((size_t)a.batch * a.Hkv * p.nsplit * G * 2 * sizeof(float)));
-  a.split_done = p.nsplit <= kFusedMerge ? a.counters : nullptr;
-  cudaError_t e;
-  if (D == 128) e = G <= 8 ? launch_nt<128, 1>(a, p, stream) : launch_nt<128, 2>(a, p, stream);
-  else e = G <= 8 ? launch_nt<64, 1>(a, p, stream) : launch_nt<64, 2>(a, p, stream);
-  if (e != cudaSuccess || p.nsplit <= kFusedMerge) return e;
-  return launch_attn_merge(a.part_ml, a.part_o, a.batch, a.H, a.Hkv, D, p.nsplit, a.out, a.lse, stream);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.pieces * 2 * G * 2 * sizeof(float)));
+  // (the most pieces that a unit can lie in; with counts of its own per sequence
+  // the line is shorter and a unit lies in more of them)
+  const long long most = a.lens.any() ? (blocks < a.pieces ? blocks : a.pieces) : a.pieces / units + 2;
+  a.split_done = units <= kWorkspaceCounters && G <= 2 && most <= kFusedPieces ? a.counters : nullptr;
+  if (D == 128) return G <= 8 ? launch_nt<128, 1>(a, stream) : launch_nt<128, 2>(a, stream);
+  return G <= 8 ? launch_nt<64, 1>(a, stream) : launch_nt<64, 2>(a, stream);
 }
 
 }  // namespace sv
