@@ -735,8 +735,8 @@ sv_status sv_kv8_append(const void* q, int64_t q_stride, const void* k, int64_t 
 
 /*
  * sv_retrieve_topk from the 8-bit cache (the scores are of the keys' values).
- * The selection is that of the scores in 64 bits: tokens whose fp32 scores are
- * too near to the k-th one to tell are scored again.  Exact ties go to the lower
+ * The selection is that of the exact scores: tokens whose fp32 scores are too
+ * near to the k-th one to tell are scored again with 48 bits.  Ties go to the lower
  * index.  scores (optional out) are the fp32 ones.  With scores that are not
  * finite the choice is unspecified (but valid).
  * ws : sv_kv8_retrieve_workspace_bytes(B, H, n_kv_heads, head_dim, n_vis, k);
