@@ -293,6 +293,7 @@ def retrieve(c, q, seqs, k, scores=True):
     (1, 1, 64, 1, 1, 1, 1), (4, 2, 64, 1, 1, 17, 5), (4, 2, 64, 2, 32, 576, 144), (28, 4, 128, 2, 3, 1000, 999),
     (32, 32, 128, 1, 1, 2880, 1440), (7, 1, 128, 1, 193, 300, 300), (16, 1, 64, 3, 2, 5000, 1),
     (8, 4, 128, 1, 1, 20011, 5002), (2, 2, 64, 1, 1, 60001, 15000), (5, 1, 64, 2, 40, 9000, 4500),
+    (1, 1, 64, 1, 2, 420007, 100003), (2, 1, 128, 2, 1, 16384, 16383), (3, 1, 64, 1, 1, 16385, 2),
 ])
 def test_retrieval(lib, H, Hkv, d, B, R, n_vis, k):
     from visual_token_sparsity_gb300 import binding as sv
@@ -324,7 +325,7 @@ def test_retrieval_of_different_lengths(lib, Hkv, d, n_vis, k):
     assert (vis[5:] == -1).all()
 
 
-@pytest.mark.parametrize("n_vis,k", [(2000, 700), (20000, 9000)])
+@pytest.mark.parametrize("n_vis,k", [(2000, 700), (20000, 9000), (410000, 70000)])
 def test_scores_that_fp32_cannot_tell_apart(lib, n_vis, k):
     """The scores differ beyond fp32's last bit: 2^20 from one element, less than 2^-8
     from another; the selection is the exact one."""
@@ -345,7 +346,7 @@ def test_scores_that_fp32_cannot_tell_apart(lib, n_vis, k):
     assert status == 0 and np.array_equal(vis, want)
 
 
-@pytest.mark.parametrize("n_vis,k,kinds", [(600, 100, 3), (5000, 2500, 2), (30000, 11111, 7), (40, 39, 1)])
+@pytest.mark.parametrize("n_vis,k,kinds", [(600, 100, 3), (5000, 2500, 2), (30000, 11111, 7), (40, 39, 1), (411000, 200000, 2)])
 def test_tied_tokens_go_to_the_lower_index(lib, n_vis, k, kinds):
     """A few different rows, each many times over."""
     from visual_token_sparsity_gb300 import binding as sv

@@ -18,19 +18,25 @@
 // 48 bits and the best of them taken, ties to the lower index.
 #include "kernels.h"
 #include "kv8.cuh"
-#include "topk_block.cuh"
+#include "topk_cluster.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace sv {
 
 namespace {
 
 constexpr int kScoreWarps = 8;
-// |fp32 score - score| <= e = 137 * 2^-24 |qbar|_1 448 s: eight tiles of 17 terms,
-// each of which loses at most the last of 24 bits beside the largest, and the
-// rounding of the sum times s; 448 s bounds a key's elements.  2 e, rounded up:
-constexpr float kBand = 1.f / 32768.f;
+// |fp32 score - score| <= e = 2^-24 (272 |qbar|_max + 12 |qbar|_1) 448 s, as 448 s
+// bounds a key's elements: a tile's 16 products lose at most the last of 24 bits
+// beside the largest, and their sum, at most 16 of the largest, as much again (eight
+// tiles, and their parts' columns); seven sums of tiles, two of columns and three
+// products with factors round to 2^-24 of what is below |qbar|_1 448 s.  Two tokens
+// are told apart by 2 e; twice that is taken:
+constexpr float kBand = 448.f / 4194304.f;
+constexpr float kBandMax = 272.f, kBandSum = 12.f;
 constexpr int kListed = 1024;            // tokens next to the border that are ranked in shared memory
-constexpr int kStagedKeys = 52 * 1024;   // keys in shared memory
+constexpr int kStagedKeys = 16384;       // keys of a row whose selection one CTA makes in shared memory
 
 // hi + lo = a + b.
 __device__ __forceinline__ void two_sum(float a, float b, float& hi, float& lo) {
@@ -47,9 +53,10 @@ __device__ __forceinline__ void add48(float& hi, float& lo, float x, float y) {
   lo = __fadd_rn(e, -__fadd_rn(hi, -s));
 }
 
-__device__ __forceinline__ uint64_t order_key64(double x) {
-  const uint64_t f = (uint64_t)__double_as_longlong(x + 0.0);   // (-0 to 0)
-  return (f >> 63) ? ~f : (f | 0x8000000000000000ull);
+// An integer that orders like hi + lo, hi being the nearest float to it: hi
+// decides, then lo.  (Comparing doubles would take a unit that has two lanes.)
+__device__ __forceinline__ uint64_t order_key64(float hi, float lo) {
+  return (uint64_t)order_key(hi) << 32 | order_key(lo);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -65,41 +72,46 @@ template <int D>
 struct Query8 {
   float2 qbar[D];        // hi + lo
   uint16_t part[4][D];   // halves: qbar over 2^e in three parts, and 0
-  float back[2], l1;     // 2^e in two factors, sum of |qbar|
-  uint32_t top;          // largest factor of the pages that were scored (fp32 bits)
-  uint32_t pad[12];
+  float back[2];         // 2^e in two factors
+  float slack;           // 272 |qbar|_max + 12 |qbar|_1
+  uint32_t pad[13];
 };
 
 }  // namespace
 
+namespace {
+
+constexpr int kFusedRows = 16;       // query rows times heads that every scoring CTA sums itself
+
+// The row's query from R x G rows, by threads 0 .. D - 1 of a block of at least D
+// (all threads call this); the caller synchronises before it reads *o.
 template <int D>
-__global__ void __launch_bounds__(D)
-kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>* rows) {
+__device__ __forceinline__ void sum_query(const uint16_t* q, int R, int H, int Hkv, int row, Query8<D>* o) {
   __shared__ float part[2][D / 32];
-  grid_dep_sync();
-  const int row = blockIdx.x, b = row / Hkv, g = row - b * Hkv, G = H / Hkv, e = threadIdx.x;
+  const int b = row / Hkv, g = row - b * Hkv, G = H / Hkv, e = threadIdx.x;
   float hi = 0.f, lo = 0.f;
-  const uint16_t* src = q + ((size_t)b * R * H + (size_t)g * G) * D + e;
-  const int n = R * G;
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    float x[8];
+  if (e < D) {
+    const uint16_t* src = q + ((size_t)b * R * H + (size_t)g * G) * D + e;
+    const int n = R * G;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j, r = i / G;
-      x[j] = i < n ? __uint_as_float((uint32_t)__ldg(src + ((size_t)r * H + (i - r * G)) * D) << 16) : 0.f;
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j, r = i / G;
+        x[j] = i < n ? __uint_as_float((uint32_t)__ldg(src + ((size_t)r * H + (i - r * G)) * D) << 16) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) add48(hi, lo, x[j], 0.f);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) add48(hi, lo, x[j], 0.f);
-  }
-  const float a = fabsf(hi);
-  float s = warp_sum(a), top = warp_max(a);
-  if ((e & 31) == 0) {
-    part[0][e >> 5] = s;
-    part[1][e >> 5] = top;
+    const float a = fabsf(hi), s = warp_sum(a), top = warp_max(a);
+    if ((e & 31) == 0) {
+      part[0][e >> 5] = s;
+      part[1][e >> 5] = top;
+    }
   }
   __syncthreads();
-  s = 0.f;
-  top = 0.f;
+  if (e >= D) return;
+  float s = 0.f, top = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     s += part[0][i];
@@ -110,7 +122,6 @@ kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>
   const int x = (int)(__float_as_uint(top) >> 23) - 127 - 14;
   const float f0 = __uint_as_float((uint32_t)(127 - x / 2) << 23), f1 = __uint_as_float((uint32_t)(127 - (x - x / 2)) << 23);
   float h = hi * f0 * f1, l = lo * f0 * f1;
-  Query8<D>* o = rows + row;
   o->qbar[e] = make_float2(hi, lo);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -124,17 +135,28 @@ kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>
   if (e == 0) {
     o->back[0] = __uint_as_float((uint32_t)(127 + x / 2) << 23);
     o->back[1] = __uint_as_float((uint32_t)(127 + x - x / 2) << 23);
-    o->l1 = s;
-    o->top = 0u;
+    o->slack = kBandMax * top + kBandSum * s;
   }
 }
 
-// A warp per page, two pages in flight.
+}  // namespace
+
 template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32, 4)
+__global__ void __launch_bounds__(D)
+kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>* rows) {
+  grid_dep_sync();
+  sum_query<D>(q, R, H, Hkv, blockIdx.x, rows + blockIdx.x);
+}
+
+// A warp per page, one page in flight, as many warps as 48 registers allow.  SUM:
+// the query's rows are few, and every CTA adds them up itself (the first of a row
+// leaves the sum for the selection).
+template <int D, bool SUM>
+__global__ void __launch_bounds__(kScoreWarps * 32, 5)
 kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, float* __restrict__ scores,
-                 int pages_per_cta) {
-  constexpr int KS = D / 16, KC = D / 64;
+                 float* __restrict__ factors, int pages_per_cta) {
+  constexpr int KS = D / 16, KC = D / 64, W = kScoreWarps;
+  __shared__ __align__(16) Query8<D> query;
   grid_dep_sync();
   const int g = blockIdx.y, b = blockIdx.z, row = b * a.Hkv + g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q4 = lane & 3;
@@ -143,21 +165,17 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
     flag_status(a.status, kStatusBadLength);
   const int end = min((nv + 15) / 16, ((int)blockIdx.x + 1) * pages_per_cta);
   const int first = blockIdx.x * pages_per_cta + warp;
-  if (first >= end) return;
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
 
-  struct Page {
-    uint4 k[2][KC];        // keys r and r + 8
-    float s;
-    bool ok;
-  };
-  auto load = [&](int p, Page& x) {
-    x.ok = false;
-    if (p >= end) return;
-    const int page = __ldg(bt + p);
-    x.ok = page >= 0 && page < a.num_blocks;
-    if (!x.ok) {
-      if (lane == 0) flag_status(a.status, kStatusBadBlock);
+  uint4 k[2][KC];            // keys r and r + 8
+  float factor = 0.f;
+  bool ok = false;
+  // (the page's id was asked for a page of this warp before)
+  auto id_of = [&](int p) { return p < end ? __ldg(bt + p) : -1; };
+  auto load = [&](int p, int page) {
+    ok = page >= 0 && page < a.num_blocks;
+    if (!ok) {
+      if (p < end && lane == 0) flag_status(a.status, kStatusBadBlock);
       return;
     }
     const size_t unit = (size_t)page * a.Hkv + g;
@@ -165,63 +183,69 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < KC; ++c) x.k[i][c] = ld_stream16(src + i * 8 * D + c * 64);
-    x.s = __ldg(a.scales + unit * 2);
+      for (int c = 0; c < KC; ++c) k[i][c] = ld_stream16(src + i * 8 * D + c * 64);
+    factor = __ldg(a.scales + unit * 2);
   };
-  Page x, y;
-  load(first, x);
-  // (the query's parts: column r of a tile is part r, the columns behind are 0)
-  uint32_t qf[KS][2];
-  const Query8<D>* query = rows + row;
-#pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    const uint2 p = __ldg(reinterpret_cast<const uint2*>(&query->part[min(r, 3)][(k >> 2) * 64 + q4 * 16 + (k & 3) * 4]));
-    qf[k][0] = p.x;
-    qf[k][1] = p.y;
+  int next = id_of(first);
+  load(first, next);
+  next = id_of(first + W);
+  if constexpr (SUM) {
+    sum_query<D>(static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, row, &query);
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
+        reinterpret_cast<uint4*>(rows + row)[i] = reinterpret_cast<const uint4*>(&query)[i];
+  } else {
+    for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
+      reinterpret_cast<uint4*>(&query)[i] = reinterpret_cast<const uint4*>(rows + row)[i];
+    __syncthreads();
   }
-  const float back0 = query->back[0], back1 = query->back[1];
-  uint32_t top = 0;
+  // (the query's parts: column r of a tile is part r, the columns behind are 0)
+  const uint16_t* part = &query.part[min(r, 3)][q4 * 16];
   float* out = scores + (size_t)row * a.n_vis;
-  auto score = [&](int p, const Page& x) {
-    float c[2][4] = {};
+  float top = 0.f;             // the largest factor
+  for (int p = first; p < end; p += W) {
+    float c[4] = {};
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&x.k[0][k >> 2]);
-      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&x.k[1][k >> 2]);
-      const uint32_t y0 = w0[k & 3], y1 = w1[k & 3];
-      mma_f16(c[k & 1], kv8::e4m3x2_to_half2((uint16_t)y0), kv8::e4m3x2_to_half2((uint16_t)y1),
-              kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16)), qf[k][0], qf[k][1]);
+    for (int i = 0; i < KS; ++i) {
+      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&k[0][i >> 2]);
+      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&k[1][i >> 2]);
+      const uint32_t y0 = w0[i & 3], y1 = w1[i & 3];
+      const uint2 q = *reinterpret_cast<const uint2*>(part + (i >> 2) * 64 + (i & 3) * 4);
+      float z[4] = {};         // (a chain of tiles would lose bits beside their running sum)
+      mma_f16(z, kv8::e4m3x2_to_half2((uint16_t)y0), kv8::e4m3x2_to_half2((uint16_t)y1),
+              kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16)), q.x, q.y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = __fadd_rn(c[e], z[e]);
     }
+    const bool there = ok;
+    const float f = factor;
+    load(p + W, next);
+    next = id_of(p + 2 * W);
     // columns 0 and 1 are lane 4 r's, column 2 is its neighbour's
-    const float z0 = __shfl_down_sync(0xffffffffu, c[0][0] + c[1][0], 1), z1 = __shfl_down_sync(0xffffffffu, c[0][2] + c[1][2], 1);
-    const float s0 = (c[0][0] + c[1][0]) + ((c[0][1] + c[1][1]) + z0), s1 = (c[0][2] + c[1][2]) + ((c[0][3] + c[1][3]) + z1);
+    const float z0 = __shfl_down_sync(0xffffffffu, c[0], 1), z1 = __shfl_down_sync(0xffffffffu, c[2], 1);
+    const float s0 = c[0] + (c[1] + z0), s1 = c[2] + (c[3] + z1);
     const int pos = p * 16 + r;
     if (q4 == 0) {
       // (NaN without a sign, so that its key is the largest)
       auto value = [&](float v) {
-        v = (v * back0) * (x.s * back1);
-        return !x.ok ? 0.f : isnan(v) ? __uint_as_float(0x7fffffffu) : v;
+        v = (v * query.back[0]) * (f * query.back[1]);
+        return !there ? 0.f : isnan(v) ? __uint_as_float(0x7fffffffu) : v;
       };
       if (pos < nv) out[pos] = value(s0);
       if (pos + 8 < nv) out[pos + 8] = value(s1);
     }
-    if (x.ok) top = max(top, __float_as_uint(fabsf(x.s)));
-  };
-  for (int p = first; p < end; p += 2 * kScoreWarps) {
-    load(p + kScoreWarps, y);
-    score(p, x);
-    load(p + 2 * kScoreWarps, x);
-    if (p + kScoreWarps < end) score(p + kScoreWarps, y);
+    if (there) top = fmaxf(top, fabsf(f));
   }
-  if (lane == 0 && top != 0) atomicMax(&rows[row].top, top);   // (a maximum: the order does not matter)
+  if (lane == 0) factors[((size_t)row * gridDim.x + blockIdx.x) * W + warp] = top;
 }
 
 namespace {
 
 struct BorderShared {
-  double list_v[kListed];
+  uint64_t list_v[kListed];
   int list_j[kListed];
-  int sure, near, listed, digit, above, last_j;
+  int sure, near, digit, above, last_j;
   unsigned long long last;
   uint32_t kth[32];
   uint32_t scan_tmp[33];
@@ -230,7 +254,7 @@ struct BorderShared {
 
 // The score of token j with 48 bits, by eight lanes (lane % 8 == 0 has it).
 template <int D>
-__device__ __forceinline__ double score48(const Kv8RetrieveArgs& a, const Query8<D>* query, int b, int g, int j, bool on,
+__device__ __forceinline__ uint64_t score48(const Kv8RetrieveArgs& a, const Query8<D>* query, int b, int g, int j, bool on,
                                           int lane) {
   float hi = 0.f, lo = 0.f, s = 0.f;
   if (on) {
@@ -264,34 +288,64 @@ __device__ __forceinline__ double score48(const Kv8RetrieveArgs& a, const Query8
     hi = x;
     lo = xl;
   }
-  return ((double)hi + (double)lo) * (double)s;
+  // times s, which need not be a power of two
+  const float p = __fmul_rn(hi, s), e = __fadd_rn(fmaf(hi, s, -p), __fmul_rn(lo, s));
+  two_sum(p, e, hi, lo);
+  return order_key64(hi, lo);
 }
 
-// Selects the k tokens of a row, given its keys (in shared memory) and the k-th
-// largest of them.  All threads of the block call this.
+// Keys [lo, hi] around a border may lie on its other side.  Every selected fp32
+// score is at least the border's value and every other one below it, so that is as
+// good a middle as the k-th score.  Scores or a band that are not finite: the fp32
+// order, ties included.
+struct Near {
+  uint32_t lo, hi;
+  bool wide;
+};
+__device__ __forceinline__ Near near_border(const TopkBorder& t, float band) {
+  const float at = (t.prefix & 0x80000000u) ? __uint_as_float(t.prefix ^ 0x80000000u) : __uint_as_float(~t.prefix);
+  Near x;
+  x.wide = band > 0.f && isfinite(band) && isfinite(at);
+  x.lo = x.wide ? order_key(at - band) : t.prefix;
+  x.hi = x.wide ? order_key(at + band) : t.prefix | ~t.pmask;
+  return x;
+}
+
+// The largest of a row's factors, by a whole warp.
+__device__ __forceinline__ float largest_factor(const float* factors, int n, int lane) {
+  float x = 0.f;
+  for (int i = lane; i < n; i += 32) x = fmaxf(x, __ldcg(factors + i));
+  return warp_max(x);
+}
+
+// Selects the k tokens of a row, given its keys and their border.  All threads of
+// the block call this.
 template <int D>
 __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query8<D>* query, int b, int g, int n, int k,
-                                           uint32_t* keys, uint32_t kth, double* exact, int32_t* dst, BorderShared& sh) {
+                                           uint32_t* keys, const TopkBorder& border, float factor, uint64_t* exact,
+                                           int32_t* dst, BorderShared& sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  const float at = (kth & 0x80000000u) ? __uint_as_float(kth ^ 0x80000000u) : __uint_as_float(~kth);
-  const float band = query->l1 * (448.f * kBand) * __uint_as_float(query->top);
-  // (scores or a band that are not finite: the fp32 order, ties included)
-  const bool wide = band > 0.f && isfinite(band) && isfinite(at);
-  const uint32_t hi = wide ? order_key(at + band) : kth, lo = wide ? order_key(at - band) : kth;
-  if (tid == 0) sh.sure = sh.near = sh.listed = 0;
+  const Near near = near_border(border, query->slack * kBand * factor);
+  const uint32_t lo = near.lo, hi = near.hi;
+  const bool wide = near.wide;
+  if (tid == 0) sh.sure = sh.near = 0;
   __syncthreads();
-  int in = 0, by = 0;
-  for (int i = tid; i < n; i += nt) {
-    const uint32_t key = keys[i];
-    in += key > hi;
-    by += key >= lo && key <= hi;
+  int in = 0;
+  for (int i0 = tid; i0 < n; i0 += 4 * nt) {
+    uint32_t key[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) key[j] = i0 + j * nt < n ? keys[i0 + j * nt] : 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      in += key[j] > hi;
+      if (key[j] >= lo && key[j] <= hi) {
+        const int at_list = atomicAdd(&sh.near, 1);
+        if (at_list < kListed) sh.list_j[at_list] = i0 + j * nt;
+      }
+    }
   }
   in = __reduce_add_sync(0xffffffffu, in);
-  by = __reduce_add_sync(0xffffffffu, by);
-  if (lane == 0) {
-    atomicAdd(&sh.sure, in);
-    atomicAdd(&sh.near, by);
-  }
+  if (lane == 0) atomicAdd(&sh.sure, in);
   __syncthreads();
   const int need = k - sh.sure, m = sh.near;     // of the m tokens next to the border
   bool by_value = false;                         // taken by (value, index), not all
@@ -299,25 +353,21 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
     const bool listed = m <= kListed;
     by_value = !listed;
     if (listed) {
-      for (int i = tid; i < n; i += nt) {
-        const uint32_t key = keys[i];
-        if (key >= lo && key <= hi) sh.list_j[atomicAdd(&sh.listed, 1)] = i;
-      }
-      __syncthreads();
       for (int i0 = warp * 4; i0 < m; i0 += nw * 4) {
         const int i = i0 + (lane >> 3);
         const int j = i < m ? sh.list_j[i] : 0;
         // (exact ties of scores that are not told apart at all: by index alone)
-        const double v = wide ? score48<D>(a, query, b, g, j, i < m, lane) : 0.0;
+        const uint64_t v = wide ? score48<D>(a, query, b, g, j, i < m, lane) : 0ull;
         if (i < m && (lane & 7) == 0) sh.list_v[i] = v;
       }
       __syncthreads();
-      for (int i = tid; i < m; i += nt) {
-        const double v = sh.list_v[i];
+      for (int i = warp; i < m; i += nw) {
+        const uint64_t v = sh.list_v[i];
         const int j = sh.list_j[i];
         int better = 0;
-        for (int o = 0; o < m; ++o) better += sh.list_v[o] > v || (sh.list_v[o] == v && sh.list_j[o] < j);
-        if (better >= need) keys[j] = 0u;             // (no score's key)
+        for (int o = lane; o < m; o += 32) better += sh.list_v[o] > v || (sh.list_v[o] == v && sh.list_j[o] < j);
+        better = __reduce_add_sync(0xffffffffu, better);
+        if (lane == 0 && better >= need) keys[j] = 0u;             // (no score's key)
       }
     } else {
       for (int i0 = warp * 32; i0 < n; i0 += nt) {
@@ -332,7 +382,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
             if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
             todo &= todo - 1;
           }
-          const double v = wide ? score48<D>(a, query, b, g, max(j, 0), j >= 0, lane) : 0.0;
+          const uint64_t v = wide ? score48<D>(a, query, b, g, max(j, 0), j >= 0, lane) : 0ull;
           if (j >= 0 && (lane & 7) == 0) exact[j] = v;
         }
       }
@@ -346,7 +396,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
         for (int i = tid; i < n; i += nt) {
           const uint32_t key = keys[i];
           if (key < lo || key > hi) continue;
-          const uint64_t kv = order_key64(exact[i]);
+          const uint64_t kv = exact[i];
           const uint32_t ki = ~(uint32_t)i;
           if (pass < 8) {
             if (pass > 0 && (kv ^ top) >> (64 - 8 * pass)) continue;
@@ -379,7 +429,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
   auto taken = [&](int i) {
     const uint32_t key = keys[i];
     if (!by_value || key < lo || key > hi) return key >= lo;
-    const uint64_t v = order_key64(exact[i]);
+    const uint64_t v = exact[i];
     return v > sh.last || (v == sh.last && i <= sh.last_j);
   };
   const int seg = (n + nt - 1) / nt, s0 = min(n, tid * seg), s1 = min(n, s0 + seg);
@@ -392,54 +442,229 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
 
 }  // namespace
 
-// The selection of one row per CTA.  KNOWN: a cluster has already taken the k
-// largest fp32 scores (vis_idx), and the k-th is their smallest.
+// The selection of one row per CTA.  KNOWN: the keys of rows that are too long for
+// shared memory go to `far_keys`, the k largest fp32 scores have been taken
+// (vis_idx), and the k-th is their smallest.
 template <int D, bool KNOWN>
 __global__ void __launch_bounds__(1024)
 kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows, const float* __restrict__ scores,
-                  double* __restrict__ exact, uint32_t* __restrict__ far_keys) {
+                  const float* __restrict__ factors, int n_factors, uint64_t* __restrict__ exact,
+                  uint32_t* __restrict__ far_keys) {
   extern __shared__ __align__(16) uint32_t staged[];
   __shared__ TopkShared ts;
   __shared__ BorderShared sh;
   grid_dep_sync();
   const int row = blockIdx.x, b = row / a.Hkv, g = row - b * a.Hkv;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  (void)warp;
   int n = a.n_vis, k = a.k;
   if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
   int32_t* dst = a.vis_idx + (size_t)row * a.k;
   const float* src = scores + (size_t)row * a.n_vis;
-  uint32_t* keys = far_keys != nullptr ? far_keys + (size_t)row * a.n_vis : staged;
+  uint32_t* keys = KNOWN ? far_keys + (size_t)row * a.n_vis : staged;
   if (!KNOWN) fill_unselected(dst, k, a.k);
   if (k <= 0) return;
-  uint32_t kth = 0xffffffffu;
+  const float factor = largest_factor(factors + (size_t)row * n_factors, n_factors, lane);
+  TopkBorder border;
   if (KNOWN) {
-    for (int i = tid; i < k; i += nt) kth = min(kth, order_key(__ldcg(src + __ldcg(dst + i))));
-    for (int i = tid; i < n; i += nt) keys[i] = order_key(__ldcg(src + i));
+    uint32_t kth = 0xffffffffu;
+    for (int i0 = tid; i0 < n; i0 += 8 * nt) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __ldcg(src + min(i0 + j * nt, n - 1));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * nt < n) keys[i0 + j * nt] = order_key(x[j]);
+    }
+    __syncthreads();
+    for (int i0 = tid; i0 < k; i0 += 4 * nt) {
+      int at[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) at[j] = __ldcg(dst + min(i0 + j * nt, k - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kth = min(kth, keys[at[j]]);
+    }
+    kth = __reduce_min_sync(0xffffffffu, kth);
+    if (lane == 0) sh.kth[warp] = kth;
+    __syncthreads();
+    for (int w = 0; w < nt / 32; ++w) kth = min(kth, sh.kth[w]);
+    border = TopkBorder{kth, 0xffffffffu, 0};
   } else {
-    const TopkBorder t = block_topk_border(src, n, k, keys, ts);
-    for (int i = tid; i < n; i += nt) {
-      const uint32_t key = keys[i];
-      if ((key & t.pmask) >= t.prefix) kth = min(kth, key);
+    border = block_topk_border(src, n, k, keys, ts);
+  }
+  select_row<D>(a, rows + row, b, g, n, k, keys, border, factor, exact + (size_t)row * a.n_vis, dst, sh);
+}
+
+// The same for a long row by a cluster: CTA r has its r-th slice.
+template <int D>
+__global__ void __cluster_dims__(kTopkClusterCtas, 1, 1) __launch_bounds__(kTopkClusterThreads)
+kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows,
+                          const float* __restrict__ scores, const float* __restrict__ factors, int n_factors,
+                          uint64_t* __restrict__ exact_rows) {
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ ClusterTopkShared ts;
+  __shared__ BorderShared sh;
+  grid_dep_sync();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), row = blockIdx.y, b = row / a.Hkv, g = row - b * a.Hkv;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  int n = a.n_vis, k = a.k;
+  if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
+  int32_t* dst = a.vis_idx + (size_t)row * a.k;
+  if (rank == 0) fill_unselected(dst, k, a.k);
+  if (k <= 0) return;                        // (the whole cluster)
+  const int slice = (n + kTopkClusterCtas - 1) / kTopkClusterCtas;
+  const int first = min(n, rank * slice), len = min(n, first + slice) - first;
+  const Query8<D>* query = rows + row;
+  uint64_t* exact = exact_rows + (size_t)row * a.n_vis + first;
+  const float factor = largest_factor(factors + (size_t)row * n_factors, n_factors, lane);
+  if (tid == 0) sh.sure = sh.near = 0;       // (the search below has barriers)
+  const TopkBorder t = cluster_topk_border(scores + (size_t)row * a.n_vis + first, len, k, keys, ts);
+  const Near x = near_border(t, query->slack * kBand * factor);
+  const uint32_t lo = x.lo, hi = x.hi;
+  const bool wide = x.wide;
+  int in = 0;
+  for (int i = tid; i < len; i += nt) {
+    const uint32_t key = keys[i];
+    in += key > hi;
+    if (key >= lo && key <= hi) {
+      const int at_list = atomicAdd(&sh.near, 1);
+      if (at_list < kListed) sh.list_j[at_list] = i;
     }
   }
-  kth = __reduce_min_sync(0xffffffffu, kth);
-  if (lane == 0) sh.kth[warp] = kth;
-  __syncthreads();
-  for (int w = 0; w < nt / 32; ++w) kth = min(kth, sh.kth[w]);
-  select_row<D>(a, rows + row, b, g, n, k, keys, kth, exact + (size_t)row * a.n_vis, dst, sh);
+  in = __reduce_add_sync(0xffffffffu, in);
+  if (lane == 0) atomicAdd(&sh.sure, in);
+  cluster.sync();
+  int sure = 0, m = 0, most = 0;
+#pragma unroll
+  for (int r = 0; r < kTopkClusterCtas; ++r) {
+    const int near = *cluster.map_shared_rank(&sh.near, r);
+    sure += *cluster.map_shared_rank(&sh.sure, r);
+    m += near;
+    most = max(most, near);
+  }
+  const int need = k - sure, mine = sh.near;
+  bool by_value = false;
+  if (m > need) {
+    by_value = most > kListed;
+    if (!by_value) {
+      for (int i0 = warp * 4; i0 < mine; i0 += nw * 4) {
+        const int i = i0 + (lane >> 3);
+        const int j = i < mine ? sh.list_j[i] : 0;
+        const uint64_t v = wide ? score48<D>(a, query, b, g, first + j, i < mine, lane) : 0ull;
+        if (i < mine && (lane & 7) == 0) sh.list_v[i] = v;
+      }
+      cluster.sync();
+      // ranked against every CTA's list (slices are in order of index)
+      for (int i = warp; i < mine; i += nw) {
+        const uint64_t v = sh.list_v[i];
+        const int j = sh.list_j[i];
+        int better = 0;
+        for (int r = 0; r < kTopkClusterCtas; ++r) {
+          const int theirs = *cluster.map_shared_rank(&sh.near, r);
+          const uint64_t* values = cluster.map_shared_rank(&sh.list_v[0], r);
+          const int* indices = cluster.map_shared_rank(&sh.list_j[0], r);
+          for (int o = lane; o < theirs; o += 32)
+            better += values[o] > v || (values[o] == v && (r < rank || (r == rank && indices[o] < j)));
+        }
+        better = __reduce_add_sync(0xffffffffu, better);
+        if (lane == 0 && better >= need) keys[j] = 0u;             // (no score's key)
+      }
+    } else {
+      for (int i0 = warp * 32; i0 < len; i0 += nt) {
+        const uint32_t key = i0 + lane < len ? keys[i0 + lane] : 0u;
+        uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < len && key >= lo && key <= hi);
+        while (todo) {
+          int j = -1;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int bit = __ffs(todo) - 1;
+            if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
+            todo &= todo - 1;
+          }
+          const uint64_t v = wide ? score48<D>(a, query, b, g, first + max(j, 0), j >= 0, lane) : 0ull;
+          if (j >= 0 && (lane & 7) == 0) exact[j] = v;
+        }
+      }
+      for (int i = tid; i < 512; i += nt) (&ts.hist[0][0])[i] = 0;
+      unsigned long long top = 0;
+      uint32_t low = 0;
+      int left = need;
+      cluster.sync();
+      for (int pass = 0; pass < 12; ++pass) {
+        int* hist = ts.hist[pass & 1];
+        for (int i = tid; i < len; i += nt) {
+          const uint32_t key = keys[i];
+          if (key < lo || key > hi) continue;
+          const uint64_t kv = exact[i];
+          const uint32_t ki = ~(uint32_t)(first + i);
+          if (pass < 8) {
+            if (pass > 0 && (kv ^ top) >> (64 - 8 * pass)) continue;
+            atomicAdd(&hist[(kv >> (56 - 8 * pass)) & 255], 1);
+          } else {
+            if (kv != top || (pass > 8 && (ki ^ low) >> (32 - 8 * (pass - 8)))) continue;
+            atomicAdd(&hist[(ki >> (24 - 8 * (pass - 8))) & 255], 1);
+          }
+        }
+        cluster.sync();
+        for (int i = tid; i < 256; i += nt) {
+          int sum = 0;
+#pragma unroll
+          for (int r = 0; r < kTopkClusterCtas; ++r) sum += cluster.map_shared_rank(hist, r)[i];
+          ts.total[i] = sum;
+          ts.hist[(pass + 1) & 1][i] = 0;            // (last read by peers before this pass's barrier)
+        }
+        __syncthreads();
+        if (tid == 0) {
+          int sum = 0, d = 255;
+          while (d > 0 && sum + ts.total[d] < left) sum += ts.total[d--];
+          sh.digit = d;
+          sh.above = sum;
+        }
+        __syncthreads();
+        left -= sh.above;
+        if (pass < 8) top |= (unsigned long long)sh.digit << (56 - 8 * pass);
+        else low |= (uint32_t)sh.digit << (24 - 8 * (pass - 8));
+        __syncthreads();
+      }
+      if (tid == 0) {
+        sh.last = top;
+        sh.last_j = (int)~low;
+      }
+    }
+    __syncthreads();
+  }
+  auto taken = [&](int i) {
+    const uint32_t key = keys[i];
+    if (!by_value || key < lo || key > hi) return key >= lo;
+    const uint64_t v = exact[i];
+    return v > sh.last || (v == sh.last && first + i <= sh.last_j);
+  };
+  const int seg = (len + nt - 1) / nt, s0 = min(len, tid * seg), s1 = min(len, s0 + seg);
+  uint32_t count = 0;
+  for (int i = s0; i < s1; ++i) count += taken(i);
+  uint32_t o = block_exclusive_scan<uint32_t>(count, sh.scan_tmp);
+  if (tid == nt - 1) ts.cnt[0] = (int)(o + count);
+  cluster.sync();
+  for (int r = 0; r < rank; ++r) o += (uint32_t)*cluster.map_shared_rank(&ts.cnt[0], r);
+  for (int i = s0; i < s1; ++i)
+    if (taken(i)) dst[o++] = first + i;
+  cluster.sync();     // keep this CTA's shared memory alive until every peer has read it
 }
 
 // Workspace: queries | 48-bit scores of tokens next to a crowded border | fp32
-// scores | keys of rows that are too long for shared memory
+// scores | the largest factor of each scoring CTA's pages | keys of rows that are
+// too long for shared memory
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t kv8_retrieve_workspace_bytes(int B, int Hkv, int D, int n_vis) {
   const size_t rows = (size_t)B * Hkv;
-  return up256(rows * (D == 128 ? sizeof(Query8<128>) : sizeof(Query8<64>))) + up256(rows * n_vis * sizeof(double)) +
-         up256(rows * n_vis * sizeof(float)) * (n_vis > kStagedKeys ? 2 : 1);
+  return up256(rows * (D == 128 ? sizeof(Query8<128>) : sizeof(Query8<64>))) + up256(rows * n_vis * sizeof(uint64_t)) +
+         up256(rows * ((n_vis + 15) / 16 + kScoreWarps) * sizeof(float)) + up256(rows * n_vis * sizeof(float)) * (n_vis > kStagedKeys && !topk_cluster_fits(n_vis) ? 2 : 1);
 }
 
 template <int D, bool KNOWN>
-static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores, double* exact,
+static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores,
+                                 const float* factors, int n_factors, uint64_t* exact,
                                  uint32_t* far_keys, cudaStream_t stream) {
   auto kernel = kv8_select_kernel<D, KNOWN>;
   static bool attr_set[64] = {};
@@ -451,9 +676,27 @@ static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int threads = a.n_vis >= 16384 ? 1024 : (a.n_vis >= 8192 ? 512 : 256);
+  const int threads = KNOWN ? 1024 : a.n_vis >= 8192 ? 512 : 256;
   return launch_dependent(kernel, dim3((unsigned)(a.batch * a.Hkv)), dim3(threads),
-                          far_keys != nullptr ? (size_t)0 : (size_t)a.n_vis * 4, stream, a, rows, scores, exact, far_keys);
+                          KNOWN ? (size_t)0 : (size_t)a.n_vis * 4, stream, a, rows, scores, factors, n_factors, exact, far_keys);
+}
+
+template <int D>
+static cudaError_t launch_select_cluster(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores,
+                                         const float* factors, int n_factors, uint64_t* exact, cudaStream_t stream) {
+  auto kernel = kv8_select_cluster_kernel<D>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int slice = (a.n_vis + kTopkClusterCtas - 1) / kTopkClusterCtas;
+  return launch_dependent(kernel, dim3(kTopkClusterCtas, (unsigned)(a.batch * a.Hkv)), dim3(kTopkClusterThreads),
+                          (size_t)slice * sizeof(uint32_t), stream, a, rows, scores, factors, n_factors, exact);
 }
 
 template <int D>
@@ -466,30 +709,38 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
     return p;
   };
   Query8<D>* query = reinterpret_cast<Query8<D>*>(take((size_t)rows * sizeof(Query8<D>)));
-  double* exact = reinterpret_cast<double*>(take((size_t)rows * a.n_vis * sizeof(double)));
+  uint64_t* exact = reinterpret_cast<uint64_t*>(take((size_t)rows * a.n_vis * sizeof(uint64_t)));
   float* scores = reinterpret_cast<float*>(take((size_t)rows * a.n_vis * sizeof(float)));
-  uint32_t* far_keys = a.n_vis > kStagedKeys ? reinterpret_cast<uint32_t*>(at) : nullptr;
+  float* factors = reinterpret_cast<float*>(take((size_t)rows * ((a.n_vis + 15) / 16 + kScoreWarps) * sizeof(float)));
+  uint32_t* far_keys = reinterpret_cast<uint32_t*>(at);      // (there where it is used)
   if (a.scores != nullptr) scores = a.scores;
-  cudaError_t e = launch_dependent(kv8_qbar_kernel<D>, dim3(rows), dim3(D), 0, stream,
-                                   static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, query);
-  if (e != cudaSuccess) return e;
-  // pages per CTA: two per warp at a time
+  // pages per CTA: a multiple of its warps, for two rounds of resident CTAs (of 4, 5,
+  // 10, 12 and 20 CTAs per SM ten are the fastest: LLaVA-NeXT batch 16 48 us at 10 and
+  // more, 50 at 5; LongVILA batch 8 58, 62 at 5)
   const int pages = (a.n_vis + 15) / 16;
-  const long long ctas = (long long)num_sms * 12;
+  const long long ctas = (long long)num_sms * 10;
   long long per = ((long long)pages * rows + ctas - 1) / ctas;
-  per = (per + 2 * kScoreWarps - 1) / (2 * kScoreWarps) * (2 * kScoreWarps);
+  per = (per + kScoreWarps - 1) / kScoreWarps * kScoreWarps;
   if (per > pages) per = pages;
-  e = launch_dependent(kv8_score_kernel<D>, dim3((unsigned)((pages + per - 1) / per), a.Hkv, a.batch),
-                       dim3(kScoreWarps * 32), 0, stream, a, query, scores, (int)per);
+  const long long per_row = (pages + per - 1) / per;
+  // (the sums of few rows in every CTA cost less than a launch before them:
+  // LongVILA batch 8, seven heads, 58 us, not 71)
+  const bool sum = (long long)a.R * (a.H / a.Hkv) <= kFusedRows;
+  cudaError_t e = cudaSuccess;
+  if (!sum)
+    e = launch_dependent(kv8_qbar_kernel<D>, dim3(rows), dim3(D), 0, stream, static_cast<const uint16_t*>(a.q), a.R, a.H,
+                         a.Hkv, query);
   if (e != cudaSuccess) return e;
-  // (a CTA per row as long as rows are short: as topk_prefers_cluster)
-  if (!topk_prefers_cluster(a.n_vis) && far_keys == nullptr)
-    return launch_select<D, false>(a, query, scores, exact, nullptr, stream);
-  e = topk_prefers_cluster(a.n_vis)
-          ? launch_topk_cluster(scores, rows, a.n_vis, a.k, a.vis_idx, stream, a.lens, a.Hkv)
-          : launch_topk_rows(scores, rows, a.n_vis, a.k, a.vis_idx, stream, a.lens, a.Hkv);
+  e = launch_dependent(sum ? kv8_score_kernel<D, true> : kv8_score_kernel<D, false>, dim3((unsigned)per_row, a.Hkv, a.batch),
+                       dim3(kScoreWarps * 32), 0, stream, a, query, scores, factors, (int)per);
   if (e != cudaSuccess) return e;
-  return launch_select<D, true>(a, query, scores, exact, far_keys, stream);
+  // a CTA per row as long as rows are short, else a cluster (as topk_prefers_cluster),
+  // and for rows that do not fit one either a CTA over their keys in memory
+  if (a.n_vis <= kStagedKeys) return launch_select<D, false>(a, query, scores, factors, (int)per_row * kScoreWarps, exact, nullptr, stream);
+  if (topk_cluster_fits(a.n_vis)) return launch_select_cluster<D>(a, query, scores, factors, (int)per_row * kScoreWarps, exact, stream);
+  e = launch_topk_rows(scores, rows, a.n_vis, a.k, a.vis_idx, stream, a.lens, a.Hkv);
+  if (e != cudaSuccess) return e;
+  return launch_select<D, true>(a, query, scores, factors, (int)per_row * kScoreWarps, exact, far_keys, stream);
 }
 
 cudaError_t launch_kv8_retrieve(const Kv8RetrieveArgs& a, int D, int num_sms, cudaStream_t stream) {
