@@ -259,7 +259,7 @@ struct Kv8AttnArgs {
   // set by launch_kv8_attn: pieces that the work is cut into, their partial
   // results and the counters of the units that they share (nullptr: the merge
   // kernel joins them)
-  int pieces;
+  int pieces, per_unit;            // (blocks of a unit, with equal counts)
   float* part_ml;
   float* part_o;
   int* split_done;

@@ -22,6 +22,10 @@ using namespace nr;
 namespace {
 
 constexpr int kWarps = 4;
+// Groups of query rows at a time, and CTAs per SM that the registers leave: of 1 to 3
+// groups and 6 to 8 CTAs within 2 % of one another (a prompt of 13441 tokens of 36
+// heads 67 to 69 us; one group 74), eight the fastest for single tokens.
+constexpr int kAhead = 2, kCtas = 8;
 constexpr int kWarpsPerSm = 64;   // warps that the queries spread over before a warp takes more rows
 
 // Token range of sequence b: [begin, end) of the packed rows.  False where the
@@ -83,15 +87,7 @@ struct Turns {
     cs[0] = cs[1] = fm::splat2(1.f);
     sn[0] = sn[1] = 0;
   }
-  __device__ __forceinline__ void load(const Kv8AppendArgs& a, const int* p, int j) {
-    const int half = a.rot >> 1;
-    float2 f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int pr = 4 * j + i;
-      const int px = pr < a.sec_end[0] ? p[0] : pr < a.sec_end[1] ? p[1] : p[2];
-      f[i] = __ldg(reinterpret_cast<const float2*>(a.cos_sin) + (size_t)px * half + pr);
-    }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       cs[i] = fm::pack2(f[2 * i].x, f[2 * i + 1].x);
@@ -99,6 +95,15 @@ struct Turns {
     }
   }
 };
+__device__ __forceinline__ void load_turns(const Kv8AppendArgs& a, const int* p, int j, float2 (&f)[4]) {
+  const int half = a.rot >> 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pr = 4 * j + i;
+    const int px = pr < a.sec_end[0] ? p[0] : pr < a.sec_end[1] ? p[1] : p[2];
+    f[i] = __ldg(reinterpret_cast<const float2*>(a.cos_sin) + (size_t)px * half + pr);
+  }
+}
 
 // This lane's part of a row.
 template <int L, bool INTER>
@@ -258,7 +263,7 @@ __device__ __forceinline__ uint32_t warp_top(uint32_t top) {
 // Warps [0, q_warps): query rows, `per_warp` of one token each; behind them a
 // warp for the keys and one for the values of every (page, KV head).
 template <int L, bool INTER, bool NORM, bool PARTLY>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kCtas)
 kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_t warps_per_token, uint32_t q_warps,
                   uint32_t kv_warps) {
   constexpr int D = 8 * L, RPG = 32 / L;
@@ -278,7 +283,6 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
     }
   }
   const Place<L, INTER> at(a.rot, lane);
-  const bool mine = at.sub < RPG;
   Turns t;
   t.none();
 
@@ -286,27 +290,45 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
     const int tok = (int)(w / warps_per_token);
     const int r0 = (int)(w - (uint32_t)tok * warps_per_token) * per_warp, r1 = min(r0 + per_warp, a.H);
     if (a.seq_start != nullptr && (tok < __ldg(a.seq_start) || tok >= __ldg(a.seq_start + a.batch))) return;
+    const uint16_t* src = a.q + (size_t)tok * a.q_stride;
+    uint16_t* dst = a.q_out + (size_t)tok * a.H * D;
+    // kAhead groups of rows at a time, the next ones on their way
+    Lane8<INTER> x[kAhead], next[kAhead];
+    auto load = [&](Lane8<INTER>* to, int r) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = r + i * RPG + at.sub;
+        to[i].u = make_uint4(0u, 0u, 0u, 0u);
+        if (row < r1) to[i].load(src + (size_t)row * D, at.off0, at.off1);
+      }
+    };
+    load(x, r0);
     int p[3] = {0, 0, 0};
     if (!positions(a, tok, p)) {
       if (r0 == 0 && lane == 0) flag_status(a.status, kStatusBadPosition);
       return;
     }
-    if (at.turned) t.load(a, p, at.j);
+    if (at.turned) {
+      float2 f[4];
+      load_turns(a, p, at.j, f);
+      t.set(f);
+    }
     uint64_t gp[2], gy[2];
     if (NORM && a.q_weight != nullptr) {
       Lane8<INTER> g;
       g.load(a.q_weight, at.off0, at.off1);
       g.unpack(gp, gy);
     }
-    const uint16_t* src = a.q + (size_t)tok * a.q_stride;
-    uint16_t* dst = a.q_out + (size_t)tok * a.H * D;
-    for (int r = r0; r < r1; r += RPG) {
-      const int row = r + at.sub;
-      Lane8<INTER> x;
-      x.u = make_uint4(0u, 0u, 0u, 0u);
-      if (mine && row < r1) x.load(src + (size_t)row * D, at.off0, at.off1);
-      x = turn_rows<L, INTER, NORM, PARTLY>(x, gp, gy, NORM ? a.q_weight : nullptr, t, at, a.eps);
-      if (mine && row < r1) x.store(dst + (size_t)row * D, at.off0, at.off1);
+#pragma unroll 1
+    for (int r = r0; r < r1; r += kAhead * RPG) {
+      load(next, r + kAhead * RPG);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = r + i * RPG + at.sub;
+        x[i] = turn_rows<L, INTER, NORM, PARTLY>(x[i], gp, gy, NORM ? a.q_weight : nullptr, t, at, a.eps);
+        if (row < r1) x[i].store(dst + (size_t)row * D, at.off0, at.off1);
+        x[i] = next[i];
+      }
     }
     return;
   }
@@ -316,7 +338,12 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
   Unit x;
   if (!unit_of(a, (item >> 1) / (uint32_t)a.Hkv, lane, lane == 0 && g == 0 && which == 0, x)) return;
   uint16_t* sm = rows[warp];
-  uint32_t top = 0, there = 0;        // slots (from r0 on) whose tokens are written
+  uint32_t top = 0;
+  // the tokens' positions, a lane each; which of them are written
+  int p[3] = {0, 0, 0};
+  const bool fine = lane < x.n && positions(a, x.t0 + lane, p);
+  const uint32_t there = __ballot_sync(0xffffffffu, fine);
+  if (lane < x.n && !fine && g == 0 && which == 0) flag_status(a.status, kStatusBadPosition);
 
   if (which == 0) {
     uint64_t gp[2], gy[2];
@@ -325,37 +352,52 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
       gw.load(a.k_weight, at.off0, at.off1);
       gw.unpack(gp, gy);
     }
-    for (int i = 0; i < x.n; i += RPG) {
-      const int tok = x.t0 + i + at.sub;
-      const bool in = mine && i + at.sub < x.n;
-      int p[3] = {0, 0, 0};
-      const bool ok = in && positions(a, tok, p);
-      if (in && !ok && g == 0 && at.j == 0) flag_status(a.status, kStatusBadPosition);
-      t.none();
-      if (ok && at.turned) t.load(a, p, at.j);
-      Lane8<INTER> v;
-      v.u = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) v.load(a.k + (size_t)tok * a.k_stride + (size_t)g * D, at.off0, at.off1);
-      v = turn_rows<L, INTER, NORM, PARTLY>(v, gp, gy, NORM ? a.k_weight : nullptr, t, at, a.eps);
-      const uint32_t oks = __ballot_sync(0xffffffffu, ok && at.j == 0);
+    // one group of rows with its turns, the next one on its way
+    Lane8<INTER> v, next;
+    float2 f[4], next_f[4];
+    auto load = [&](int i0, Lane8<INTER>& to, float2 (&turns)[4]) {
+      const int i = i0 + at.sub;
+      int q[3];
 #pragma unroll
-      for (int r = 0; r < RPG; ++r) there |= ((oks >> (r * L)) & 1u) << (i + r);
+      for (int e = 0; e < 3; ++e) q[e] = __shfl_sync(0xffffffffu, p[e], i & 31);
+      to.u = make_uint4(0u, 0u, 0u, 0u);
+      if (i < 16 && (there >> i) & 1) {
+        to.load(a.k + (size_t)(x.t0 + i) * a.k_stride + (size_t)g * D, at.off0, at.off1);
+        if (at.turned) load_turns(a, q, at.j, turns);
+      }
+    };
+    load(0, v, f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < x.n; i0 += RPG) {
+      const int i = i0 + at.sub;
+      const bool ok = (there >> i) & 1;
+      load(i0 + RPG, next, next_f);
+      t.none();
+      if (ok && at.turned) t.set(f);
+      v = turn_rows<L, INTER, NORM, PARTLY>(v, gp, gy, NORM ? a.k_weight : nullptr, t, at, a.eps);
       if (ok) {
-        v.store(sm + (i + at.sub) * D, at.off0, at.off1);
-        if (a.k_out != nullptr) v.store(a.k_out + ((size_t)tok * a.Hkv + g) * D, at.off0, at.off1);
+        v.store(sm + i * D, at.off0, at.off1);
+        if (a.k_out != nullptr) v.store(a.k_out + ((size_t)(x.t0 + i) * a.Hkv + g) * D, at.off0, at.off1);
         top = kv8::max_finite2(kv8::max_finite2(kv8::max_finite2(kv8::max_finite2(top, v.u.x), v.u.y), v.u.z), v.u.w);
       }
+      v = next;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = next_f[e];
     }
   } else {
-    int p[3];
-    const bool ok = lane < x.n && positions(a, x.t0 + lane, p);
-    there = __ballot_sync(0xffffffffu, ok);
-    for (int c = lane; c < x.n * L; c += 32) {
-      const int i = c / L, j = c - i * L;
-      if (!((there >> i) & 1)) continue;
-      const uint4 v = *reinterpret_cast<const uint4*>(a.v + (size_t)(x.t0 + i) * a.v_stride + (size_t)g * D + 8 * j);
-      *reinterpret_cast<uint4*>(sm + i * D + 8 * j) = v;
-      top = kv8::max_finite2(kv8::max_finite2(kv8::max_finite2(kv8::max_finite2(top, v.x), v.y), v.z), v.w);
+    // 16 rows of L pieces of 16 bytes, all on their way at once
+    uint4 v[L / 2];
+#pragma unroll
+    for (int c = 0; c < L / 2; ++c) {
+      const int i = (c * 32 + lane) / L, j = (c * 32 + lane) % L;
+      v[c] = make_uint4(0u, 0u, 0u, 0u);
+      if ((there >> i) & 1)
+        v[c] = *reinterpret_cast<const uint4*>(a.v + (size_t)(x.t0 + i) * a.v_stride + (size_t)g * D + 8 * j);
+    }
+#pragma unroll
+    for (int c = 0; c < L / 2; ++c) {
+      *reinterpret_cast<uint4*>(sm + (c * 32 + lane) * 8) = v[c];
+      top = kv8::max_finite2(kv8::max_finite2(kv8::max_finite2(kv8::max_finite2(top, v[c].x), v[c].y), v[c].z), v[c].w);
     }
   }
   if (x.page < 0 || there == 0) return;

@@ -42,7 +42,7 @@ constexpr int kSms = 152;
 constexpr int kBlock = 32;               // tokens whose rows a warp looks up at a time
 constexpr int kStep = 16;                // tokens of a step
 constexpr float kRaise = 8.f;            // log2: a reference is raised when a score outgrows it by more
-constexpr int kMinBlocks = 2;            // of a piece
+constexpr int kMinBlocks = 1;            // of a piece (a call of 201 tokens 7.1 us; at 2, 4 and 8: 8.1, 9.9, 10.0)
 constexpr int kFusedPieces = 16;         // of a unit of at most two heads that its last warp joins itself
 
 // A warp's ring: per stage K and V rows of 16 tokens, the blocks' factors beside.
@@ -123,39 +123,57 @@ __device__ __forceinline__ uint32_t scan_blocks(const Kv8AttnArgs& a, int b0, in
   }
   return inc;
 }
+// With equal counts the host has laid the line out (a.per_unit blocks a unit).
 __device__ __forceinline__ uint32_t line_total(const Kv8AttnArgs& a, int lane) {
-  if (!a.lens.any()) {
-    Seq s;
-    seq_of(a, 0, s);
-    return (uint32_t)s.blocks() * (uint32_t)a.Hkv * (uint32_t)a.batch;
-  }
   uint32_t total = 0, mine;
   for (int b0 = 0; b0 < a.batch; b0 += 32) total += __shfl_sync(0xffffffffu, scan_blocks(a, b0, lane, mine), 31);
   return total;
 }
-// The sequence that block `at` of the line lies in, and the blocks before it.
-__device__ __forceinline__ void line_find(const Kv8AttnArgs& a, uint32_t at, int lane, int& b, uint32_t& before) {
-  if (!a.lens.any()) {
-    Seq s;
-    seq_of(a, 0, s);
-    const uint32_t per = (uint32_t)s.blocks() * (uint32_t)a.Hkv;
-    b = (int)(at / per);
-    before = (uint32_t)b * per;
-    return;
+
+// Piece `piece` of the line: its first block, its length, and the sequence that it
+// begins in with the blocks before that one.
+struct Piece {
+  uint32_t total, C, from, before;
+  int left, b;
+  __device__ __forceinline__ void cut(int piece, int pieces) {
+    C = min((uint32_t)pieces, total);
+    left = 0;
+    if (piece >= (int)C) return;
+    from = piece_begin(total, piece, C);
+    left = (int)(piece_begin(total, piece + 1, C) - from);
   }
-  before = 0;
-  for (b = 0; b < a.batch; b += 32) {
-    uint32_t mine;
-    const uint32_t inc = scan_blocks(a, b, lane, mine);
-    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > at);
+};
+__device__ __forceinline__ Piece equal_piece(const Kv8AttnArgs& a, int piece) {
+  Piece p;
+  const uint32_t in_seq = (uint32_t)a.per_unit * (uint32_t)a.Hkv;
+  p.total = in_seq * (uint32_t)a.batch;
+  p.cut(piece, a.pieces);
+  p.b = p.left > 0 ? (int)(p.from / in_seq) : 0;
+  p.before = (uint32_t)p.b * in_seq;
+  return p;
+}
+__device__ __forceinline__ Piece ragged_piece(const Kv8AttnArgs& a, int piece, int lane) {
+  Piece p;
+  uint32_t mine, inc = scan_blocks(a, 0, lane, mine);
+  p.total = __shfl_sync(0xffffffffu, inc, 31);
+  for (int b0 = 32; b0 < a.batch; b0 += 32) {
+    uint32_t other;
+    p.total += __shfl_sync(0xffffffffu, scan_blocks(a, b0, lane, other), 31);
+  }
+  p.cut(piece, a.pieces);
+  p.before = 0;
+  for (p.b = 0; p.left > 0 && p.b < a.batch; p.b += 32) {
+    if (p.b > 0) inc = scan_blocks(a, p.b, lane, mine);
+    const uint32_t past = __ballot_sync(0xffffffffu, p.before + inc > p.from);
     if (past) {
       const int f = __ffs(past) - 1;
-      before += __shfl_sync(0xffffffffu, inc - mine, f);
-      b += f;
-      return;
+      p.before += __shfl_sync(0xffffffffu, inc - mine, f);
+      p.b += f;
+      break;
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    p.before += __shfl_sync(0xffffffffu, inc, 31);
   }
+  return p;
 }
 
 // (m, l) and O of a piece's part of a unit: slot 0 of a piece continues a unit,
@@ -215,11 +233,18 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   using R = Ring<D>;
   constexpr int KS = D / 16, KC = D / 64, VB = D / 8, VW = VB / 4, S = R::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  grid_dep_sync();
   const int G = a.H / a.Hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q4 = lane & 3;
-  // sequences without a token (or with a length out of range): 0 and -inf
-  if (a.lens.any()) {
+  uint8_t* ring = smem + warp * R::kBytes;
+  const uint32_t ring_at = smem_u32(ring);
+  const int piece = blockIdx.x * kWarps + warp;
+  const bool ragged = a.lens.any();
+  // (equal counts: nothing here waits for the kernel before)
+  Piece line;
+  if (!ragged) line = equal_piece(a, piece);
+  grid_dep_sync();
+  if (ragged) {
+    // sequences without a token (or with a length out of range): 0 and -inf
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
       Seq s;
       const bool ok = seq_of(a, b, s);
@@ -230,18 +255,11 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       if (a.lse != nullptr)
         for (int i = threadIdx.x; i < a.H; i += kWarps * 32) a.lse[(size_t)b * a.H + i] = -INFINITY;
     }
+    line = ragged_piece(a, piece, lane);
   }
-  const uint32_t total = line_total(a, lane);
-  const uint32_t C = min((uint32_t)a.pieces, total);
-  uint8_t* ring = smem + warp * R::kBytes;
-  const uint32_t ring_at = smem_u32(ring);
-  const int piece = blockIdx.x * kWarps + warp;
-  if (piece >= (int)C) return;
-  const uint32_t from = piece_begin(total, piece, C);
-  int left = (int)(piece_begin(total, piece + 1, C) - from), b;
-  uint32_t before;
-  line_find(a, from, lane, b, before);
-  uint32_t off = from - before;
+  const uint32_t total = line.total, C = line.C;
+  uint32_t before = line.before, off = line.from - before;
+  int left = line.left, b = line.b;
 
 #pragma unroll 1
   for (; left > 0; ++b, off = 0) {
@@ -288,6 +306,14 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   Ahead n1, n2;
   load_pos(first, n1);
   load_pos(first + stride, n2);
+  uint2 raw[NT][KS];            // the queries, on their way with the positions
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + ((size_t)b * a.H + (size_t)g * G + 8 * t + r) * D + q4 * 16;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      raw[t][k] = 8 * t + r < G ? __ldg(reinterpret_cast<const uint2*>(src + (k >> 2) * 64 + (k & 3) * 4)) : make_uint2(0u, 0u);
+  }
   load_page(first, n1);
   // Requests the rows and factors of step `i` (its tokens' ids are looked up with
   // the first of a block's two steps); tokens that are not there read as zeros.
@@ -320,6 +346,9 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     cp_async_commit();
   };
 
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) request(i);
+
   // ---- the queries: each head's elements over 2^e, so that the largest lies in
   // [2^14, 2^15); those that are not finite stay what they are
   uint32_t qf[NT][KS][2];
@@ -328,15 +357,10 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
     float mine[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int h = 8 * t + r;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + ((size_t)b * a.H + (size_t)g * G + h) * D;
-      uint2 x[KS];
+      const uint2* x = raw[t];
       uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        x[k] = h < G ? __ldg(reinterpret_cast<const uint2*>(src + (k >> 2) * 64 + q4 * 16 + (k & 3) * 4)) : make_uint2(0u, 0u);
-        top = kv8::max_finite2(kv8::max_finite2(top, x[k].x), x[k].y);
-      }
+      for (int k = 0; k < KS; ++k) top = kv8::max_finite2(kv8::max_finite2(top, x[k].x), x[k].y);
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -375,8 +399,6 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   uint32_t vtop = 0x00800000u;      // the largest factor of V so far, rounded down to a power of two (bits)
 
   const int steps = (end - first + kStep - 1) / kStep;
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) request(i);
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
       cp_async_wait<S - 2>();
@@ -558,22 +580,23 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
   grid_dep_sync();
   const int G = a.H / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, g = h / G;
-  const uint32_t total = line_total(a, lane), C = min((uint32_t)a.pieces, total);
   Seq s;
   seq_of(a, b, s);
   const int per_unit = s.blocks();
   if (per_unit == 0) return;
-  uint32_t before = 0;
+  uint32_t before = 0, total;
   if (!a.lens.any()) {
     before = (uint32_t)b * (uint32_t)per_unit * (uint32_t)a.Hkv;
+    total = (uint32_t)a.batch * (uint32_t)per_unit * (uint32_t)a.Hkv;
   } else {
+    total = line_total(a, lane);
     for (int b0 = 0; b0 <= b; b0 += 32) {
       uint32_t mine;
       const uint32_t inc = scan_blocks(a, b0, lane, mine);
       before += b - b0 < 32 ? __shfl_sync(0xffffffffu, inc - mine, b - b0) : __shfl_sync(0xffffffffu, inc, 31);
     }
   }
-  const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
+  const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
   const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
   if (n == 1) return;
   float M, L, acc[E];
@@ -655,6 +678,7 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int D, cudaStream_t stream)
   const int G = a.H / a.Hkv;
   const long long units = (long long)a.batch * a.Hkv, blocks = (a.k_vis + a.n_text + kBlock - 1) / kBlock;
   a.pieces = pieces_of(units, blocks);
+  a.per_unit = (int)blocks;
   a.part_ml = static_cast<float*>(a.ws);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.pieces * 2 * G * 2 * sizeof(float)));
   // (the most pieces that a unit can lie in; with counts of its own per sequence
