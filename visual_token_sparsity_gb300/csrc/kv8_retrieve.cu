@@ -248,6 +248,7 @@ struct BorderShared {
   int sure, near, digit, above, last_j;
   unsigned long long last;
   uint32_t kth[32];
+  float factor[32];
   uint32_t scan_tmp[33];
   int hist[256];
 };
@@ -294,28 +295,66 @@ __device__ __forceinline__ uint64_t score48(const Kv8RetrieveArgs& a, const Quer
   return order_key64(hi, lo);
 }
 
-// Keys [lo, hi] around a border may lie on its other side.  Every selected fp32
-// score is at least the border's value and every other one below it, so that is as
-// good a middle as the k-th score.  Scores or a band that are not finite: the fp32
-// order, ties included.
+// Keys [lo, hi] around a border may lie on its other side: those within the band of
+// it (every selected fp32 score is at least the border's value and every other one
+// below it, so that is as good a middle as the k-th score), and where the search for
+// it ended with few keys in the border's bin, those of the bin and within the band of
+// both its ends.  Scores or a band that are not finite: the fp32 order, ties included.
+constexpr int kFew = 6;
 struct Near {
   uint32_t lo, hi;
   bool wide;
 };
 __device__ __forceinline__ Near near_border(const TopkBorder& t, float band) {
-  const float at = (t.prefix & 0x80000000u) ? __uint_as_float(t.prefix ^ 0x80000000u) : __uint_as_float(~t.prefix);
+  auto value = [](uint32_t key) {
+    return (key & 0x80000000u) ? __uint_as_float(key ^ 0x80000000u) : __uint_as_float(~key);
+  };
+  const uint32_t bin = t.prefix | ~t.pmask, top = t.open ? bin : t.prefix;
   Near x;
-  x.wide = band > 0.f && isfinite(band) && isfinite(at);
-  x.lo = x.wide ? order_key(at - band) : t.prefix;
-  x.hi = x.wide ? order_key(at + band) : t.prefix | ~t.pmask;
+  x.wide = band > 0.f && isfinite(band) && isfinite(value(t.prefix)) && isfinite(value(top));
+  x.lo = x.wide ? order_key(value(t.prefix) - band) : t.prefix;
+  x.hi = x.wide ? order_key(value(top) + band) : bin;
   return x;
 }
 
-// The largest of a row's factors, by a whole warp.
-__device__ __forceinline__ float largest_factor(const float* factors, int n, int lane) {
+// Writes the indices (first + i) of the keys that are taken in ascending order, by a
+// block whose warps have stretches of 32 keys; before(n) tells how many come before
+// the block's n.
+template <typename Taken, typename Before>
+__device__ __forceinline__ void emit_taken(int n, int first, int32_t* dst, uint32_t* scan_tmp, Taken taken, Before before) {
+  const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = nt >> 5;
+  const int per = ((n + 31) / 32 + nw - 1) / nw * 32, w0 = min(n, warp * per), w1 = min(n, w0 + per);
+  uint32_t count = 0;
+  for (int i0 = w0; i0 < w1; i0 += 32) count += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && taken(i0 + lane)));
+  if (lane == 0) scan_tmp[warp] = count;
+  __syncthreads();
+  uint32_t o = 0, all = 0;
+  for (int w = 0; w < nw; ++w) {
+    const uint32_t c = scan_tmp[w];
+    o += w < warp ? c : 0u;
+    all += c;
+  }
+  o += before(all);
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const bool take = i0 + lane < w1 && taken(i0 + lane);
+    const uint32_t mask = __ballot_sync(0xffffffffu, take);
+    if (take) dst[o + __popc(mask & ((1u << lane) - 1u))] = first + i0 + lane;
+    o += __popc(mask);
+  }
+}
+
+// This thread's part of the largest of a row's factors, and the block's.
+__device__ __forceinline__ float some_factor(const float* factors, int n) {
   float x = 0.f;
-  for (int i = lane; i < n; i += 32) x = fmaxf(x, __ldcg(factors + i));
-  return warp_max(x);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) x = fmaxf(x, __ldcg(factors + i));
+  return x;
+}
+__device__ __forceinline__ float largest_factor(float x, float* tmp) {
+  x = warp_max(x);
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = x;
+  __syncthreads();
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x = fmaxf(x, tmp[w]);
+  return x;
 }
 
 // Selects the k tokens of a row, given its keys and their border.  All threads of
@@ -356,8 +395,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
       for (int i0 = warp * 4; i0 < m; i0 += nw * 4) {
         const int i = i0 + (lane >> 3);
         const int j = i < m ? sh.list_j[i] : 0;
-        // (exact ties of scores that are not told apart at all: by index alone)
-        const uint64_t v = wide ? score48<D>(a, query, b, g, j, i < m, lane) : 0ull;
+        const uint64_t v = wide ? score48<D>(a, query, b, g, j, i < m, lane) : (uint64_t)keys[j] << 32;
         if (i < m && (lane & 7) == 0) sh.list_v[i] = v;
       }
       __syncthreads();
@@ -382,7 +420,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
             if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
             todo &= todo - 1;
           }
-          const uint64_t v = wide ? score48<D>(a, query, b, g, max(j, 0), j >= 0, lane) : 0ull;
+          const uint64_t v = wide ? score48<D>(a, query, b, g, max(j, 0), j >= 0, lane) : (uint64_t)keys[max(j, 0)] << 32;
           if (j >= 0 && (lane & 7) == 0) exact[j] = v;
         }
       }
@@ -432,12 +470,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
     const uint64_t v = exact[i];
     return v > sh.last || (v == sh.last && i <= sh.last_j);
   };
-  const int seg = (n + nt - 1) / nt, s0 = min(n, tid * seg), s1 = min(n, s0 + seg);
-  uint32_t mine = 0;
-  for (int i = s0; i < s1; ++i) mine += taken(i);
-  uint32_t o = block_exclusive_scan<uint32_t>(mine, sh.scan_tmp);
-  for (int i = s0; i < s1; ++i)
-    if (taken(i)) dst[o++] = i;
+  emit_taken(n, 0, dst, sh.scan_tmp, taken, [](uint32_t) { return 0u; });
 }
 
 }  // namespace
@@ -464,7 +497,7 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
   uint32_t* keys = KNOWN ? far_keys + (size_t)row * a.n_vis : staged;
   if (!KNOWN) fill_unselected(dst, k, a.k);
   if (k <= 0) return;
-  const float factor = largest_factor(factors + (size_t)row * n_factors, n_factors, lane);
+  float factor = some_factor(factors + (size_t)row * n_factors, n_factors);
   TopkBorder border;
   if (KNOWN) {
     uint32_t kth = 0xffffffffu;
@@ -488,10 +521,11 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
     if (lane == 0) sh.kth[warp] = kth;
     __syncthreads();
     for (int w = 0; w < nt / 32; ++w) kth = min(kth, sh.kth[w]);
-    border = TopkBorder{kth, 0xffffffffu, 0};
+    border = TopkBorder{kth, 0xffffffffu, 0, false};
   } else {
-    border = block_topk_border(src, n, k, keys, ts);
+    border = block_topk_border(src, n, k, keys, ts, kFew);
   }
+  factor = largest_factor(factor, sh.factor);
   select_row<D>(a, rows + row, b, g, n, k, keys, border, factor, exact + (size_t)row * a.n_vis, dst, sh);
 }
 
@@ -517,9 +551,10 @@ kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query
   const int first = min(n, rank * slice), len = min(n, first + slice) - first;
   const Query8<D>* query = rows + row;
   uint64_t* exact = exact_rows + (size_t)row * a.n_vis + first;
-  const float factor = largest_factor(factors + (size_t)row * n_factors, n_factors, lane);
+  float factor = some_factor(factors + (size_t)row * n_factors, n_factors);
   if (tid == 0) sh.sure = sh.near = 0;       // (the search below has barriers)
-  const TopkBorder t = cluster_topk_border(scores + (size_t)row * a.n_vis + first, len, k, keys, ts);
+  const TopkBorder t = cluster_topk_border(scores + (size_t)row * a.n_vis + first, len, k, keys, ts, kFew);
+  factor = largest_factor(factor, sh.factor);
   const Near x = near_border(t, query->slack * kBand * factor);
   const uint32_t lo = x.lo, hi = x.hi;
   const bool wide = x.wide;
@@ -551,7 +586,7 @@ kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query
       for (int i0 = warp * 4; i0 < mine; i0 += nw * 4) {
         const int i = i0 + (lane >> 3);
         const int j = i < mine ? sh.list_j[i] : 0;
-        const uint64_t v = wide ? score48<D>(a, query, b, g, first + j, i < mine, lane) : 0ull;
+        const uint64_t v = wide ? score48<D>(a, query, b, g, first + j, i < mine, lane) : (uint64_t)keys[j] << 32;
         if (i < mine && (lane & 7) == 0) sh.list_v[i] = v;
       }
       cluster.sync();
@@ -560,12 +595,15 @@ kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query
         const uint64_t v = sh.list_v[i];
         const int j = sh.list_j[i];
         int better = 0;
-        for (int r = 0; r < kTopkClusterCtas; ++r) {
-          const int theirs = *cluster.map_shared_rank(&sh.near, r);
-          const uint64_t* values = cluster.map_shared_rank(&sh.list_v[0], r);
-          const int* indices = cluster.map_shared_rank(&sh.list_j[0], r);
-          for (int o = lane; o < theirs; o += 32)
-            better += values[o] > v || (values[o] == v && (r < rank || (r == rank && indices[o] < j)));
+        // (four lanes for each CTA, so that no list waits for another)
+        const int r = lane >> 2;
+        static_assert(kTopkClusterCtas == 8, "four lanes a CTA");
+        const int theirs = *cluster.map_shared_rank(&sh.near, r);
+        const uint64_t* values = cluster.map_shared_rank(&sh.list_v[0], r);
+        const int* indices = cluster.map_shared_rank(&sh.list_j[0], r);
+        for (int o = lane & 3; o < theirs; o += 4) {
+          const uint64_t y = values[o];
+          better += y > v || (y == v && (r < rank || (r == rank && indices[o] < j)));
         }
         better = __reduce_add_sync(0xffffffffu, better);
         if (lane == 0 && better >= need) keys[j] = 0u;             // (no score's key)
@@ -582,7 +620,8 @@ kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query
             if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
             todo &= todo - 1;
           }
-          const uint64_t v = wide ? score48<D>(a, query, b, g, first + max(j, 0), j >= 0, lane) : 0ull;
+          const uint64_t v =
+              wide ? score48<D>(a, query, b, g, first + max(j, 0), j >= 0, lane) : (uint64_t)keys[max(j, 0)] << 32;
           if (j >= 0 && (lane & 7) == 0) exact[j] = v;
         }
       }
@@ -640,15 +679,14 @@ kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query
     const uint64_t v = exact[i];
     return v > sh.last || (v == sh.last && first + i <= sh.last_j);
   };
-  const int seg = (len + nt - 1) / nt, s0 = min(len, tid * seg), s1 = min(len, s0 + seg);
-  uint32_t count = 0;
-  for (int i = s0; i < s1; ++i) count += taken(i);
-  uint32_t o = block_exclusive_scan<uint32_t>(count, sh.scan_tmp);
-  if (tid == nt - 1) ts.cnt[0] = (int)(o + count);
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) o += (uint32_t)*cluster.map_shared_rank(&ts.cnt[0], r);
-  for (int i = s0; i < s1; ++i)
-    if (taken(i)) dst[o++] = first + i;
+  emit_taken(len, first, dst, sh.scan_tmp, taken, [&](uint32_t all) {
+    if (tid == 0) ts.cnt[0] = (int)all;
+    cluster.sync();
+    uint32_t o = 0;
+#pragma unroll
+    for (int r = 0; r < kTopkClusterCtas; ++r) o += r < rank ? (uint32_t)*cluster.map_shared_rank(&ts.cnt[0], r) : 0u;
+    return o;
+  });
   cluster.sync();     // keep this CTA's shared memory alive until every peer has read it
 }
 

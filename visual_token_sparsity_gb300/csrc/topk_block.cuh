@@ -76,18 +76,22 @@ __device__ __forceinline__ void fill_unselected(int32_t* dst, int from, int k) {
 }
 
 // The known high bits of a row's k-th largest key, and how many keys that equal
-// it on those bits are still to be taken (the lowest indices).
+// it on those bits are still to be taken (the lowest indices); open: there are more
+// of them, and the bits below would tell which.
 struct TopkBorder {
   uint32_t prefix, pmask;
   int remaining;
+  bool open;
 };
 
 // Stages the row's keys and finds its border.  All threads of the block call
 // this.  keys: shared memory for n keys, or nullptr to re-read `src` (through L2)
 // on every pass.  `src` may have been written by other CTAs of the running grid:
 // it is read with ld.global.cg.
+// The search may end as soon as `few` keys or fewer have the border's bits (0: not
+// before it is exact, or those keys are all taken).
 __device__ __forceinline__ TopkBorder block_topk_border(const float* src, int n, int k, uint32_t* keys,
-                                                        TopkShared& ts) {
+                                                        TopkShared& ts, int few = 0) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   // stage the keys (four independent loads in flight per thread) and find
   // the smallest and largest key
@@ -155,6 +159,7 @@ __device__ __forceinline__ TopkBorder block_topk_border(const float* src, int n,
   // keys equal to it on those bits are still to be taken
   uint32_t prefix, pmask;
   int remaining = k;
+  bool open = false;
   const uint32_t diff = kmin ^ kmax;
   if (diff == 0) {
     prefix = kmin;
@@ -208,14 +213,15 @@ __device__ __forceinline__ TopkBorder block_topk_border(const float* src, int n,
       remaining -= ts.sel_above;
       const int cnt = ts.sel_count;
       __syncthreads();                       // every thread has read the selection
-      if (cnt == remaining || lo == 0) break;  // the bin is taken whole, or the key is exact
+      open = cnt != remaining && lo > 0;
+      if (!open || cnt <= few) break;  // the bin is taken whole, or the key is exact
       for (int i = tid; i < 256; i += nt) ts.hist[i] = 0;
       __syncthreads();
       hi = lo;
     }
   }
 
-  return TopkBorder{prefix, pmask, remaining};
+  return TopkBorder{prefix, pmask, remaining, open};
 }
 
 // The k largest scores of a row; all threads of the block call this (arguments

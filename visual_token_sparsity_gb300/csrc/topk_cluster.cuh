@@ -24,9 +24,10 @@ struct ClusterTopkShared {
 };
 
 // Stages keys [0, m) of this CTA's slice `src` of a row and finds the border of
-// the k largest of the whole row.  All threads of the cluster call this.
+// the k largest of the whole row (`few` as for block_topk_border).  All threads of
+// the cluster call this.
 __device__ __forceinline__ TopkBorder cluster_topk_border(const float* src, int m, int k, uint32_t* keys,
-                                                          ClusterTopkShared& sh) {
+                                                          ClusterTopkShared& sh, int few = 0) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
@@ -79,6 +80,7 @@ __device__ __forceinline__ TopkBorder cluster_topk_border(const float* src, int 
 
   uint32_t prefix, pmask;
   int remaining = k;
+  bool open = false;
   const uint32_t diff = kmin ^ kmax;
   if (diff == 0) {
     prefix = kmin;
@@ -138,11 +140,12 @@ __device__ __forceinline__ TopkBorder cluster_topk_border(const float* src, int 
       remaining -= sh.sel_above;
       const int cnt_sel = sh.sel_count;
       __syncthreads();          // sh.total / sel_* are rewritten by the next pass
-      if (cnt_sel == remaining || lo == 0) break;
+      open = cnt_sel != remaining && lo > 0;
+      if (!open || cnt_sel <= few) break;
       hi = lo;
     }
   }
-  return TopkBorder{prefix, pmask, remaining};
+  return TopkBorder{prefix, pmask, remaining, open};
 }
 
 }  // namespace sv
