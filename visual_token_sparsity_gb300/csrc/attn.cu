@@ -502,12 +502,6 @@ attn_merge_kernel(const float* __restrict__ part_ml, const float* __restrict__ p
   if (lse != nullptr && tid == 0) lse[bh] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-cudaError_t launch_attn_merge(const float* part_ml, const float* part_o, int batch, int H, int Hkv, int D, int nsplit,
-                              void* out, float* lse, cudaStream_t stream) {
-  return launch_dependent(attn_merge_kernel, dim3(batch * H), dim3(256), (size_t)nsplit * sizeof(float), stream,
-                          part_ml, part_o, H, Hkv, H / Hkv, D, nsplit, static_cast<uint16_t*>(out), lse);
-}
-
 cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t stream) {
   const int G = a.H / a.Hkv;
   // a fused append attends one token more
@@ -522,6 +516,8 @@ cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t stream) {
     e = a.D == 128 ? dispatch_g<128>(b, p, stream) : dispatch_g<64>(b, p, stream);
   }
   if (e != cudaSuccess || fused_merge) return e;
-  return launch_attn_merge(a.part_ml, a.part_o, a.batch, a.H, a.Hkv, a.D, p.nsplit, a.out, a.lse, stream);
+  return launch_dependent(attn_merge_kernel, dim3(a.batch * a.H), dim3(256), (size_t)p.nsplit * sizeof(float),
+                          stream, a.part_ml, a.part_o, a.H, a.Hkv, G, a.D, p.nsplit, static_cast<uint16_t*>(a.out),
+                          a.lse);
 }
 }  // namespace sv

@@ -106,8 +106,6 @@ struct AttnArgs {
 };
 cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t stream);
 // joins nsplit partials per (sequence, query head), [batch][Hkv][nsplit][G]
-cudaError_t launch_attn_merge(const float* part_ml, const float* part_o, int batch, int H, int Hkv, int D, int nsplit,
-                              void* out, float* lse, cudaStream_t stream);
 cudaError_t launch_sparse_attn_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
 
 // ---- compaction gather (prune.cu)
@@ -260,6 +258,7 @@ struct Kv8AttnArgs {
   // results and the counters of the units that they share (nullptr: the merge
   // kernel joins them)
   int pieces, per_unit;            // (blocks of a unit, with equal counts)
+  bool cut;                        // a unit may lie in several pieces
   float* part_ml;
   float* part_o;
   int* split_done;

@@ -27,9 +27,19 @@
 // 2^-20 of the reference and vanishes below 2^-30.
 //
 // Work is cut evenly: the blocks of 32 tokens of all (sequence, KV head) units
-// form one line, cut into equal pieces, one per warp.  A unit that lies in several
-// pieces leaves fp32 partials, which the last of its warps joins (few pieces) or a
-// second kernel (many), always in the order of the pieces.
+// form one line, cut into equal pieces, one per CTA, whose four warps take every
+// fourth block and are joined in shared memory.  A unit that lies in several pieces
+// leaves fp32 partials, which the last of its CTAs joins (few rows) or a second
+// kernel (many), always in the order of the pieces.
+//
+// Measured, inputs out of L2: 4 query heads over 2 KV heads, 201 tokens 5.3 us; 16
+// sequences of 32 heads, 1440 + 128 tokens 42.8 us, 4.9 TB/s of cache rows; 8 ragged
+// sequences of 28 heads over 4, up to 12544 + 256 tokens 27.7 us, of which the join's
+// kernel is 5.  With a piece per warp they took 7.2, 41.8 and 28.0; with the rows
+// prefetched in registers instead of the ring the second took 45.  What is left is the
+// chain index -> page -> row at the start of every unit (some 3 us), and in the rest
+// the latency of the rows and of turning them, with three warps a scheduler (45 % of
+// issue slots taken).
 #include "kernels.h"
 #include "kv8.cuh"
 
@@ -42,8 +52,10 @@ constexpr int kSms = 152;
 constexpr int kBlock = 32;               // tokens whose rows a warp looks up at a time
 constexpr int kStep = 16;                // tokens of a step
 constexpr float kRaise = 8.f;            // log2: a reference is raised when a score outgrows it by more
-constexpr int kMinBlocks = 1;            // of a piece (a call of 201 tokens 7.1 us; at 2, 4 and 8: 8.1, 9.9, 10.0)
-constexpr int kFusedPieces = 16;         // of a unit of at most two heads that its last warp joins itself
+constexpr int kMinBlocks = 4;            // of a piece: a block for each warp
+constexpr int kFusedRows = 32;           // pieces x heads of a unit that its last CTA joins itself (joining 7
+                                         // heads of 14 and more pieces so takes 32.3 us against 27.7 for
+                                         // LongVILA's call; 8 to 128 are equal)
 
 // A warp's ring: per stage K and V rows of 16 tokens, the blocks' factors beside.
 template <int D>
@@ -180,49 +192,51 @@ __device__ __forceinline__ Piece ragged_piece(const Kv8AttnArgs& a, int piece, i
 // slot 1 begins one that goes on.
 __device__ __forceinline__ size_t part_slot(int piece, bool begins) { return (size_t)piece * 2 + (begins ? 1 : 0); }
 
-// (M, L, O) of head h of a unit over pieces p0 + w0, + step, ... < p0 + n, by a warp:
-// D / 32 dims a lane, eight pieces in flight.
+// (M, L, O) of dims e and e + 1 of head h of a unit over pieces p0 + w0, + step, ...
+// < p0 + n, eight in flight.
 template <int D>
-__device__ __forceinline__ void gather_pieces(const Kv8AttnArgs& a, int p0, int n, int w0, int step, int lane, int h,
-                                              float& M, float& L, float (&acc)[D / 32]) {
-  constexpr int E = D / 32, kBatch = 8;
+__device__ __forceinline__ void gather_pieces(const Kv8AttnArgs& a, int p0, int n, int w0, int step, int h, int e,
+                                              float& M, float& L, float2& v) {
+  constexpr int kBatch = 8;
   const int G = a.H / a.Hkv;
   M = -INFINITY;
   L = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  v = make_float2(0.f, 0.f);
 #pragma unroll 1
   for (int s0 = w0; s0 < n; s0 += kBatch * step) {
-    float x[kBatch][E];
-    float2 ml[kBatch];
+    float2 x[kBatch], ml[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int s = s0 + i * step;
       const size_t at = part_slot(p0 + s, s == 0) * G + h;
       ml[i] = s < n ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 y = s < n ? __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D + lane * E + e)) : make_float2(0.f, 0.f);
-        x[i][e] = y.x;
-        x[i][e + 1] = y.y;
-      }
+      x[i] = s < n ? __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D + e)) : make_float2(0.f, 0.f);
     }
     float top = M;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
     const float old = M == -INFINITY ? 0.f : fast_exp2(M - top);
     L *= old;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= old;
+    v.x *= old;
+    v.y *= old;
     M = top;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const float w = ml[i].x == -INFINITY ? 0.f : fast_exp2(ml[i].x - top);
       L = fmaf(ml[i].y, w, L);                              // (a NaN stays)
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+      v.x = fmaf(w, x[i].x, v.x);
+      v.y = fmaf(w, x[i].y, v.y);
     }
   }
+}
+
+// Dims e and e + 1 of an output row, and its log-sum-exp with the first.
+template <int D>
+__device__ __forceinline__ void write_pair(const Kv8AttnArgs& a, size_t row, int e, float M, float L, float2 v) {
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + e) =
+      f32_to_bf16_bits(v.x * inv) | f32_to_bf16_bits(v.y * inv) << 16;
+  if (e == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 }  // namespace
@@ -237,7 +251,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q4 = lane & 3;
   uint8_t* ring = smem + warp * R::kBytes;
   const uint32_t ring_at = smem_u32(ring);
-  const int piece = blockIdx.x * kWarps + warp;
+  const int piece = blockIdx.x;
   const bool ragged = a.lens.any();
   // (equal counts: nothing here waits for the kernel before)
   Piece line;
@@ -274,8 +288,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   left -= blk1 - blk0;
   const int32_t* list = a.vis_idx != nullptr ? a.vis_idx + ((size_t)b * a.Hkv + g) * a.k_vis : nullptr;
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
-  const int first = blk0 * kBlock, end = min(total_tok, blk1 * kBlock);
-  constexpr int stride = kBlock;
+  const int first = (blk0 + warp) * kBlock, end = min(total_tok, blk1 * kBlock);
+  constexpr int stride = kWarps * kBlock;
 
   // ---- a block's tokens, a lane each, in three steps: position (two blocks
   // ahead), page (one ahead), row and factors
@@ -398,7 +412,8 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   }
   uint32_t vtop = 0x00800000u;      // the largest factor of V so far, rounded down to a power of two (bits)
 
-  const int steps = (end - first + kStep - 1) / kStep;
+  // (two steps a block of this warp)
+  const int steps = max(0, (end - first + stride - 1) / stride * 2);
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
       cp_async_wait<S - 2>();
@@ -507,10 +522,12 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   cp_async_wait<0>();
   __syncwarp();                                             // (the ring is free for the next unit)
 
-  // ---- this part of the unit
+  // ---- this part of the unit: the warps' results joined in shared memory
   const float back = __uint_as_float(vtop) * (1.f / 64.f);
   const bool whole = blk0 == 0 && blk1 == per_unit;
-  const size_t slot = part_slot(piece, blk0 == 0);
+  const size_t slot = part_slot(piece, blk0 == 0), row0 = (size_t)b * a.H + (size_t)g * G;
+  float* joined = reinterpret_cast<float*>(ring);          // [G][D], then (m, l)
+  static_assert(16 * (D + 2) * 4 <= R::kFactors, "a warp's rows fit its ring");
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -521,65 +538,80 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       s += __shfl_xor_sync(0xffffffffu, s, 8);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
       if (h >= G) continue;
-      if (whole) {
-        const float inv = s > 0.f ? 1.f / s : (s == 0.f ? 0.f : s);
-        const size_t row = (size_t)b * a.H + (size_t)g * G + h;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + r * VB);
+      float* dst = joined + h * D + r * VB;
 #pragma unroll
-        for (int j = 0; j < KS; ++j)
-          dst[j] = f32_to_bf16_bits(o[t][j][i] * back * inv) | f32_to_bf16_bits(o[t][j][i + 2] * back * inv) << 16;
-        if (r == 0 && a.lse != nullptr)
-          a.lse[row] = s == 0.f ? -INFINITY : (m[t][i] + log2f(s)) * 0.6931471805599453f;
-      } else {
-        float* dst = a.part_o + (slot * G + h) * D + r * VB;
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-          *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back, o[t][j][i + 2] * back);
-        if (r == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(m[t][i], s);
-      }
+      for (int j = 0; j < KS; ++j)
+        *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back, o[t][j][i + 2] * back);
+      if (r == 0) reinterpret_cast<float2*>(joined + G * D)[h] = make_float2(m[t][i], s);
     }
-  if (whole || a.split_done == nullptr) continue;
+  __syncthreads();
+  for (int i = threadIdx.x; i < G * D / 2; i += kWarps * 32) {
+    const int h = i / (D / 2), e = 2 * i - h * D;
+    float M = -INFINITY, L = 0.f;
+    float2 v = make_float2(0.f, 0.f), ml[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      ml[w] = reinterpret_cast<const float2*>(smem + w * R::kBytes + G * D * 4)[h];
+      M = fmaxf(M, ml[w].x);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ml[w].x == -INFINITY ? 0.f : fast_exp2(ml[w].x - M);
+      const float2 y = reinterpret_cast<const float2*>(smem + w * R::kBytes)[i];
+      L = fmaf(ml[w].y, f, L);                              // (a NaN stays)
+      v.x = fmaf(f, y.x, v.x);
+      v.y = fmaf(f, y.y, v.y);
+    }
+    if (whole) {
+      write_pair<D>(a, row0 + h, e, M, L, v);
+    } else {
+      *reinterpret_cast<float2*>(a.part_o + (slot * G + h) * D + e) = v;
+      if (e == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(M, L);
+    }
+  }
+  // (and the rings are free for the next unit)
+  const bool join = !whole && a.split_done != nullptr;
+  if (join) __threadfence();
+  __syncthreads();
+  if (!join) continue;
 
-  // ---- the last warp of a unit joins its pieces
+  // ---- the last CTA of a unit joins its pieces
   const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
   const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
-  const int unit = b * a.Hkv + g;
-  __threadfence();
-  __syncwarp();
-  int last = 0;
-  if (lane == 0) last = atomicAdd(a.split_done + unit, 1) == n - 1;
-  if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-  __threadfence();
-  if (lane == 0) a.split_done[unit] = 0;                  // ready for the next call
-#pragma unroll 1
-  for (int h = 0; h < G; ++h) {
-    constexpr int E = D / 32;
-    float M, L, acc[E];
-    gather_pieces<D>(a, p0, n, 0, 1, lane, h, M, L, acc);
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    const size_t row = (size_t)b * a.H + (size_t)g * G + h;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + lane * E);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = f32_to_bf16_bits(acc[e] * inv) | f32_to_bf16_bits(acc[e + 1] * inv) << 16;
-    if (lane == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  int* done = a.split_done + b * a.Hkv + g;
+  __shared__ int last;
+  if (threadIdx.x == 0) {
+    last = atomicAdd(done, 1) == n - 1;
+    if (last) *done = 0;                                    // ready for the next call
   }
+  __syncthreads();
+  if (last) {
+    __threadfence();
+    for (int i = threadIdx.x; i < G * D / 2; i += kWarps * 32) {
+      const int h = i / (D / 2), e = 2 * i - h * D;
+      float M, L;
+      float2 v;
+      gather_pieces<D>(a, p0, n, 0, 1, h, e, M, L, v);
+      write_pair<D>(a, row0 + h, e, M, L, v);
+    }
+  }
+  __syncthreads();                                          // (`last` is free)
   }
   before += in_seq;
   }
 }
 
 // Joins the units that were cut: a CTA per (unit, head), whose warps take every
-// eighth piece each.
-constexpr int kMergeWarps = 8;
+// fourth (eighth) piece each.
+constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float part[kMergeWarps][D];
-  __shared__ float2 part_ml[kMergeWarps];
-  grid_dep_sync();
-  const int G = a.H / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kPer = D / 2, kParts = kMergeThreads / kPer;
+  __shared__ float2 part[kParts][kPer], part_ml[kParts];
+  const int G = a.H / a.Hkv, lane = threadIdx.x & 31;
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, g = h / G;
+  grid_dep_sync();
   Seq s;
   seq_of(a, b, s);
   const int per_unit = s.blocks();
@@ -599,47 +631,42 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
   const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
   if (n == 1) return;
-  float M, L, acc[E];
-  gather_pieces<D>(a, p0, n, warp, kMergeWarps, lane, h - g * G, M, L, acc);
-#pragma unroll
-  for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-  if (lane == 0) part_ml[warp] = make_float2(M, L);
+  const int w = threadIdx.x / kPer, i = threadIdx.x - w * kPer;
+  float M, L;
+  float2 v;
+  gather_pieces<D>(a, p0, n, w, kParts, h - g * G, 2 * i, M, L, v);
+  part[w][i] = v;
+  if (i == 0) part_ml[w] = make_float2(M, L);
   __syncthreads();
-  if (threadIdx.x >= D) return;
+  if (w != 0) return;
   M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, part_ml[w].x);
+  for (int p = 0; p < kParts; ++p) M = fmaxf(M, part_ml[p].x);
   L = 0.f;
-  float v = 0.f;
+  v = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = part_ml[w].x == -INFINITY ? 0.f : fast_exp2(part_ml[w].x - M);
-    L += part_ml[w].y * f;
-    v += part[w][threadIdx.x] * f;
+  for (int p = 0; p < kParts; ++p) {
+    const float f = part_ml[p].x == -INFINITY ? 0.f : fast_exp2(part_ml[p].x - M);
+    L = fmaf(part_ml[p].y, f, L);
+    v.x = fmaf(f, part[p][i].x, v.x);
+    v.y = fmaf(f, part[p][i].y, v.y);
   }
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-  const size_t row = (size_t)b * a.H + h;
-  static_cast<uint16_t*>(a.out)[row * D + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v * inv);
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  write_pair<D>(a, (size_t)b * a.H + h, 2 * i, M, L, v);
 }
 
 namespace {
 
-// Pieces of the line: one per resident warp, of kMinBlocks blocks at least.  Where
-// that is four or more to a unit, the same number to each, so that none lies across
-// two units (a warp's second unit begins with the whole chain of lookups).
-int pieces_of(long long units, long long blocks) {
-  const long long most = (long long)kSms * kCtas * kWarps;
-  long long each = blocks / kMinBlocks;
-  each = each > 1 ? each : 1;
-  if (units * each <= most) return (int)(units * each > 1 ? units * each : 1);
-  each = units > 0 ? most / units : 0;
-  return (int)(each >= 4 ? units * each : most);
-}
-// No fewer pieces, for any smaller call.
+// Pieces of the line, one per resident CTA at most and of kMinBlocks blocks at
+// least.  Where that is four or more to a unit, the same number to each, so that
+// none lies across two units (a warp's second unit begins with the whole chain of
+// lookups).
 long long pieces_bound(long long units, long long blocks) {
-  const long long most = (long long)kSms * kCtas * kWarps, c = units * (blocks / kMinBlocks > 1 ? blocks / kMinBlocks : 1);
+  const long long most = (long long)kSms * kCtas, each = blocks / kMinBlocks, c = units * (each > 1 ? each : 1);
   return c < 1 ? 1 : c < most ? c : most;
+}
+int pieces_of(long long units, long long blocks) {
+  const long long c = pieces_bound(units, blocks), each = units > 0 ? c / units : 0;
+  return (int)(each >= 4 ? units * each : c);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -667,9 +694,9 @@ static cudaError_t launch_nt(const Kv8AttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  e = launch_dependent(kernel, dim3((unsigned)((a.pieces + kWarps - 1) / kWarps)), dim3(kWarps * 32), (size_t)smem, stream, a);
-  if (e != cudaSuccess || a.split_done != nullptr) return e;
-  return launch_dependent(kv8_merge_kernel<D>, dim3((unsigned)((long long)a.batch * a.H)), dim3(kMergeWarps * 32), 0,
+  e = launch_dependent(kernel, dim3((unsigned)a.pieces), dim3(kWarps * 32), (size_t)smem, stream, a);
+  if (e != cudaSuccess || !a.cut || a.split_done != nullptr) return e;
+  return launch_dependent(kv8_merge_kernel<D>, dim3((unsigned)((long long)a.batch * a.H)), dim3(kMergeThreads), 0,
                           stream, a);
 }
 
@@ -683,8 +710,10 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int D, cudaStream_t stream)
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.pieces * 2 * G * 2 * sizeof(float)));
   // (the most pieces that a unit can lie in; with counts of its own per sequence
   // the line is shorter and a unit lies in more of them)
-  const long long most = a.lens.any() ? (blocks < a.pieces ? blocks : a.pieces) : a.pieces / units + 2;
-  a.split_done = units <= kWorkspaceCounters && G <= 2 && most <= kFusedPieces ? a.counters : nullptr;
+  const long long most = a.lens.any() ? (blocks < a.pieces ? blocks : a.pieces)
+                                      : a.pieces % units == 0 ? a.pieces / units : a.pieces / units + 2;
+  a.cut = a.lens.any() || units % a.pieces != 0;
+  a.split_done = units <= kWorkspaceCounters && most * G <= kFusedRows ? a.counters : nullptr;
   if (D == 128) return G <= 8 ? launch_nt<128, 1>(a, stream) : launch_nt<128, 2>(a, stream);
   return G <= 8 ? launch_nt<64, 1>(a, stream) : launch_nt<64, 2>(a, stream);
 }
