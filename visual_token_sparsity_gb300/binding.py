@@ -383,18 +383,21 @@ class _Call:
         return t.data_ptr(), st if T > 1 else sb if B > 1 else h * d
 
 
-    def packed(self, t, heads, d, name):
+    def packed(self, t, N, heads, d, name):
         """Pointer and token stride of bf16 [N][heads][d] rows that lie evenly apart."""
+        st = t.stride()
+        if t.dtype is _BF16 and t.shape == (N, heads, d) and t.get_device() == self.dev and st[1:] == (d, 1):
+            return t.data_ptr(), st[0] if N > 1 else heads * d
+        # what is wrong, if anything (an axis of one element may have any stride)
         if t.dtype != _BF16:
             raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-            raise ValueError(f"{name} must have shape (N, {heads}, {d}), got {tuple(t.shape)}")
+        if t.shape != (N, heads, d):
+            raise ValueError(f"{name} must have shape {(N, heads, d)}, got {tuple(t.shape)}")
         if t.get_device() != self.dev:
             raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{self.dev}, is on {t.device}")
-        st, sh, sd = t.stride()
-        if t.numel() and ((sd != 1 and d > 1) or (sh != d and heads > 1)):
-            raise ValueError(f"{name}: heads must be contiguous, strides {t.stride()}")
-        return t.data_ptr(), st if t.shape[0] > 1 else heads * d
+        if t.numel() and ((st[2] != 1 and d > 1) or (st[1] != d and heads > 1)):
+            raise ValueError(f"{name}: heads must be contiguous, strides {st}")
+        return t.data_ptr(), st[0] if N > 1 else heads * d
 
 
 # ------------------------------------------------------------------ sizes
@@ -692,13 +695,11 @@ def sv_prompt_attn(q, k, v, seq_start, scale, out, lse, ws, stream=None):
     lib = load()
     N, H, d = q.shape
     Hkv, B = k.shape[1], seq_start.shape[0] - 1
-    if k.shape[0] != N or v.shape != k.shape:
-        raise ValueError(f"k and v must have {N} tokens and one shape, got {tuple(k.shape)}, {tuple(v.shape)}")
     if B < 0:
         raise ValueError("seq_start must have batch + 1 entries")
     c = _Call(ws, stream)
-    _check(lib.sv_prompt_attn(*c.packed(q, H, d, "q"), *c.packed(k, Hkv, d, "k"), *c.packed(v, Hkv, d, "v"), N, H, Hkv,
-                              d, scale, c.ptr(seq_start, _I32, (B + 1,), "seq_start"), B,
+    _check(lib.sv_prompt_attn(*c.packed(q, N, H, d, "q"), *c.packed(k, N, Hkv, d, "k"), *c.packed(v, N, Hkv, d, "v"), N,
+                              H, Hkv, d, scale, c.ptr(seq_start, _I32, (B + 1,), "seq_start"), B,
                               c.ptr(out, _BF16, (N, H, d), "out"), c.ptr(lse, _F32, (N, H), "lse"), *c.ws, c.stream))
 
 
@@ -710,12 +711,10 @@ def sv_kv8_append(q, k, v, rot, layer, seqs, q_out, ws, seq_start=None, k_out=No
     lib = load()
     N, H, d = q.shape
     Hkv = layer.n_kv_heads
-    if k.shape[0] != N or v.shape[0] != N:
-        raise ValueError(f"k and v must have {N} tokens, got {k.shape[0]}, {v.shape[0]}")
     c = _Call(ws, stream, rot, layer, seqs)
     rot.check_packed(N, d)
-    _check(lib.sv_kv8_append(*c.packed(q, H, layer.head_dim, "q"), *c.packed(k, Hkv, d, "k"),
-                             *c.packed(v, Hkv, d, "v"), N, H, rot.by_ref, layer.by_ref, seqs.by_ref,
+    _check(lib.sv_kv8_append(*c.packed(q, N, H, layer.head_dim, "q"), *c.packed(k, N, Hkv, d, "k"),
+                             *c.packed(v, N, Hkv, d, "v"), N, H, rot.by_ref, layer.by_ref, seqs.by_ref,
                              c.ptr(seq_start, _I32, (seqs.batch + 1,), "seq_start"),
                              c.ptr(q_out, _BF16, q.shape, "q_out"), c.ptr(k_out, _BF16, (N, Hkv, d), "k_out"), *c.ws,
                              c.stream))

@@ -105,7 +105,6 @@ struct AttnArgs {
   const void* v_new = nullptr;
 };
 cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t stream);
-// joins nsplit partials per (sequence, query head), [batch][Hkv][nsplit][G]
 cudaError_t launch_sparse_attn_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
 
 // ---- compaction gather (prune.cu)
