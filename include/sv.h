@@ -738,7 +738,8 @@ sv_status sv_kv8_append(const void* q, int64_t q_stride, const void* k, int64_t 
  * The selection is that of the exact scores: tokens whose fp32 scores are too
  * near to the k-th one to tell are scored again with 48 bits.  Ties go to the lower
  * index.  scores (optional out) are the fp32 ones.  With scores that are not
- * finite the choice is unspecified (but valid).
+ * finite the choice is unspecified (but valid).  At most 65535 sequences, and
+ * 2^24 of them times KV heads.
  * ws : sv_kv8_retrieve_workspace_bytes(B, H, n_kv_heads, head_dim, n_vis, k);
  *      sized for the largest B and n_vis it serves every smaller call.
  */
@@ -749,7 +750,10 @@ sv_status sv_kv8_retrieve_topk(const void* q, int R, int H, const sv_kv8_layer* 
 /*
  * sv_sparse_decode_attn over the 8-bit cache; arguments, per-sequence lengths
  * and skipped loads as there.  A row that attends to no token has out 0 and
- * lse -inf.  out: 16-byte aligned, apart from q.
+ * lse -inf.  out: 16-byte aligned, apart from q.  The weights of the product with
+ * V are rounded to fp16's eleven bits; of a value whose weight times factor is
+ * below 2^-20 of the row's largest weight times the largest factor among its pages
+ * fewer are left, below 2^-30 none.
  * ws : sv_kv8_attn_workspace_bytes(B, H, n_kv_heads, head_dim, n_tokens),
  *      n_tokens = k + n_text (k = n_vis when vis_idx is NULL); the size never
  *      shrinks as B or n_tokens grow.

@@ -489,7 +489,6 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
   grid_dep_sync();
   const int row = blockIdx.x, b = row / a.Hkv, g = row - b * a.Hkv;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  (void)warp;
   int n = a.n_vis, k = a.k;
   if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
   int32_t* dst = a.vis_idx + (size_t)row * a.k;
@@ -540,7 +539,7 @@ kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query
   __shared__ BorderShared sh;
   grid_dep_sync();
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), row = blockIdx.y, b = row / a.Hkv, g = row - b * a.Hkv;
+  const int rank = (int)cluster.block_rank(), row = blockIdx.x / kTopkClusterCtas, b = row / a.Hkv, g = row - b * a.Hkv;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   int n = a.n_vis, k = a.k;
   if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
@@ -733,7 +732,7 @@ static cudaError_t launch_select_cluster(const Kv8RetrieveArgs& a, const Query8<
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const int slice = (a.n_vis + kTopkClusterCtas - 1) / kTopkClusterCtas;
-  return launch_dependent(kernel, dim3(kTopkClusterCtas, (unsigned)(a.batch * a.Hkv)), dim3(kTopkClusterThreads),
+  return launch_dependent(kernel, dim3((unsigned)(kTopkClusterCtas * a.batch * a.Hkv)), dim3(kTopkClusterThreads),
                           (size_t)slice * sizeof(uint32_t), stream, a, rows, scores, factors, n_factors, exact);
 }
 
