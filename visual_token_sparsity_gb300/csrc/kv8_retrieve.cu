@@ -16,9 +16,20 @@
 // score is within e of the true one, so a token more than 2 e above it is in
 // and one more than 2 e below it is out.  Those in between are scored again with
 // 48 bits and the best of them taken, ties to the lower index.
+//
+// Measured, keys out of L2, head dim 128: 16 sequences of 32 KV heads and 2880 keys
+// 47.3 us (4.2 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 53.8 us
+// (2.9 TB/s).  Scoring takes 37 and 36 us of it by itself, bound by the latency of one
+// page in flight in each of 40 warps an SM (two pages in 20 warps: 53 and more); the
+// selection 10 and 18, a chain of some ten waits (scores, counts, pages of the tokens
+// next to the border, and a cluster's barriers) that little work lies between.  With a
+// search by the bits of the keys they were 48.3 and 56.2.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
-#include "topk_cluster.cuh"
+#include "topk_block.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -35,8 +46,8 @@ constexpr int kScoreWarps = 8;
 // are told apart by 2 e; twice that is taken:
 constexpr float kBand = 448.f / 4194304.f;
 constexpr float kBandMax = 272.f, kBandSum = 12.f;
-constexpr int kListed = 1024;            // tokens next to the border that are ranked in shared memory
-constexpr int kStagedKeys = 16384;       // keys of a row whose selection one CTA makes in shared memory
+constexpr int kStagedKeys = 16384;       // keys of a row whose selection one CTA makes
+constexpr int kSliceKeys = 50176;        // keys that a CTA of a cluster keeps in shared memory
 
 // hi + lo = a + b.
 __device__ __forceinline__ void two_sum(float a, float b, float& hi, float& lo) {
@@ -148,13 +159,20 @@ kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>
   sum_query<D>(q, R, H, Hkv, blockIdx.x, rows + blockIdx.x);
 }
 
+// What a scoring warp leaves for the selection: the largest factor of its pages, and
+// its smallest and largest score as ordered keys.
+struct __align__(16) Part {
+  float factor;
+  uint32_t lo, hi, pad;
+};
+
 // A warp per page, one page in flight, as many warps as 48 registers allow.  SUM:
 // the query's rows are few, and every CTA adds them up itself (the first of a row
 // leaves the sum for the selection).
 template <int D, bool SUM>
 __global__ void __launch_bounds__(kScoreWarps * 32, 5)
 kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, float* __restrict__ scores,
-                 float* __restrict__ factors, int pages_per_cta) {
+                 Part* __restrict__ parts, int pages_per_cta) {
   constexpr int KS = D / 16, KC = D / 64, W = kScoreWarps;
   __shared__ __align__(16) Query8<D> query;
   grid_dep_sync();
@@ -203,7 +221,7 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
   // (the query's parts: column r of a tile is part r, the columns behind are 0)
   const uint16_t* part = &query.part[min(r, 3)][q4 * 16];
   float* out = scores + (size_t)row * a.n_vis;
-  float top = 0.f;             // the largest factor
+  Part left = {0.f, 0xffffffffu, 0u, 0u};
   for (int p = first; p < end; p += W) {
     float c[4] = {};
 #pragma unroll
@@ -232,28 +250,72 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
         v = (v * query.back[0]) * (f * query.back[1]);
         return !there ? 0.f : isnan(v) ? __uint_as_float(0x7fffffffu) : v;
       };
-      if (pos < nv) out[pos] = value(s0);
-      if (pos + 8 < nv) out[pos + 8] = value(s1);
+      auto put = [&](int at, float v) {
+        if (at >= nv) return;
+        out[at] = v;
+        left.lo = min(left.lo, order_key(v));
+        left.hi = max(left.hi, order_key(v));
+      };
+      put(pos, value(s0));
+      put(pos + 8, value(s1));
     }
-    if (there) top = fmaxf(top, fabsf(f));
+    if (there) left.factor = fmaxf(left.factor, fabsf(f));
   }
-  if (lane == 0) factors[((size_t)row * gridDim.x + blockIdx.x) * W + warp] = top;
+  left.lo = __reduce_min_sync(0xffffffffu, left.lo);
+  left.hi = __reduce_max_sync(0xffffffffu, left.hi);
+  if (lane == 0)
+    *reinterpret_cast<uint4*>(parts + ((size_t)row * gridDim.x + blockIdx.x) * W + warp) =
+        make_uint4(__float_as_uint(left.factor), left.lo, left.hi, 0u);
 }
 
 namespace {
 
-struct BorderShared {
-  uint64_t list_v[kListed];
-  int list_j[kListed];
-  int sure, near, digit, above, last_j;
+constexpr int kCluster = 8, kClusterThreads = 512;   // of a long row's selection
+constexpr int kBins = 2048;
+constexpr int kCrowd = 320, kPasses = 4;   // a border's bin of more keys is cut again, up to so often
+constexpr int kListed = 512;               // tokens next to the border that are ranked in shared memory
+
+struct __align__(16) SelectShared {
+  uint2 mine[kListed], all[kListed];       // (key, index) of this CTA's tokens next to the border, and of every CTA's
+  uint64_t exact[kListed];
+  uint32_t key[kListed];                   // (16-byte aligned)
+  int inside[kListed];                     // those of `all` that fp32 cannot tell
+  int hist[kBins], coarse[32];
+  int sure, near;                          // (read together by other CTAs)
+  int bin, count, clear, n_inside, kept;
   unsigned long long last;
-  uint32_t kth[32];
+  int last_j;
+  uint32_t kth, lo[32], hi[32], scan[32];
   float factor[32];
-  uint32_t scan_tmp[33];
-  int hist[256];
 };
 
-// The score of token j with 48 bits, by eight lanes (lane % 8 == 0 has it).
+// The parts of a row together; all threads of the block call this.
+__device__ __forceinline__ Part whole_row(const Part* parts, int n, SelectShared& sh) {
+  Part x = {0.f, 0xffffffffu, 0u, 0u};
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint4 y = __ldcg(reinterpret_cast<const uint4*>(parts) + i);
+    x.factor = fmaxf(x.factor, __uint_as_float(y.x));
+    x.lo = min(x.lo, y.y);
+    x.hi = max(x.hi, y.z);
+  }
+  x.factor = warp_max(x.factor);
+  x.lo = __reduce_min_sync(0xffffffffu, x.lo);
+  x.hi = __reduce_max_sync(0xffffffffu, x.hi);
+  if ((threadIdx.x & 31) == 0) {
+    sh.factor[threadIdx.x >> 5] = x.factor;
+    sh.lo[threadIdx.x >> 5] = x.lo;
+    sh.hi[threadIdx.x >> 5] = x.hi;
+  }
+  __syncthreads();
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+    x.factor = fmaxf(x.factor, sh.factor[w]);
+    x.lo = min(x.lo, sh.lo[w]);
+    x.hi = max(x.hi, sh.hi[w]);
+  }
+  return x;
+}
+
+// The score of token j with 48 bits, by eight lanes, all of which have it.
 template <int D>
 __device__ __forceinline__ uint64_t score48(const Kv8RetrieveArgs& a, const Query8<D>* query, int b, int g, int j, bool on,
                                           int lane) {
@@ -268,6 +330,7 @@ __device__ __forceinline__ uint64_t score48(const Kv8RetrieveArgs& a, const Quer
       uint32_t w[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
+      float hi1 = 0.f, lo1 = 0.f;                          // (two sums side by side: each waits for its last step)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const float2 x = kv8::e4m3x2_to_float2((uint16_t)(w[i >> 1] >> ((i & 1) * 16)));
@@ -275,8 +338,9 @@ __device__ __forceinline__ uint64_t score48(const Kv8RetrieveArgs& a, const Quer
         float p = __fmul_rn(q2.x, x.x);
         add48(hi, lo, p, fmaf(q2.y, x.x, fmaf(q2.x, x.x, -p)));
         p = __fmul_rn(q2.z, x.y);
-        add48(hi, lo, p, fmaf(q2.w, x.y, fmaf(q2.z, x.y, -p)));
+        add48(hi1, lo1, p, fmaf(q2.w, x.y, fmaf(q2.z, x.y, -p)));
       }
+      add48(hi, lo, hi1, lo1);
     }
   }
 #pragma unroll
@@ -295,445 +359,399 @@ __device__ __forceinline__ uint64_t score48(const Kv8RetrieveArgs& a, const Quer
   return order_key64(hi, lo);
 }
 
-// Keys [lo, hi] around a border may lie on its other side: those within the band of
-// it (every selected fp32 score is at least the border's value and every other one
-// below it, so that is as good a middle as the k-th score), and where the search for
-// it ended with few keys in the border's bin, those of the bin and within the band of
-// both its ends.  Scores or a band that are not finite: the fp32 order, ties included.
-constexpr int kFew = 6;
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return (key & 0x80000000u) ? __uint_as_float(key ^ 0x80000000u) : __uint_as_float(~key);
+}
+
+// Keys [lo, hi] around a border: those above are in and those below are out.
 struct Near {
   uint32_t lo, hi;
-  bool wide;
 };
-__device__ __forceinline__ Near near_border(const TopkBorder& t, float band) {
-  auto value = [](uint32_t key) {
-    return (key & 0x80000000u) ? __uint_as_float(key ^ 0x80000000u) : __uint_as_float(~key);
-  };
-  const uint32_t bin = t.prefix | ~t.pmask, top = t.open ? bin : t.prefix;
-  Near x;
-  x.wide = band > 0.f && isfinite(band) && isfinite(value(t.prefix)) && isfinite(value(top));
-  x.lo = x.wide ? order_key(value(t.prefix) - band) : t.prefix;
-  x.hi = x.wide ? order_key(value(top) + band) : bin;
-  return x;
+
+// Keys within the band around values [lo, hi] that the k-th score lies in.  (Every
+// selected fp32 score is at least the border's value and every other one below it, so
+// that is as good a middle as the k-th true score.)
+__device__ __forceinline__ Near near_values(float lo, float hi, float band) {
+  return Near{order_key(lo - band), order_key(hi + band)};
 }
 
-// Writes the indices (first + i) of the keys that are taken in ascending order, by a
-// block whose warps have stretches of 32 keys; before(n) tells how many come before
-// the block's n.
-template <typename Taken, typename Before>
-__device__ __forceinline__ void emit_taken(int n, int first, int32_t* dst, uint32_t* scan_tmp, Taken taken, Before before) {
-  const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = nt >> 5;
-  const int per = ((n + 31) / 32 + nw - 1) / nw * 32, w0 = min(n, warp * per), w1 = min(n, w0 + per);
-  uint32_t count = 0;
-  for (int i0 = w0; i0 < w1; i0 += 32) count += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && taken(i0 + lane)));
-  if (lane == 0) scan_tmp[warp] = count;
-  __syncthreads();
-  uint32_t o = 0, all = 0;
-  for (int w = 0; w < nw; ++w) {
-    const uint32_t c = scan_tmp[w];
-    o += w < warp ? c : 0u;
-    all += c;
+// Finds keys around the k-th largest of a row.  Scores are cut into bins of equal width
+// between the smallest and the largest, so that they spread over most of them (the bits
+// of a float's key put nearly all keys of a row into a few bins, and finding the border
+// by them takes four rounds and more).  The bin of the k-th is cut again as long as it is
+// crowded.  (x - a) * inv, rounded, ascends with x, so bins are in order; their edges are
+// known to a few 2^-24 of the range and of the largest magnitude, of which 2^-19 is taken.
+// Rows with scores that are not finite, or all equal: every key.
+//   keys: this block's n, hist: their counts for the first cut (Cut::count); total(p): the
+//   sum of *p over the row's CTAs; sync(): waits for them.
+struct Cut {
+  float lo, hi, inv, slop;
+  bool ok;
+  __device__ __forceinline__ explicit Cut(const Part& row) : lo(value_of(row.lo)), hi(value_of(row.hi)) {
+    slop = fmaxf(fabsf(lo), fabsf(hi)) * (1.f / 524288.f);
+    inv = (float)kBins / (hi - lo);
+    ok = isfinite(hi - lo) && isfinite(inv);
   }
-  o += before(all);
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const bool take = i0 + lane < w1 && taken(i0 + lane);
-    const uint32_t mask = __ballot_sync(0xffffffffu, take);
-    if (take) dst[o + __popc(mask & ((1u << lane) - 1u))] = first + i0 + lane;
-    o += __popc(mask);
+  __device__ __forceinline__ void count(uint32_t key, int* hist, int& above) const {
+    const float t = (value_of(key) - lo) * inv;
+    above += t >= (float)(kBins - 1);                       // (with the last bin's)
+    if (t >= 0.f && t < (float)(kBins - 1)) atomicAdd(&hist[(int)t], 1);
   }
-}
-
-// This thread's part of the largest of a row's factors, and the block's.
-__device__ __forceinline__ float some_factor(const float* factors, int n) {
-  float x = 0.f;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) x = fmaxf(x, __ldcg(factors + i));
-  return x;
-}
-__device__ __forceinline__ float largest_factor(float x, float* tmp) {
-  x = warp_max(x);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = x;
-  __syncthreads();
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x = fmaxf(x, tmp[w]);
-  return x;
-}
-
-// Selects the k tokens of a row, given its keys and their border.  All threads of
-// the block call this.
-template <int D>
-__device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query8<D>* query, int b, int g, int n, int k,
-                                           uint32_t* keys, const TopkBorder& border, float factor, uint64_t* exact,
-                                           int32_t* dst, BorderShared& sh) {
+};
+template <typename Total, typename Sync>
+__device__ __forceinline__ Near near_border(const uint32_t* keys, int n, int k, const Part& row, Cut cut, int above,
+                                            float band, SelectShared& sh, Total total, Sync sync) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  const Near near = near_border(border, query->slack * kBand * factor);
-  const uint32_t lo = near.lo, hi = near.hi;
-  const bool wide = near.wide;
-  if (tid == 0) sh.sure = sh.near = 0;
-  __syncthreads();
-  int in = 0;
-  for (int i0 = tid; i0 < n; i0 += 4 * nt) {
-    uint32_t key[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) key[j] = i0 + j * nt < n ? keys[i0 + j * nt] : 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      in += key[j] > hi;
-      if (key[j] >= lo && key[j] <= hi) {
-        const int at_list = atomicAdd(&sh.near, 1);
-        if (at_list < kListed) sh.list_j[at_list] = i0 + j * nt;
-      }
+  if (!cut.ok) return Near{row.lo, row.hi};
+  const float bottom = cut.lo, top = cut.hi;
+  for (int pass = 0;; ++pass) {
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 0 && above > 0) atomicAdd(&sh.hist[kBins - 1], above);
+    // sums of 64 bins first, so that little is read from other CTAs
+    __syncthreads();
+    for (int i = warp; i < 32; i += nw) {
+      const int c = __reduce_add_sync(0xffffffffu, sh.hist[i * 64 + lane] + sh.hist[i * 64 + 32 + lane]);
+      if (lane == 0) sh.coarse[i] = c;
     }
-  }
-  in = __reduce_add_sync(0xffffffffu, in);
-  if (lane == 0) atomicAdd(&sh.sure, in);
-  __syncthreads();
-  const int need = k - sh.sure, m = sh.near;     // of the m tokens next to the border
-  bool by_value = false;                         // taken by (value, index), not all
-  if (m > need) {
-    const bool listed = m <= kListed;
-    by_value = !listed;
-    if (listed) {
-      for (int i0 = warp * 4; i0 < m; i0 += nw * 4) {
-        const int i = i0 + (lane >> 3);
-        const int j = i < m ? sh.list_j[i] : 0;
-        const uint64_t v = wide ? score48<D>(a, query, b, g, j, i < m, lane) : (uint64_t)keys[j] << 32;
-        if (i < m && (lane & 7) == 0) sh.list_v[i] = v;
-      }
-      __syncthreads();
-      for (int i = warp; i < m; i += nw) {
-        const uint64_t v = sh.list_v[i];
-        const int j = sh.list_j[i];
-        int better = 0;
-        for (int o = lane; o < m; o += 32) better += sh.list_v[o] > v || (sh.list_v[o] == v && sh.list_j[o] < j);
-        better = __reduce_add_sync(0xffffffffu, better);
-        if (lane == 0 && better >= need) keys[j] = 0u;             // (no score's key)
-      }
-    } else {
-      for (int i0 = warp * 32; i0 < n; i0 += nt) {
-        const uint32_t key = i0 + lane < n ? keys[i0 + lane] : 0u;
-        uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < n && key >= lo && key <= hi);
-        while (todo) {
-          // four of them at a time
-          int j = -1;
+    sync();
+    if (warp == 0) {
+      // the l-th of 32 counts from the top in lane l: the one that the k-th lies in
+      int left = k;
+      auto find = [&](int count) {
+        int incl = count;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int bit = __ffs(todo) - 1;
-            if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
-            todo &= todo - 1;
-          }
-          const uint64_t v = wide ? score48<D>(a, query, b, g, max(j, 0), j >= 0, lane) : (uint64_t)keys[max(j, 0)] << 32;
-          if (j >= 0 && (lane & 7) == 0) exact[j] = v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
         }
-      }
-      // a radix selection over the 96 bits of (value, ~index)
-      unsigned long long top = 0;
-      uint32_t low = 0;
-      int left = need;
-      for (int pass = 0; pass < 12; ++pass) {
-        for (int i = tid; i < 256; i += nt) sh.hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += nt) {
-          const uint32_t key = keys[i];
-          if (key < lo || key > hi) continue;
-          const uint64_t kv = exact[i];
-          const uint32_t ki = ~(uint32_t)i;
-          if (pass < 8) {
-            if (pass > 0 && (kv ^ top) >> (64 - 8 * pass)) continue;
-            atomicAdd(&sh.hist[(kv >> (56 - 8 * pass)) & 255], 1);
-          } else {
-            if (kv != top || (pass > 8 && (ki ^ low) >> (32 - 8 * (pass - 8)))) continue;
-            atomicAdd(&sh.hist[(ki >> (24 - 8 * (pass - 8))) & 255], 1);
-          }
-        }
-        __syncthreads();
-        if (tid == 0) {
-          int sum = 0, d = 255;
-          while (d > 0 && sum + sh.hist[d] < left) sum += sh.hist[d--];
-          sh.digit = d;
-          sh.above = sum;
-        }
-        __syncthreads();
-        left -= sh.above;
-        if (pass < 8) top |= (unsigned long long)sh.digit << (56 - 8 * pass);
-        else low |= (uint32_t)sh.digit << (24 - 8 * (pass - 8));
-        __syncthreads();
-      }
-      if (tid == 0) {
-        sh.last = top;
-        sh.last_j = (int)~low;
+        const int f = (__ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1) & 31;
+        left -= __shfl_sync(0xffffffffu, incl - count, f);
+        return f;
+      };
+      const int from = (31 - find(total(&sh.coarse[31 - lane]))) * 64;
+      const int c1 = total(&sh.hist[from + 63 - 2 * lane]), c0 = total(&sh.hist[from + 62 - 2 * lane]);
+      const int f = find(c0 + c1);
+      if (lane == f) {
+        const bool upper = c1 >= left;
+        sh.bin = from + 63 - 2 * f - (upper ? 0 : 1);
+        sh.count = upper ? c1 : c0;
       }
     }
     __syncthreads();
+    const int bin = sh.bin;
+    const float width = 1.f / cut.inv, from = cut.lo;
+    cut.lo = fmaxf(bottom, fmaf((float)bin, width, from) - cut.slop);
+    cut.hi = bin == kBins - 1 ? top : fminf(top, fmaf((float)(bin + 1), width, from) + cut.slop);
+    cut.inv = (float)kBins / (cut.hi - cut.lo);
+    if (sh.count <= kCrowd || pass == kPasses - 1 || cut.hi - cut.lo < 8.f * cut.slop || !isfinite(cut.inv))
+      return near_values(cut.lo, cut.hi, band);
+    sync();                                                 // (the counts have been read)
+    for (int i = tid; i < kBins; i += nt) sh.hist[i] = 0;
+    __syncthreads();
+    above = 0;
+    for (int i = tid; i < n; i += nt) cut.count(keys[i], sh.hist, above);
   }
-  auto taken = [&](int i) {
-    const uint32_t key = keys[i];
-    if (!by_value || key < lo || key > hi) return key >= lo;
-    const uint64_t v = exact[i];
-    return v > sh.last || (v == sh.last && i <= sh.last_j);
-  };
-  emit_taken(n, 0, dst, sh.scan_tmp, taken, [](uint32_t) { return 0u; });
 }
 
 }  // namespace
 
-// The selection of one row per CTA.  KNOWN: the keys of rows that are too long for
-// shared memory go to `far_keys`, the k largest fp32 scores have been taken
-// (vis_idx), and the k-th is their smallest.
-template <int D, bool KNOWN>
-__global__ void __launch_bounds__(1024)
+// The selection of one row by C CTAs, CTA r having its r-th slice.  FAR: the keys of a
+// slice do not fit shared memory and go to `far_keys`.
+template <int D, int C, bool FAR>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kClusterThreads, 2)
 kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows, const float* __restrict__ scores,
-                  const float* __restrict__ factors, int n_factors, uint64_t* __restrict__ exact,
+                  const Part* __restrict__ parts, int n_parts, uint64_t* __restrict__ exact_rows,
                   uint32_t* __restrict__ far_keys) {
   extern __shared__ __align__(16) uint32_t staged[];
-  __shared__ TopkShared ts;
-  __shared__ BorderShared sh;
-  grid_dep_sync();
-  const int row = blockIdx.x, b = row / a.Hkv, g = row - b * a.Hkv;
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  int n = a.n_vis, k = a.k;
-  if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
-  int32_t* dst = a.vis_idx + (size_t)row * a.k;
-  const float* src = scores + (size_t)row * a.n_vis;
-  uint32_t* keys = KNOWN ? far_keys + (size_t)row * a.n_vis : staged;
-  if (!KNOWN) fill_unselected(dst, k, a.k);
-  if (k <= 0) return;
-  float factor = some_factor(factors + (size_t)row * n_factors, n_factors);
-  TopkBorder border;
-  if (KNOWN) {
-    uint32_t kth = 0xffffffffu;
-    for (int i0 = tid; i0 < n; i0 += 8 * nt) {
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __ldcg(src + min(i0 + j * nt, n - 1));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i0 + j * nt < n) keys[i0 + j * nt] = order_key(x[j]);
-    }
-    __syncthreads();
-    for (int i0 = tid; i0 < k; i0 += 4 * nt) {
-      int at[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) at[j] = __ldcg(dst + min(i0 + j * nt, k - 1));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kth = min(kth, keys[at[j]]);
-    }
-    kth = __reduce_min_sync(0xffffffffu, kth);
-    if (lane == 0) sh.kth[warp] = kth;
-    __syncthreads();
-    for (int w = 0; w < nt / 32; ++w) kth = min(kth, sh.kth[w]);
-    border = TopkBorder{kth, 0xffffffffu, 0, false};
-  } else {
-    border = block_topk_border(src, n, k, keys, ts, kFew);
-  }
-  factor = largest_factor(factor, sh.factor);
-  select_row<D>(a, rows + row, b, g, n, k, keys, border, factor, exact + (size_t)row * a.n_vis, dst, sh);
-}
-
-// The same for a long row by a cluster: CTA r has its r-th slice.
-template <int D>
-__global__ void __cluster_dims__(kTopkClusterCtas, 1, 1) __launch_bounds__(kTopkClusterThreads)
-kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows,
-                          const float* __restrict__ scores, const float* __restrict__ factors, int n_factors,
-                          uint64_t* __restrict__ exact_rows) {
-  extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ ClusterTopkShared ts;
-  __shared__ BorderShared sh;
-  grid_dep_sync();
+  __shared__ SelectShared sh;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), row = blockIdx.x / kTopkClusterCtas, b = row / a.Hkv, g = row - b * a.Hkv;
+  const int rank = C > 1 ? (int)cluster.block_rank() : 0, row = blockIdx.x / C, b = row / a.Hkv, g = row - b * a.Hkv;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  auto sync = [&] {
+    if constexpr (C > 1) cluster.sync();
+    else __syncthreads();
+  };
+  auto total = [&](const int* p) {
+    if constexpr (C == 1) return *p;
+    int sum = 0;
+#pragma unroll
+    for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(p, r);
+    return sum;
+  };
+  if (tid == 0) sh.sure = sh.near = sh.clear = sh.n_inside = sh.kept = 0;
+  for (int i = tid; i < kBins; i += nt) sh.hist[i] = 0;
+  grid_dep_sync();
   int n = a.n_vis, k = a.k;
   if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
   int32_t* dst = a.vis_idx + (size_t)row * a.k;
   if (rank == 0) fill_unselected(dst, k, a.k);
   if (k <= 0) return;                        // (the whole cluster)
-  const int slice = (n + kTopkClusterCtas - 1) / kTopkClusterCtas;
-  const int first = min(n, rank * slice), len = min(n, first + slice) - first;
+  const int slice = (n + C - 1) / C, first = min(n, rank * slice), len = min(n, first + slice) - first;
+  const float* src = scores + (size_t)row * a.n_vis + first;
+  uint32_t* keys = FAR ? far_keys + (size_t)row * a.n_vis + first : staged;
+  float x[8];                                // (on their way with the parts)
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = i0 + j * nt < len ? __ldcg(src + i0 + j * nt) : 0.f;
+  };
+  load(tid);
   const Query8<D>* query = rows + row;
-  uint64_t* exact = exact_rows + (size_t)row * a.n_vis + first;
-  float factor = some_factor(factors + (size_t)row * n_factors, n_factors);
-  if (tid == 0) sh.sure = sh.near = 0;       // (the search below has barriers)
-  const TopkBorder t = cluster_topk_border(scores + (size_t)row * a.n_vis + first, len, k, keys, ts, kFew);
-  factor = largest_factor(factor, sh.factor);
-  const Near x = near_border(t, query->slack * kBand * factor);
-  const uint32_t lo = x.lo, hi = x.hi;
-  const bool wide = x.wide;
+  const Part whole = whole_row(parts + (size_t)row * n_parts, n_parts, sh);
+  const Cut cut(whole);
+  int above = 0;
+  for (int i0 = tid; i0 < len;) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (i0 + j * nt >= len) break;
+      const uint32_t key = order_key(x[j]);
+      keys[i0 + j * nt] = key;
+      if (cut.ok) cut.count(key, sh.hist, above);
+    }
+    i0 += 8 * nt;
+    load(i0);
+  }
+  const float some = query->slack * kBand * whole.factor;
+  // without a band (or with scores that are not finite) the fp32 order decides
+  const bool wide = some > 0.f && isfinite(some) && isfinite(value_of(whole.hi) - value_of(whole.lo));
+  const float band = wide ? some : 0.f;
+  const Near near = near_border(keys, len, k, whole, cut, above, band, sh, total, sync);
+  const uint32_t lo = near.lo, hi = near.hi;
+
+  // ---- the tokens next to the border, of every CTA
   int in = 0;
-  for (int i = tid; i < len; i += nt) {
-    const uint32_t key = keys[i];
-    in += key > hi;
-    if (key >= lo && key <= hi) {
-      const int at_list = atomicAdd(&sh.near, 1);
-      if (at_list < kListed) sh.list_j[at_list] = i;
+  for (int i0 = tid; i0 < len; i0 += 4 * nt) {
+    uint32_t key[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) key[j] = i0 + j * nt < len ? keys[i0 + j * nt] : 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      in += key[j] > hi;
+      if (key[j] >= lo && key[j] <= hi) {
+        const int to = atomicAdd(&sh.near, 1);
+        if (to < kListed) sh.mine[to] = make_uint2(key[j], (uint32_t)(first + i0 + j * nt));
+      }
     }
   }
   in = __reduce_add_sync(0xffffffffu, in);
-  if (lane == 0) atomicAdd(&sh.sure, in);
-  cluster.sync();
-  int sure = 0, m = 0, most = 0;
-#pragma unroll
-  for (int r = 0; r < kTopkClusterCtas; ++r) {
-    const int near = *cluster.map_shared_rank(&sh.near, r);
-    sure += *cluster.map_shared_rank(&sh.sure, r);
-    m += near;
-    most = max(most, near);
-  }
-  const int need = k - sure, mine = sh.near;
-  bool by_value = false;
-  if (m > need) {
-    by_value = most > kListed;
-    if (!by_value) {
-      for (int i0 = warp * 4; i0 < mine; i0 += nw * 4) {
-        const int i = i0 + (lane >> 3);
-        const int j = i < mine ? sh.list_j[i] : 0;
-        const uint64_t v = wide ? score48<D>(a, query, b, g, first + j, i < mine, lane) : (uint64_t)keys[j] << 32;
-        if (i < mine && (lane & 7) == 0) sh.list_v[i] = v;
-      }
-      cluster.sync();
-      // ranked against every CTA's list (slices are in order of index)
-      for (int i = warp; i < mine; i += nw) {
-        const uint64_t v = sh.list_v[i];
-        const int j = sh.list_j[i];
-        int better = 0;
-        // (four lanes for each CTA, so that no list waits for another)
-        const int r = lane >> 2;
-        static_assert(kTopkClusterCtas == 8, "four lanes a CTA");
-        const int theirs = *cluster.map_shared_rank(&sh.near, r);
-        const uint64_t* values = cluster.map_shared_rank(&sh.list_v[0], r);
-        const int* indices = cluster.map_shared_rank(&sh.list_j[0], r);
-        for (int o = lane & 3; o < theirs; o += 4) {
-          const uint64_t y = values[o];
-          better += y > v || (y == v && (r < rank || (r == rank && indices[o] < j)));
-        }
-        better = __reduce_add_sync(0xffffffffu, better);
-        if (lane == 0 && better >= need) keys[j] = 0u;             // (no score's key)
-      }
-    } else {
-      for (int i0 = warp * 32; i0 < len; i0 += nt) {
-        const uint32_t key = i0 + lane < len ? keys[i0 + lane] : 0u;
-        uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < len && key >= lo && key <= hi);
-        while (todo) {
-          int j = -1;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int bit = __ffs(todo) - 1;
-            if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
-            todo &= todo - 1;
-          }
-          const uint64_t v =
-              wide ? score48<D>(a, query, b, g, first + max(j, 0), j >= 0, lane) : (uint64_t)keys[max(j, 0)] << 32;
-          if (j >= 0 && (lane & 7) == 0) exact[j] = v;
-        }
-      }
-      for (int i = tid; i < 512; i += nt) (&ts.hist[0][0])[i] = 0;
-      unsigned long long top = 0;
-      uint32_t low = 0;
-      int left = need;
-      cluster.sync();
-      for (int pass = 0; pass < 12; ++pass) {
-        int* hist = ts.hist[pass & 1];
-        for (int i = tid; i < len; i += nt) {
-          const uint32_t key = keys[i];
-          if (key < lo || key > hi) continue;
-          const uint64_t kv = exact[i];
-          const uint32_t ki = ~(uint32_t)(first + i);
-          if (pass < 8) {
-            if (pass > 0 && (kv ^ top) >> (64 - 8 * pass)) continue;
-            atomicAdd(&hist[(kv >> (56 - 8 * pass)) & 255], 1);
-          } else {
-            if (kv != top || (pass > 8 && (ki ^ low) >> (32 - 8 * (pass - 8)))) continue;
-            atomicAdd(&hist[(ki >> (24 - 8 * (pass - 8))) & 255], 1);
-          }
-        }
-        cluster.sync();
-        for (int i = tid; i < 256; i += nt) {
-          int sum = 0;
-#pragma unroll
-          for (int r = 0; r < kTopkClusterCtas; ++r) sum += cluster.map_shared_rank(hist, r)[i];
-          ts.total[i] = sum;
-          ts.hist[(pass + 1) & 1][i] = 0;            // (last read by peers before this pass's barrier)
-        }
-        __syncthreads();
-        if (tid == 0) {
-          int sum = 0, d = 255;
-          while (d > 0 && sum + ts.total[d] < left) sum += ts.total[d--];
-          sh.digit = d;
-          sh.above = sum;
-        }
-        __syncthreads();
-        left -= sh.above;
-        if (pass < 8) top |= (unsigned long long)sh.digit << (56 - 8 * pass);
-        else low |= (uint32_t)sh.digit << (24 - 8 * (pass - 8));
-        __syncthreads();
-      }
-      if (tid == 0) {
-        sh.last = top;
-        sh.last_j = (int)~low;
-      }
+  if (lane == 0 && in > 0) atomicAdd(&sh.sure, in);
+  sync();
+  int sure = sh.sure, m = sh.near, before = 0;              // (before: taken by CTAs of lower rank)
+  uint2* const all = C > 1 ? sh.all : sh.mine;
+  if constexpr (C > 1) {
+    const int their_sure = lane < C ? *cluster.map_shared_rank(&sh.sure, lane) : 0;
+    const int theirs = lane < C ? *cluster.map_shared_rank(&sh.near, lane) : 0;
+    sure = __reduce_add_sync(0xffffffffu, their_sure);
+    before = __reduce_add_sync(0xffffffffu, lane < rank ? their_sure : 0);
+    m = __reduce_add_sync(0xffffffffu, theirs);
+    if (m <= kListed && warp < C) {
+      const int at = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0), count = __shfl_sync(0xffffffffu, theirs, warp);
+      const uint2* from = cluster.map_shared_rank(sh.mine, warp);
+      for (int i = lane; i < count; i += 32) all[at + i] = from[i];
     }
     __syncthreads();
   }
-  auto taken = [&](int i) {
-    const uint32_t key = keys[i];
-    if (!by_value || key < lo || key > hi) return key >= lo;
-    const uint64_t v = exact[i];
-    return v > sh.last || (v == sh.last && first + i <= sh.last_j);
+  const int need = k - sure;                                // of those m
+  const bool listed = m <= kListed;
+  auto drop = [&](int i) {
+    const int j = (int)all[i].y - first;
+    all[i].x = 0u;                                          // (no score's key)
+    if (j >= 0 && j < len) keys[j] = 0u;
   };
-  emit_taken(len, first, dst, sh.scan_tmp, taken, [&](uint32_t all) {
-    if (tid == 0) ts.cnt[0] = (int)all;
-    cluster.sync();
-    uint32_t o = 0;
+  if (m > need && listed) {
+    if (!wide) {
+      // by (score, index)
+      for (int i = tid; i < m; i += nt) {
+        const uint2 x = all[i];
+        const uint64_t v = (uint64_t)x.x << 32 | ~x.y;
+        int better = 0;
+        for (int o = 0; o < m; ++o) better += ((uint64_t)all[o].x << 32 | ~all[o].y) > v;
+        sh.inside[i] = better;
+      }
+      __syncthreads();
+      for (int i = tid; i < m; i += nt)
+        if (sh.inside[i] >= need) drop(i);
+      __syncthreads();
+    } else {
+      // the k-th by its fp32 score, then those within the band of it by their exact ones
+      for (int i = tid; i < kListed; i += nt) sh.key[i] = i < m ? all[i].x : 0u;
+      __syncthreads();
+      for (int i = tid; i < m; i += nt) {
+        const uint32_t key = sh.key[i];
+        int above = 0, equal = 0;
+#pragma unroll 4
+        for (int o = 0; o < m; o += 4) {
+          const uint4 y = *reinterpret_cast<const uint4*>(&sh.key[o]);
+          above += (y.x > key) + (y.y > key) + (y.z > key) + (y.w > key);
+          equal += (y.x == key) + (y.y == key) + (y.z == key) + (y.w == key);
+        }
+        if (above < need && need <= above + equal) sh.kth = key;
+      }
+      __syncthreads();
+      const float kth = value_of(sh.kth);
+      const Near close = near_values(kth, kth, band);
+      for (int i = tid; i < m; i += nt) {
+        const uint32_t key = all[i].x;
+        if (key > close.hi) atomicAdd(&sh.clear, 1);
+        else if (key >= close.lo) sh.inside[atomicAdd(&sh.n_inside, 1)] = i;
+        else drop(i);
+      }
+      __syncthreads();
+      const int open = sh.n_inside, wanted = need - sh.clear;
+      if (open > wanted) {
+        // (a cluster's CTAs share them out)
+        for (int i0 = (warp * C + rank) * 4; i0 < ((m + 3) & ~3); i0 += nw * C * 4) {
+          const int i = i0 + (lane >> 3);
+          const bool on = i < m && all[i].x >= close.lo && all[i].x <= close.hi;
+          if (!__any_sync(0xffffffffu, on)) continue;
+          const uint64_t v = score48<D>(a, query, b, g, on ? (int)all[i].y : 0, on, lane);
+          if (on && (lane & 7) < C) (C > 1 ? cluster.map_shared_rank(sh.exact, lane & 7) : sh.exact)[i] = v;
+        }
+        sync();
+        for (int t = tid; t < open; t += nt) {
+          const int i = sh.inside[t];
+          const uint64_t v = sh.exact[i];
+          const uint32_t j = all[i].y;
+          int better = 0;
+#pragma unroll 4
+          for (int o = 0; o < open; ++o) {
+            const int e = sh.inside[o];
+            const uint64_t y = sh.exact[e];
+            better += (y > v) | ((y == v) & (all[e].y < j));
+          }
+          if (better >= wanted) drop(i);                    // (no key is read here)
+        }
+        __syncthreads();
+      }
+    }
+  } else if (m > need) {
+    // too many to list: a radix selection over the 96 bits of (value, ~index)
+    uint64_t* exact = exact_rows + (size_t)row * a.n_vis + first;
+    for (int i0 = warp * 32; i0 < len; i0 += nt) {
+      const uint32_t key = i0 + lane < len ? keys[i0 + lane] : 0u;
+      uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < len && key >= lo && key <= hi);
+      while (todo) {
+        // four of them at a time
+        int j = -1;
 #pragma unroll
-    for (int r = 0; r < kTopkClusterCtas; ++r) o += r < rank ? (uint32_t)*cluster.map_shared_rank(&ts.cnt[0], r) : 0u;
-    return o;
-  });
-  cluster.sync();     // keep this CTA's shared memory alive until every peer has read it
+        for (int c = 0; c < 4; ++c) {
+          const int bit = __ffs(todo) - 1;
+          if (c == (lane >> 3) && bit >= 0) j = i0 + bit;
+          todo &= todo - 1;
+        }
+        const uint64_t v =
+            wide ? score48<D>(a, query, b, g, first + max(j, 0), j >= 0, lane) : (uint64_t)keys[max(j, 0)] << 32;
+        if (j >= 0 && (lane & 7) == 0) exact[j] = v;
+      }
+    }
+    // two histograms in turn (a cluster's CTAs read one pass's while the next fills the other)
+    int* sums = sh.hist + 512;
+    for (int i = tid; i < 256; i += nt) sh.hist[i] = 0;
+    unsigned long long top = 0;
+    uint32_t low = 0;
+    int left = need;
+    sync();
+    for (int pass = 0; pass < 12; ++pass) {
+      int* hist = sh.hist + (pass & 1) * 256;
+      for (int i = tid; i < len; i += nt) {
+        const uint32_t key = keys[i];
+        if (key < lo || key > hi) continue;
+        const uint64_t kv = exact[i];
+        const uint32_t ki = ~(uint32_t)(first + i);
+        if (pass < 8) {
+          if (pass > 0 && (kv ^ top) >> (64 - 8 * pass)) continue;
+          atomicAdd(&hist[(kv >> (56 - 8 * pass)) & 255], 1);
+        } else {
+          if (kv != top || (pass > 8 && (ki ^ low) >> (32 - 8 * (pass - 8)))) continue;
+          atomicAdd(&hist[(ki >> (24 - 8 * (pass - 8))) & 255], 1);
+        }
+      }
+      sync();
+      for (int i = tid; i < 256; i += nt) {
+        sums[i] = total(hist + i);
+        sh.hist[((pass + 1) & 1) * 256 + i] = 0;
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int sum = 0, d = 255;
+        while (d > 0 && sum + sums[d] < left) sum += sums[d--];
+        sh.bin = d;
+        sh.count = sum;
+      }
+      __syncthreads();
+      left -= sh.count;
+      if (pass < 8) top |= (unsigned long long)sh.bin << (56 - 8 * pass);
+      else low |= (uint32_t)sh.bin << (24 - 8 * (pass - 8));
+      __syncthreads();
+    }
+    for (int i = tid; i < len; i += nt) {
+      const uint32_t key = keys[i];
+      if (key < lo || key > hi) continue;
+      const uint64_t v = exact[i];
+      if (v < top || (v == top && first + i > (int)~low)) keys[i] = 0u;
+      else atomicAdd(&sh.kept, 1);
+    }
+    sync();
+    if constexpr (C > 1) before += __reduce_add_sync(0xffffffffu, lane < rank ? *cluster.map_shared_rank(&sh.kept, lane) : 0);
+  }
+  if constexpr (C > 1) {
+    if (listed) {
+      // (in order of their CTAs' ranks, so those before this one's have lower indices)
+      int kept = 0;
+      for (int i = lane; i < m; i += 32) kept += all[i].x != 0u && (int)all[i].y < first;
+      before += __reduce_add_sync(0xffffffffu, kept);
+    }
+  }
+
+  // ---- the indices of the keys that are left, ascending: stretches of 32 to a warp
+  const int per = ((len + 31) / 32 + nw - 1) / nw * 32, w0 = min(len, warp * per), w1 = min(len, w0 + per);
+  auto taken = [&](int i) { return i < w1 && keys[i] >= lo; };
+  uint32_t count = 0;
+#pragma unroll 4
+  for (int i0 = w0; i0 < w1; i0 += 32) count += __popc(__ballot_sync(0xffffffffu, taken(i0 + lane)));
+  if (lane == 0) sh.scan[warp] = count;
+  __syncthreads();
+  uint32_t o = (uint32_t)before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[lane] : 0u);
+#pragma unroll 4
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const bool take = taken(i0 + lane);
+    const uint32_t mask = __ballot_sync(0xffffffffu, take);
+    if (take) dst[o + __popc(mask & ((1u << lane) - 1u))] = first + i0 + lane;
+    o += __popc(mask);
+  }
+  if constexpr (C > 1) cluster.sync();     // (this CTA's shared memory has been read)
 }
 
 // Workspace: queries | 48-bit scores of tokens next to a crowded border | fp32
-// scores | the largest factor of each scoring CTA's pages | keys of rows that are
+// scores | what each scoring warp leaves | keys of rows that are
 // too long for shared memory
+static bool fits_cluster(int n) { return (n + kCluster - 1) / kCluster <= kSliceKeys; }
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t kv8_retrieve_workspace_bytes(int B, int Hkv, int D, int n_vis) {
   const size_t rows = (size_t)B * Hkv;
   return up256(rows * (D == 128 ? sizeof(Query8<128>) : sizeof(Query8<64>))) + up256(rows * n_vis * sizeof(uint64_t)) +
-         up256(rows * ((n_vis + 15) / 16 + kScoreWarps) * sizeof(float)) + up256(rows * n_vis * sizeof(float)) * (n_vis > kStagedKeys && !topk_cluster_fits(n_vis) ? 2 : 1);
+         up256(rows * ((n_vis + 15) / 16 + kScoreWarps) * sizeof(Part)) +
+         up256(rows * n_vis * sizeof(float)) * (n_vis > kStagedKeys && !fits_cluster(n_vis) ? 2 : 1);
 }
 
-template <int D, bool KNOWN>
-static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores,
-                                 const float* factors, int n_factors, uint64_t* exact,
-                                 uint32_t* far_keys, cudaStream_t stream) {
-  auto kernel = kv8_select_kernel<D, KNOWN>;
+template <int D, int C, bool FAR>
+static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores, const Part* parts,
+                                 int n_parts, uint64_t* exact, uint32_t* far_keys, cudaStream_t stream) {
+  auto kernel = kv8_select_kernel<D, C, FAR>;
+  const int slice = (a.n_vis + C - 1) / C;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedKeys * 4);
+    if (!FAR)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (C > 1 ? kSliceKeys : kStagedKeys) * 4);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int threads = KNOWN ? 1024 : a.n_vis >= 8192 ? 512 : 256;
-  return launch_dependent(kernel, dim3((unsigned)(a.batch * a.Hkv)), dim3(threads),
-                          KNOWN ? (size_t)0 : (size_t)a.n_vis * 4, stream, a, rows, scores, factors, n_factors, exact, far_keys);
-}
-
-template <int D>
-static cudaError_t launch_select_cluster(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores,
-                                         const float* factors, int n_factors, uint64_t* exact, cudaStream_t stream) {
-  auto kernel = kv8_select_cluster_kernel<D>;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
-  }
-  const int slice = (a.n_vis + kTopkClusterCtas - 1) / kTopkClusterCtas;
-  return launch_dependent(kernel, dim3((unsigned)(kTopkClusterCtas * a.batch * a.Hkv)), dim3(kTopkClusterThreads),
-                          (size_t)slice * sizeof(uint32_t), stream, a, rows, scores, factors, n_factors, exact);
+  const int threads = C > 1 || a.n_vis >= 8192 ? kClusterThreads : 256;
+  const size_t smem = FAR ? 0 : (size_t)slice * 4;
+  const dim3 grid((unsigned)(C * a.batch * a.Hkv));
+  return launch_dependent(kernel, grid, dim3(threads), smem, stream, a, rows, scores, parts, n_parts, exact, far_keys);
 }
 
 template <int D>
@@ -748,7 +766,7 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
   Query8<D>* query = reinterpret_cast<Query8<D>*>(take((size_t)rows * sizeof(Query8<D>)));
   uint64_t* exact = reinterpret_cast<uint64_t*>(take((size_t)rows * a.n_vis * sizeof(uint64_t)));
   float* scores = reinterpret_cast<float*>(take((size_t)rows * a.n_vis * sizeof(float)));
-  float* factors = reinterpret_cast<float*>(take((size_t)rows * ((a.n_vis + 15) / 16 + kScoreWarps) * sizeof(float)));
+  Part* parts = reinterpret_cast<Part*>(take((size_t)rows * ((a.n_vis + 15) / 16 + kScoreWarps) * sizeof(Part)));
   uint32_t* far_keys = reinterpret_cast<uint32_t*>(at);      // (there where it is used)
   if (a.scores != nullptr) scores = a.scores;
   // pages per CTA: a multiple of its warps, for two rounds of resident CTAs (of 4, 5,
@@ -769,15 +787,13 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
                          a.Hkv, query);
   if (e != cudaSuccess) return e;
   e = launch_dependent(sum ? kv8_score_kernel<D, true> : kv8_score_kernel<D, false>, dim3((unsigned)per_row, a.Hkv, a.batch),
-                       dim3(kScoreWarps * 32), 0, stream, a, query, scores, factors, (int)per);
+                       dim3(kScoreWarps * 32), 0, stream, a, query, scores, parts, (int)per);
   if (e != cudaSuccess) return e;
-  // a CTA per row as long as rows are short, else a cluster (as topk_prefers_cluster),
-  // and for rows that do not fit one either a CTA over their keys in memory
-  if (a.n_vis <= kStagedKeys) return launch_select<D, false>(a, query, scores, factors, (int)per_row * kScoreWarps, exact, nullptr, stream);
-  if (topk_cluster_fits(a.n_vis)) return launch_select_cluster<D>(a, query, scores, factors, (int)per_row * kScoreWarps, exact, stream);
-  e = launch_topk_rows(scores, rows, a.n_vis, a.k, a.vis_idx, stream, a.lens, a.Hkv);
-  if (e != cudaSuccess) return e;
-  return launch_select<D, true>(a, query, scores, factors, (int)per_row * kScoreWarps, exact, far_keys, stream);
+  // a CTA per row as long as rows are short, else a cluster
+  const int n_parts = (int)per_row * kScoreWarps;
+  if (a.n_vis <= kStagedKeys) return launch_select<D, 1, false>(a, query, scores, parts, n_parts, exact, far_keys, stream);
+  if (fits_cluster(a.n_vis)) return launch_select<D, kCluster, false>(a, query, scores, parts, n_parts, exact, far_keys, stream);
+  return launch_select<D, kCluster, true>(a, query, scores, parts, n_parts, exact, far_keys, stream);
 }
 
 cudaError_t launch_kv8_retrieve(const Kv8RetrieveArgs& a, int D, int num_sms, cudaStream_t stream) {

@@ -75,23 +75,11 @@ __device__ __forceinline__ void fill_unselected(int32_t* dst, int from, int k) {
   for (int i = from + (int)threadIdx.x; i < k; i += (int)blockDim.x) dst[i] = -1;
 }
 
-// The known high bits of a row's k-th largest key, and how many keys that equal
-// it on those bits are still to be taken (the lowest indices); open: there are more
-// of them, and the bits below would tell which.
-struct TopkBorder {
-  uint32_t prefix, pmask;
-  int remaining;
-  bool open;
-};
-
-// Stages the row's keys and finds its border.  All threads of the block call
-// this.  keys: shared memory for n keys, or nullptr to re-read `src` (through L2)
-// on every pass.  `src` may have been written by other CTAs of the running grid:
-// it is read with ld.global.cg.
-// The search may end as soon as `few` keys or fewer have the border's bits (0: not
-// before it is exact, or those keys are all taken).
-__device__ __forceinline__ TopkBorder block_topk_border(const float* src, int n, int k, uint32_t* keys,
-                                                        TopkShared& ts, int few = 0) {
+// All threads of the block call this.  keys: shared memory for n keys, or
+// nullptr to re-read `src` (through L2) on every pass.  `src` may have been
+// written by other CTAs of the running grid: it is read with ld.global.cg.
+__device__ __forceinline__ void block_topk_row(const float* src, int n, int k, int32_t* dst,
+                                               uint32_t* keys, TopkShared& ts) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   // stage the keys (four independent loads in flight per thread) and find
   // the smallest and largest key
@@ -159,7 +147,6 @@ __device__ __forceinline__ TopkBorder block_topk_border(const float* src, int n,
   // keys equal to it on those bits are still to be taken
   uint32_t prefix, pmask;
   int remaining = k;
-  bool open = false;
   const uint32_t diff = kmin ^ kmax;
   if (diff == 0) {
     prefix = kmin;
@@ -213,26 +200,13 @@ __device__ __forceinline__ TopkBorder block_topk_border(const float* src, int n,
       remaining -= ts.sel_above;
       const int cnt = ts.sel_count;
       __syncthreads();                       // every thread has read the selection
-      open = cnt != remaining && lo > 0;
-      if (!open || cnt <= few) break;  // the bin is taken whole, or the key is exact
+      if (cnt == remaining || lo == 0) break;  // the bin is taken whole, or the key is exact
       for (int i = tid; i < 256; i += nt) ts.hist[i] = 0;
       __syncthreads();
       hi = lo;
     }
   }
 
-  return TopkBorder{prefix, pmask, remaining, open};
-}
-
-// The k largest scores of a row; all threads of the block call this (arguments
-// as above).
-__device__ __forceinline__ void block_topk_row(const float* src, int n, int k, int32_t* dst,
-                                               uint32_t* keys, TopkShared& ts) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const TopkBorder border = block_topk_border(src, n, k, keys, ts);
-  const uint32_t prefix = border.prefix, pmask = border.pmask;
-  const int remaining = border.remaining;
-  auto key_at = [&](int i) -> uint32_t { return keys ? keys[i] : order_key(__ldcg(src + i)); };
   // keys above the prefix are taken; of those equal to it, the `remaining`
   // lowest indices
   const int seg = (n + nt - 1) / nt;
