@@ -168,6 +168,38 @@ def test_many_short_sequences(lib):
     assert sv.sv_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("d,interleaved,norm", [(128, False, True), (64, True, True), (128, True, False), (64, False, False)])
+def test_keys_are_rounded_from_more_than_fp32(lib, d, interleaved, norm):
+    """Keys whose turned pairs cancel among ten million elements: bf16 results on the
+    right side of every border, where fp32 alone would fall on the other now and then."""
+    from visual_token_sparsity_gb300 import binding as sv
+    N, H, Hkv, n_pos = 80000 * 64 // d, 2, 2, 500
+    g = torch.Generator().manual_seed(4)
+    angle = torch.rand(n_pos, d // 2, generator=g, dtype=torch.float64) * 2 * math.pi
+    turns = torch.stack([angle.cos(), angle.sin()], -1).float().to(DEV)
+    pos = torch.randint(n_pos, (1, N), generator=g, dtype=torch.int32).to(DEV)
+    w = (1 + 0.1 * synth.normal_bf16((d,), 12).float()).bfloat16().to(DEV) if norm else None
+    x = synth.normal_bf16((N, H + 2 * Hkv, d), 13).to(DEV)
+    k = x[:, H: H + Hkv]
+    bt = torch.arange((N + 15) // 16, dtype=torch.int32)[None].to(DEV)
+    pools = [torch.zeros(bt.numel(), Hkv, 16, d, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    layer = sv.Kv8Layer(*pools, torch.zeros(bt.numel(), Hkv, 2, device=DEV))
+    q = torch.empty(N, H, d, dtype=torch.bfloat16, device=DEV)
+    ko = torch.empty(N, Hkv, d, dtype=torch.bfloat16, device=DEV)
+    ws = sv.workspace(sv.sv_evict_workspace_bytes())
+    sv.sv_kv8_append(x[:, :H], k, x[:, H + Hkv:], sv.Rotation(turns, pos, interleaved=interleaved, q_weight=w, k_weight=w),
+                     layer, sv.SeqBatch(bt, 0, 0), q, ws, k_out=ko)
+    assert sv.sv_read_device_status(ws) == 0
+    y = k.double()
+    if norm:
+        y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + 1e-6) * w.double()
+    c, s = turns.double()[pos[0].long()][:, None].unbind(-1)
+    a, b = (y[..., 0::2], y[..., 1::2]) if interleaved else (y[..., : d // 2], y[..., d // 2:])
+    re, im = a * c - b * s, a * s + b * c
+    want = (torch.stack([re, im], -1).flatten(-2) if interleaved else torch.cat([re, im], -1)).bfloat16()
+    assert int((want.view(torch.int16) != ko.view(torch.int16)).sum()) == 0
+
+
 RUN = textwrap.dedent("""
     import sys, torch
     sys.path.insert(0, {root!r})

@@ -23,8 +23,9 @@ namespace {
 
 constexpr int kWarps = 4;
 // Groups of query rows at a time, and CTAs per SM that the registers leave: of 1 to 3
-// groups and 6 to 8 CTAs within 2 % of one another (a prompt of 13441 tokens of 36
-// heads 67 to 69 us; one group 74), eight the fastest for single tokens.
+// groups and 6 to 8 CTAs within 2 % of one another (a prompt of 27136 tokens of 36
+// heads, before keys were checked, 67 to 69 us; one group 74), eight the fastest for
+// single tokens.
 constexpr int kAhead = 2, kCtas = 8;
 constexpr int kWarpsPerSm = 64;   // warps that the queries spread over before a warp takes more rows
 
@@ -123,8 +124,14 @@ struct Place {
 
 // One group of rows side by side: normalised, rotated and rounded to bf16, with
 // twice the bits where fp32's last ones could decide the rounding.  The whole
-// warp takes part.
-template <int L, bool INTER, bool NORM, bool PARTLY>
+// warp takes part.  KEYS: wherever they could, as a key's 8 bits follow from its
+// bf16 ones and one bit less there may be half a step of e4m3.  Counted in 2^-24 of
+// t = |x cos| + |y sin|, however small their difference: the sum of squares is off by
+// 9 of itself at most, its root by half of that and 1.5, the element by one more
+// (weight times bf16 is exact), the product and the sum by one each, the edges of the
+// interval by one: 11, and 3 without a norm.  (Queries, which stay bf16, are looked at
+// in terms of the result: where a pair cancels, one may be off by its last bit.)
+template <int L, bool INTER, bool NORM, bool PARTLY, bool KEYS>
 __device__ __forceinline__ Lane8<INTER> turn_rows(const Lane8<INTER>& x, const uint64_t* gp, const uint64_t* gy,
                                                   const uint16_t* weight, const Turns& t, const Place<L, INTER>& at,
                                                   float eps) {
@@ -149,6 +156,17 @@ __device__ __forceinline__ Lane8<INTER> turn_rows(const Lane8<INTER>& x, const u
       y[e] = fm::mul2(fm::mul2(y[e], gy[e]), inv);
     }
   }
+  bool doubt = false;
+  uint64_t tp[2], ty[2];           // t of both members
+  if constexpr (KEYS) {
+    constexpr uint64_t kAbs = 0x7fffffff7fffffffull;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint64_t ap = p[e] & kAbs, ay = y[e] & kAbs, ac = t.cs[e] & kAbs, as = t.sn[e] & kAbs;
+      tp[e] = fm::fma2(ap, ac, fm::mul2(ay, as));
+      ty[e] = fm::fma2(ap, as, fm::mul2(ay, ac));
+    }
+  }
   if (!PARTLY || at.turned) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -160,17 +178,28 @@ __device__ __forceinline__ Lane8<INTER> turn_rows(const Lane8<INTER>& x, const u
   }
   const bool changed = !PARTLY || at.turned || normed;
   Lane8<INTER> out = x;
-  uint32_t near = 0xffffffffu;
   if (changed) {
     out.pack(p, y);
-    constexpr uint32_t kOff = (0x8000u + kDoubt) * 0x10001u;
+    if constexpr (KEYS) {
+      const float off = (normed ? 11.f : 3.f) / 16777216.f;
+      const uint64_t up = fm::splat2(off), down = fm::splat2(-off);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      near = __viaddmin_u16x2(__byte_perm((uint32_t)p[e], (uint32_t)(p[e] >> 32), 0x5410), kOff, near);
-      near = __viaddmin_u16x2(__byte_perm((uint32_t)y[e], (uint32_t)(y[e] >> 32), 0x5410), kOff, near);
+      for (int e = 0; e < 2; ++e) {
+        doubt = doubt || bf16x2(fm::fma2(tp[e], up, p[e])) != bf16x2(fm::fma2(tp[e], down, p[e]));
+        doubt = doubt || bf16x2(fm::fma2(ty[e], up, y[e])) != bf16x2(fm::fma2(ty[e], down, y[e]));
+      }
+    } else {
+      constexpr uint32_t kOff = (0x8000u + kDoubt) * 0x10001u;
+      uint32_t near = 0xffffffffu;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        near = __viaddmin_u16x2(__byte_perm((uint32_t)p[e], (uint32_t)(p[e] >> 32), 0x5410), kOff, near);
+        near = __viaddmin_u16x2(__byte_perm((uint32_t)y[e], (uint32_t)(y[e] >> 32), 0x5410), kOff, near);
+      }
+      doubt = min(near & 0xffffu, near >> 16) <= 2 * kDoubt;
     }
   }
-  if (__any_sync(0xffffffffu, min(near & 0xffffu, near >> 16) <= 2 * kDoubt)) {
+  if (__any_sync(0xffffffffu, doubt)) {
     const uint4 u = exact_row<L, INTER>(x.u, out.u, normed ? weight : nullptr, at.off0, at.off1, eps, t.cs[0], t.cs[1],
                                         t.sn[0], t.sn[1]);
     if (changed) out.u = u;
@@ -260,8 +289,9 @@ __device__ __forceinline__ uint32_t warp_top(uint32_t top) {
 
 }  // namespace
 
-// Warps [0, q_warps): query rows, `per_warp` of one token each; behind them a
-// warp for the keys and one for the values of every (page, KV head).
+// Warps [0, kv_warps): one for the keys and one for the values of every (page, KV
+// head); behind them query rows, `per_warp` of one token each (a page's keys are the
+// longest work, which must not be the last).
 template <int L, bool INTER, bool NORM, bool PARTLY>
 __global__ void __launch_bounds__(kWarps * 32, kCtas)
 kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_t warps_per_token, uint32_t q_warps,
@@ -286,9 +316,11 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
   Turns t;
   t.none();
 
-  if (w < q_warps) {
-    const int tok = (int)(w / warps_per_token);
-    const int r0 = (int)(w - (uint32_t)tok * warps_per_token) * per_warp, r1 = min(r0 + per_warp, a.H);
+  if (w >= kv_warps) {
+    const uint32_t item = w - kv_warps;
+    if (item >= q_warps) return;
+    const int tok = (int)(item / warps_per_token);
+    const int r0 = (int)(item - (uint32_t)tok * warps_per_token) * per_warp, r1 = min(r0 + per_warp, a.H);
     if (a.seq_start != nullptr && (tok < __ldg(a.seq_start) || tok >= __ldg(a.seq_start + a.batch))) return;
     const uint16_t* src = a.q + (size_t)tok * a.q_stride;
     uint16_t* dst = a.q_out + (size_t)tok * a.H * D;
@@ -325,18 +357,16 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int row = r + i * RPG + at.sub;
-        x[i] = turn_rows<L, INTER, NORM, PARTLY>(x[i], gp, gy, NORM ? a.q_weight : nullptr, t, at, a.eps);
+        x[i] = turn_rows<L, INTER, NORM, PARTLY, false>(x[i], gp, gy, NORM ? a.q_weight : nullptr, t, at, a.eps);
         if (row < r1) x[i].store(dst + (size_t)row * D, at.off0, at.off1);
         x[i] = next[i];
       }
     }
     return;
   }
-  if (w - q_warps >= kv_warps) return;
-  const uint32_t item = w - q_warps;
-  const int which = (int)(item & 1u), g = (int)((item >> 1) % (uint32_t)a.Hkv);
+  const int which = (int)(w & 1u), g = (int)((w >> 1) % (uint32_t)a.Hkv);
   Unit x;
-  if (!unit_of(a, (item >> 1) / (uint32_t)a.Hkv, lane, lane == 0 && g == 0 && which == 0, x)) return;
+  if (!unit_of(a, (w >> 1) / (uint32_t)a.Hkv, lane, lane == 0 && g == 0 && which == 0, x)) return;
   uint16_t* sm = rows[warp];
   uint32_t top = 0;
   // the tokens' positions, a lane each; which of them are written
@@ -374,7 +404,7 @@ kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a, int per_warp, uint32_
       load(i0 + RPG, next, next_f);
       t.none();
       if (ok && at.turned) t.set(f);
-      v = turn_rows<L, INTER, NORM, PARTLY>(v, gp, gy, NORM ? a.k_weight : nullptr, t, at, a.eps);
+      v = turn_rows<L, INTER, NORM, PARTLY, true>(v, gp, gy, NORM ? a.k_weight : nullptr, t, at, a.eps);
       if (ok) {
         v.store(sm + i * D, at.off0, at.off1);
         if (a.k_out != nullptr) v.store(a.k_out + ((size_t)(x.t0 + i) * a.Hkv + g) * D, at.off0, at.off1);
