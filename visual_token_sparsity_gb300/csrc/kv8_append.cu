@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kWarps = 4;
 // Groups of query rows at a time, and CTAs per SM that the registers leave: of 1 to 3
-// groups and 6 to 8 CTAs within 2 % of one another (a prompt of 27136 tokens of 36
+// groups and 6 to 8 CTAs within 2 % of one another (a prompt of some 15,000 tokens of 36
 // heads, before keys were checked, 67 to 69 us; one group 74), eight the fastest for
 // single tokens.
 constexpr int kAhead = 2, kCtas = 8;
