@@ -738,8 +738,7 @@ sv_status sv_kv8_append(const void* q, int64_t q_stride, const void* k, int64_t 
  * The selection is that of the exact scores: tokens whose fp32 scores are too
  * near to the k-th one to tell are scored again with 48 bits.  Ties go to the lower
  * index.  scores (optional out) are the fp32 ones.  With scores that are not
- * finite the choice is unspecified (but valid).  At most 65535 sequences, and
- * 2^24 of them times KV heads.
+ * finite the choice is unspecified (but valid).  B * n_kv_heads: at most 2^24.
  * ws : sv_kv8_retrieve_workspace_bytes(B, H, n_kv_heads, head_dim, n_vis, k);
  *      sized for the largest B and n_vis it serves every smaller call.
  */

@@ -86,7 +86,7 @@ def test_retrieve_arguments(lib):
     assert call(q=P(0x10008)) == call(S=seqs(n_vis=0, n_text=10)) == call(L=layer8(scales=0)) == INVALID
     assert call(L=layer8(d=96)) == UNSUPPORTED
     assert call(nb=300) == WORKSPACE
-    assert call(S=seqs(batch=65535)) == WORKSPACE and call(S=seqs(batch=65536)) == UNSUPPORTED
+    assert call(S=seqs(batch=2 ** 23)) == WORKSPACE and call(S=seqs(batch=2 ** 23 + 1)) == UNSUPPORTED
     assert call(S=seqs(batch=0)) == 0
 
 

@@ -936,8 +936,9 @@ sv_status sv_kv8_retrieve_topk(const void* q, int R, int H, const sv_kv8_layer* 
   const sv_kv_layer as = {layer->k_pool, nullptr, layer->num_blocks, layer->n_kv_heads, layer->head_dim};
   s = sv::check_retrieve_args(q, R, H, &as, seqs, k, vis_idx);
   if (s != SV_OK) return s;
-  if (seqs->batch > 65535 || (long long)seqs->batch * layer->n_kv_heads > (1 << 24))
-    return fail(SV_ERR_UNSUPPORTED, "more than 65535 sequences, or 2^24 rows");
+  if ((long long)seqs->batch * layer->n_kv_heads > (1 << 24) ||
+      (long long)seqs->batch * layer->n_kv_heads * (seqs->n_vis / 16 + 1) > 0x7fffffffLL)
+    return fail(SV_ERR_UNSUPPORTED, "batch * n_kv_heads beyond 2^24, or 2^31 pages");
   s = check_ws(ws, ws_bytes, sv_kv8_retrieve_workspace_bytes(seqs->batch, H, layer->n_kv_heads, layer->head_dim,
                                                              seqs->n_vis, k));
   if (s != SV_OK) return s;

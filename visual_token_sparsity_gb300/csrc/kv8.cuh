@@ -47,5 +47,15 @@ __device__ __forceinline__ uint32_t max_finite2(uint32_t top, uint32_t v) {
   return __vmaxu2(top, v);
 }
 
+// A line of `total` things cut into C pieces of one size, give or take one: the first
+// thing of piece c, floor(total * c / C), in 32 bits, and the piece that thing s lies in.
+__host__ __device__ __forceinline__ uint32_t piece_begin(uint32_t total, uint32_t c, uint32_t C) {
+  const uint32_t q = total / C;
+  return q * c + (total - q * C) * c / C;
+}
+__device__ __forceinline__ int piece_of(uint32_t total, uint32_t s, uint32_t C) {
+  return (int)(((unsigned long long)(s + 1) * C - 1) / total);
+}
+
 }  // namespace kv8
 }  // namespace sv

@@ -101,16 +101,6 @@ __device__ __forceinline__ uint32_t exponent_of(float x, float y) {
   return min(max(__float_as_uint(fmaxf(fabsf(x), fabsf(y))) & 0x7f800000u, 0x00800000u), 253u << 23);
 }
 
-// First block of piece c of C: floor(total * c / C), in 32 bits.
-__host__ __device__ __forceinline__ uint32_t piece_begin(uint32_t total, uint32_t c, uint32_t C) {
-  const uint32_t q = total / C;
-  return q * c + (total - q * C) * c / C;
-}
-// The piece that block s lies in.
-__device__ __forceinline__ int piece_of(uint32_t total, uint32_t s, uint32_t C) {
-  return (int)(((unsigned long long)(s + 1) * C - 1) / total);
-}
-
 struct Seq {
   int nv, nt, kb;       // visual, text, attended visual tokens
   __device__ int blocks() const { return (kb + nt + kBlock - 1) / kBlock; }
@@ -151,8 +141,8 @@ struct Piece {
     C = min((uint32_t)pieces, total);
     left = 0;
     if (piece >= (int)C) return;
-    from = piece_begin(total, piece, C);
-    left = (int)(piece_begin(total, piece + 1, C) - from);
+    from = kv8::piece_begin(total, piece, C);
+    left = (int)(kv8::piece_begin(total, piece + 1, C) - from);
   }
 };
 __device__ __forceinline__ Piece equal_piece(const Kv8AttnArgs& a, int piece) {
@@ -577,7 +567,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 
   // ---- the last CTA of a unit joins its pieces
   const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
-  const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
+  const int p0 = kv8::piece_of(total, start, C), n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
   int* done = a.split_done + b * a.Hkv + g;
   __shared__ int last;
   if (threadIdx.x == 0) {
@@ -629,7 +619,7 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
     }
   }
   const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
-  const int p0 = piece_of(total, start, C), n = piece_of(total, start + per_unit - 1, C) - p0 + 1;
+  const int p0 = kv8::piece_of(total, start, C), n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
   if (n == 1) return;
   const int w = threadIdx.x / kPer, i = threadIdx.x - w * kPer;
   float M, L;

@@ -18,12 +18,17 @@
 // 48 bits and the best of them taken, ties to the lower index.
 //
 // Measured, keys out of L2, head dim 128: 16 sequences of 32 KV heads and 2880 keys
-// 47.3 us (4.2 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 53.8 us
-// (2.9 TB/s).  Scoring takes 37 and 36 us of it by itself, bound by the latency of one
-// page in flight in each of 40 warps an SM (two pages in 20 warps: 53 and more); the
-// selection 10 and 18, a chain of some ten waits (scores, counts, pages of the tokens
-// next to the border, and a cluster's barriers) that little work lies between.  With a
-// search by the bits of the keys they were 48.3 and 56.2.
+// 46.6 us (4.3 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 52.9 us
+// (3.0 TB/s).  Scoring takes 37 and 36 us of it by itself: a page in flight in each of
+// 40 warps an SM, 59 % of issue slots, and 17 % of an SM's time before its first page and
+// behind its last (two pages in 24 warps 48.3 / 54.5, in 32 warps with spills 62.7 /
+// 61.5; packed adds the same; two and four times the CTAs 48.8 / 56.8 and 52.6 / 65.6;
+// a grid of equal shares of a row instead of one line 47.3 / 53.8).  The selection
+// takes 10 and 17, a chain of some ten waits (scores, counts, pages of the tokens next
+// to the border, and a cluster's barriers) that little work lies between; with a search
+// by the bits of the keys the two calls were 1 and 2.4 us longer.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -37,7 +42,7 @@ namespace sv {
 
 namespace {
 
-constexpr int kScoreWarps = 8;
+constexpr int kScoreWarps = 8, kScoreCtas = 5;   // per CTA, and CTAs per SM
 // |fp32 score - score| <= e = 2^-24 (272 |qbar|_max + 12 |qbar|_1) 448 s, as 448 s
 // bounds a key's elements: a tile's 16 products lose at most the last of 24 bits
 // beside the largest, and their sum, at most 16 of the largest, as much again (eight
@@ -166,25 +171,105 @@ struct __align__(16) Part {
   uint32_t lo, hi, pad;
 };
 
+// The pages of all (sequence, KV head) rows form one line, cut evenly between the
+// CTAs.  A CTA leaves a part per warp for each of its rows: one that it has all of, one
+// that it goes on with (slot 0) and one that it begins and others go on with (slot 1).
+struct Parts {
+  Part* whole;             // [rows][kScoreWarps]
+  Part* cut;               // [CTAs][2][kScoreWarps]
+  int ctas;
+  int pages;               // of a row, with equal counts
+};
+
+__device__ __forceinline__ uint32_t pages_of(const Kv8RetrieveArgs& a, int b) {
+  int nv = 0, nt, kb;
+  if (b < a.batch) seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, nv, nt, kb);
+  return (uint32_t)(nv + 15) >> 4;
+}
+// Pages of all heads of sequences [b0, b0 + 32) up to this lane's (and its own), by a
+// whole warp.
+__device__ __forceinline__ uint32_t scan_pages(const Kv8RetrieveArgs& a, int b0, int lane, uint32_t& mine) {
+  mine = pages_of(a, b0 + lane) * (uint32_t)a.Hkv;
+  uint32_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  return inc;
+}
+// The line's length and, where b < batch, what lies before sequence b.
+__device__ __forceinline__ uint32_t line_of(const Kv8RetrieveArgs& a, const Parts& parts, int b, int lane, uint32_t& before) {
+  if (!a.lens.any()) {
+    before = (uint32_t)b * (uint32_t)a.Hkv * (uint32_t)parts.pages;
+    return (uint32_t)a.batch * (uint32_t)a.Hkv * (uint32_t)parts.pages;
+  }
+  uint32_t total = 0, mine;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const uint32_t inc = scan_pages(a, b0, lane, mine);
+    if (b >= b0 && b < b0 + 32) before = total + __shfl_sync(0xffffffffu, inc - mine, b - b0);
+    total += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return total;
+}
+
 // A warp per page, one page in flight, as many warps as 48 registers allow.  SUM:
 // the query's rows are few, and every CTA adds them up itself (the first of a row
 // leaves the sum for the selection).
 template <int D, bool SUM>
-__global__ void __launch_bounds__(kScoreWarps * 32, 5)
-kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, float* __restrict__ scores,
-                 Part* __restrict__ parts, int pages_per_cta) {
+__global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas)
+kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, float* __restrict__ scores, const Parts parts) {
   constexpr int KS = D / 16, KC = D / 64, W = kScoreWarps;
   __shared__ __align__(16) Query8<D> query;
-  grid_dep_sync();
-  const int g = blockIdx.y, b = blockIdx.z, row = b * a.Hkv + g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q4 = lane & 3;
-  int nv, nt, kb;
-  if (!seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, nv, nt, kb) && threadIdx.x == 0 && blockIdx.x == 0)
-    flag_status(a.status, kStatusBadLength);
-  const int end = min((nv + 15) / 16, ((int)blockIdx.x + 1) * pages_per_cta);
-  const int first = blockIdx.x * pages_per_cta + warp;
-  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+  grid_dep_sync();
+  uint32_t off = 0;                        // of this CTA's first page in sequence b
+  int left, b = 0;
+  {
+    uint32_t before = 0;
+    const uint32_t total = line_of(a, parts, 0, lane, before), C = min((uint32_t)parts.ctas, total);
+    if (blockIdx.x >= C) left = 0;
+    else {
+      off = kv8::piece_begin(total, blockIdx.x, C);
+      left = (int)(kv8::piece_begin(total, blockIdx.x + 1, C) - off);
+    }
+  }
+  if (!a.lens.any()) {
+    const uint32_t in_seq = (uint32_t)a.Hkv * (uint32_t)parts.pages;
+    if (left > 0) {
+      b = (int)(off / in_seq);
+      off -= (uint32_t)b * in_seq;
+    }
+  } else {
+    for (int i = blockIdx.x * W * 32 + threadIdx.x; i < a.batch; i += gridDim.x * W * 32) {
+      int nv, nt, kb;
+      if (!seq_lengths(a.lens, i, a.n_vis, a.n_text, a.k, nv, nt, kb)) flag_status(a.status, kStatusBadLength);
+    }
+    for (; left > 0 && b < a.batch; b += 32) {
+      uint32_t mine;
+      const uint32_t inc = scan_pages(a, b, lane, mine), past = __ballot_sync(0xffffffffu, inc > off);
+      if (past) {
+        const int f = __ffs(past) - 1;
+        off -= __shfl_sync(0xffffffffu, inc - mine, f);
+        b += f;
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
 
+#pragma unroll 1
+  for (; left > 0; ++b, off = 0) {
+  int nv, nt, kb;
+  seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, nv, nt, kb);
+  const int pages = (nv + 15) >> 4;
+#pragma unroll 1
+  while (left > 0 && off < (uint32_t)pages * (uint32_t)a.Hkv) {
+  const int g = (int)(off / (uint32_t)pages), row = b * a.Hkv + g, p0 = (int)off - g * pages, end = min(pages, p0 + left);
+  off += end - p0;
+  left -= end - p0;
+  const int first = p0 + warp;
+  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
   uint4 k[2][KC];            // keys r and r + 8
   float factor = 0.f;
   bool ok = false;
@@ -207,10 +292,11 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
   int next = id_of(first);
   load(first, next);
   next = id_of(first + W);
+  __syncthreads();                         // (the query of the row before has been read)
   if constexpr (SUM) {
     sum_query<D>(static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, row, &query);
     __syncthreads();
-    if (blockIdx.x == 0)
+    if (p0 == 0)
       for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
         reinterpret_cast<uint4*>(rows + row)[i] = reinterpret_cast<const uint4*>(&query)[i];
   } else {
@@ -221,7 +307,7 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
   // (the query's parts: column r of a tile is part r, the columns behind are 0)
   const uint16_t* part = &query.part[min(r, 3)][q4 * 16];
   float* out = scores + (size_t)row * a.n_vis;
-  Part left = {0.f, 0xffffffffu, 0u, 0u};
+  Part mine = {0.f, 0xffffffffu, 0u, 0u};
   for (int p = first; p < end; p += W) {
     float c[4] = {};
 #pragma unroll
@@ -253,19 +339,22 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
       auto put = [&](int at, float v) {
         if (at >= nv) return;
         out[at] = v;
-        left.lo = min(left.lo, order_key(v));
-        left.hi = max(left.hi, order_key(v));
+        mine.lo = min(mine.lo, order_key(v));
+        mine.hi = max(mine.hi, order_key(v));
       };
       put(pos, value(s0));
       put(pos + 8, value(s1));
     }
-    if (there) left.factor = fmaxf(left.factor, fabsf(f));
+    if (there) mine.factor = fmaxf(mine.factor, fabsf(f));
   }
-  left.lo = __reduce_min_sync(0xffffffffu, left.lo);
-  left.hi = __reduce_max_sync(0xffffffffu, left.hi);
+  mine.lo = __reduce_min_sync(0xffffffffu, mine.lo);
+  mine.hi = __reduce_max_sync(0xffffffffu, mine.hi);
+  Part* to = p0 == 0 && end == pages ? parts.whole + (size_t)row * W
+                                     : parts.cut + ((size_t)blockIdx.x * 2 + (p0 == 0)) * W;
   if (lane == 0)
-    *reinterpret_cast<uint4*>(parts + ((size_t)row * gridDim.x + blockIdx.x) * W + warp) =
-        make_uint4(__float_as_uint(left.factor), left.lo, left.hi, 0u);
+    *reinterpret_cast<uint4*>(to + warp) = make_uint4(__float_as_uint(mine.factor), mine.lo, mine.hi, 0u);
+  }
+  }
 }
 
 namespace {
@@ -290,10 +379,18 @@ struct __align__(16) SelectShared {
 };
 
 // The parts of a row together; all threads of the block call this.
-__device__ __forceinline__ Part whole_row(const Part* parts, int n, SelectShared& sh) {
+__device__ __forceinline__ Part whole_row(const Kv8RetrieveArgs& a, const Parts& parts, int row, int n, SelectShared& sh) {
+  const int b = row / a.Hkv, lane = threadIdx.x & 31, pages = (n + 15) >> 4;
+  uint32_t before = 0;
+  const uint32_t total = line_of(a, parts, b, lane, before), C = min((uint32_t)parts.ctas, total);
+  const uint32_t start = before + (uint32_t)(row - b * a.Hkv) * (uint32_t)pages;
+  const int c0 = kv8::piece_of(total, start, C), c1 = kv8::piece_of(total, start + pages - 1, C);
   Part x = {0.f, 0xffffffffu, 0u, 0u};
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const uint4 y = __ldcg(reinterpret_cast<const uint4*>(parts) + i);
+  for (int i = threadIdx.x; i < (c1 - c0 + 1) * kScoreWarps; i += blockDim.x) {
+    const int c = c0 + i / kScoreWarps;
+    const Part* at = c0 == c1 ? parts.whole + (size_t)row * kScoreWarps
+                              : parts.cut + ((size_t)c * 2 + (c == c0)) * kScoreWarps;
+    const uint4 y = __ldcg(reinterpret_cast<const uint4*>(at + i % kScoreWarps));
     x.factor = fmaxf(x.factor, __uint_as_float(y.x));
     x.lo = min(x.lo, y.y);
     x.hi = max(x.hi, y.z);
@@ -460,7 +557,7 @@ __device__ __forceinline__ Near near_border(const uint32_t* keys, int n, int k, 
 template <int D, int C, bool FAR>
 __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kClusterThreads, 2)
 kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows, const float* __restrict__ scores,
-                  const Part* __restrict__ parts, int n_parts, uint64_t* __restrict__ exact_rows,
+                  const Parts parts, uint64_t* __restrict__ exact_rows,
                   uint32_t* __restrict__ far_keys) {
   extern __shared__ __align__(16) uint32_t staged[];
   __shared__ SelectShared sh;
@@ -496,7 +593,7 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
   };
   load(tid);
   const Query8<D>* query = rows + row;
-  const Part whole = whole_row(parts + (size_t)row * n_parts, n_parts, sh);
+  const Part whole = whole_row(a, parts, row, n, sh);
   const Cut cut(whole);
   int above = 0;
   for (int i0 = tid; i0 < len;) {
@@ -724,18 +821,19 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
 // Workspace: queries | 48-bit scores of tokens next to a crowded border | fp32
 // scores | what each scoring warp leaves | keys of rows that are
 // too long for shared memory
+constexpr int kMostCtas = 1024;          // (of 152 SMs: 760)
 static bool fits_cluster(int n) { return (n + kCluster - 1) / kCluster <= kSliceKeys; }
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t kv8_retrieve_workspace_bytes(int B, int Hkv, int D, int n_vis) {
   const size_t rows = (size_t)B * Hkv;
   return up256(rows * (D == 128 ? sizeof(Query8<128>) : sizeof(Query8<64>))) + up256(rows * n_vis * sizeof(uint64_t)) +
-         up256(rows * ((n_vis + 15) / 16 + kScoreWarps) * sizeof(Part)) +
+         up256(rows * kScoreWarps * sizeof(Part)) + up256(kMostCtas * 2 * kScoreWarps * sizeof(Part)) +
          up256(rows * n_vis * sizeof(float)) * (n_vis > kStagedKeys && !fits_cluster(n_vis) ? 2 : 1);
 }
 
 template <int D, int C, bool FAR>
-static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores, const Part* parts,
-                                 int n_parts, uint64_t* exact, uint32_t* far_keys, cudaStream_t stream) {
+static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores, const Parts& parts,
+                                 uint64_t* exact, uint32_t* far_keys, cudaStream_t stream) {
   auto kernel = kv8_select_kernel<D, C, FAR>;
   const int slice = (a.n_vis + C - 1) / C;
   static bool attr_set[64] = {};
@@ -751,7 +849,7 @@ static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows
   const int threads = C > 1 || a.n_vis >= 8192 ? kClusterThreads : 256;
   const size_t smem = FAR ? 0 : (size_t)slice * 4;
   const dim3 grid((unsigned)(C * a.batch * a.Hkv));
-  return launch_dependent(kernel, grid, dim3(threads), smem, stream, a, rows, scores, parts, n_parts, exact, far_keys);
+  return launch_dependent(kernel, grid, dim3(threads), smem, stream, a, rows, scores, parts, exact, far_keys);
 }
 
 template <int D>
@@ -766,18 +864,14 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
   Query8<D>* query = reinterpret_cast<Query8<D>*>(take((size_t)rows * sizeof(Query8<D>)));
   uint64_t* exact = reinterpret_cast<uint64_t*>(take((size_t)rows * a.n_vis * sizeof(uint64_t)));
   float* scores = reinterpret_cast<float*>(take((size_t)rows * a.n_vis * sizeof(float)));
-  Part* parts = reinterpret_cast<Part*>(take((size_t)rows * ((a.n_vis + 15) / 16 + kScoreWarps) * sizeof(Part)));
+  Parts parts;
+  parts.pages = (a.n_vis + 15) / 16;
+  const long long pages = (long long)parts.pages * rows;
+  parts.ctas = (int)std::min<long long>(std::min((long long)num_sms * kScoreCtas, (long long)kMostCtas), (pages + kScoreWarps - 1) / kScoreWarps);
+  parts.whole = reinterpret_cast<Part*>(take((size_t)rows * kScoreWarps * sizeof(Part)));
+  parts.cut = reinterpret_cast<Part*>(take((size_t)kMostCtas * 2 * kScoreWarps * sizeof(Part)));
   uint32_t* far_keys = reinterpret_cast<uint32_t*>(at);      // (there where it is used)
   if (a.scores != nullptr) scores = a.scores;
-  // pages per CTA: a multiple of its warps, for two rounds of resident CTAs (of 4, 5,
-  // 10, 12 and 20 CTAs per SM ten are the fastest: LLaVA-NeXT batch 16 48 us at 10 and
-  // more, 50 at 5; LongVILA batch 8 58, 62 at 5)
-  const int pages = (a.n_vis + 15) / 16;
-  const long long ctas = (long long)num_sms * 10;
-  long long per = ((long long)pages * rows + ctas - 1) / ctas;
-  per = (per + kScoreWarps - 1) / kScoreWarps * kScoreWarps;
-  if (per > pages) per = pages;
-  const long long per_row = (pages + per - 1) / per;
   // (the sums of few rows in every CTA cost less than a launch before them:
   // LongVILA batch 8, seven heads, 58 us, not 71)
   const bool sum = (long long)a.R * (a.H / a.Hkv) <= kFusedRows;
@@ -786,14 +880,13 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
     e = launch_dependent(kv8_qbar_kernel<D>, dim3(rows), dim3(D), 0, stream, static_cast<const uint16_t*>(a.q), a.R, a.H,
                          a.Hkv, query);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(sum ? kv8_score_kernel<D, true> : kv8_score_kernel<D, false>, dim3((unsigned)per_row, a.Hkv, a.batch),
-                       dim3(kScoreWarps * 32), 0, stream, a, query, scores, parts, (int)per);
+  e = launch_dependent(sum ? kv8_score_kernel<D, true> : kv8_score_kernel<D, false>, dim3((unsigned)parts.ctas),
+                       dim3(kScoreWarps * 32), 0, stream, a, query, scores, parts);
   if (e != cudaSuccess) return e;
   // a CTA per row as long as rows are short, else a cluster
-  const int n_parts = (int)per_row * kScoreWarps;
-  if (a.n_vis <= kStagedKeys) return launch_select<D, 1, false>(a, query, scores, parts, n_parts, exact, far_keys, stream);
-  if (fits_cluster(a.n_vis)) return launch_select<D, kCluster, false>(a, query, scores, parts, n_parts, exact, far_keys, stream);
-  return launch_select<D, kCluster, true>(a, query, scores, parts, n_parts, exact, far_keys, stream);
+  if (a.n_vis <= kStagedKeys) return launch_select<D, 1, false>(a, query, scores, parts, exact, far_keys, stream);
+  if (fits_cluster(a.n_vis)) return launch_select<D, kCluster, false>(a, query, scores, parts, exact, far_keys, stream);
+  return launch_select<D, kCluster, true>(a, query, scores, parts, exact, far_keys, stream);
 }
 
 cudaError_t launch_kv8_retrieve(const Kv8RetrieveArgs& a, int D, int num_sms, cudaStream_t stream) {
