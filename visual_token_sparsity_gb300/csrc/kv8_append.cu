@@ -11,6 +11,11 @@
 // A power of two costs e4m3 nothing (its precision is the same at every
 // magnitude but the smallest), makes x / s exact, and makes the old rows of a
 // growing page exact too, but for those that fall below e4m3's 2^-6.
+//
+// Measured: prompts of some 15,000 tokens in all, 28 query heads over 4, d 128, normed,
+// with three axes and the keys' bf16 rows 72.9 us, 4.0 TB/s, bound by instructions (65
+// % of issue slots); 16 single tokens of 32 heads 3.6 us, a launch; two questions of
+// 193 tokens, 4 heads over 2 4.7 us, the 16 rows that a warp forms one after the other.
 #include "kernels.h"
 #include "kv8.cuh"
 #include "norm_rope.cuh"
