@@ -601,11 +601,11 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
   __shared__ float2 part[kParts][kPer], part_ml[kParts];
   const int G = a.H / a.Hkv, lane = threadIdx.x & 31;
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, g = h / G;
-  grid_dep_sync();
+  // The lengths are read before the wait for the attention: it writes none, and let
+  // this kernel begin only when those before it had completed.
   Seq s;
   seq_of(a, b, s);
   const int per_unit = s.blocks();
-  if (per_unit == 0) return;
   uint32_t before = 0, total;
   if (!a.lens.any()) {
     before = (uint32_t)b * (uint32_t)per_unit * (uint32_t)a.Hkv;
@@ -619,8 +619,13 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
     }
   }
   const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
-  const int p0 = kv8::piece_of(total, start, C), n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
-  if (n == 1) return;
+  int p0 = 0, n = 0;
+  if (per_unit > 0) {
+    p0 = kv8::piece_of(total, start, C);
+    n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
+  }
+  grid_dep_sync();
+  if (n <= 1) return;                                       // (no token, or not cut)
   const int w = threadIdx.x / kPer, i = threadIdx.x - w * kPer;
   float M, L;
   float2 v;

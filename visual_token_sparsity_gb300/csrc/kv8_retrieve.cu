@@ -18,13 +18,13 @@
 // 48 bits and the best of them taken, ties to the lower index.
 //
 // Measured, keys out of L2, head dim 128: 16 sequences of 32 KV heads and 2880 keys
-// 46.6 us (4.3 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 52.9 us
-// (3.0 TB/s).  Scoring takes 37 and 36 us of it by itself: a page in flight in each of
+// 46.1 us (4.3 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 51.6 us
+// (3.1 TB/s).  Scoring takes 37 and 36 us of it by itself: a page in flight in each of
 // 40 warps an SM, 59 % of issue slots, and 17 % of an SM's time before its first page and
 // behind its last (two pages in 24 warps 48.3 / 54.5, in 32 warps with spills 62.7 /
 // 61.5; packed adds the same; two and four times the CTAs 48.8 / 56.8 and 52.6 / 65.6;
 // a grid of equal shares of a row instead of one line 47.3 / 53.8).  The selection
-// takes 10 and 17, a chain of some ten waits (scores, counts, pages of the tokens next
+// takes 9 and 16, a chain of some ten waits (scores, counts, pages of the tokens next
 // to the border, and a cluster's barriers) that little work lies between; with a search
 // by the bits of the keys the two calls were 1 and 2.4 us longer.
 #include <algorithm>
@@ -378,18 +378,21 @@ struct __align__(16) SelectShared {
   float factor[32];
 };
 
-// The parts of a row together; all threads of the block call this.
-__device__ __forceinline__ Part whole_row(const Kv8RetrieveArgs& a, const Parts& parts, int row, int n, SelectShared& sh) {
-  const int b = row / a.Hkv, lane = threadIdx.x & 31, pages = (n + 15) >> 4;
+// The first and the last CTA that scored pages of a row of n > 0 keys.
+__device__ __forceinline__ int2 scorers_of(const Kv8RetrieveArgs& a, const Parts& parts, int row, int n, int lane) {
+  const int b = row / a.Hkv, pages = (n + 15) >> 4;
   uint32_t before = 0;
   const uint32_t total = line_of(a, parts, b, lane, before), C = min((uint32_t)parts.ctas, total);
   const uint32_t start = before + (uint32_t)(row - b * a.Hkv) * (uint32_t)pages;
-  const int c0 = kv8::piece_of(total, start, C), c1 = kv8::piece_of(total, start + pages - 1, C);
+  return make_int2(kv8::piece_of(total, start, C), kv8::piece_of(total, start + pages - 1, C));
+}
+// The parts of a row together; all threads of the block call this.
+__device__ __forceinline__ Part whole_row(const Parts& parts, int row, int2 by, SelectShared& sh) {
   Part x = {0.f, 0xffffffffu, 0u, 0u};
-  for (int i = threadIdx.x; i < (c1 - c0 + 1) * kScoreWarps; i += blockDim.x) {
-    const int c = c0 + i / kScoreWarps;
-    const Part* at = c0 == c1 ? parts.whole + (size_t)row * kScoreWarps
-                              : parts.cut + ((size_t)c * 2 + (c == c0)) * kScoreWarps;
+  for (int i = threadIdx.x; i < (by.y - by.x + 1) * kScoreWarps; i += blockDim.x) {
+    const int c = by.x + i / kScoreWarps;
+    const Part* at = by.x == by.y ? parts.whole + (size_t)row * kScoreWarps
+                                  : parts.cut + ((size_t)c * 2 + (c == by.x)) * kScoreWarps;
     const uint4 y = __ldcg(reinterpret_cast<const uint4*>(at + i % kScoreWarps));
     x.factor = fmaxf(x.factor, __uint_as_float(y.x));
     x.lo = min(x.lo, y.y);
@@ -577,9 +580,12 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
   };
   if (tid == 0) sh.sure = sh.near = sh.clear = sh.n_inside = sh.kept = 0;
   for (int i = tid; i < kBins; i += nt) sh.hist[i] = 0;
-  grid_dep_sync();
+  // The lengths are read before the wait for the scores: that kernel writes none, and
+  // let this one begin only when those before it had completed.
   int n = a.n_vis, k = a.k;
   if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
+  const int2 by = n > 0 ? scorers_of(a, parts, row, n, lane) : make_int2(0, 0);
+  grid_dep_sync();
   int32_t* dst = a.vis_idx + (size_t)row * a.k;
   if (rank == 0) fill_unselected(dst, k, a.k);
   if (k <= 0) return;                        // (the whole cluster)
@@ -593,7 +599,7 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
   };
   load(tid);
   const Query8<D>* query = rows + row;
-  const Part whole = whole_row(a, parts, row, n, sh);
+  const Part whole = whole_row(parts, row, by, sh);
   const Cut cut(whole);
   int above = 0;
   for (int i0 = tid; i0 < len;) {
