@@ -13,7 +13,7 @@
 // growing page exact too, but for those that fall below e4m3's 2^-6.
 //
 // Measured: prompts of some 15,000 tokens in all, 28 query heads over 4, d 128, normed,
-// with three axes and the keys' bf16 rows 72.9 us, 4.0 TB/s, bound by instructions (65
+// with three axes and the keys' bf16 rows 72.0 us, 4.1 TB/s, bound by instructions (65
 // % of issue slots); 16 single tokens of 32 heads 3.6 us, a launch; two questions of
 // 193 tokens, 4 heads over 2 4.7 us, the 16 rows that a warp forms one after the other.
 #include "kernels.h"
@@ -130,12 +130,13 @@ struct Place {
 // One group of rows side by side: normalised, rotated and rounded to bf16, with
 // twice the bits where fp32's last ones could decide the rounding.  The whole
 // warp takes part.  KEYS: wherever they could, as a key's 8 bits follow from its
-// bf16 ones and one bit less there may be half a step of e4m3.  Counted in 2^-24 of
-// t = |x cos| + |y sin|, however small their difference: the sum of squares is off by
-// 9 of itself at most, its root by half of that and 1.5, the element by one more
-// (weight times bf16 is exact), the product and the sum by one each, the edges of the
-// interval by one: 11, and 3 without a norm.  (Queries, which stay bf16, are looked at
-// in terms of the result: where a pair cancels, one may be off by its last bit.)
+// bf16 ones and one bit less there may be half a step of e4m3.  Counted in 2^-24: the
+// sum of squares is off by 9 at most, its root by half of that and 1.5, which is 6 of
+// the result; the element by one more (weight times bf16 is exact) and the product by
+// one, which is 2 of t = |x cos| + |y sin|, however small their difference; the sum by
+// one of the result and the interval's edges by another: 8 of the result and 2 of t;
+// without a norm 2 and 1.  (Queries, which stay bf16, are looked at in terms of the
+// result: where a pair cancels, one may be off by its last bit.)
 template <int L, bool INTER, bool NORM, bool PARTLY, bool KEYS>
 __device__ __forceinline__ Lane8<INTER> turn_rows(const Lane8<INTER>& x, const uint64_t* gp, const uint64_t* gy,
                                                   const uint16_t* weight, const Turns& t, const Place<L, INTER>& at,
@@ -163,8 +164,8 @@ __device__ __forceinline__ Lane8<INTER> turn_rows(const Lane8<INTER>& x, const u
   }
   bool doubt = false;
   uint64_t tp[2], ty[2];           // t of both members
+  constexpr uint64_t kAbs = 0x7fffffff7fffffffull;
   if constexpr (KEYS) {
-    constexpr uint64_t kAbs = 0x7fffffff7fffffffull;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint64_t ap = p[e] & kAbs, ay = y[e] & kAbs, ac = t.cs[e] & kAbs, as = t.sn[e] & kAbs;
@@ -186,12 +187,16 @@ __device__ __forceinline__ Lane8<INTER> turn_rows(const Lane8<INTER>& x, const u
   if (changed) {
     out.pack(p, y);
     if constexpr (KEYS) {
-      const float off = (normed ? 11.f : 3.f) / 16777216.f;
-      const uint64_t up = fm::splat2(off), down = fm::splat2(-off);
+      constexpr float kUnit = 1.f / 16777216.f;
+      const uint64_t of_it = fm::splat2((normed ? 8.f : 2.f) * kUnit), of_t = fm::splat2((normed ? 2.f : 1.f) * kUnit);
+      auto differ = [&](uint64_t v, uint64_t terms) {
+        const uint64_t off = fm::fma2(v & kAbs, of_it, fm::mul2(terms, of_t));
+        return bf16x2(fm::add2(v, off)) != bf16x2(fm::add2(v, off ^ 0x8000000080000000ull));
+      };
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        doubt = doubt || bf16x2(fm::fma2(tp[e], up, p[e])) != bf16x2(fm::fma2(tp[e], down, p[e]));
-        doubt = doubt || bf16x2(fm::fma2(ty[e], up, y[e])) != bf16x2(fm::fma2(ty[e], down, y[e]));
+        doubt = doubt || differ(p[e], tp[e]);
+        doubt = doubt || differ(y[e], ty[e]);
       }
     } else {
       constexpr uint32_t kOff = (0x8000u + kDoubt) * 0x10001u;
