@@ -19,7 +19,7 @@
 //
 // Measured, keys out of L2, head dim 128: 16 sequences of 32 KV heads and 2880 keys
 // 46.1 us (4.3 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 51.6 us
-// (3.1 TB/s).  Scoring takes 37 and 36 us of it by itself: a page in flight in each of
+// (3.1 TB/s); 193 question rows of 28 heads over 4 and 576 keys 13.7 us.  Scoring takes 37 and 36 us of it by itself: a page in flight in each of
 // 40 warps an SM, 59 % of issue slots, and 17 % of an SM's time before its first page and
 // behind its last (two pages in 24 warps 48.3 / 54.5, in 32 warps with spills 62.7 /
 // 61.5; packed adds the same; two and four times the CTAs 48.8 / 56.8 and 52.6 / 65.6;
@@ -97,28 +97,17 @@ struct Query8 {
 
 namespace {
 
-constexpr int kFusedRows = 16;       // query rows times heads that every scoring CTA sums itself
+// Query rows times heads that every scoring CTA sums itself: 7 of LongVILA batch 8 so
+// 51.6 us, by a launch before 60.4; 14 of two sequences of 3000 keys 20.3 and 14.9.
+constexpr int kFusedRows = 8;
 
-// The row's query from R x G rows, by threads 0 .. D - 1 of a block of at least D
-// (all threads call this); the caller synchronises before it reads *o.
+// *o from element e = threadIdx.x of a row's sum, by threads 0 .. D - 1 of a block of at
+// least D (all threads call this); the caller synchronises before it reads *o.
 template <int D>
-__device__ __forceinline__ void sum_query(const uint16_t* q, int R, int H, int Hkv, int row, Query8<D>* o) {
+__device__ __forceinline__ void write_query(float hi, float lo, Query8<D>* o) {
   __shared__ float part[2][D / 32];
-  const int b = row / Hkv, g = row - b * Hkv, G = H / Hkv, e = threadIdx.x;
-  float hi = 0.f, lo = 0.f;
+  const int e = threadIdx.x;
   if (e < D) {
-    const uint16_t* src = q + ((size_t)b * R * H + (size_t)g * G) * D + e;
-    const int n = R * G;
-    for (int i0 = 0; i0 < n; i0 += 8) {
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j, r = i / G;
-        x[j] = i < n ? __uint_as_float((uint32_t)__ldg(src + ((size_t)r * H + (i - r * G)) * D) << 16) : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) add48(hi, lo, x[j], 0.f);
-    }
     const float a = fabsf(hi), s = warp_sum(a), top = warp_max(a);
     if ((e & 31) == 0) {
       part[0][e >> 5] = s;
@@ -155,13 +144,115 @@ __device__ __forceinline__ void sum_query(const uint16_t* q, int R, int H, int H
   }
 }
 
+// The row's query from few rows, an element a thread.
+template <int D>
+__device__ __forceinline__ void sum_query(const uint16_t* q, int R, int H, int Hkv, int row, Query8<D>* o) {
+  const int b = row / Hkv, g = row - b * Hkv, G = H / Hkv, e = threadIdx.x;
+  float hi = 0.f, lo = 0.f;
+  if (e < D) {
+    const uint16_t* src = q + ((size_t)b * R * H + (size_t)g * G) * D + e;
+    const int n = R * G;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j, r = i / G;
+        x[j] = i < n ? __uint_as_float((uint32_t)__ldg(src + ((size_t)r * H + (i - r * G)) * D) << 16) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) add48(hi, lo, x[j], 0.f);
+    }
+  }
+  write_query<D>(hi, lo, o);
+}
+
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(D)
-kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>* rows) {
+// The queries of rows with many: C CTAs per row of the cache, a warp per query row at a
+// time, eight on their way.
+constexpr int kSumWarps = 32, kSumCtas = 8;
+template <int D, int C>
+__device__ __forceinline__ void sum_queries(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>* rows) {
+  constexpr int E = D / 32, kAhead = 8, kParts = kSumWarps * 32 / D, kEach = kSumWarps / kParts, kStep = kSumWarps * C;
+  __shared__ float2 sums[kSumWarps][D];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = C > 1 ? (int)cluster.block_rank() : 0, row = blockIdx.x / C;
+  const int b = row / Hkv, g = row - b * Hkv, G = H / Hkv, n = R * G;
+  // query row i is head h of the group at question row r; the next one of a warp is
+  // kStep further on
+  int i = rank * kSumWarps + warp, r = i / G, h = i - r * G;
+  const int dr = kStep / G, dh = kStep - dr * G;
   grid_dep_sync();
-  sum_query<D>(q, R, H, Hkv, blockIdx.x, rows + blockIdx.x);
+  const uint16_t* src = q + ((size_t)b * R * H + (size_t)g * G) * D + lane * E;
+  float hi[E], lo[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) hi[e] = lo[e] = 0.f;
+#pragma unroll 1
+  while (i < n) {
+    uint32_t x[kAhead][E / 2];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(src + ((size_t)r * H + h) * D);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) x[j][e] = i < n ? __ldg(at + e) : 0u;
+      i += kStep;
+      r += dr;
+      h += dh;
+      if (h >= G) {
+        h -= G;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        add48(hi[2 * e], lo[2 * e], bf16_lo(x[j][e]), 0.f);
+        add48(hi[2 * e + 1], lo[2 * e + 1], bf16_hi(x[j][e]), 0.f);
+      }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = make_float2(hi[e], lo[e]);
+  __syncthreads();
+  // kParts threads an element, then one of the CTA, then one of the cluster
+  const int e = threadIdx.x % D, part = threadIdx.x / D;
+  float t = 0.f, l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kEach; ++w) add48(t, l, sums[part * kEach + w][e].x, sums[part * kEach + w][e].y);
+  __syncthreads();
+  sums[part][e] = make_float2(t, l);
+  __syncthreads();
+  t = l = 0.f;
+  if (threadIdx.x < D)
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) add48(t, l, sums[p][e].x, sums[p][e].y);
+  if constexpr (C > 1) {
+    __syncthreads();
+    if (threadIdx.x < D) sums[0][e] = make_float2(t, l);
+    cluster.sync();
+    if (rank == 0 && threadIdx.x < D) {
+      float2 theirs[C];
+#pragma unroll
+      for (int c = 1; c < C; ++c) theirs[c] = *cluster.map_shared_rank(&sums[0][e], c);
+#pragma unroll
+      for (int c = 1; c < C; ++c) add48(t, l, theirs[c].x, theirs[c].y);
+    }
+    cluster.sync();                                          // (its shared memory has been read)
+    if (rank != 0) return;
+  }
+  write_query<D>(t, l, rows + row);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSumWarps * 32)
+kv8_qbar_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>* rows) {
+  sum_queries<D, 1>(q, R, H, Hkv, rows);
+}
+template <int D>
+__global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kSumWarps * 32)
+kv8_qbar_cluster_kernel(const uint16_t* __restrict__ q, int R, int H, int Hkv, Query8<D>* rows) {
+  sum_queries<D, kSumCtas>(q, R, H, Hkv, rows);
 }
 
 // What a scoring warp leaves for the selection: the largest factor of its pages, and
@@ -558,10 +649,9 @@ __device__ __forceinline__ Near near_border(const uint32_t* keys, int n, int k, 
 // The selection of one row by C CTAs, CTA r having its r-th slice.  FAR: the keys of a
 // slice do not fit shared memory and go to `far_keys`.
 template <int D, int C, bool FAR>
-__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kClusterThreads, 2)
-kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows, const float* __restrict__ scores,
-                  const Parts parts, uint64_t* __restrict__ exact_rows,
-                  uint32_t* __restrict__ far_keys) {
+__device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* __restrict__ scores,
+                                           const Parts& parts, uint64_t* __restrict__ exact_rows,
+                                           uint32_t* __restrict__ far_keys) {
   extern __shared__ __align__(16) uint32_t staged[];
   __shared__ SelectShared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -824,6 +914,20 @@ kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* ro
   if constexpr (C > 1) cluster.sync();     // (this CTA's shared memory has been read)
 }
 
+template <int D>
+__global__ void __launch_bounds__(kClusterThreads, 2)
+kv8_select_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows, const float* __restrict__ scores,
+                  const Parts parts, uint64_t* __restrict__ exact, uint32_t* __restrict__ far_keys) {
+  select_row<D, 1, false>(a, rows, scores, parts, exact, far_keys);
+}
+template <int D, bool FAR>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads, 2)
+kv8_select_cluster_kernel(const __grid_constant__ Kv8RetrieveArgs a, const Query8<D>* rows,
+                          const float* __restrict__ scores, const Parts parts, uint64_t* __restrict__ exact,
+                          uint32_t* __restrict__ far_keys) {
+  select_row<D, kCluster, FAR>(a, rows, scores, parts, exact, far_keys);
+}
+
 // Workspace: queries | 48-bit scores of tokens next to a crowded border | fp32
 // scores | what each scoring warp leaves | keys of rows that are
 // too long for shared memory
@@ -837,25 +941,21 @@ size_t kv8_retrieve_workspace_bytes(int B, int Hkv, int D, int n_vis) {
          up256(rows * n_vis * sizeof(float)) * (n_vis > kStagedKeys && !fits_cluster(n_vis) ? 2 : 1);
 }
 
-template <int D, int C, bool FAR>
-static cudaError_t launch_select(const Kv8RetrieveArgs& a, const Query8<D>* rows, const float* scores, const Parts& parts,
-                                 uint64_t* exact, uint32_t* far_keys, cudaStream_t stream) {
-  auto kernel = kv8_select_kernel<D, C, FAR>;
-  const int slice = (a.n_vis + C - 1) / C;
-  static bool attr_set[64] = {};
+// `kernel`: of C CTAs a row, with `most` keys in shared memory at most
+template <typename Kernel, typename... Args>
+static cudaError_t launch_select(Kernel kernel, bool (&attr_set)[64], int C, int most, const Kv8RetrieveArgs& a,
+                                 cudaStream_t stream, Args... args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    if (!FAR)
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (C > 1 ? kSliceKeys : kStagedKeys) * 4);
+  if (most > 0 && (dev < 0 || dev >= 64 || !attr_set[dev])) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const int threads = C > 1 || a.n_vis >= 8192 ? kClusterThreads : 256;
-  const size_t smem = FAR ? 0 : (size_t)slice * 4;
-  const dim3 grid((unsigned)(C * a.batch * a.Hkv));
-  return launch_dependent(kernel, grid, dim3(threads), smem, stream, a, rows, scores, parts, exact, far_keys);
+  const size_t smem = most > 0 ? (size_t)((a.n_vis + C - 1) / C) * 4 : 0;
+  return launch_dependent(kernel, dim3((unsigned)(C * a.batch * a.Hkv)), dim3(threads), smem, stream, a, args...);
 }
 
 template <int D>
@@ -878,21 +978,28 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
   parts.cut = reinterpret_cast<Part*>(take((size_t)kMostCtas * 2 * kScoreWarps * sizeof(Part)));
   uint32_t* far_keys = reinterpret_cast<uint32_t*>(at);      // (there where it is used)
   if (a.scores != nullptr) scores = a.scores;
-  // (the sums of few rows in every CTA cost less than a launch before them:
-  // LongVILA batch 8, seven heads, 58 us, not 71)
   const bool sum = (long long)a.R * (a.H / a.Hkv) <= kFusedRows;
+  // (16000 rows for one key row by a CTA 227 us in all, by a cluster 30; 1351 29.7 and 13.3)
+  const bool wide = (long long)a.R * (a.H / a.Hkv) >= 512 && rows <= num_sms;
   cudaError_t e = cudaSuccess;
   if (!sum)
-    e = launch_dependent(kv8_qbar_kernel<D>, dim3(rows), dim3(D), 0, stream, static_cast<const uint16_t*>(a.q), a.R, a.H,
-                         a.Hkv, query);
+    e = wide ? launch_dependent(kv8_qbar_cluster_kernel<D>, dim3(kSumCtas * rows), dim3(kSumWarps * 32), 0, stream,
+                                static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, query)
+             : launch_dependent(kv8_qbar_kernel<D>, dim3(rows), dim3(kSumWarps * 32), 0, stream,
+                                static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, query);
   if (e != cudaSuccess) return e;
   e = launch_dependent(sum ? kv8_score_kernel<D, true> : kv8_score_kernel<D, false>, dim3((unsigned)parts.ctas),
                        dim3(kScoreWarps * 32), 0, stream, a, query, scores, parts);
   if (e != cudaSuccess) return e;
   // a CTA per row as long as rows are short, else a cluster
-  if (a.n_vis <= kStagedKeys) return launch_select<D, 1, false>(a, query, scores, parts, exact, far_keys, stream);
-  if (fits_cluster(a.n_vis)) return launch_select<D, kCluster, false>(a, query, scores, parts, exact, far_keys, stream);
-  return launch_select<D, kCluster, true>(a, query, scores, parts, exact, far_keys, stream);
+  static bool set[3][64] = {};
+  if (a.n_vis <= kStagedKeys)
+    return launch_select(kv8_select_kernel<D>, set[0], 1, kStagedKeys, a, stream, query, scores, parts, exact, far_keys);
+  if (fits_cluster(a.n_vis))
+    return launch_select(kv8_select_cluster_kernel<D, false>, set[1], kCluster, kSliceKeys, a, stream, query, scores, parts,
+                         exact, far_keys);
+  return launch_select(kv8_select_cluster_kernel<D, true>, set[2], kCluster, 0, a, stream, query, scores, parts, exact,
+                       far_keys);
 }
 
 cudaError_t launch_kv8_retrieve(const Kv8RetrieveArgs& a, int D, int num_sms, cudaStream_t stream) {
