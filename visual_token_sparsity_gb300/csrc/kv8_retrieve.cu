@@ -19,11 +19,13 @@
 //
 // Measured, keys out of L2, head dim 128: 16 sequences of 32 KV heads and 2880 keys
 // 46.1 us (4.3 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 51.6 us
-// (3.1 TB/s); 193 question rows of 28 heads over 4 and 576 keys 13.7 us.  Scoring takes 37 and 36 us of it by itself: a page in flight in each of
-// 40 warps an SM, 59 % of issue slots, and 17 % of an SM's time before its first page and
-// behind its last (two pages in 24 warps 48.3 / 54.5, in 32 warps with spills 62.7 /
-// 61.5; packed adds the same; two and four times the CTAs 48.8 / 56.8 and 52.6 / 65.6;
-// a grid of equal shares of a row instead of one line 47.3 / 53.8).  The selection
+// (3.1 TB/s); 193 question rows of 28 heads over 4 and 576 keys 13.7 us.  Scoring takes 37 and 36 us of it by itself: with a page in flight in each of
+// 40 warps an SM pages go by at 6.2 TB/s, and 17 % of an SM's time lies before its first
+// page and behind its last.  More pages on their way are no faster (two in registers of
+// 24 warps 48.3 / 54.5, of 32 warps with spills 62.7 / 61.5; two or three in a cp.async
+// ring of 32 warps 51.0 / 56.8 and 56.4 / 56.7), nor are packed adds; two and four times
+// the CTAs 48.8 / 56.8 and 52.6 / 65.6; equal shares of each row instead of one line
+// 47.3 / 53.8.  The selection
 // takes 9 and 16, a chain of some ten waits (scores, counts, pages of the tokens next
 // to the border, and a cluster's barriers) that little work lies between; with a search
 // by the bits of the keys the two calls were 1 and 2.4 us longer.
