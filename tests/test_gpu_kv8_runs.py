@@ -200,6 +200,25 @@ def test_keys_are_rounded_from_more_than_fp32(lib, d, interleaved, norm):
     assert int((want.view(torch.int16) != ko.view(torch.int16)).sum()) == 0
 
 
+@pytest.mark.parametrize("times", [40.0, 3e4, 2.0 ** 70])
+@pytest.mark.parametrize("n_vis,k", [(3000, 700), (20000, 9000)])
+def test_retrieval_beside_keys_of_another_magnitude(lib, n_vis, k, times):
+    """One page's keys are many times larger: its scores stretch the range that the
+    others lie in a small part of, and its factor the error that fp32 may have made."""
+    from visual_token_sparsity_gb300 import binding as sv
+    H, Hkv, d, per = 4, 2, 64, -(-n_vis // 16)
+    factor = np.ones((1, Hkv, per, 2))
+    factor[:, 0, 5], factor[:, 1, per - 1] = times, times
+    c = Cache8(1, Hkv, d, n_vis, seed=44, factor=factor)
+    q = synth.normal_bf16((1, 2, H, d), 16).to(DEV)
+    vis = torch.full((1, Hkv, k), -7, dtype=torch.int32, device=DEV)
+    ws = sv.workspace(sv.sv_kv8_retrieve_workspace_bytes(1, H, Hkv, d, n_vis, k))
+    sv.sv_kv8_retrieve_topk(q, c.layer(), sv.SeqBatch(c.bt.to(DEV), n_vis, 0), k, vis, None, ws)
+    assert sv.sv_read_device_status(ws) == 0
+    want, _ = oracle_select(q, c.rows(0), [n_vis], [k])
+    assert np.array_equal(vis.cpu().numpy(), want)
+
+
 RUN = textwrap.dedent("""
     import sys, torch
     sys.path.insert(0, {root!r})
