@@ -267,327 +267,332 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 
 #pragma unroll 1
   for (; left > 0; ++b, off = 0) {
-  Seq sq;
-  seq_of(a, b, sq);
-  const int nv = sq.nv, kb = sq.kb, total_tok = sq.kb + sq.nt, per_unit = sq.blocks();
-  const uint32_t in_seq = (uint32_t)per_unit * (uint32_t)a.Hkv;
+    Seq sq;
+    seq_of(a, b, sq);
+    const int nv = sq.nv, kb = sq.kb, total_tok = sq.kb + sq.nt, per_unit = sq.blocks();
+    const uint32_t in_seq = (uint32_t)per_unit * (uint32_t)a.Hkv;
 #pragma unroll 1
-  while (left > 0 && off < in_seq) {
-  const int g = (int)(off / (uint32_t)per_unit), blk0 = (int)off - g * per_unit, blk1 = min(per_unit, blk0 + left);
-  off += blk1 - blk0;
-  left -= blk1 - blk0;
-  const int32_t* list = a.vis_idx != nullptr ? a.vis_idx + ((size_t)b * a.Hkv + g) * a.k_vis : nullptr;
-  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
-  const int first = (blk0 + warp) * kBlock, end = min(total_tok, blk1 * kBlock);
-  constexpr int stride = kWarps * kBlock;
+    while (left > 0 && off < in_seq) {
+      const int g = (int)(off / (uint32_t)per_unit), blk0 = (int)off - g * per_unit, blk1 = min(per_unit, blk0 + left);
+      off += blk1 - blk0;
+      left -= blk1 - blk0;
+      const int32_t* list = a.vis_idx != nullptr ? a.vis_idx + ((size_t)b * a.Hkv + g) * a.k_vis : nullptr;
+      const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+      const int first = (blk0 + warp) * kBlock, end = min(total_tok, blk1 * kBlock);
+      constexpr int stride = kWarps * kBlock;
 
-  // ---- a block's tokens, a lane each, in three steps: position (two blocks
-  // ahead), page (one ahead), row and factors
-  struct Ahead {
-    int pos, page;
-    bool there;
-  };
-  auto load_pos = [&](int t0, Ahead& n) {
-    const int t = t0 + lane;
-    n.there = t < end;
-    n.pos = t < kb ? t : nv + t - kb;
-    if (n.there && t < kb && list != nullptr) n.pos = __ldg(list + t);
-  };
-  auto load_page = [&](int t0, Ahead& n) {
-    if (n.there && t0 + lane < kb && (n.pos < 0 || n.pos >= nv)) {
-      flag_status(a.status, kStatusBadIndex);
-      n.there = false;
-    }
-    n.page = n.there ? __ldg(bt + (n.pos >> 4)) : -1;
-  };
-  uint32_t rid, there;
-  auto load_row = [&](const Ahead& n) {
-    const bool ok = n.there && n.page >= 0 && n.page < a.num_blocks;
-    if (n.there && !ok) flag_status(a.status, kStatusBadBlock);
-    rid = ok ? ((uint32_t)n.page * (uint32_t)a.Hkv + (uint32_t)g) * 16u + (uint32_t)(n.pos & 15) : 0u;
-    there = __ballot_sync(0xffffffffu, ok);
-  };
-  Ahead n1, n2;
-  load_pos(first, n1);
-  load_pos(first + stride, n2);
-  uint2 raw[NT][KS];            // the queries, on their way with the positions
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + ((size_t)b * a.H + (size_t)g * G + 8 * t + r) * D + q4 * 16;
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-      raw[t][k] = 8 * t + r < G ? __ldg(reinterpret_cast<const uint2*>(src + (k >> 2) * 64 + (k & 3) * 4)) : make_uint2(0u, 0u);
-  }
-  load_page(first, n1);
-  // Requests the rows and factors of step `i` (its tokens' ids are looked up with
-  // the first of a block's two steps); tokens that are not there read as zeros.
-  int t_ahead = first;
-  auto request = [&](int i) {
-    if ((i & 1) == 0) {
-      load_row(n1);
-      n1 = n2;
-      load_page(t_ahead + stride, n1);
-      load_pos(t_ahead + 2 * stride, n2);
-      t_ahead += stride;
-    }
-    const int h = (i & 1) * 16;
-    const uint32_t stage = (uint32_t)i % S;
-    constexpr int U = D / 16, RPI = 32 / U;                 // 16-byte units of a row, rows of an instruction
-    const uint32_t u = lane % U, t0 = lane / U;
-#pragma unroll
-    for (int c = 0; c < kStep / RPI; ++c) {
-      const uint32_t t = t0 + c * RPI, row = __shfl_sync(0xffffffffu, rid, h + t), n = (there >> (h + t)) & 1 ? 16u : 0u;
-      const uint32_t to = ring_at + stage * R::kStage + unit_at<D>(t, u);
-      cp_async16(to, a.k_pool + (size_t)row * D + u * 16, n);
-      cp_async16(to + R::kPool, a.v_pool + (size_t)row * D + u * 16, n);
-    }
-    const uint32_t mine = __shfl_sync(0xffffffffu, rid, h + (lane & 15));
-    if (lane < 16)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(ring_at + R::kFactors + (stage * kStep + lane) * 8),
-                   "l"(a.scales + (size_t)(mine >> 4) * 2), "r"((there >> (h + lane)) & 1 ? 8u : 0u)
-                   : "memory");
-    if (lane == 0) reinterpret_cast<uint32_t*>(ring + R::kThere)[stage] = there >> h;
-    cp_async_commit();
-  };
-
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) request(i);
-
-  // ---- the queries: each head's elements over 2^e, so that the largest lies in
-  // [2^14, 2^15); those that are not finite stay what they are
-  uint32_t qf[NT][KS][2];
-  float qs[NT][2];              // of heads 2 q4 and 2 q4 + 1: scale log2(e) 2^e
-  {
-    float mine[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const uint2* x = raw[t];
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) top = kv8::max_finite2(kv8::max_finite2(top, x[k].x), x[k].y);
-      top = max(top & 0xffffu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^(14 - e) in two factors, as its exponent may be out of range
-      const int e = (int)((top << 16) >> 23) - 127 - 14;              // (a head without a normal element: 2^-127 on)
-      const float f0 = __uint_as_float((uint32_t)(127 - e / 2) << 23), f1 = __uint_as_float((uint32_t)(127 - (e - e / 2)) << 23);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qf[t][k][0] = half2_of(bf16_lo(x[k].x) * f0 * f1, bf16_hi(x[k].x) * f0 * f1);
-        qf[t][k][1] = half2_of(bf16_lo(x[k].y) * f0 * f1, bf16_hi(x[k].y) * f0 * f1);
-      }
-      mine[t] = (float)e;
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = (int)__shfl_sync(0xffffffffu, mine[t], (2 * q4 + i) * 4);
-        qs[t][i] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e / 2) << 23) * __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
-      }
-  }
-
-  float m[NT][2], l[NT][2], o[NT][KS][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[t][i] = -INFINITY;
-      l[t][i] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < KS; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][j][e] = 0.f;
-  }
-  uint32_t vtop = 0x00800000u;      // the largest factor of V so far, rounded down to a power of two (bits)
-
-  // (two steps a block of this warp)
-  const int steps = max(0, (end - first + stride - 1) / stride * 2);
-#pragma unroll 1
-  for (int i = 0; i < steps; ++i) {
-      cp_async_wait<S - 2>();
-      __syncwarp();
-      request(i + S - 1);
-      const uint32_t stage = (uint32_t)i % S;
-      const uint8_t* at = ring + stage * R::kStage;
-      const float2* fac = reinterpret_cast<const float2*>(ring + R::kFactors + stage * kStep * 8);
-      const float2 f0 = fac[r], f1 = fac[r + 8];
-      const float sk0 = f0.x, sv0 = f0.y, sk1 = f1.x, sv1 = f1.y;
-      const uint32_t seen = reinterpret_cast<const uint32_t*>(ring + R::kThere)[stage];
-      const bool ok0 = (seen >> r) & 1, ok1 = (seen >> (8 + r)) & 1;
-      uint4 xk[2][KC];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int c = 0; c < KC; ++c) xk[n][c] = *reinterpret_cast<const uint4*>(at + unit_at<D>(r + 8 * n, 4 * c + q4));
-      float z[NT][4];
+      // ---- a block's tokens, a lane each, in three steps: position (two blocks
+      // ahead), page (one ahead), row and factors
+      struct Ahead {
+        int pos, page;
+        bool there;
+      };
+      auto load_pos = [&](int t0, Ahead& n) {
+        const int t = t0 + lane;
+        n.there = t < end;
+        n.pos = t < kb ? t : nv + t - kb;
+        if (n.there && t < kb && list != nullptr) n.pos = __ldg(list + t);
+      };
+      auto load_page = [&](int t0, Ahead& n) {
+        if (n.there && t0 + lane < kb && (n.pos < 0 || n.pos >= nv)) {
+          flag_status(a.status, kStatusBadIndex);
+          n.there = false;
+        }
+        n.page = n.there ? __ldg(bt + (n.pos >> 4)) : -1;
+      };
+      uint32_t rid, there;
+      auto load_row = [&](const Ahead& n) {
+        const bool ok = n.there && n.page >= 0 && n.page < a.num_blocks;
+        if (n.there && !ok) flag_status(a.status, kStatusBadBlock);
+        rid = ok ? ((uint32_t)n.page * (uint32_t)a.Hkv + (uint32_t)g) * 16u + (uint32_t)(n.pos & 15) : 0u;
+        there = __ballot_sync(0xffffffffu, ok);
+      };
+      Ahead n1, n2;
+      load_pos(first, n1);
+      load_pos(first + stride, n2);
+      uint2 raw[NT][KS];            // the queries, on their way with the positions
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
+        const size_t head = (size_t)b * a.H + (size_t)g * G + 8 * t + r;
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + head * D + q4 * 16;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[t][e] = 0.f;
+        for (int k = 0; k < KS; ++k)
+          raw[t][k] = 8 * t + r < G ? __ldg(reinterpret_cast<const uint2*>(src + (k >> 2) * 64 + (k & 3) * 4))
+                                    : make_uint2(0u, 0u);
       }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&xk[0][k >> 2]);
-        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&xk[1][k >> 2]);
-        const uint32_t y0 = w0[k & 3], y1 = w1[k & 3];
-        const uint32_t a0 = kv8::e4m3x2_to_half2((uint16_t)y0), a1 = kv8::e4m3x2_to_half2((uint16_t)y1);
-        const uint32_t a2 = kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), a3 = kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(z[t], a0, a1, a2, a3, qf[t][k][0], qf[t][k][1]);
-      }
-      bool raise = false;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[t][e] = (e < 2 ? ok0 : ok1) ? z[t][e] * (e < 2 ? sk0 : sk1) * qs[t][e & 1] : -INFINITY;
-          raise = raise || z[t][e] > m[t][e & 1] + kRaise || (m[t][e & 1] == -INFINITY && z[t][e] > -INFINITY);
+      load_page(first, n1);
+      // Requests the rows and factors of step `i` (its tokens' ids are looked up with
+      // the first of a block's two steps); tokens that are not there read as zeros.
+      int t_ahead = first;
+      auto request = [&](int i) {
+        if ((i & 1) == 0) {
+          load_row(n1);
+          n1 = n2;
+          load_page(t_ahead + stride, n1);
+          load_pos(t_ahead + 2 * stride, n2);
+          t_ahead += stride;
         }
-      raise = raise || exponent_of(sv0, sv1) > vtop;
-      if (__any_sync(0xffffffffu, raise)) {
-        // the factors' largest, and each head's
-        const uint32_t top = __reduce_max_sync(0xffffffffu, max(vtop, exponent_of(sv0, sv1)));
-        const float down = __uint_as_float(vtop) / __uint_as_float(top);
-        vtop = top;
+        const int h = (i & 1) * 16;
+        const uint32_t stage = (uint32_t)i % S;
+        constexpr int U = D / 16, RPI = 32 / U;                 // 16-byte units of a row, rows of an instruction
+        const uint32_t u = lane % U, t0 = lane / U;
+#pragma unroll
+        for (int c = 0; c < kStep / RPI; ++c) {
+          const uint32_t t = t0 + c * RPI, row = __shfl_sync(0xffffffffu, rid, h + t);
+          const uint32_t n = (there >> (h + t)) & 1 ? 16u : 0u;
+          const uint32_t to = ring_at + stage * R::kStage + unit_at<D>(t, u);
+          cp_async16(to, a.k_pool + (size_t)row * D + u * 16, n);
+          cp_async16(to + R::kPool, a.v_pool + (size_t)row * D + u * 16, n);
+        }
+        const uint32_t mine = __shfl_sync(0xffffffffu, rid, h + (lane & 15));
+        if (lane < 16)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(ring_at + R::kFactors + (stage * kStep + lane) * 8),
+                       "l"(a.scales + (size_t)(mine >> 4) * 2), "r"((there >> (h + lane)) & 1 ? 8u : 0u)
+                       : "memory");
+        if (lane == 0) reinterpret_cast<uint32_t*>(ring + R::kThere)[stage] = there >> h;
+        cp_async_commit();
+      };
+
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) request(i);
+
+      // ---- the queries: each head's elements over 2^e, so that the largest lies in
+      // [2^14, 2^15); those that are not finite stay what they are
+      uint32_t qf[NT][KS][2];
+      float qs[NT][2];              // of heads 2 q4 and 2 q4 + 1: scale log2(e) 2^e
+      {
+        float mine[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint2* x = raw[t];
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) top = kv8::max_finite2(kv8::max_finite2(top, x[k].x), x[k].y);
+          top = max(top & 0xffffu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^(14 - e) in two factors, as its exponent may be out of range
+          const int e = (int)((top << 16) >> 23) - 127 - 14;              // (a head without a normal element: 2^-127 on)
+          const float f0 = __uint_as_float((uint32_t)(127 - e / 2) << 23);
+          const float f1 = __uint_as_float((uint32_t)(127 - (e - e / 2)) << 23);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            qf[t][k][0] = half2_of(bf16_lo(x[k].x) * f0 * f1, bf16_hi(x[k].x) * f0 * f1);
+            qf[t][k][1] = half2_of(bf16_lo(x[k].y) * f0 * f1, bf16_hi(x[k].y) * f0 * f1);
+          }
+          mine[t] = (float)e;
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float mx = fmaxf(m[t][i], fmaxf(z[t][i], z[t][i + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float alpha = m[t][i] == -INFINITY ? 0.f : fast_exp2(m[t][i] - mx);
-            m[t][i] = mx;
-            l[t][i] *= alpha;
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
-              o[t][j][i] *= alpha * down;
-              o[t][j][i + 2] *= alpha * down;
-            }
+            const int e = (int)__shfl_sync(0xffffffffu, mine[t], (2 * q4 + i) * 4);
+            qs[t][i] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e / 2) << 23) *
+                       __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
           }
       }
-      // 2^6 s_v over the largest factor
-      const float unit_v = __uint_as_float((254u - (vtop >> 23)) << 23);
-      const float w0 = sv0 * unit_v * 64.f, w1 = sv1 * unit_v * 64.f;
-      uint32_t p[NT][2];
+
+      float m[NT][2], l[NT][2], o[NT][KS][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[t][e & 1];
-          y[e] = fast_exp2(z[t][e] - (ref == -INFINITY ? 0.f : ref));
-          l[t][e & 1] += y[e];
+        for (int i = 0; i < 2; ++i) {
+          m[t][i] = -INFINITY;
+          l[t][i] = 0.f;
         }
-        p[t][0] = transposed(half2_of(y[0] * w0, y[1] * w0));
-        p[t][1] = transposed(half2_of(y[2] * w1, y[3] * w1));
-      }
-      uint32_t xv[4][VW];                         // tokens 2 q4, + 1, + 8, + 9
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const uint32_t t = 2 * q4 + (n & 1) + (n >> 1) * 8;
-        if constexpr (D == 128) {
-          const uint4 y = *reinterpret_cast<const uint4*>(at + R::kPool + unit_at<D>(t, r));
-          xv[n][0] = y.x; xv[n][1] = y.y; xv[n][2] = y.z; xv[n][3] = y.w;
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][j][e] = 0.f;
+      }
+      uint32_t vtop = 0x00800000u;      // the largest factor of V so far, rounded down to a power of two (bits)
+
+      // (two steps a block of this warp)
+      const int steps = max(0, (end - first + stride - 1) / stride * 2);
+#pragma unroll 1
+      for (int i = 0; i < steps; ++i) {
+        cp_async_wait<S - 2>();
+        __syncwarp();
+        request(i + S - 1);
+        const uint32_t stage = (uint32_t)i % S;
+        const uint8_t* at = ring + stage * R::kStage;
+        const float2* fac = reinterpret_cast<const float2*>(ring + R::kFactors + stage * kStep * 8);
+        const float2 f0 = fac[r], f1 = fac[r + 8];
+        const float sk0 = f0.x, sv0 = f0.y, sk1 = f1.x, sv1 = f1.y;
+        const uint32_t seen = reinterpret_cast<const uint32_t*>(ring + R::kThere)[stage];
+        const bool ok0 = (seen >> r) & 1, ok1 = (seen >> (8 + r)) & 1;
+        uint4 xk[2][KC];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < KC; ++c) xk[n][c] = *reinterpret_cast<const uint4*>(at + unit_at<D>(r + 8 * n, 4 * c + q4));
+        float z[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[t][e] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&xk[0][k >> 2]);
+          const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&xk[1][k >> 2]);
+          const uint32_t y0 = w0[k & 3], y1 = w1[k & 3];
+          const uint32_t a0 = kv8::e4m3x2_to_half2((uint16_t)y0), a1 = kv8::e4m3x2_to_half2((uint16_t)y1);
+          const uint32_t a2 = kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), a3 = kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(z[t], a0, a1, a2, a3, qf[t][k][0], qf[t][k][1]);
+        }
+        bool raise = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[t][e] = (e < 2 ? ok0 : ok1) ? z[t][e] * (e < 2 ? sk0 : sk1) * qs[t][e & 1] : -INFINITY;
+            raise = raise || z[t][e] > m[t][e & 1] + kRaise || (m[t][e & 1] == -INFINITY && z[t][e] > -INFINITY);
+          }
+        raise = raise || exponent_of(sv0, sv1) > vtop;
+        if (__any_sync(0xffffffffu, raise)) {
+          // the factors' largest, and each head's
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max(vtop, exponent_of(sv0, sv1)));
+          const float down = __uint_as_float(vtop) / __uint_as_float(top);
+          vtop = top;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float mx = fmaxf(m[t][i], fmaxf(z[t][i], z[t][i + 2]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float alpha = m[t][i] == -INFINITY ? 0.f : fast_exp2(m[t][i] - mx);
+              m[t][i] = mx;
+              l[t][i] *= alpha;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                o[t][j][i] *= alpha * down;
+                o[t][j][i + 2] *= alpha * down;
+              }
+            }
+        }
+        // 2^6 s_v over the largest factor
+        const float unit_v = __uint_as_float((254u - (vtop >> 23)) << 23);
+        const float w0 = sv0 * unit_v * 64.f, w1 = sv1 * unit_v * 64.f;
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ref = m[t][e & 1];
+            y[e] = fast_exp2(z[t][e] - (ref == -INFINITY ? 0.f : ref));
+            l[t][e & 1] += y[e];
+          }
+          p[t][0] = transposed(half2_of(y[0] * w0, y[1] * w0));
+          p[t][1] = transposed(half2_of(y[2] * w1, y[3] * w1));
+        }
+        uint32_t xv[4][VW];                         // tokens 2 q4, + 1, + 8, + 9
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t t = 2 * q4 + (n & 1) + (n >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 y = *reinterpret_cast<const uint4*>(at + R::kPool + unit_at<D>(t, r));
+            xv[n][0] = y.x; xv[n][1] = y.y; xv[n][2] = y.z; xv[n][3] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(at + R::kPool + unit_at<D>(t, r >> 1) + (r & 1) * 8);
+            xv[n][0] = y.x; xv[n][1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2) {
+            const uint32_t sel = i2 ? 0x7362u : 0x5140u;      // (token, next token) x two bytes
+            const uint32_t lo = __byte_perm(xv[0][w], xv[1][w], sel), hi = __byte_perm(xv[2][w], xv[3][w], sel);
+            const uint32_t a0 = kv8::e4m3x2_to_half2((uint16_t)lo), a1 = kv8::e4m3x2_to_half2((uint16_t)(lo >> 16));
+            const uint32_t a2 = kv8::e4m3x2_to_half2((uint16_t)hi), a3 = kv8::e4m3x2_to_half2((uint16_t)(hi >> 16));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + i2], a0, a1, a2, a3, p[t][0], p[t][1]);
+          }
+      }
+      cp_async_wait<0>();
+      __syncwarp();                                             // (the ring is free for the next unit)
+
+      // ---- this part of the unit: the warps' results joined in shared memory
+      const float back = __uint_as_float(vtop) * (1.f / 64.f);
+      const bool whole = blk0 == 0 && blk1 == per_unit;
+      const size_t slot = part_slot(piece, blk0 == 0), row0 = (size_t)b * a.H + (size_t)g * G;
+      float* joined = reinterpret_cast<float*>(ring);          // [G][D], then (m, l)
+      static_assert(16 * (D + 2) * 4 <= R::kFactors, "a warp's rows fit its ring");
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = 8 * t + 2 * q4 + i;
+          float s = l[t][i];
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          s += __shfl_xor_sync(0xffffffffu, s, 8);
+          s += __shfl_xor_sync(0xffffffffu, s, 16);
+          if (h >= G) continue;
+          float* dst = joined + h * D + r * VB;
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+            *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back, o[t][j][i + 2] * back);
+          if (r == 0) reinterpret_cast<float2*>(joined + G * D)[h] = make_float2(m[t][i], s);
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < G * D / 2; i += kWarps * 32) {
+        const int h = i / (D / 2), e = 2 * i - h * D;
+        float M = -INFINITY, L = 0.f;
+        float2 v = make_float2(0.f, 0.f), ml[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          ml[w] = reinterpret_cast<const float2*>(smem + w * R::kBytes + G * D * 4)[h];
+          M = fmaxf(M, ml[w].x);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ml[w].x == -INFINITY ? 0.f : fast_exp2(ml[w].x - M);
+          const float2 y = reinterpret_cast<const float2*>(smem + w * R::kBytes)[i];
+          L = fmaf(ml[w].y, f, L);                              // (a NaN stays)
+          v.x = fmaf(f, y.x, v.x);
+          v.y = fmaf(f, y.y, v.y);
+        }
+        if (whole) {
+          write_pair<D>(a, row0 + h, e, M, L, v);
         } else {
-          const uint2 y = *reinterpret_cast<const uint2*>(at + R::kPool + unit_at<D>(t, r >> 1) + (r & 1) * 8);
-          xv[n][0] = y.x; xv[n][1] = y.y;
+          *reinterpret_cast<float2*>(a.part_o + (slot * G + h) * D + e) = v;
+          if (e == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(M, L);
         }
       }
-#pragma unroll
-      for (int w = 0; w < VW; ++w)
-#pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const uint32_t sel = i2 ? 0x7362u : 0x5140u;      // (token, next token) x two bytes
-          const uint32_t lo = __byte_perm(xv[0][w], xv[1][w], sel), hi = __byte_perm(xv[2][w], xv[3][w], sel);
-          const uint32_t a0 = kv8::e4m3x2_to_half2((uint16_t)lo), a1 = kv8::e4m3x2_to_half2((uint16_t)(lo >> 16));
-          const uint32_t a2 = kv8::e4m3x2_to_half2((uint16_t)hi), a3 = kv8::e4m3x2_to_half2((uint16_t)(hi >> 16));
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + i2], a0, a1, a2, a3, p[t][0], p[t][1]);
+      // (and the rings are free for the next unit)
+      const bool join = !whole && a.split_done != nullptr;
+      if (join) __threadfence();
+      __syncthreads();
+      if (!join) continue;
+
+      // ---- the last CTA of a unit joins its pieces
+      const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
+      const int p0 = kv8::piece_of(total, start, C), n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
+      int* done = a.split_done + b * a.Hkv + g;
+      __shared__ int last;
+      if (threadIdx.x == 0) {
+        last = atomicAdd(done, 1) == n - 1;
+        if (last) *done = 0;                                    // ready for the next call
+      }
+      __syncthreads();
+      if (last) {
+        __threadfence();
+        for (int i = threadIdx.x; i < G * D / 2; i += kWarps * 32) {
+          const int h = i / (D / 2), e = 2 * i - h * D;
+          float M, L;
+          float2 v;
+          gather_pieces<D>(a, p0, n, 0, 1, h, e, M, L, v);
+          write_pair<D>(a, row0 + h, e, M, L, v);
         }
-  }
-  cp_async_wait<0>();
-  __syncwarp();                                             // (the ring is free for the next unit)
-
-  // ---- this part of the unit: the warps' results joined in shared memory
-  const float back = __uint_as_float(vtop) * (1.f / 64.f);
-  const bool whole = blk0 == 0 && blk1 == per_unit;
-  const size_t slot = part_slot(piece, blk0 == 0), row0 = (size_t)b * a.H + (size_t)g * G;
-  float* joined = reinterpret_cast<float*>(ring);          // [G][D], then (m, l)
-  static_assert(16 * (D + 2) * 4 <= R::kFactors, "a warp's rows fit its ring");
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int h = 8 * t + 2 * q4 + i;
-      float s = l[t][i];
-      s += __shfl_xor_sync(0xffffffffu, s, 4);
-      s += __shfl_xor_sync(0xffffffffu, s, 8);
-      s += __shfl_xor_sync(0xffffffffu, s, 16);
-      if (h >= G) continue;
-      float* dst = joined + h * D + r * VB;
-#pragma unroll
-      for (int j = 0; j < KS; ++j)
-        *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back, o[t][j][i + 2] * back);
-      if (r == 0) reinterpret_cast<float2*>(joined + G * D)[h] = make_float2(m[t][i], s);
+      }
+      __syncthreads();                                          // (`last` is free)
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < G * D / 2; i += kWarps * 32) {
-    const int h = i / (D / 2), e = 2 * i - h * D;
-    float M = -INFINITY, L = 0.f;
-    float2 v = make_float2(0.f, 0.f), ml[kWarps];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      ml[w] = reinterpret_cast<const float2*>(smem + w * R::kBytes + G * D * 4)[h];
-      M = fmaxf(M, ml[w].x);
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ml[w].x == -INFINITY ? 0.f : fast_exp2(ml[w].x - M);
-      const float2 y = reinterpret_cast<const float2*>(smem + w * R::kBytes)[i];
-      L = fmaf(ml[w].y, f, L);                              // (a NaN stays)
-      v.x = fmaf(f, y.x, v.x);
-      v.y = fmaf(f, y.y, v.y);
-    }
-    if (whole) {
-      write_pair<D>(a, row0 + h, e, M, L, v);
-    } else {
-      *reinterpret_cast<float2*>(a.part_o + (slot * G + h) * D + e) = v;
-      if (e == 0) reinterpret_cast<float2*>(a.part_ml)[slot * G + h] = make_float2(M, L);
-    }
-  }
-  // (and the rings are free for the next unit)
-  const bool join = !whole && a.split_done != nullptr;
-  if (join) __threadfence();
-  __syncthreads();
-  if (!join) continue;
-
-  // ---- the last CTA of a unit joins its pieces
-  const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit;
-  const int p0 = kv8::piece_of(total, start, C), n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
-  int* done = a.split_done + b * a.Hkv + g;
-  __shared__ int last;
-  if (threadIdx.x == 0) {
-    last = atomicAdd(done, 1) == n - 1;
-    if (last) *done = 0;                                    // ready for the next call
-  }
-  __syncthreads();
-  if (last) {
-    __threadfence();
-    for (int i = threadIdx.x; i < G * D / 2; i += kWarps * 32) {
-      const int h = i / (D / 2), e = 2 * i - h * D;
-      float M, L;
-      float2 v;
-      gather_pieces<D>(a, p0, n, 0, 1, h, e, M, L, v);
-      write_pair<D>(a, row0 + h, e, M, L, v);
-    }
-  }
-  __syncthreads();                                          // (`last` is free)
-  }
-  before += in_seq;
+    before += in_seq;
   }
 }
 

@@ -19,9 +19,10 @@
 //
 // Measured, keys out of L2, head dim 128: 16 sequences of 32 KV heads and 2880 keys
 // 46.1 us (4.3 TB/s of keys), 8 ragged ones of 4 heads and up to 50176 keys 51.6 us
-// (3.1 TB/s); 193 question rows of 28 heads over 4 and 576 keys 13.7 us.  Scoring takes 37 and 36 us of it by itself: with a page in flight in each of
-// 40 warps an SM pages go by at 6.2 TB/s, and 17 % of an SM's time lies before its first
-// page and behind its last.  More pages on their way are no faster (two in registers of
+// (3.1 TB/s); 193 question rows of 28 heads over 4 and 576 keys 13.7 us.  Scoring takes
+// 37 and 36 us of the first two by itself: with a page in flight in each of 40 warps an
+// SM pages go by at 6.2 TB/s, and 17 % of an SM's time lies before its first page and
+// behind its last.  More pages on their way are no faster (two in registers of
 // 24 warps 48.3 / 54.5, of 32 warps with spills 62.7 / 61.5; two or three in a cp.async
 // ring of 32 warps 51.0 / 56.8 and 56.4 / 56.7), nor are packed adds; two and four times
 // the CTAs 48.8 / 56.8 and 52.6 / 65.6; equal shares of each row instead of one line
@@ -127,7 +128,8 @@ __device__ __forceinline__ void write_query(float hi, float lo, Query8<D>* o) {
   // the largest element comes to lie in [2^14, 2^15), by two factors as 2^(14 - e) may
   // be out of range
   const int x = (int)(__float_as_uint(top) >> 23) - 127 - 14;
-  const float f0 = __uint_as_float((uint32_t)(127 - x / 2) << 23), f1 = __uint_as_float((uint32_t)(127 - (x - x / 2)) << 23);
+  const float f0 = __uint_as_float((uint32_t)(127 - x / 2) << 23);
+  const float f1 = __uint_as_float((uint32_t)(127 - (x - x / 2)) << 23);
   float h = hi * f0 * f1, l = lo * f0 * f1;
   o->qbar[e] = make_float2(hi, lo);
 #pragma unroll
@@ -292,7 +294,8 @@ __device__ __forceinline__ uint32_t scan_pages(const Kv8RetrieveArgs& a, int b0,
   return inc;
 }
 // The line's length and, where b < batch, what lies before sequence b.
-__device__ __forceinline__ uint32_t line_of(const Kv8RetrieveArgs& a, const Parts& parts, int b, int lane, uint32_t& before) {
+__device__ __forceinline__ uint32_t line_of(const Kv8RetrieveArgs& a, const Parts& parts, int b, int lane,
+                                            uint32_t& before) {
   if (!a.lens.any()) {
     before = (uint32_t)b * (uint32_t)a.Hkv * (uint32_t)parts.pages;
     return (uint32_t)a.batch * (uint32_t)a.Hkv * (uint32_t)parts.pages;
@@ -311,7 +314,8 @@ __device__ __forceinline__ uint32_t line_of(const Kv8RetrieveArgs& a, const Part
 // leaves the sum for the selection).
 template <int D, bool SUM>
 __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas)
-kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, float* __restrict__ scores, const Parts parts) {
+kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, float* __restrict__ scores,
+                 const Parts parts) {
   constexpr int KS = D / 16, KC = D / 64, W = kScoreWarps;
   __shared__ __align__(16) Query8<D> query;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q4 = lane & 3;
@@ -353,100 +357,101 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
 
 #pragma unroll 1
   for (; left > 0; ++b, off = 0) {
-  int nv, nt, kb;
-  seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, nv, nt, kb);
-  const int pages = (nv + 15) >> 4;
+    int nv, nt, kb;
+    seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, nv, nt, kb);
+    const int pages = (nv + 15) >> 4;
 #pragma unroll 1
-  while (left > 0 && off < (uint32_t)pages * (uint32_t)a.Hkv) {
-  const int g = (int)(off / (uint32_t)pages), row = b * a.Hkv + g, p0 = (int)off - g * pages, end = min(pages, p0 + left);
-  off += end - p0;
-  left -= end - p0;
-  const int first = p0 + warp;
-  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
-  uint4 k[2][KC];            // keys r and r + 8
-  float factor = 0.f;
-  bool ok = false;
-  // (the page's id was asked for a page of this warp before)
-  auto id_of = [&](int p) { return p < end ? __ldg(bt + p) : -1; };
-  auto load = [&](int p, int page) {
-    ok = page >= 0 && page < a.num_blocks;
-    if (!ok) {
-      if (p < end && lane == 0) flag_status(a.status, kStatusBadBlock);
-      return;
-    }
-    const size_t unit = (size_t)page * a.Hkv + g;
-    const uint8_t* src = a.k_pool + (unit * 16 + r) * D + q4 * 16;
+    while (left > 0 && off < (uint32_t)pages * (uint32_t)a.Hkv) {
+      const int g = (int)(off / (uint32_t)pages), row = b * a.Hkv + g;
+      const int p0 = (int)off - g * pages, end = min(pages, p0 + left);
+      off += end - p0;
+      left -= end - p0;
+      const int first = p0 + warp;
+      const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+      uint4 k[2][KC];            // keys r and r + 8
+      float factor = 0.f;
+      bool ok = false;
+      // (the page's id was asked for a page of this warp before)
+      auto id_of = [&](int p) { return p < end ? __ldg(bt + p) : -1; };
+      auto load = [&](int p, int page) {
+        ok = page >= 0 && page < a.num_blocks;
+        if (!ok) {
+          if (p < end && lane == 0) flag_status(a.status, kStatusBadBlock);
+          return;
+        }
+        const size_t unit = (size_t)page * a.Hkv + g;
+        const uint8_t* src = a.k_pool + (unit * 16 + r) * D + q4 * 16;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < KC; ++c) k[i][c] = ld_stream16(src + i * 8 * D + c * 64);
-    factor = __ldg(a.scales + unit * 2);
-  };
-  int next = id_of(first);
-  load(first, next);
-  next = id_of(first + W);
-  __syncthreads();                         // (the query of the row before has been read)
-  if constexpr (SUM) {
-    sum_query<D>(static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, row, &query);
-    __syncthreads();
-    if (p0 == 0)
-      for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
-        reinterpret_cast<uint4*>(rows + row)[i] = reinterpret_cast<const uint4*>(&query)[i];
-  } else {
-    for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
-      reinterpret_cast<uint4*>(&query)[i] = reinterpret_cast<const uint4*>(rows + row)[i];
-    __syncthreads();
-  }
-  // (the query's parts: column r of a tile is part r, the columns behind are 0)
-  const uint16_t* part = &query.part[min(r, 3)][q4 * 16];
-  float* out = scores + (size_t)row * a.n_vis;
-  Part mine = {0.f, 0xffffffffu, 0u, 0u};
-  for (int p = first; p < end; p += W) {
-    float c[4] = {};
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&k[0][i >> 2]);
-      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&k[1][i >> 2]);
-      const uint32_t y0 = w0[i & 3], y1 = w1[i & 3];
-      const uint2 q = *reinterpret_cast<const uint2*>(part + (i >> 2) * 64 + (i & 3) * 4);
-      float z[4] = {};         // (a chain of tiles would lose bits beside their running sum)
-      mma_f16(z, kv8::e4m3x2_to_half2((uint16_t)y0), kv8::e4m3x2_to_half2((uint16_t)y1),
-              kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16)), q.x, q.y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = __fadd_rn(c[e], z[e]);
-    }
-    const bool there = ok;
-    const float f = factor;
-    load(p + W, next);
-    next = id_of(p + 2 * W);
-    // columns 0 and 1 are lane 4 r's, column 2 is its neighbour's
-    const float z0 = __shfl_down_sync(0xffffffffu, c[0], 1), z1 = __shfl_down_sync(0xffffffffu, c[2], 1);
-    const float s0 = c[0] + (c[1] + z0), s1 = c[2] + (c[3] + z1);
-    const int pos = p * 16 + r;
-    if (q4 == 0) {
-      // (NaN without a sign, so that its key is the largest)
-      auto value = [&](float v) {
-        v = (v * query.back[0]) * (f * query.back[1]);
-        return !there ? 0.f : isnan(v) ? __uint_as_float(0x7fffffffu) : v;
+          for (int c = 0; c < KC; ++c) k[i][c] = ld_stream16(src + i * 8 * D + c * 64);
+        factor = __ldg(a.scales + unit * 2);
       };
-      auto put = [&](int at, float v) {
-        if (at >= nv) return;
-        out[at] = v;
-        mine.lo = min(mine.lo, order_key(v));
-        mine.hi = max(mine.hi, order_key(v));
-      };
-      put(pos, value(s0));
-      put(pos + 8, value(s1));
+      int next = id_of(first);
+      load(first, next);
+      next = id_of(first + W);
+      __syncthreads();                         // (the query of the row before has been read)
+      if constexpr (SUM) {
+        sum_query<D>(static_cast<const uint16_t*>(a.q), a.R, a.H, a.Hkv, row, &query);
+        __syncthreads();
+        if (p0 == 0)
+          for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
+            reinterpret_cast<uint4*>(rows + row)[i] = reinterpret_cast<const uint4*>(&query)[i];
+      } else {
+        for (int i = threadIdx.x; i < (int)(sizeof(Query8<D>) / 16); i += W * 32)
+          reinterpret_cast<uint4*>(&query)[i] = reinterpret_cast<const uint4*>(rows + row)[i];
+        __syncthreads();
+      }
+      // (the query's parts: column r of a tile is part r, the columns behind are 0)
+      const uint16_t* part = &query.part[min(r, 3)][q4 * 16];
+      float* out = scores + (size_t)row * a.n_vis;
+      Part mine = {0.f, 0xffffffffu, 0u, 0u};
+      for (int p = first; p < end; p += W) {
+        float c[4] = {};
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&k[0][i >> 2]);
+          const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&k[1][i >> 2]);
+          const uint32_t y0 = w0[i & 3], y1 = w1[i & 3];
+          const uint2 q = *reinterpret_cast<const uint2*>(part + (i >> 2) * 64 + (i & 3) * 4);
+          float z[4] = {};         // (a chain of tiles would lose bits beside their running sum)
+          mma_f16(z, kv8::e4m3x2_to_half2((uint16_t)y0), kv8::e4m3x2_to_half2((uint16_t)y1),
+                  kv8::e4m3x2_to_half2((uint16_t)(y0 >> 16)), kv8::e4m3x2_to_half2((uint16_t)(y1 >> 16)), q.x, q.y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[e] = __fadd_rn(c[e], z[e]);
+        }
+        const bool there = ok;
+        const float f = factor;
+        load(p + W, next);
+        next = id_of(p + 2 * W);
+        // columns 0 and 1 are lane 4 r's, column 2 is its neighbour's
+        const float z0 = __shfl_down_sync(0xffffffffu, c[0], 1), z1 = __shfl_down_sync(0xffffffffu, c[2], 1);
+        const float s0 = c[0] + (c[1] + z0), s1 = c[2] + (c[3] + z1);
+        const int pos = p * 16 + r;
+        if (q4 == 0) {
+          // (NaN without a sign, so that its key is the largest)
+          auto value = [&](float v) {
+            v = (v * query.back[0]) * (f * query.back[1]);
+            return !there ? 0.f : isnan(v) ? __uint_as_float(0x7fffffffu) : v;
+          };
+          auto put = [&](int at, float v) {
+            if (at >= nv) return;
+            out[at] = v;
+            mine.lo = min(mine.lo, order_key(v));
+            mine.hi = max(mine.hi, order_key(v));
+          };
+          put(pos, value(s0));
+          put(pos + 8, value(s1));
+        }
+        if (there) mine.factor = fmaxf(mine.factor, fabsf(f));
+      }
+      mine.lo = __reduce_min_sync(0xffffffffu, mine.lo);
+      mine.hi = __reduce_max_sync(0xffffffffu, mine.hi);
+      Part* to = p0 == 0 && end == pages ? parts.whole + (size_t)row * W
+                                         : parts.cut + ((size_t)blockIdx.x * 2 + (p0 == 0)) * W;
+      if (lane == 0)
+        *reinterpret_cast<uint4*>(to + warp) = make_uint4(__float_as_uint(mine.factor), mine.lo, mine.hi, 0u);
     }
-    if (there) mine.factor = fmaxf(mine.factor, fabsf(f));
-  }
-  mine.lo = __reduce_min_sync(0xffffffffu, mine.lo);
-  mine.hi = __reduce_max_sync(0xffffffffu, mine.hi);
-  Part* to = p0 == 0 && end == pages ? parts.whole + (size_t)row * W
-                                     : parts.cut + ((size_t)blockIdx.x * 2 + (p0 == 0)) * W;
-  if (lane == 0)
-    *reinterpret_cast<uint4*>(to + warp) = make_uint4(__float_as_uint(mine.factor), mine.lo, mine.hi, 0u);
-  }
   }
 }
 
@@ -463,10 +468,8 @@ struct __align__(16) SelectShared {
   uint32_t key[kListed];                   // (16-byte aligned)
   int inside[kListed];                     // those of `all` that fp32 cannot tell
   int hist[kBins], coarse[32];
-  int sure, near;                          // (read together by other CTAs)
+  int sure, near;                          // this CTA's tokens above the border, and next to it
   int bin, count, clear, n_inside, kept;
-  unsigned long long last;
-  int last_j;
   uint32_t kth, lo[32], hi[32], scan[32];
   float factor[32];
 };
@@ -739,7 +742,8 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
     before = __reduce_add_sync(0xffffffffu, lane < rank ? their_sure : 0);
     m = __reduce_add_sync(0xffffffffu, theirs);
     if (m <= kListed && warp < C) {
-      const int at = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0), count = __shfl_sync(0xffffffffu, theirs, warp);
+      const int at = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0);
+      const int count = __shfl_sync(0xffffffffu, theirs, warp);
       const uint2* from = cluster.map_shared_rank(sh.mine, warp);
       for (int i = lane; i < count; i += 32) all[at + i] = from[i];
     }
@@ -886,7 +890,8 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
       else atomicAdd(&sh.kept, 1);
     }
     sync();
-    if constexpr (C > 1) before += __reduce_add_sync(0xffffffffu, lane < rank ? *cluster.map_shared_rank(&sh.kept, lane) : 0);
+    if constexpr (C > 1)
+      before += __reduce_add_sync(0xffffffffu, lane < rank ? *cluster.map_shared_rank(&sh.kept, lane) : 0);
   }
   if constexpr (C > 1) {
     if (listed) {
@@ -975,7 +980,7 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
   Parts parts;
   parts.pages = (a.n_vis + 15) / 16;
   const long long pages = (long long)parts.pages * rows;
-  parts.ctas = (int)std::min<long long>(std::min((long long)num_sms * kScoreCtas, (long long)kMostCtas), (pages + kScoreWarps - 1) / kScoreWarps);
+  parts.ctas = (int)std::min<long long>(std::min(num_sms * kScoreCtas, kMostCtas), (pages + kScoreWarps - 1) / kScoreWarps);
   parts.whole = reinterpret_cast<Part*>(take((size_t)rows * kScoreWarps * sizeof(Part)));
   parts.cut = reinterpret_cast<Part*>(take((size_t)kMostCtas * 2 * kScoreWarps * sizeof(Part)));
   uint32_t* far_keys = reinterpret_cast<uint32_t*>(at);      // (there where it is used)
