@@ -460,6 +460,7 @@ namespace {
 constexpr int kCluster = 8, kClusterThreads = 512;   // of a long row's selection
 constexpr int kBins = 2048;
 constexpr int kCrowd = 320, kPasses = 4;   // a border's bin of more keys is cut again, up to so often
+constexpr int kMany = 320;                 // tokens next to the border whose factors are worth a look
 constexpr int kListed = 512;               // tokens next to the border that are ranked in shared memory
 
 struct __align__(16) SelectShared {
@@ -469,7 +470,7 @@ struct __align__(16) SelectShared {
   int inside[kListed];                     // those of `all` that fp32 cannot tell
   int hist[kBins], coarse[32];
   int sure, near;                          // this CTA's tokens above the border, and next to it
-  int bin, count, clear, n_inside, kept;
+  int bin, count, clear, n_inside, kept, top;
   uint32_t kth, lo[32], hi[32], scan[32];
   float factor[32];
 };
@@ -594,11 +595,13 @@ struct Cut {
     if (t >= 0.f && t < (float)(kBins - 1)) atomicAdd(&hist[(int)t], 1);
   }
 };
+struct Bin {
+  float lo, hi;
+};
 template <typename Total, typename Sync>
-__device__ __forceinline__ Near near_border(const uint32_t* keys, int n, int k, const Part& row, Cut cut, int above,
-                                            float band, SelectShared& sh, Total total, Sync sync) {
+__device__ __forceinline__ Bin border_bin(const uint32_t* keys, int n, int k, Cut cut, int above,
+                                          SelectShared& sh, Total total, Sync sync) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  if (!cut.ok) return Near{row.lo, row.hi};
   const float bottom = cut.lo, top = cut.hi;
   for (int pass = 0;; ++pass) {
     above = __reduce_add_sync(0xffffffffu, above);
@@ -640,7 +643,7 @@ __device__ __forceinline__ Near near_border(const uint32_t* keys, int n, int k, 
     cut.hi = bin == kBins - 1 ? top : fminf(top, fmaf((float)(bin + 1), width, from) + cut.slop);
     cut.inv = (float)kBins / (cut.hi - cut.lo);
     if (sh.count <= kCrowd || pass == kPasses - 1 || cut.hi - cut.lo < 8.f * cut.slop || !isfinite(cut.inv))
-      return near_values(cut.lo, cut.hi, band);
+      return Bin{cut.lo, cut.hi};
     sync();                                                 // (the counts have been read)
     for (int i = tid; i < kBins; i += nt) sh.hist[i] = 0;
     __syncthreads();
@@ -673,7 +676,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
     for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(p, r);
     return sum;
   };
-  if (tid == 0) sh.sure = sh.near = sh.clear = sh.n_inside = sh.kept = 0;
+  if (tid == 0) sh.sure = sh.near = sh.clear = sh.n_inside = sh.kept = sh.top = 0;
   for (int i = tid; i < kBins; i += nt) sh.hist[i] = 0;
   // The lengths are read before the wait for the scores: that kernel writes none, and
   // let this one begin only when those before it had completed.
@@ -711,36 +714,69 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
   const float some = query->slack * kBand * whole.factor;
   // without a band (or with scores that are not finite) the fp32 order decides
   const bool wide = some > 0.f && isfinite(some) && isfinite(value_of(whole.hi) - value_of(whole.lo));
-  const float band = wide ? some : 0.f;
-  const Near near = near_border(keys, len, k, whole, cut, above, band, sh, total, sync);
-  const uint32_t lo = near.lo, hi = near.hi;
+  float band = wide ? some : 0.f;
+  Bin bin = {0.f, 0.f};
+  if (cut.ok) bin = border_bin(keys, len, k, cut, above, sh, total, sync);
+  Near near = cut.ok ? near_values(bin.lo, bin.hi, band) : Near{whole.lo, whole.hi};
 
   // ---- the tokens next to the border, of every CTA
-  int in = 0;
-  for (int i0 = tid; i0 < len; i0 += 4 * nt) {
-    uint32_t key[4];
+  int sure, m, their_sure = 0, theirs = 0;                  // (of CTA `lane`)
+  auto find_near = [&] {
+    int in = 0;
+    for (int i0 = tid; i0 < len; i0 += 4 * nt) {
+      uint32_t key[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) key[j] = i0 + j * nt < len ? keys[i0 + j * nt] : 0u;
+      for (int j = 0; j < 4; ++j) key[j] = i0 + j * nt < len ? keys[i0 + j * nt] : 0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      in += key[j] > hi;
-      if (key[j] >= lo && key[j] <= hi) {
-        const int to = atomicAdd(&sh.near, 1);
-        if (to < kListed) sh.mine[to] = make_uint2(key[j], (uint32_t)(first + i0 + j * nt));
+      for (int j = 0; j < 4; ++j) {
+        in += key[j] > near.hi;
+        if (key[j] >= near.lo && key[j] <= near.hi) {
+          const int to = atomicAdd(&sh.near, 1);
+          if (to < kListed) sh.mine[to] = make_uint2(key[j], (uint32_t)(first + i0 + j * nt));
+        }
       }
     }
+    in = __reduce_add_sync(0xffffffffu, in);
+    if (lane == 0 && in > 0) atomicAdd(&sh.sure, in);
+    sync();
+    if constexpr (C > 1) {
+      their_sure = lane < C ? *cluster.map_shared_rank(&sh.sure, lane) : 0;
+      theirs = lane < C ? *cluster.map_shared_rank(&sh.near, lane) : 0;
+      sure = __reduce_add_sync(0xffffffffu, their_sure);
+      m = __reduce_add_sync(0xffffffffu, theirs);
+    } else {
+      sure = sh.sure;
+      m = sh.near;
+    }
+  };
+  find_near();
+  if (m > kMany && cut.ok && band > 0.f) {
+    // Many.  The k-th score is one of theirs, so only their factors count for the error,
+    // not the largest of the row (of a page whose scores lie elsewhere).
+    float factor = 0.f;
+    for (int i = tid; i < len; i += nt) {
+      if (keys[i] < near.lo || keys[i] > near.hi) continue;
+      const int page = __ldg(a.block_table + (size_t)b * a.max_blocks + ((first + i) >> 4));
+      if (page >= 0 && page < a.num_blocks) factor = fmaxf(factor, fabsf(__ldg(a.scales + ((size_t)page * a.Hkv + g) * 2)));
+    }
+    factor = warp_max(factor);
+    if (lane == 0) atomicMax(&sh.top, __float_as_int(factor));         // (not negative)
+    sync();                                                 // (and the counts have been read)
+    int top = sh.top;
+    if constexpr (C > 1) top = __reduce_max_sync(0xffffffffu, lane < C ? *cluster.map_shared_rank(&sh.top, lane) : 0);
+    if (__int_as_float(top) < 0.5f * whole.factor) {
+      band = query->slack * kBand * __int_as_float(top);
+      near = near_values(bin.lo, bin.hi, band);
+      if (tid == 0) sh.sure = sh.near = 0;
+      __syncthreads();
+      find_near();
+    }
   }
-  in = __reduce_add_sync(0xffffffffu, in);
-  if (lane == 0 && in > 0) atomicAdd(&sh.sure, in);
-  sync();
-  int sure = sh.sure, m = sh.near, before = 0;              // (before: taken by CTAs of lower rank)
+  const uint32_t lo = near.lo, hi = near.hi;
   uint2* const all = C > 1 ? sh.all : sh.mine;
+  int before = 0;                                           // taken by CTAs of lower rank
   if constexpr (C > 1) {
-    const int their_sure = lane < C ? *cluster.map_shared_rank(&sh.sure, lane) : 0;
-    const int theirs = lane < C ? *cluster.map_shared_rank(&sh.near, lane) : 0;
-    sure = __reduce_add_sync(0xffffffffu, their_sure);
     before = __reduce_add_sync(0xffffffffu, lane < rank ? their_sure : 0);
-    m = __reduce_add_sync(0xffffffffu, theirs);
     if (m <= kListed && warp < C) {
       const int at = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0);
       const int count = __shfl_sync(0xffffffffu, theirs, warp);
