@@ -277,3 +277,26 @@ def test_programmatic_launch_does_not_change_a_run(lib, tmp_path):
     for key, t in runs[0].items():
         assert torch.equal(t, runs[1][key]), key
         assert t.float().abs().max() > 0, key
+
+
+def test_many_ragged_sequences(lib):
+    """3001 sequences of 0 to 40 tokens: each row's own selection and attention."""
+    from visual_token_sparsity_gb300 import binding as sv
+    B, H, Hkv, d, n_vis, n_text, k = 3001, 4, 1, 64, 33, 7, 9
+    g = np.random.default_rng(5)
+    nv, nt = g.integers(0, n_vis + 1, B), g.integers(0, n_text + 1, B)
+    ks = np.minimum(nv, g.integers(0, k + 1, B))
+    c = Cache8(B, Hkv, d, n_vis + n_text, seed=91)
+    layer, seqs = c.layer(), sv.SeqBatch(c.bt.to(DEV), n_vis, n_text, i32(nv), i32(nt), i32(ks))
+    q = synth.normal_bf16((B, 1, H, d), 17).to(DEV)
+    vis = torch.full((B, Hkv, k), -7, dtype=torch.int32, device=DEV)
+    out, lse = torch.full((B, H, d), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((B, H), 7.0, device=DEV)
+    ws = sv.workspace(max(sv.sv_kv8_retrieve_workspace_bytes(B, H, Hkv, d, n_vis, k),
+                          sv.sv_kv8_attn_workspace_bytes(B, H, Hkv, d, k + n_text)))
+    sv.sv_kv8_retrieve_topk(q, layer, seqs, k, vis, None, ws)
+    sv.sv_kv8_decode_attn(q[:, 0], 0.125, layer, seqs, vis, k, out, lse, ws)
+    assert sv.sv_read_device_status(ws) == 0
+    K, V, got = c.rows(0), c.rows(1), vis.cpu().numpy()
+    want, _ = oracle_select(q, K, nv.tolist(), ks.tolist())
+    assert np.array_equal(got[..., : want.shape[2]], want) and (got[..., want.shape[2]:] == -1).all()
+    assert_close(out, lse, *oracle_decode(q[:, 0], K, V, got, nv.tolist(), nt.tolist(), ks.tolist(), 0.125), KV8_WEIGHTS)

@@ -125,13 +125,6 @@ __device__ __forceinline__ uint32_t scan_blocks(const Kv8AttnArgs& a, int b0, in
   }
   return inc;
 }
-// With equal counts the host has laid the line out (a.per_unit blocks a unit).
-__device__ __forceinline__ uint32_t line_total(const Kv8AttnArgs& a, int lane) {
-  uint32_t total = 0, mine;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) total += __shfl_sync(0xffffffffu, scan_blocks(a, b0, lane, mine), 31);
-  return total;
-}
-
 // Piece `piece` of the line: its first block, its length, and the sequence that it
 // begins in with the blocks before that one.
 struct Piece {
@@ -606,29 +599,37 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
   __shared__ float2 part[kParts][kPer], part_ml[kParts];
   const int G = a.H / a.Hkv, lane = threadIdx.x & 31;
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, g = h / G;
-  // The lengths are read before the wait for the attention: it writes none, and let
-  // this kernel begin only when those before it had completed.
-  Seq s;
-  seq_of(a, b, s);
-  const int per_unit = s.blocks();
-  uint32_t before = 0, total;
-  if (!a.lens.any()) {
-    before = (uint32_t)b * (uint32_t)per_unit * (uint32_t)a.Hkv;
-    total = (uint32_t)a.batch * (uint32_t)per_unit * (uint32_t)a.Hkv;
-  } else {
-    total = line_total(a, lane);
-    for (int b0 = 0; b0 <= b; b0 += 32) {
-      uint32_t mine;
-      const uint32_t inc = scan_blocks(a, b0, lane, mine);
-      before += b - b0 < 32 ? __shfl_sync(0xffffffffu, inc - mine, b - b0) : __shfl_sync(0xffffffffu, inc, 31);
+  // The lengths are read before the wait for the attention (it writes none, and let
+  // this kernel begin only when those before it had completed), by one warp, as it
+  // looks at all sequences.
+  __shared__ int2 pieces;                                   // the first of the unit's, and their number
+  if (threadIdx.x < 32) {
+    Seq s;
+    seq_of(a, b, s);
+    const int per_unit = s.blocks();
+    uint32_t before = 0, total;
+    if (!a.lens.any()) {
+      before = (uint32_t)b * (uint32_t)per_unit * (uint32_t)a.Hkv;
+      total = (uint32_t)a.batch * (uint32_t)per_unit * (uint32_t)a.Hkv;
+    } else {
+      total = 0;
+      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        uint32_t mine;
+        const uint32_t inc = scan_blocks(a, b0, lane, mine);
+        if (b >= b0 && b < b0 + 32) before = total + __shfl_sync(0xffffffffu, inc - mine, b - b0);
+        total += __shfl_sync(0xffffffffu, inc, 31);
+      }
     }
+    const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
+    int2 p = make_int2(0, 0);
+    if (per_unit > 0) {
+      p.x = kv8::piece_of(total, start, C);
+      p.y = kv8::piece_of(total, start + per_unit - 1, C) - p.x + 1;
+    }
+    if (lane == 0) pieces = p;
   }
-  const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
-  int p0 = 0, n = 0;
-  if (per_unit > 0) {
-    p0 = kv8::piece_of(total, start, C);
-    n = kv8::piece_of(total, start + per_unit - 1, C) - p0 + 1;
-  }
+  __syncthreads();
+  const int p0 = pieces.x, n = pieces.y;
   grid_dep_sync();
   if (n <= 1) return;                                       // (no token, or not cut)
   const int w = threadIdx.x / kPer, i = threadIdx.x - w * kPer;

@@ -473,6 +473,7 @@ struct __align__(16) SelectShared {
   int bin, count, clear, n_inside, kept, top;
   uint32_t kth, lo[32], hi[32], scan[32];
   float factor[32];
+  int2 by;
 };
 
 // The first and the last CTA that scored pages of a row of n > 0 keys.
@@ -682,7 +683,11 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
   // let this one begin only when those before it had completed.
   int n = a.n_vis, k = a.k;
   if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
-  const int2 by = n > 0 ? scorers_of(a, parts, row, n, lane) : make_int2(0, 0);
+  if (warp == 0 && n > 0) {                  // (by one warp: it looks at all sequences)
+    const int2 by = scorers_of(a, parts, row, n, lane);
+    if (lane == 0) sh.by = by;
+  }
+  __syncthreads();
   grid_dep_sync();
   int32_t* dst = a.vis_idx + (size_t)row * a.k;
   if (rank == 0) fill_unselected(dst, k, a.k);
@@ -697,7 +702,7 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
   };
   load(tid);
   const Query8<D>* query = rows + row;
-  const Part whole = whole_row(parts, row, by, sh);
+  const Part whole = whole_row(parts, row, sh.by, sh);
   const Cut cut(whole);
   int above = 0;
   for (int i0 = tid; i0 < len;) {
