@@ -1,0 +1,66 @@
+"""GPU: calls of the 8-bit cache at the edges of what the header allows: sequences
+that are skipped for any of their counts, rows that are taken whole."""
+
+import numpy as np
+import pytest
+import torch
+
+from kv8_util import DEV, Cache8, i32, oracle_select
+from visual_token_sparsity_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 4096          # elements behind the indices, left as they were
+
+
+def retrieve(c, q, seqs, k):
+    """(indices, fp32 scores, status); nothing is written behind the indices."""
+    from visual_token_sparsity_gb300 import binding as sv
+    B, R, H, d = q.shape
+    n = B * c.Hkv * k
+    buf = torch.full((n + GUARD,), -7, dtype=torch.int32, device=DEV)
+    sc = torch.full((B, c.Hkv, seqs.n_vis), 7.0, device=DEV)
+    ws = sv.workspace(sv.sv_kv8_retrieve_workspace_bytes(B, H, c.Hkv, d, seqs.n_vis, k))
+    sv.sv_kv8_retrieve_topk(q, c.layer(), seqs, k, buf[:n].view(B, c.Hkv, k), sc, ws)
+    status = sv.sv_read_device_status(ws)
+    assert (buf[n:] == -7).all()
+    return buf[:n].view(B, c.Hkv, k).cpu().numpy(), sc, status
+
+
+def long_cache(B, Hkv, d, tokens, seed):
+    """A cache whose pages come again behind 8192 tokens: (cache, block table, keys of `tokens`)."""
+    c = Cache8(B, Hkv, d, min(tokens, 8192), seed)
+    bt = c.bt.repeat(1, -(-tokens // (c.per * 16)))[:, : synth.blocks_for(tokens)].contiguous()
+    return c, bt.to(DEV), c.rows(0)[:, :, np.arange(tokens) % (c.per * 16)]
+
+
+@pytest.mark.parametrize("Hkv,d,n_vis,k", [(2, 64, 700, 200), (4, 64, 5000, 5000), (4, 64, 20011, 6000),
+                                           (1, 64, 402000, 90000)])
+@pytest.mark.parametrize("which", ["some", "all"])
+def test_retrieval_skips_sequences_whose_text_count_is_out_of_range(lib, Hkv, d, n_vis, k, which):
+    """They are not scored, so their rows have no selection either: all -1.  The valid
+    ones, a short one first, are as they would be without them."""
+    from visual_token_sparsity_gb300 import binding as sv
+    n_text = 9
+    nv = [16, n_vis, n_vis // 2, n_vis]
+    nt = [0, n_text + 1, n_text, -1] if which == "some" else [n_text + 1, -1, 2 ** 31 - 1, -2 ** 31]
+    ks = [min(3, k), k, k // 3, k]
+    good = [b for b in range(4) if 0 <= nt[b] <= n_text]
+    c, bt, K = long_cache(4, Hkv, d, n_vis + n_text, seed=91)
+    q = synth.normal_bf16((4, 1, 2 * Hkv, d), 6).to(DEV)
+    vis, sc, status = retrieve(c, q, sv.SeqBatch(bt, n_vis, n_text, i32(nv), i32(nt), i32(ks)), k)
+    assert status == sv.SV_DEV_BAD_LENGTH
+    for b in range(4):
+        if b not in good:
+            assert (vis[b] == -1).all() and (sc[b] == 7.0).all()
+    if good:
+        want, _ = oracle_select(q[good], K[good], [nv[b] for b in good], [ks[b] for b in good])
+        assert np.array_equal(vis[good][..., :want.shape[2]], want) and (vis[good][..., want.shape[2]:] == -1).all()
+    # the text counts alone, the others uniform
+    vis, _, status = retrieve(c, q, sv.SeqBatch(bt, n_vis, n_text, None, i32(nt), None), k)
+    assert status == sv.SV_DEV_BAD_LENGTH
+    for b in range(4):
+        if b not in good:
+            assert (vis[b] == -1).all()
+        else:
+            assert np.array_equal(vis[b: b + 1], oracle_select(q[b: b + 1], K[b: b + 1], [n_vis], [k])[0])

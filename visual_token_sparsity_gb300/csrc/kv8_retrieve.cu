@@ -681,8 +681,10 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
   for (int i = tid; i < kBins; i += nt) sh.hist[i] = 0;
   // The lengths are read before the wait for the scores: that kernel writes none, and
   // let this one begin only when those before it had completed.
-  int n = a.n_vis, k = a.k;
-  if (a.lens.any()) row_lengths(a.lens, row, a.Hkv, a.n_vis, a.k, n, k);
+  // As the scoring takes them, the text's among them: a sequence with one out of range
+  // has no page in the line, and nothing here may look for its scores.
+  int n, nt_text, k;
+  seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, n, nt_text, k);
   if (warp == 0 && n > 0) {                  // (by one warp: it looks at all sequences)
     const int2 by = scorers_of(a, parts, row, n, lane);
     if (lane == 0) sh.by = by;
