@@ -64,3 +64,70 @@ def test_retrieval_skips_sequences_whose_text_count_is_out_of_range(lib, Hkv, d,
             assert (vis[b] == -1).all()
         else:
             assert np.array_equal(vis[b: b + 1], oracle_select(q[b: b + 1], K[b: b + 1], [n_vis], [k])[0])
+
+
+LONG = [5000, 20011, 402000]       # a CTA per row, a cluster, a cluster whose keys lie in global memory
+
+
+def kinds_of_rows(n, kinds, seed):
+    """A cache of one head whose keys are `kinds` different rows, row i's kind pick[i]; d 64."""
+    c, bt, _ = long_cache(1, 1, 64, n, seed)
+    cap = c.codes[0].shape[2]
+    pick = np.random.default_rng(seed).integers(0, kinds, cap)
+    c.codes[0] = np.ascontiguousarray(c.codes[0][:, :, pick])
+    c.scales[...] = 0.25
+    return c, bt, pick[np.arange(n) % cap]
+
+
+@pytest.mark.parametrize("n", LONG)
+def test_rows_taken_whole_without_a_difference(lib, n):
+    """k == n_vis and all scores equal: every token lies next to the border and is needed."""
+    from visual_token_sparsity_gb300 import binding as sv
+    c, bt, _ = long_cache(2, 2, 64, n, seed=92)
+    q = torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    vis, sc, status = retrieve(c, q, sv.SeqBatch(bt, n, 0), n)
+    assert status == 0 and (sc == 0).all() and (vis == np.arange(n)).all()
+
+
+@pytest.mark.parametrize("kinds,better", [(2, 1), (3, 2), (2, 2)])
+@pytest.mark.parametrize("n", LONG)
+def test_ties_that_the_selection_uses_up(lib, n, kinds, better):
+    """k is the number of tokens of the better kinds: the last of them is needed."""
+    from visual_token_sparsity_gb300 import binding as sv
+    c, bt, pick = kinds_of_rows(n, kinds, seed=93)
+    q = synth.normal_bf16((1, 1, 1, 64), 16).to(DEV)
+    qn = q.double().cpu().numpy()[0, 0, 0]
+    K = c.rows(0)[0, 0]
+    cap = K.shape[0]
+    value = {p: (K[np.flatnonzero(pick[:cap] == p)[0]] @ qn) for p in range(kinds)}
+    best = sorted(value, key=value.get)[-better:]
+    want = np.flatnonzero(np.isin(pick, best))
+    assert len(set(value.values())) == kinds and want.size > 600
+    vis, _, status = retrieve(c, q, sv.SeqBatch(bt, n, 0), want.size)
+    assert status == 0 and np.array_equal(vis[0, 0], want)
+
+
+@pytest.mark.parametrize("less", [0, 1, 1000])
+@pytest.mark.parametrize("n", LONG)
+def test_one_key_that_is_not_finite_in_a_long_row(lib, n, less):
+    """The choice is open, but ascending, distinct and in range."""
+    from visual_token_sparsity_gb300 import binding as sv
+    c, bt, _ = long_cache(1, 1, 64, n, seed=94)
+    c.codes[0][0, 0, 4321, 3] = 0x7F
+    q = synth.normal_bf16((1, 1, 1, 64), 17).to(DEV)
+    vis, _, status = retrieve(c, q, sv.SeqBatch(bt, n, 0), n - less)
+    assert status == 0
+    assert (np.diff(vis[0, 0]) > 0).all() and vis.min() >= 0 and vis.max() < n
+
+
+@pytest.mark.parametrize("n", LONG)
+def test_a_short_sequence_taken_whole_beside_long_ones(lib, n):
+    """The kernel is chosen by the capacity; equal scores, k_seq == n_vis_seq or one less."""
+    from visual_token_sparsity_gb300 import binding as sv
+    nv, ks = [n, 3000, 4001, 513, 512], [n // 3, 3000, 4000, 513, 512]
+    c, bt, _ = long_cache(5, 1, 64, n, seed=95)
+    q = torch.zeros(5, 1, 1, 64, dtype=torch.bfloat16, device=DEV)
+    vis, _, status = retrieve(c, q, sv.SeqBatch(bt, n, 0, i32(nv), None, i32(ks)), max(ks))
+    assert status == 0
+    for b in range(5):
+        assert np.array_equal(vis[b, 0, : ks[b]], np.arange(ks[b])) and (vis[b, 0, ks[b]:] == -1).all()

@@ -942,6 +942,8 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
       int kept = 0;
       for (int i = lane; i < m; i += 32) kept += all[i].x != 0u && (int)all[i].y < first;
       before += __reduce_add_sync(0xffffffffu, kept);
+    } else if (m <= need) {
+      before += __reduce_add_sync(0xffffffffu, lane < rank ? theirs : 0);   // (all of them are taken)
     }
   }
 
