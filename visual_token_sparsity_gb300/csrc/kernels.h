@@ -50,14 +50,16 @@ cudaError_t launch_retrieve_softmax(const void* q, int R, int H, float scale, co
 // per row for long rows).  n and k are the row stride of scores and idx; with
 // per-sequence lengths (rows_per_seq rows per sequence) row r uses
 // lens.n_vis / lens.k of sequence r / rows_per_seq and fills its slots past
-// that k with -1 (out-of-range lengths: the whole row is -1).
+// that k with -1 (out-of-range lengths, lens.n_text beyond n_text included: the
+// whole row is -1).
 cudaError_t launch_topk_rows(const float* scores, int rows, int n, int k, int32_t* idx,
-                             cudaStream_t stream, const SeqLens& lens = SeqLens{}, int rows_per_seq = 1);
+                             cudaStream_t stream, const SeqLens& lens = SeqLens{}, int rows_per_seq = 1,
+                             int n_text = 0);
 bool topk_cluster_fits(int n);
 bool topk_prefers_cluster(int n);   // long rows that fit: use launch_topk_cluster
 cudaError_t launch_topk_cluster(const float* scores, int rows, int n, int k, int32_t* idx,
                                 cudaStream_t stream, const SeqLens& lens = SeqLens{},
-                                int rows_per_seq = 1);
+                                int rows_per_seq = 1, int n_text = 0);
 
 // ---- pack-once KV (pack.cu): selected visual + text rows of src copied to
 // positions [0, k + n_text) of every sequence of dst (same Hkv and D)

@@ -195,8 +195,8 @@ cudaError_t launch_retrieve(const void* q, int R, int H, int G, const void* k_po
                                   vis_idx, lens, n_text);
   if (e != cudaSuccess || fuse) return e;
   if (topk_prefers_cluster(n_vis))
-    return launch_topk_cluster(scores, rows, n_vis, k, vis_idx, stream, lens, Hkv);
-  return launch_topk_rows(scores, rows, n_vis, k, vis_idx, stream, lens, Hkv);
+    return launch_topk_cluster(scores, rows, n_vis, k, vis_idx, stream, lens, Hkv, n_text);
+  return launch_topk_rows(scores, rows, n_vis, k, vis_idx, stream, lens, Hkv, n_text);
 }
 
 }  // namespace sv

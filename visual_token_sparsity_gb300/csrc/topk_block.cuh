@@ -59,14 +59,13 @@ __device__ __forceinline__ T block_exclusive_scan(T v, T* warp_tmp) {
 }
 
 // Row `row`'s key count nr and selection size kr under per-sequence lengths
-// (rows_per_seq rows per sequence; n and k are the capacities); (0, 0) when
-// a length is out of range.
-__device__ __forceinline__ void row_lengths(const SeqLens& lens, int row, int rows_per_seq, int n, int k,
+// (rows_per_seq rows per sequence; n, n_text and k are the capacities); (0, 0)
+// when a length is out of range, the text's included: scoring skips the sequence
+// then, so there is nothing to select from.
+__device__ __forceinline__ void row_lengths(const SeqLens& lens, int row, int rows_per_seq, int n, int n_text, int k,
                                             int& nr, int& kr) {
-  SeqLens l = lens;
-  l.n_text = nullptr;
   int nt;
-  seq_lengths(l, row / rows_per_seq, n, 0, k, nr, nt, kr);
+  seq_lengths(lens, row / rows_per_seq, n, n_text, k, nr, nt, kr);
 }
 
 // Index slots [from, k) of a row that selected fewer than k tokens get -1

@@ -32,7 +32,7 @@ constexpr int kTopkClusterThreads = 512;
 
 __global__ void __cluster_dims__(kTopkClusterCtas, 1, 1) __launch_bounds__(kTopkClusterThreads)
 topk_cluster_kernel(const float* __restrict__ scores, int n_cap, int k_cap, int32_t* __restrict__ idx,
-                    SeqLens lens, int rows_per_seq) {
+                    SeqLens lens, int rows_per_seq, int n_text) {
   extern __shared__ uint32_t keys[];
   __shared__ int hist[2][256];    // double-buffered: peers read pass p's while pass p+1 fills the other
   __shared__ int total[256];
@@ -49,7 +49,7 @@ topk_cluster_kernel(const float* __restrict__ scores, int n_cap, int k_cap, int3
   // this row's key count and selection size (the same for every CTA of the
   // cluster, so an empty selection leaves the cluster together)
   int n = n_cap, k = k_cap;
-  if (lens.any()) row_lengths(lens, row, rows_per_seq, n_cap, k_cap, n, k);
+  if (lens.any()) row_lengths(lens, row, rows_per_seq, n_cap, n_text, k_cap, n, k);
   int32_t* dst = idx + (size_t)row * k_cap;
   if (rank == 0) fill_unselected(dst, k, k_cap);
   if (k <= 0) return;
@@ -226,7 +226,7 @@ bool topk_cluster_fits(int n) {
 bool topk_prefers_cluster(int n) { return n > 16384 && topk_cluster_fits(n); }
 
 cudaError_t launch_topk_cluster(const float* scores, int rows, int n, int k, int32_t* idx,
-                                cudaStream_t stream, const SeqLens& lens, int rows_per_seq) {
+                                cudaStream_t stream, const SeqLens& lens, int rows_per_seq, int n_text) {
   if (rows == 0) return cudaSuccess;
   const int slice = (n + kTopkClusterCtas - 1) / kTopkClusterCtas;
   const size_t smem = (size_t)slice * sizeof(uint32_t);
@@ -241,7 +241,7 @@ cudaError_t launch_topk_cluster(const float* scores, int rows, int n, int k, int
   }
   dim3 grid(kTopkClusterCtas, rows);
   return launch_dependent(topk_cluster_kernel, grid, dim3(kTopkClusterThreads), smem, stream, scores, n, k, idx,
-                          lens, rows_per_seq > 0 ? rows_per_seq : 1);
+                          lens, rows_per_seq > 0 ? rows_per_seq : 1, n_text);
 }
 
 }  // namespace sv
