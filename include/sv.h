@@ -750,9 +750,8 @@ sv_status sv_kv8_retrieve_topk(const void* q, int R, int H, const sv_kv8_layer* 
  * sv_sparse_decode_attn over the 8-bit cache; arguments, per-sequence lengths
  * and skipped loads as there.  A row that attends to no token has out 0 and
  * lse -inf.  out: 16-byte aligned, apart from q.  The weights of the product with
- * V are rounded to fp16's eleven bits; of a value whose weight times factor is
- * below 2^-20 of the row's largest weight times the largest factor among its pages
- * fewer are left, below 2^-30 none.
+ * V, a token's softmax weight times its page's factor, are rounded to fp16's eleven
+ * bits; of one below 2^-20 of the largest of its row fewer are left, below 2^-30 none.
  * ws : sv_kv8_attn_workspace_bytes(B, H, n_kv_heads, head_dim, n_tokens),
  *      n_tokens = k + n_text (k = n_vis when vis_idx is NULL); the size never
  *      shrinks as B or n_tokens grow.

@@ -21,10 +21,16 @@
 // ahead (six of half the bytes at head dim 64); the indices, pages and factors
 // that lead to them run two blocks of 32 tokens before that.
 //
-// The weights carry the factor s_v of their page relative to the largest so far
-// (and 2^6), the scores a reference that is raised only when one outgrows it by
-// 2^8, so that most steps need no maximum.  A weight keeps its eleven bits down to
-// 2^-20 of the reference and vanishes below 2^-30.
+// A weight of the value product carries the factor s_v of its page, and has a
+// reference of its own beside the sum's:
+//
+//   l += 2^(z - m),   p = 2^(z + log2 s_v - u) 2^6   in fp16,   O = 2^(u - m - 6) sum p V8
+//
+// m and u are raised only when a term outgrows them by 2^8, so that most steps need
+// no maximum.  A weight keeps its eleven bits down to 2^-20 of the largest and vanishes
+// below 2^-30: a page of large values that no row looks at takes none from the others.
+// (One exponential more; with the factor relative to the largest so far, and one
+// reference, such a page took all of them.)
 //
 // Work is cut evenly: the blocks of 32 tokens of all (sequence, KV head) units
 // form one line, cut into equal pieces, one per CTA, whose four warps take every
@@ -95,10 +101,12 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   return r;
 }
 
-// The power of two 2^e, as fp32 bits, with 2^e <= max(|x|, |y|) < 2^(e + 1), within
-// 2^-126 and 2^126.
-__device__ __forceinline__ uint32_t exponent_of(float x, float y) {
-  return min(max(__float_as_uint(fmaxf(fabsf(x), fabsf(y))) & 0x7f800000u, 0x00800000u), 253u << 23);
+// A factor s as 2^e times what is left, 2^e <= |s| < 2^(e + 1) within 2^-126 and
+// 2^126; what is left times 2^6.
+__device__ __forceinline__ void split_factor(float s, float& e, float& rest) {
+  const uint32_t x = min(max(__float_as_uint(s) & 0x7f800000u, 0x00800000u), 253u << 23);
+  e = __uint_as_float(0x4b000000u | x >> 23) - 8388735.f;                   // (2^23 + the exponent) - (2^23 + 127)
+  rest = s * __uint_as_float((254u << 23) - x) * 64.f;
 }
 
 struct Seq {
@@ -385,12 +393,12 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           }
       }
 
-      float m[NT][2], l[NT][2], o[NT][KS][4];
+      float m[NT][2], u[NT][2], l[NT][2], o[NT][KS][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          m[t][i] = -INFINITY;
+          m[t][i] = u[t][i] = -INFINITY;
           l[t][i] = 0.f;
         }
 #pragma unroll
@@ -398,7 +406,6 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[t][j][e] = 0.f;
       }
-      uint32_t vtop = 0x00800000u;      // the largest factor of V so far, rounded down to a power of two (bits)
 
       // (two steps a block of this warp)
       const int steps = max(0, (end - first + stride - 1) / stride * 2);
@@ -411,7 +418,10 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
         const uint8_t* at = ring + stage * R::kStage;
         const float2* fac = reinterpret_cast<const float2*>(ring + R::kFactors + stage * kStep * 8);
         const float2 f0 = fac[r], f1 = fac[r + 8];
-        const float sk0 = f0.x, sv0 = f0.y, sk1 = f1.x, sv1 = f1.y;
+        const float sk0 = f0.x, sk1 = f1.x;
+        float ev[2], rest[2];
+        split_factor(f0.y, ev[0], rest[0]);
+        split_factor(f1.y, ev[1], rest[1]);
         const uint32_t seen = reinterpret_cast<const uint32_t*>(ring + R::kThere)[stage];
         const bool ok0 = (seen >> r) & 1, ok1 = (seen >> (8 + r)) & 1;
         uint4 xk[2][KC];
@@ -441,47 +451,44 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             z[t][e] = (e < 2 ? ok0 : ok1) ? z[t][e] * (e < 2 ? sk0 : sk1) * qs[t][e & 1] : -INFINITY;
-            raise = raise || z[t][e] > m[t][e & 1] + kRaise || (m[t][e & 1] == -INFINITY && z[t][e] > -INFINITY);
+            // (of a row without a token so far both references are -inf)
+            raise = raise || z[t][e] > m[t][e & 1] + kRaise || z[t][e] + ev[e >> 1] > u[t][e & 1] + kRaise;
           }
-        raise = raise || exponent_of(sv0, sv1) > vtop;
         if (__any_sync(0xffffffffu, raise)) {
-          // the factors' largest, and each head's
-          const uint32_t top = __reduce_max_sync(0xffffffffu, max(vtop, exponent_of(sv0, sv1)));
-          const float down = __uint_as_float(vtop) / __uint_as_float(top);
-          vtop = top;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float mx = fmaxf(m[t][i], fmaxf(z[t][i], z[t][i + 2]));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float alpha = m[t][i] == -INFINITY ? 0.f : fast_exp2(m[t][i] - mx);
+              float ux = fmaxf(u[t][i], fmaxf(z[t][i] + ev[0], z[t][i + 2] + ev[1]));
+#pragma unroll
+              for (int x = 4; x <= 16; x *= 2) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                ux = fmaxf(ux, __shfl_xor_sync(0xffffffffu, ux, x));
+              }
+              l[t][i] *= m[t][i] == -INFINITY ? 0.f : fast_exp2(m[t][i] - mx);
+              const float down = u[t][i] == -INFINITY ? 0.f : fast_exp2(u[t][i] - ux);
               m[t][i] = mx;
-              l[t][i] *= alpha;
+              u[t][i] = ux;
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
-                o[t][j][i] *= alpha * down;
-                o[t][j][i + 2] *= alpha * down;
+                o[t][j][i] *= down;
+                o[t][j][i + 2] *= down;
               }
             }
         }
-        // 2^6 s_v over the largest factor
-        const float unit_v = __uint_as_float((254u - (vtop >> 23)) << 23);
-        const float w0 = sv0 * unit_v * 64.f, w1 = sv1 * unit_v * 64.f;
         uint32_t p[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float ref = m[t][e & 1];
-            y[e] = fast_exp2(z[t][e] - (ref == -INFINITY ? 0.f : ref));
-            l[t][e & 1] += y[e];
+            const float mr = m[t][e & 1], ur = u[t][e & 1];
+            l[t][e & 1] += fast_exp2(z[t][e] - (mr == -INFINITY ? 0.f : mr));
+            y[e] = fast_exp2(z[t][e] + ev[e >> 1] - (ur == -INFINITY ? 0.f : ur)) * rest[e >> 1];
           }
-          p[t][0] = transposed(half2_of(y[0] * w0, y[1] * w0));
-          p[t][1] = transposed(half2_of(y[2] * w1, y[3] * w1));
+          p[t][0] = transposed(half2_of(y[0], y[1]));
+          p[t][1] = transposed(half2_of(y[2], y[3]));
         }
         uint32_t xv[4][VW];                         // tokens 2 q4, + 1, + 8, + 9
 #pragma unroll
@@ -511,7 +518,6 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
       __syncwarp();                                             // (the ring is free for the next unit)
 
       // ---- this part of the unit: the warps' results joined in shared memory
-      const float back = __uint_as_float(vtop) * (1.f / 64.f);
       const bool whole = blk0 == 0 && blk1 == per_unit;
       const size_t slot = part_slot(piece, blk0 == 0), row0 = (size_t)b * a.H + (size_t)g * G;
       float* joined = reinterpret_cast<float*>(ring);          // [G][D], then (m, l)
@@ -526,10 +532,12 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
           s += __shfl_xor_sync(0xffffffffu, s, 8);
           s += __shfl_xor_sync(0xffffffffu, s, 16);
           if (h >= G) continue;
+          // O relative to m, by two factors as 2^(u - m) may be out of range
+          const float back = m[t][i] == -INFINITY ? 0.f : fast_exp2(0.5f * (u[t][i] - m[t][i])), back64 = back * (1.f / 64.f);
           float* dst = joined + h * D + r * VB;
 #pragma unroll
           for (int j = 0; j < KS; ++j)
-            *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back, o[t][j][i + 2] * back);
+            *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[t][j][i] * back64 * back, o[t][j][i + 2] * back64 * back);
           if (r == 0) reinterpret_cast<float2*>(joined + G * D)[h] = make_float2(m[t][i], s);
         }
       __syncthreads();
