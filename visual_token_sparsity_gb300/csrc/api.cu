@@ -996,7 +996,8 @@ sv_status sv_kv8_decode_attn(const void* q, int H, float scale, const sv_kv8_lay
   a.lens = lens_of(seqs);
   a.out = out; a.lse = lse;
   a.ws = data_of(ws); a.counters = counters_of(ws); a.status = status_word(ws);
-  return cuda_status(sv::launch_kv8_attn(a, layer->head_dim, static_cast<cudaStream_t>(stream)), "sv_kv8_decode_attn");
+  return cuda_status(sv::launch_kv8_attn(a, layer->head_dim, num_sms(), static_cast<cudaStream_t>(stream)),
+                     "sv_kv8_decode_attn");
 }
 
 sv_status sv_read_device_status(void* ws, int clear, int32_t* status_out, void* stream) {

@@ -265,7 +265,7 @@ struct Kv8AttnArgs {
   int* split_done;
 };
 size_t kv8_attn_workspace_bytes(int B, int H, int Hkv, int D, int n_tokens);
-cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int D, cudaStream_t stream);
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, int D, int num_sms, cudaStream_t stream);
 
 // ---- causal attention of packed prompts (prompt_attn.cu)
 struct PromptArgs {

@@ -54,7 +54,7 @@ namespace sv {
 namespace {
 
 constexpr int kWarps = 4, kCtas = 3;      // per CTA, and CTAs per SM (shared memory and 168 registers)
-constexpr int kSms = 152;
+constexpr int kMostSms = 152;            // that a call is cut for (the workspace is sized without a device)
 constexpr int kBlock = 32;               // tokens whose rows a warp looks up at a time
 constexpr int kStep = 16;                // tokens of a step
 constexpr float kRaise = 8.f;            // log2: a reference is raised when a score outgrows it by more
@@ -669,12 +669,12 @@ namespace {
 // least.  Where that is four or more to a unit, the same number to each, so that
 // none lies across two units (a warp's second unit begins with the whole chain of
 // lookups).
-long long pieces_bound(long long units, long long blocks) {
-  const long long most = (long long)kSms * kCtas, each = blocks / kMinBlocks, c = units * (each > 1 ? each : 1);
+long long pieces_bound(long long units, long long blocks, int sms) {
+  const long long most = (long long)(sms < kMostSms ? sms : kMostSms) * kCtas, each = blocks / kMinBlocks, c = units * (each > 1 ? each : 1);
   return c < 1 ? 1 : c < most ? c : most;
 }
-int pieces_of(long long units, long long blocks) {
-  const long long c = pieces_bound(units, blocks), each = units > 0 ? c / units : 0;
+int pieces_of(long long units, long long blocks, int sms) {
+  const long long c = pieces_bound(units, blocks, sms), each = units > 0 ? c / units : 0;
   return (int)(each >= 4 ? units * each : c);
 }
 
@@ -685,7 +685,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // (m, l) | O of two parts of every piece: a bound that no smaller call exceeds
 size_t kv8_attn_workspace_bytes(int B, int H, int Hkv, int D, int n_tokens) {
   const int G = H / Hkv;
-  const size_t parts = 2 * (size_t)pieces_bound((long long)B * Hkv, ((long long)n_tokens + kBlock - 1) / kBlock);
+  const size_t parts = 2 * (size_t)pieces_bound((long long)B * Hkv, ((long long)n_tokens + kBlock - 1) / kBlock, kMostSms);
   return up256(parts * G * 2 * sizeof(float)) + up256(parts * G * D * sizeof(float));
 }
 
@@ -709,11 +709,11 @@ static cudaError_t launch_nt(const Kv8AttnArgs& a, cudaStream_t stream) {
                           stream, a);
 }
 
-cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int D, cudaStream_t stream) {
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int D, int num_sms, cudaStream_t stream) {
   Kv8AttnArgs a = args;
   const int G = a.H / a.Hkv;
   const long long units = (long long)a.batch * a.Hkv, blocks = (a.k_vis + a.n_text + kBlock - 1) / kBlock;
-  a.pieces = pieces_of(units, blocks);
+  a.pieces = pieces_of(units, blocks, num_sms);
   a.per_unit = (int)blocks;
   a.part_ml = static_cast<float*>(a.ws);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.pieces * 2 * G * 2 * sizeof(float)));
