@@ -568,6 +568,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       if (live && a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       // rows that are not finite, over exactly the tokens that they see
       uint32_t again = __ballot_sync(0xffffffffu, odd && live);
+      if (again) __syncwarp();                            // (their lanes have stored what is written again)
       while (again) {
         const int f = __ffs(again) - 1;
         again &= again - 1;
