@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from kv8_util import DEV, Cache8, i32, oracle_select
+from kv8_util import DEV, KV8_WEIGHTS, Cache8, assert_close, i32, oracle_decode, oracle_select
+from test_gpu_kv8 import attend
 from visual_token_sparsity_gb300 import synth
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +132,37 @@ def test_a_short_sequence_taken_whole_beside_long_ones(lib, n):
     assert status == 0
     for b in range(5):
         assert np.array_equal(vis[b, 0, : ks[b]], np.arange(ks[b])) and (vis[b, 0, ks[b]:] == -1).all()
+
+
+@pytest.mark.parametrize("arrays", [True, False])
+@pytest.mark.parametrize("B,H,Hkv,d", [(700, 8, 1, 128), (2100, 4, 2, 64), (1100, 20, 4, 128), (460, 16, 1, 64)])
+def test_attention_of_more_rows_than_pieces(lib, B, H, Hkv, d, arrays):
+    """The cut of the line leaves most rows whole and some in two pieces or, where a long
+    sequence stands among short ones, in many; each is joined once.  Sequences share the
+    pages of a small pool; a few are compared with the oracle, the others with their like."""
+    from visual_token_sparsity_gb300 import binding as sv
+    n_vis, n_text, kinds = (1500, 20, 9) if arrays else (130, 20, 9)
+    g = np.random.default_rng(96)
+    c = Cache8(kinds, Hkv, d, n_vis + n_text, seed=97)
+    kind = g.integers(0, kinds, B)
+    if arrays:
+        long = g.random(kinds) < 0.3
+        long[:2] = True, False
+        kv = np.where(long, g.integers(600, n_vis + 1, kinds), g.integers(0, 40, kinds))
+        kt = g.integers(0, n_text + 1, kinds)
+        kv[2] = kt[2] = 0
+        kind[[b for b in range(B) if long[kind[b]] and b % 37]] = 1            # (few long ones)
+        kind[[5, B - 1]] = 0
+    else:
+        kv, kt = np.full(kinds, n_vis), np.full(kinds, n_text)
+    q9 = synth.normal_bf16((kinds, H, d), 20)
+    q, bt = q9[torch.from_numpy(kind)].to(DEV), c.bt[torch.from_numpy(kind)].contiguous().to(DEV)
+    seqs = sv.SeqBatch(bt, n_vis, n_text, *((i32(kv[kind]), i32(kt[kind])) if arrays else (None, None)))
+    out, lse, status = attend(c, q, seqs, None, 0, 0.11)
+    assert status == 0
+    first = [int(np.flatnonzero(kind == i)[0]) for i in range(kinds) if (kind == i).any()]
+    used = [int(kind[f]) for f in first]
+    ref = oracle_decode(q9[used], c.rows(0)[used], c.rows(1)[used], None, kv[used].tolist(), kt[used].tolist(), None, 0.11)
+    for nth, i in enumerate(used):
+        for b in np.flatnonzero(kind == i):
+            assert_close(out[b], lse[b], *(r[nth] for r in ref), KV8_WEIGHTS, f"sequence {b} of kind {i}")

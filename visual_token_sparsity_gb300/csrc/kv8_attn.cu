@@ -597,21 +597,59 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   }
 }
 
-// Joins the units that were cut: a CTA per (unit, head), whose warps take every
-// fourth (eighth) piece each.
+// Joins the units that were cut: a CTA per head of a unit, whose warps take every
+// fourth (eighth) piece each.  BY_PIECE: of the unit that begins in a piece and goes on
+// (with more units than pieces most are not cut, and looking each one's place up, which
+// means looking at all sequences, would cost the square of the batch: 3001 sequences of
+// their own lengths, 28 heads over 4, 4615 us).
 constexpr int kMergeThreads = 256;
-template <int D>
+template <int D, bool BY_PIECE>
 __global__ void __launch_bounds__(kMergeThreads)
 kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  constexpr int kPer = D / 2, kParts = kMergeThreads / kPer;
+  constexpr int kPer = D / 2, kParts = kMergeThreads / kPer, kMergeWarps = kMergeThreads / 32;
   __shared__ float2 part[kParts][kPer], part_ml[kParts];
   const int G = a.H / a.Hkv, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, g = h / G;
+  const int unit = blockIdx.x / G, h = blockIdx.x - unit * G;       // (a piece, BY_PIECE)
   // The lengths are read before the wait for the attention (it writes none, and let
-  // this kernel begin only when those before it had completed), by one warp, as it
-  // looks at all sequences.
-  __shared__ int2 pieces;                                   // the first of the unit's, and their number
-  if (threadIdx.x < 32) {
+  // this kernel begin only when those before it had completed).
+  __shared__ int3 found;                                    // the first of the unit's pieces, their number, its first head
+  if constexpr (BY_PIECE) {
+    // a stretch of sequences to a warp
+    __shared__ uint32_t sums[kMergeWarps];
+    const int warp = threadIdx.x >> 5, each = ((a.batch + 31) / 32 + kMergeWarps - 1) / kMergeWarps * 32;
+    const int b0 = warp * each, b1 = min(a.batch, b0 + each);
+    uint32_t mine, sum = 0, before = 0, total = 0;
+    for (int b = b0; b < b1; b += 32) sum += __shfl_sync(0xffffffffu, scan_blocks(a, b, lane, mine), 31);
+    if (lane == 0) sums[warp] = sum;
+    if (threadIdx.x == 0) found = make_int3(0, 0, 0);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      before += w < warp ? sums[w] : 0u;
+      total += sums[w];
+    }
+    const uint32_t C = min((uint32_t)a.pieces, total);
+    if ((uint32_t)unit + 1 < C) {
+      const uint32_t end = kv8::piece_begin(total, unit + 1, C);
+      if (end >= before && end < before + sum)
+        for (int b = b0; b < b1; b += 32) {
+          const uint32_t inc = scan_blocks(a, b, lane, mine), past = __ballot_sync(0xffffffffu, before + inc > end);
+          if (past == 0) {
+            before += __shfl_sync(0xffffffffu, inc, 31);
+            continue;
+          }
+          // the unit that the next piece's first block lies in
+          if (lane == __ffs(past) - 1) {
+            before += inc - mine;
+            const uint32_t per_unit = mine / (uint32_t)a.Hkv, g = (end - before) / per_unit, start = before + g * per_unit;
+            if (start < end && kv8::piece_of(total, start, C) == unit)
+              found = make_int3(unit, kv8::piece_of(total, start + per_unit - 1, C) - unit + 1, (b + lane) * a.H + (int)g * G);
+          }
+          break;
+        }
+    }
+  } else if (threadIdx.x < 32) {                            // (by one warp, as it looks at all sequences)
+    const int b = unit / a.Hkv, g = unit - b * a.Hkv;
     Seq s;
     seq_of(a, b, s);
     const int per_unit = s.blocks();
@@ -629,21 +667,21 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
       }
     }
     const uint32_t start = before + (uint32_t)g * (uint32_t)per_unit, C = min((uint32_t)a.pieces, total);
-    int2 p = make_int2(0, 0);
+    int3 p = make_int3(0, 0, unit * G);
     if (per_unit > 0) {
       p.x = kv8::piece_of(total, start, C);
       p.y = kv8::piece_of(total, start + per_unit - 1, C) - p.x + 1;
     }
-    if (lane == 0) pieces = p;
+    if (lane == 0) found = p;
   }
   __syncthreads();
-  const int p0 = pieces.x, n = pieces.y;
+  const int p0 = found.x, n = found.y;
   grid_dep_sync();
   if (n <= 1) return;                                       // (no token, or not cut)
   const int w = threadIdx.x / kPer, i = threadIdx.x - w * kPer;
   float M, L;
   float2 v;
-  gather_pieces<D>(a, p0, n, w, kParts, h - g * G, 2 * i, M, L, v);
+  gather_pieces<D>(a, p0, n, w, kParts, h, 2 * i, M, L, v);
   part[w][i] = v;
   if (i == 0) part_ml[w] = make_float2(M, L);
   __syncthreads();
@@ -660,7 +698,7 @@ kv8_merge_kernel(const __grid_constant__ Kv8AttnArgs a) {
     v.x = fmaf(f, part[p][i].x, v.x);
     v.y = fmaf(f, part[p][i].y, v.y);
   }
-  write_pair<D>(a, (size_t)b * a.H + h, 2 * i, M, L, v);
+  write_pair<D>(a, (size_t)found.z + h, 2 * i, M, L, v);
 }
 
 namespace {
@@ -705,8 +743,10 @@ static cudaError_t launch_nt(const Kv8AttnArgs& a, cudaStream_t stream) {
   }
   e = launch_dependent(kernel, dim3((unsigned)a.pieces), dim3(kWarps * 32), (size_t)smem, stream, a);
   if (e != cudaSuccess || !a.cut || a.split_done != nullptr) return e;
-  return launch_dependent(kv8_merge_kernel<D>, dim3((unsigned)((long long)a.batch * a.H)), dim3(kMergeThreads), 0,
-                          stream, a);
+  const long long units = (long long)a.batch * a.Hkv;
+  const bool by_piece = units > a.pieces;
+  return launch_dependent(by_piece ? kv8_merge_kernel<D, true> : kv8_merge_kernel<D, false>,
+                          dim3((unsigned)((by_piece ? a.pieces : units) * (a.H / a.Hkv))), dim3(kMergeThreads), 0, stream, a);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& args, int D, int num_sms, cudaStream_t stream) {
