@@ -166,3 +166,33 @@ def test_attention_of_more_rows_than_pieces(lib, B, H, Hkv, d, arrays):
     for nth, i in enumerate(used):
         for b in np.flatnonzero(kind == i):
             assert_close(out[b], lse[b], *(r[nth] for r in ref), KV8_WEIGHTS, f"sequence {b} of kind {i}")
+
+
+@pytest.mark.parametrize("B,Hkv,n_vis,k", [(33, 2, 400, 90), (300, 1, 150, 40), (1000, 3, 70, 20), (65, 1, 17000, 60)])
+@pytest.mark.parametrize("bad", [False, True])
+def test_retrieval_of_many_sequences_of_their_own_lengths(lib, B, Hkv, n_vis, k, bad):
+    """Empty ones and, bad, some that are skipped among them; sequences share the pages of a
+    small pool, so that each can be compared with its like."""
+    from visual_token_sparsity_gb300 import binding as sv
+    g = np.random.default_rng(98)
+    kinds = 7
+    c = Cache8(kinds, Hkv, 64, min(n_vis, 800), seed=99)
+    kind = g.integers(0, kinds, B)
+    nv = g.integers(0, min(n_vis, 800) + 1, B)
+    nv[[3, B - 1]] = 0, min(n_vis, 800)
+    ks = np.minimum(nv, g.integers(0, k + 1, B))
+    ks[B - 1] = min(k, nv[B - 1])
+    nt = g.integers(0, 6, B)
+    if bad:
+        nt[[0, 5, B // 2]] = 6, -1, 99
+        nv[7], ks[9] = n_vis + 1, nv[9] + 1
+    good = (nt >= 0) & (nt <= 5) & (nv <= n_vis) & (ks <= nv) & (ks <= k)
+    bt = torch.zeros(B, synth.blocks_for(n_vis + 5), dtype=torch.int32)
+    bt[:, : c.per] = c.bt[torch.from_numpy(kind)][:, : bt.shape[1]]
+    q = synth.normal_bf16((B, 1, Hkv, 64), 21).to(DEV)
+    vis, _, status = retrieve(c, q, sv.SeqBatch(bt.to(DEV), n_vis, 5, i32(nv), i32(nt), i32(ks)), k)
+    assert status == (sv.SV_DEV_BAD_LENGTH if bad else 0)
+    assert bad != good.all() and (vis[~good] == -1).all()
+    at = np.flatnonzero(good)
+    want, _ = oracle_select(q[at], c.rows(0)[kind[at]], nv[at].tolist(), ks[at].tolist())
+    assert np.array_equal(vis[at][..., : want.shape[2]], want) and (vis[at][..., want.shape[2]:] == -1).all()

@@ -309,6 +309,17 @@ __device__ __forceinline__ uint32_t line_of(const Kv8RetrieveArgs& a, const Part
   return total;
 }
 
+// With many sequences of their own lengths a stretch of them to each warp: W warps' sums
+// of pages.  (By each warp for itself 3001 sequences of 320 keys, 4 KV heads, 712 us a call
+// instead of 358; 256 sequences 41 and 34.)
+__device__ __forceinline__ bool by_stretches(const Kv8RetrieveArgs& a) { return a.lens.any() && a.batch > 32; }
+__device__ __forceinline__ int stretch_of(const Kv8RetrieveArgs& a, int W) { return ((a.batch + 31) / 32 + W - 1) / W * 32; }
+__device__ __forceinline__ uint32_t stretch_pages(const Kv8RetrieveArgs& a, int b0, int b1, int lane) {
+  uint32_t sum = 0, mine;
+  for (; b0 < b1; b0 += 32) sum += __shfl_sync(0xffffffffu, scan_pages(a, b0, lane, mine), 31);
+  return sum;
+}
+
 // A warp per page, one page in flight, as many warps as 48 registers allow.  SUM:
 // the query's rows are few, and every CTA adds them up itself (the first of a row
 // leaves the sum for the selection).
@@ -322,9 +333,20 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
   grid_dep_sync();
   uint32_t off = 0;                        // of this CTA's first page in sequence b
   int left, b = 0;
+  __shared__ uint32_t stretch[W];
   {
-    uint32_t before = 0;
-    const uint32_t total = line_of(a, parts, 0, lane, before), C = min((uint32_t)parts.ctas, total);
+    uint32_t before = 0, total = 0;
+    if (by_stretches(a)) {
+      const int each = stretch_of(a, W);
+      const uint32_t sum = stretch_pages(a, warp * each, min(a.batch, (warp + 1) * each), lane);
+      if (lane == 0) stretch[warp] = sum;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) total += stretch[w];
+    } else {
+      total = line_of(a, parts, 0, lane, before);
+    }
+    const uint32_t C = min((uint32_t)parts.ctas, total);
     if (blockIdx.x >= C) left = 0;
     else {
       off = kv8::piece_begin(total, blockIdx.x, C);
@@ -341,6 +363,11 @@ kv8_score_kernel(const __grid_constant__ Kv8RetrieveArgs a, Query8<D>* rows, flo
     for (int i = blockIdx.x * W * 32 + threadIdx.x; i < a.batch; i += gridDim.x * W * 32) {
       int nv, nt, kb;
       if (!seq_lengths(a.lens, i, a.n_vis, a.n_text, a.k, nv, nt, kb)) flag_status(a.status, kStatusBadLength);
+    }
+    if (by_stretches(a) && left > 0) {
+      int w = 0;
+      for (; w < W - 1 && off >= stretch[w]; ++w) off -= stretch[w];
+      b = w * stretch_of(a, W);
     }
     for (; left > 0 && b < a.batch; b += 32) {
       uint32_t mine;
@@ -476,11 +503,12 @@ struct __align__(16) SelectShared {
   int2 by;
 };
 
-// The first and the last CTA that scored pages of a row of n > 0 keys.
-__device__ __forceinline__ int2 scorers_of(const Kv8RetrieveArgs& a, const Parts& parts, int row, int n, int lane) {
+// The first and the last CTA that scored pages of a row of n > 0 keys, in a line of
+// `total` with `before` ahead of its sequence.
+__device__ __forceinline__ int2 scorers_of(const Kv8RetrieveArgs& a, const Parts& parts, int row, int n, uint32_t total,
+                                           uint32_t before) {
   const int b = row / a.Hkv, pages = (n + 15) >> 4;
-  uint32_t before = 0;
-  const uint32_t total = line_of(a, parts, b, lane, before), C = min((uint32_t)parts.ctas, total);
+  const uint32_t C = min((uint32_t)parts.ctas, total);
   const uint32_t start = before + (uint32_t)(row - b * a.Hkv) * (uint32_t)pages;
   return make_int2(kv8::piece_of(total, start, C), kv8::piece_of(total, start + pages - 1, C));
 }
@@ -685,9 +713,30 @@ __device__ __forceinline__ void select_row(const Kv8RetrieveArgs& a, const Query
   // has no page in the line, and nothing here may look for its scores.
   int n, nt_text, k;
   seq_lengths(a.lens, b, a.n_vis, a.n_text, a.k, n, nt_text, k);
-  if (warp == 0 && n > 0) {                  // (by one warp: it looks at all sequences)
-    const int2 by = scorers_of(a, parts, row, n, lane);
-    if (lane == 0) sh.by = by;
+  if (n > 0 && by_stretches(a)) {
+    const int each = stretch_of(a, nw), b0 = warp * each, b1 = min(a.batch, b0 + each);
+    if (b >= b0 && b < b1) {
+      uint32_t mine;
+      const int at = b0 + ((b - b0) & ~31);
+      const uint32_t ahead = stretch_pages(a, b0, at, lane), inc = scan_pages(a, at, lane, mine);
+      const uint32_t before = ahead + __shfl_sync(0xffffffffu, inc - mine, b - at);
+      if (lane == 0) sh.hi[0] = before;                     // (of the stretch)
+    }
+    const uint32_t sum = stretch_pages(a, b0, b1, lane);
+    if (lane == 0) sh.lo[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t total = 0, before = sh.hi[0];
+      for (int w = 0; w < nw; ++w) {
+        total += sh.lo[w];
+        before += (w + 1) * each <= b ? sh.lo[w] : 0u;
+      }
+      sh.by = scorers_of(a, parts, row, n, total, before);
+    }
+  } else if (n > 0 && warp == 0) {           // (by one warp: it looks at all sequences)
+    uint32_t before = 0;
+    const uint32_t total = line_of(a, parts, b, lane, before);
+    if (lane == 0) sh.by = scorers_of(a, parts, row, n, total, before);
   }
   __syncthreads();
   grid_dep_sync();
