@@ -696,8 +696,11 @@ typedef struct {
 
 /*
  * New tokens into the 8-bit cache: queries and keys are normalised and rotated
- * as by sv_qk_norm_rope_append (results rounded to bf16 from more than fp32),
- * keys and values then rounded to e4m3.
+ * as by sv_qk_norm_rope_append, keys and values then rounded to e4m3.  Keys of
+ * finite rows are the exact results rounded to bf16 wherever fp32's error could
+ * decide it; queries are formed with more than fp32 within four of its last bits of a
+ * rounding boundary, so that one may be off by its last bf16 bit where the terms of its
+ * pair nearly cancel.
  *
  * q, k, v   : bf16 [N][H][d], [N][Hkv][d] twice, packed, with token strides as
  *             above.

@@ -13,9 +13,12 @@
 // growing page exact too, but for those that fall below e4m3's 2^-6.
 //
 // Measured: prompts of some 15,000 tokens in all, 28 query heads over 4, d 128, normed,
-// with three axes and the keys' bf16 rows 72.0 us, 4.1 TB/s, bound by instructions (65
-// % of issue slots); 16 single tokens of 32 heads 3.6 us, a launch; two questions of
-// 193 tokens, 4 heads over 2 4.7 us, the 16 rows that a warp forms one after the other.
+// with three axes and the keys' bf16 rows 72.2 us, 4.0 TB/s.  Neither issue (65 % of the
+// slots) nor memory (45 %) is full: 24.5 warps an SM, with 1.6 of a scheduler's 6.2 ready,
+// wait for one another's arithmetic, and at 64 registers the normed forms spill (rotate-half
+// 80 bytes stored and 148 loaded, interleaved 84 and 160, partly turned 96 and 180).  16
+// single tokens of 32 heads 3.6 us, a launch; two questions of 193 tokens, 4 heads over 2
+// 4.7 us, the 16 rows that a warp forms one after the other.
 #include "kernels.h"
 #include "kv8.cuh"
 #include "norm_rope.cuh"

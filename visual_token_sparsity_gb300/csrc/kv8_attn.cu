@@ -38,12 +38,14 @@
 // leaves fp32 partials, which the last of its CTAs joins (few rows) or a second
 // kernel (many), always in the order of the pieces.
 //
-// Measured, inputs out of L2: 4 query heads over 2 KV heads, 201 tokens 5.3 us; 16
-// sequences of 32 heads, 1440 + 128 tokens 43.0 us, 4.9 TB/s of cache rows; 8 ragged
-// sequences of 28 heads over 4, up to 12544 + 256 tokens 25.6 us, 3 of them the join's
-// kernel.  With a piece per warp they took 7.2, 41.8 and 28.0; with the rows
-// prefetched in registers instead of the ring the second took 45; with the next part's
-// lookups ahead of this one's join 5.6, 42.9 and 25.4 (registers spill at 16 heads).
+// Measured, inputs out of L2: 4 query heads over 2 KV heads, 201 tokens 5.0 us; 16
+// sequences of 32 heads, 1440 + 128 tokens 42.2 us, 5.0 TB/s of cache rows; 8 ragged
+// sequences of 28 heads over 4, up to 12544 + 256 tokens 25.2 us, 3 of them the join's
+// kernel; 3001 sequences of 320 + 32 tokens, 28 heads over 4, 196, with lengths of their
+// own 279.  Before the value product's reference of its own the first three took 5.3, 42.9
+// and 25.4; with a piece per warp 7.2, 41.8 and 28.0; with the rows prefetched in registers
+// instead of the ring the second took 45; with the next part's lookups ahead of this one's
+// join 5.6, 42.9 and 25.4 (registers spill at 16 heads).
 // Steps run at 6.5 TB/s in all; what is left is the chain lengths -> index -> page -> row
 // before the first one (some 7000 cycles of 38,000 in the third call) and the joins.
 #include "kernels.h"

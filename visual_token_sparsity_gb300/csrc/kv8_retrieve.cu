@@ -54,7 +54,12 @@ constexpr int kScoreWarps = 8, kScoreCtas = 5;   // per CTA, and CTAs per SM
 // are told apart by 2 e; twice that is taken:
 constexpr float kBand = 448.f / 4194304.f;
 constexpr float kBandMax = 272.f, kBandSum = 12.f;
-constexpr int kStagedKeys = 16384;       // keys of a row whose selection one CTA makes
+// Keys of a row whose selection one CTA makes.  Whole calls, head dim 128, by a CTA / by a
+// cluster: 4 rows of 6000 keys 20.4 / 15.2 us, of 16384 24.9 / 18.3, of 20000 31.4 / 22.2;
+// 32 rows 27.0 / 24.1, 38.5 / 31.9, 50.9 / 34.9; 128 rows 49.8 / 66.3, 73.6 / 97.0,
+// 113.9 / 109.2 (and of 30000 105.6 / 139.6).  One border for all: right for many rows, late
+// for few.
+constexpr int kStagedKeys = 16384;
 constexpr int kSliceKeys = 50176;        // keys that a CTA of a cluster keeps in shared memory
 
 // hi + lo = a + b.
@@ -1054,6 +1059,8 @@ static cudaError_t launch_select(Kernel kernel, bool (&attr_set)[64], int C, int
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
+  // (256 / 512 threads: 512 rows of 2880 keys 44.6 / 50.3 us, of 5000 75.1 / 76.6, of 8200
+  // 123.6 / 114.4; 4 rows 12.2 / 11.8, 15.4 / 15.0, 19.2 / 18.1)
   const int threads = C > 1 || a.n_vis >= 8192 ? kClusterThreads : 256;
   const size_t smem = most > 0 ? (size_t)((a.n_vis + C - 1) / C) * 4 : 0;
   return launch_dependent(kernel, dim3((unsigned)(C * a.batch * a.Hkv)), dim3(threads), smem, stream, a, args...);
@@ -1080,7 +1087,10 @@ static cudaError_t launch_d(const Kv8RetrieveArgs& a, int num_sms, cudaStream_t 
   uint32_t* far_keys = reinterpret_cast<uint32_t*>(at);      // (there where it is used)
   if (a.scores != nullptr) scores = a.scores;
   const bool sum = (long long)a.R * (a.H / a.Hkv) <= kFusedRows;
-  // (16000 rows for one key row by a CTA 227 us in all, by a cluster 30; 1351 29.7 and 13.3)
+  // (Query rows for one key row by a CTA / by a cluster, whole calls of 576 keys: 256 rows
+  // 12.3 / 13.1 us, 496 13.6 / 12.4, 1351 29.7 / 13.3, 16000 227 / 30.  Where key rows are
+  // many the clusters queue: 32 key rows of 512 16.9 / 25.3, of 2048 31.3 / 27.0; 128 of 512
+  // 25.4 / 60.5, of 2048 58.7 / 65.7.)
   const bool wide = (long long)a.R * (a.H / a.Hkv) >= 512 && rows <= num_sms;
   cudaError_t e = cudaSuccess;
   if (!sum)

@@ -21,10 +21,12 @@
 // stream), 10 the units and the TMA loads (11 makes the group of four whole that
 // gives registers up).
 //
-// Measured, inputs out of L2: 12800 tokens of 28 heads over 4, d 128 728 us, 1.61
-// PFLOP/s (82 % of what the device reaches on a plain matrix product); 4 x 3008 tokens
-// of 32 heads 227 us; 48 questions of up to 97 tokens 17.9 us; one of 176 tokens, 4
-// heads over 2, d 64 6.7 us.  What bounds the long ones: a tile takes a stream some
+// Measured, inputs out of L2: 12800 tokens of 28 heads over 4, d 128 730 us, 1.61
+// PFLOP/s (82 % of what the device reaches on a plain matrix product in a short burst),
+// and 790 us, 1.49 PFLOP/s, in seconds of calls at the power limit (85 % of a matrix
+// product there; SM clock 1.85 to 1.90 GHz against 2.07); 4 x 3008 tokens of 32 heads 228
+// and 245 us; 48 questions of up to 97 tokens 18.1 us; one of 176 tokens, 4 heads over 2,
+// d 64 6.6 us.  What bounds the long ones: a tile takes a stream some
 // 3100 cycles against 2048 in the products, as load and maximum of S (600) and the
 // weights (850) of a stream stand between its own two products; and some 3000 a unit
 // for its rows.  With sixteen softmax warps 880 / 264 us (registers spill), the
